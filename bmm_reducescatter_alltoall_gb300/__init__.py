@@ -102,6 +102,7 @@ def library() -> ctypes.CDLL:
     lib.bra_wait_selftest.restype = c_int
     lib.bra_version.argtypes = []
     lib.bra_version.restype = ctypes.c_char_p
+    moe.declare(lib)
     _lib = lib
     return lib
 
@@ -637,3 +638,9 @@ def fault_status(clear: bool = False) -> int:
     v = ctypes.c_int32(0)
     _check(library().bra_fault_status(ctypes.byref(v), 1 if clear else 0), "bra_fault_status")
     return int(v.value)
+
+
+from . import moe                      # noqa: E402  (uses the helpers above)
+from .moe import *                     # noqa: E402,F401,F403
+
+__all__ += moe.__all__

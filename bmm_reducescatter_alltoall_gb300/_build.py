@@ -67,6 +67,9 @@ KERNEL_SOURCES = {
     "repack_rows_kernel": "repack.cu",
     "mma_probe_kernel": "mma_probe.cu",
     "gather_probe_kernel": "gather_probe.cu",
+    "grouped_kernel": "grouped_tc.cu",
+    "bias_grad_kernel": "grouped_aux.cu",
+    "pack_rows_kernel": "grouped_aux.cu",
 }
 
 

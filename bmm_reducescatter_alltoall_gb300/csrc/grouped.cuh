@@ -1,0 +1,228 @@
+// What the kernels over ragged row groups share: the table of group offsets
+// and row tiles each CTA builds from the device counts, and the epilogue that
+// turns one accumulator quarter into masked row stores of any alignment.
+#pragma once
+
+#include "moe_internal.h"
+#include "tc_ptx.cuh"
+
+namespace bra {
+namespace grp {
+
+using namespace tc;
+
+// Offsets of the groups' rows and of their row tiles, in shared memory.
+struct GroupTable {
+  int32_t off[kMaxGroups + 1];    // first row of each group; off[E] = rows used
+  int32_t tile[kMaxGroups + 1];   // first row tile of each group; tile[E] = row tiles
+  int32_t bad;                    // a count is negative or the counts pass R
+};
+
+// Built by one warp.  The counts are loaded together (one latency), scanned in
+// 64 bits: counts may hold anything, and a table is only used when it is good.
+template <int BM>
+__device__ __forceinline__ void build_table(GroupTable* t, const int64_t* counts, int E, int64_t R,
+                                            int lane) {
+  int64_t c[kMaxGroups / 32];
+#pragma unroll
+  for (int i = 0; i < kMaxGroups / 32; ++i)
+    c[i] = i * 32 + lane < E ? __ldg(reinterpret_cast<const long long*>(counts) + i * 32 + lane) : 0;
+  int64_t rows = 0;
+  int32_t tiles = 0;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kMaxGroups / 32; ++i) {
+    if (i * 32 >= E) break;
+    bad = bad || c[i] < 0 || c[i] > R;
+    int64_t n = bad ? 0 : c[i];
+    int32_t m = (int32_t)((n + BM - 1) / BM);
+    const int64_t n0 = n;
+    const int32_t m0 = m;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t a = __shfl_up_sync(0xffffffffu, n, d);
+      const int32_t b = __shfl_up_sync(0xffffffffu, m, d);
+      if (lane >= d) {
+        n += a;
+        m += b;
+      }
+    }
+    if (i * 32 + lane < E) {
+      t->off[i * 32 + lane] = (int32_t)(rows + n - n0);
+      t->tile[i * 32 + lane] = tiles + m - m0;
+    }
+    rows += __shfl_sync(0xffffffffu, n, 31);
+    tiles += __shfl_sync(0xffffffffu, m, 31);
+  }
+  bad = __any_sync(0xffffffffu, bad) || rows > R;
+  if (lane == 0) {
+    t->off[E] = (int32_t)rows;
+    t->tile[E] = tiles;
+    t->bad = bad ? 1 : 0;
+  }
+}
+
+// Arrive on a leader's barrier (shared::cluster address) and add the bytes
+// this CTA's copies will complete on it.
+__device__ __forceinline__ void mbar_expect_tx_cluster(uint32_t cluster_bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
+                   cluster_bar),
+               "r"(bytes)
+               : "memory");
+}
+// Wait on a barrier that CTAs of the cluster arrive on (acquire at cluster
+// scope); bounded as mbar_wait.
+__device__ __forceinline__ bool mbar_try_acq(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+static __device__ __noinline__ bool mbar_wait_acq_slow(uint32_t bar, uint32_t parity,
+                                                       volatile int* abort_flag, int32_t* fault) {
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+      if (mbar_try_acq(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > kWaitTimeoutNs) {
+      *abort_flag = 1;
+      atomicExch(fault, (int32_t)BRA_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait_acq(uint32_t bar, uint32_t parity,
+                                              volatile int* abort_flag, int32_t* fault) {
+  return mbar_try_acq(bar, parity) || mbar_wait_acq_slow(bar, parity, abort_flag, fault);
+}
+
+// 16-bit element access of the two output types, and their bias type.
+template <typename T>
+struct Num;
+template <>
+struct Num<__half> {
+  static __device__ __forceinline__ float bias(const void* p, int64_t i) {
+    return __half2float(static_cast<const __half*>(p)[i]);
+  }
+};
+template <>
+struct Num<__nv_bfloat16> {
+  static __device__ __forceinline__ float bias(const void* p, int64_t i) {
+    return static_cast<const float*>(p)[i];
+  }
+};
+
+// Staging of one epilogue warp: 32 row segments of 64 outputs (128 bytes, and
+// up to 14 bytes of shift), 144 bytes apart: 16-byte writes of consecutive
+// lanes' rows and 16-byte reads along a row are both free of bank conflicts.
+constexpr int kSegStride = 144;
+constexpr int kSegBytes = 32 * kSegStride;
+
+// One warp's 32 accumulator rows (TMEM address t_base, this warp's lane
+// quarter), columns n0 .. n0+BN-1, to rows y0, y0 + ldy, ... of which `valid`
+// (<= 32, > 0) are stored, columns below N.  bias_s: BN floats in shared
+// memory, or 0.  zero: the accumulator holds nothing (an empty sum).
+// `aligned`: every row starts on a 16-byte boundary and N % 8 == 0.
+// tmem_done() runs after the last TMEM load.  Each value is rounded once.
+template <typename T, int BN, typename Done>
+__device__ __forceinline__ void store_rows(uint32_t t_base, T* y0, int64_t ldy, int valid, int n0,
+                                           int N, uint32_t seg, uint32_t bias_s, bool zero,
+                                           bool aligned, int lane, Done&& tmem_done) {
+  const uint32_t my = seg + (uint32_t)lane * kSegStride;
+  uint32_t v[64];
+  tmem_ld32(t_base, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+  tmem_ld32(t_base + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+#pragma unroll 1
+  for (int ch = 0; ch < BN / 64; ++ch) {
+    const int nc = n0 + ch * 64;
+    const int cols = min(64, N - nc);          // <= 0: past the matrix
+    tmem_ld_wait();
+    if (ch + 1 == BN / 64) tmem_done();
+    if (bias_s) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint4 b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = lds128e(bias_s + (uint32_t)(ch * 64 + q * 16 + i * 4) * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t* w = &v[q * 16 + i * 4];
+          w[0] = __float_as_uint(__uint_as_float(w[0]) + __uint_as_float(b[i].x));
+          w[1] = __float_as_uint(__uint_as_float(w[1]) + __uint_as_float(b[i].y));
+          w[2] = __float_as_uint(__uint_as_float(w[2]) + __uint_as_float(b[i].z));
+          w[3] = __float_as_uint(__uint_as_float(w[3]) + __uint_as_float(b[i].w));
+        }
+      }
+    }
+    uint32_t o[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      o[k] = zero ? 0u : Out<T>::pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+    if (aligned) {
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        sts128(my + g * 16, make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]));
+    } else {
+      // the segment shifted to its destination's place in a 16-byte chunk
+      const uint32_t d = (uint32_t)(reinterpret_cast<uintptr_t>(y0 + lane * ldy + nc) & 15u) >> 1;
+      const uint32_t at = my + (d >> 1) * 4;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const uint32_t w = (d & 1) ? __funnelshift_l(k ? o[k - 1] : 0u, o[k], 16) : o[k];
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + k * 4), "r"(w) : "memory");
+      }
+      if (d & 1) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 128), "r"(o[31] >> 16) : "memory");
+    }
+    if (ch + 1 < BN / 64) {
+      tmem_ld32(t_base + (ch + 1) * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+      tmem_ld32(t_base + (ch + 1) * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+    }
+    __syncwarp();
+    if (aligned) {
+      // 8 lanes to a row's 128 bytes, 4 rows an instruction
+      const int c8 = (lane & 7) * 8, r0 = lane >> 3;
+      if (c8 < cols) {
+        uint4 w[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[q] = lds128e(seg + (uint32_t)(4 * q + r0) * kSegStride + c8 * 2);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (4 * q + r0 < valid)
+            *reinterpret_cast<uint4*>(y0 + (4 * q + r0) * ldy + nc + c8) = w[q];
+      }
+    } else if (cols > 0) {
+      // (row, chunk) pairs: whole chunks as vectors, the partial ones at the
+      // segment's two ends element by element
+#pragma unroll 1
+      for (int u = lane; u < valid * 9; u += 32) {
+        const int r = u / 9, c = u - r * 9;
+        T* dst = y0 + r * ldy + nc;
+        const int d = (int)((reinterpret_cast<uintptr_t>(dst) & 15u) >> 1);
+        const int lo = max(c * 8, d), hi = min(c * 8 + 8, d + cols);   // in the shifted segment
+        if (lo >= hi) continue;
+        const uint4 w = lds128e(seg + (uint32_t)r * kSegStride + c * 16);
+        if (hi - lo == 8) {
+          *reinterpret_cast<uint4*>(dst - d + c * 8) = w;
+        } else {
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c * 8 + i >= lo && c * 8 + i < hi)
+              reinterpret_cast<uint16_t*>(dst)[c * 8 + i - d] =
+                  (uint16_t)(ws[i >> 1] >> ((i & 1) * 16));
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
+}  // namespace grp
+}  // namespace bra

@@ -1,0 +1,499 @@
+// Products grouped by expert with ragged row groups, on tcgen05 (sm_103a).
+//
+//   forward  y[r,:]  = x[r,:] W_e + b_e     for the rows r of group e
+//   wgrad    dW_e    = x_e^T dy_e           (zero for an empty group)
+//
+// (the gradient of x is the forward form with the weight read the other way).
+// The group sizes are on the device.  Every CTA builds the table of group
+// offsets and row tiles in shared memory (grouped.cuh) and walks the same
+// static tile list, so one launch covers all groups with no host sync.
+//
+// Tiles are 128*CG rows x BN columns with a K loop of 64, one CTA (CG = 1) or
+// a CTA pair (CG = 2, tcgen05.mma.cta_group::2) per tile; roles as in
+// fused_tc2.cu: a TMA producer, an MMA issuer, four epilogue warps on
+// alternating accumulators.  What is ragged:
+//   forward: a tile's rows start at any row (a TMA row coordinate has no
+//     alignment rule).  Rows past the group belong to the next group: they
+//     are computed and not stored, as an accumulator row depends on its own
+//     operand row alone.  At most 64 valid rows are fetched as 32-row boxes,
+//     so that a decoding batch's tiles move little beside the weights; operand
+//     rows that were not fetched hold whatever the stage held before.
+//   wgrad: the K loop runs over the group's rows, 64 at a time; both operands
+//     are read transposed (M- and N-major boxes of 64 columns x 64 rows).  In
+//     a group's last block the rows past its end must add nothing, and zero
+//     times another group's infinity would: warp 3 zeroes them in both
+//     operands (a box row is 128 bytes of shared memory, whatever the
+//     swizzle), up to the next multiple of 16, where the block's MMAs stop.
+// Every wait is bounded (about 4 s) and reports through the fault word.
+#include <cstring>
+#include <mutex>
+
+#include "grouped.cuh"
+
+namespace bra {
+
+__device__ int32_t g_bra_fault_word_grouped = 0;
+
+namespace {
+
+using namespace tc;
+using namespace grp;
+
+constexpr int BK = 64;
+constexpr int kGroupM = 8;                  // raster: row tiles of a super-row
+constexpr int THREADS = 256;                // 4 role warps, 4 epilogue warps
+constexpr int EPI_WARP0 = 4;
+constexpr int BAR_BYTES = 512;
+
+struct GroupedParams {
+  CUtensorMap ta;      // forward: x, boxes of 128 rows; wgrad: x, 64 x 64 boxes
+  CUtensorMap ta32;    // forward: x, boxes of 32 rows
+  CUtensorMap tb;      // forward: weights; wgrad: dy, 64 x 64 boxes
+  const void* bias;
+  void* y;
+  const int64_t* counts;
+  int32_t* status;
+  int64_t R, ldy;
+  int E, K, N;
+  int m_tiles, n_tiles, k_blocks;   // wgrad: row tiles of K; forward: K blocks
+  int b_kmajor, aligned;
+  uint32_t idesc;
+};
+
+template <int CG, int BN>
+struct GShape {
+  static constexpr int A_BYTES = 128 * BK * 2;
+  static constexpr int B_COLS = BN / CG;                 // columns held by one CTA
+  static constexpr int B_BYTES = B_COLS * BK * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int EPI_BYTES = 4 * (kSegBytes + BN * 4);
+  static constexpr int FIXED = BAR_BYTES + EPI_BYTES + (int)sizeof(GroupTable) + 1024;
+  static constexpr int FIT = (232448 - FIXED) / STAGE_BYTES;
+  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + FIXED;
+  static constexpr uint32_t TMEM_COLS = 2 * BN;
+  static_assert(STAGES >= 4, "ring");
+};
+
+// One tile of the walk.
+struct Tile {
+  int e, mt, nt;
+};
+
+template <bool WG>
+__device__ __forceinline__ Tile find_tile(const GroupedParams& p, const GroupTable* gt, int t,
+                                          int& e_hint) {
+  Tile r;
+  if (WG) {
+    const TileCoord c = tile_coord(t, p.m_tiles, p.n_tiles, kGroupM);
+    r.e = c.g;
+    r.mt = c.mt;
+    r.nt = c.nt;
+  } else {
+    // t only grows along a CTA's walk: go on from the last group
+    int e = e_hint;
+    while (gt->tile[e + 1] * p.n_tiles <= t) ++e;
+    e_hint = e;
+    const int first = gt->tile[e];
+    const TileCoord c =
+        tile_coord(t - first * p.n_tiles, gt->tile[e + 1] - first, p.n_tiles, kGroupM);
+    r.e = e;
+    r.mt = c.mt;
+    r.nt = c.nt;
+  }
+  return r;
+}
+
+template <typename T, int CG, int BN, bool WG>
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
+    grouped_kernel(const __grid_constant__ GroupedParams p) {
+  using S = GShape<CG, BN>;
+  constexpr int STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, A_BYTES = S::A_BYTES;
+  constexpr int BM = 128 * CG;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const uint32_t smem_base = smem_u32(smem);
+  uint8_t* bars = smem + STAGES * STAGE_BYTES;
+  const uint32_t bar_base = smem_u32(bars);
+  // barriers (8 bytes each): full, empty, tail (wgrad) per stage; tfull[2], tempty[2]
+  auto full_bar = [&](int s) { return bar_base + 8u * s; };
+  auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
+  auto tail_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (3 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (3 * STAGES + 2 + a); };
+  static_assert(8 * (3 * STAGES + 4) + 16 <= BAR_BYTES, "barrier area");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BAR_BYTES - 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_BYTES - 8);
+  GroupTable* gt = reinterpret_cast<GroupTable*>(bars + BAR_BYTES);
+  uint8_t* epi = bars + BAR_BYTES + ((sizeof(GroupTable) + 15) & ~15);
+  int32_t* fault = &g_bra_fault_word_grouped;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), CG);    // leader: one arrival per CTA of the pair
+      mbar_init(empty_bar(s), 1);
+      mbar_init(tail_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 4 * CG);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&p.ta);
+    if (!WG) tma_prefetch_desc(&p.ta32);
+    tma_prefetch_desc(&p.tb);
+  }
+  if (warp == 2) {
+    tmem_alloc<CG>(smem_u32(tmem_slot), S::TMEM_COLS);
+    tmem_relinquish<CG>();
+  }
+  if (warp == 3) build_table<BM>(gt, p.counts, p.E, p.R, lane);
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = gt->bad ? 0 : (WG ? p.E * p.m_tiles : gt->tile[p.E]) * p.n_tiles;
+  const int walk0 = blockIdx.x / CG, step = gridDim.x / CG;
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- TMA producer (every CTA) ----------------
+    const uint32_t leader_full0 = CG == 2 ? map_to_rank(full_bar(0), 0) : full_bar(0);
+    int stage = 0, hint = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    auto next = [&] {
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
+      if (CG == 2) tma_load_3d_pair(dst, m, bar, c0, c1, c2);
+      else tma_load_3d(dst, m, bar, c0, c1, c2);
+    };
+    auto expect = [&](uint32_t bar, uint32_t bytes) {
+      if (CG == 2) mbar_expect_tx_cluster(bar, bytes);
+      else mbar_expect_tx(bar, bytes);
+    };
+    for (int t = walk0; ok && t < total; t += step) {
+      const Tile c = find_tile<WG>(p, gt, t, hint);
+      const int r0 = gt->off[c.e], r1 = gt->off[c.e + 1];
+      const int b_col = c.nt * BN + (int)rank * S::B_COLS;
+      if (WG) {
+        const int a_col = c.mt * BM + (int)rank * 128;
+        for (int row = r0; row < r1; row += BK) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, fault)) {
+            ok = false;
+            break;
+          }
+          const uint32_t a_dst = smem_base + stage * STAGE_BYTES, b_dst = a_dst + A_BYTES;
+          const bool tail = r1 - row < BK;
+          const uint32_t fb = leader_full0 + 8u * stage, tb = tail_bar(stage);
+          if (tail) mbar_expect_tx(tb, STAGE_BYTES);   // warp 3 passes it on
+          else expect(fb, STAGE_BYTES);
+#pragma unroll
+          for (int i = 0; i < 2 + S::B_COLS / 64; ++i) {
+            const uint32_t dst = i < 2 ? a_dst + i * 8192 : b_dst + (i - 2) * 8192;
+            const CUtensorMap* m = i < 2 ? &p.ta : &p.tb;
+            const int col = i < 2 ? a_col + i * 64 : b_col + (i - 2) * 64;
+            if (tail) tma_load_3d(dst, m, tb, col, row, 0);
+            else load(dst, m, fb, col, row, 0);
+          }
+          next();
+        }
+      } else {
+        const int row = r0 + c.mt * BM + (int)rank * 128;
+        const int valid = min(128, r1 - row);        // <= 0: nothing of A to fetch
+        const int small = valid <= 64 ? (max(valid, 0) + 31) / 32 : -1;
+        const uint32_t bytes = (small < 0 ? A_BYTES : small * (A_BYTES / 4)) + S::B_BYTES;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, fault)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = leader_full0 + 8u * stage;
+          const uint32_t a_dst = smem_base + stage * STAGE_BYTES, b_dst = a_dst + A_BYTES;
+          expect(fb, bytes);
+          if (p.b_kmajor) {
+            load(b_dst, &p.tb, fb, kb * BK, b_col, c.e);
+          } else {
+#pragma unroll
+            for (int i = 0; i < S::B_COLS / 64; ++i)
+              load(b_dst + i * 8192, &p.tb, fb, b_col + i * 64, kb * BK, c.e);
+          }
+          if (small < 0) load(a_dst, &p.ta, fb, kb * BK, row, 0);
+          else
+            for (int i = 0; i < small; ++i)
+              load(a_dst + i * (A_BYTES / 4), &p.ta32, fb, kb * BK, row + i * 32, 0);
+          next();
+        }
+      }
+    }
+    if (!ok) spin_ns(2000000ull);   // let copies already issued land
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---------------- MMA issuer (leader only) ----------------
+    // K-major operands step 32 bytes per K = 16, transposed ones 16 box rows
+    const uint64_t a0 = WG ? smem_desc_sw128(smem_base, 8192, 1024)
+                           : smem_desc_sw128(smem_base, 16, 1024);
+    const bool bk = !WG && p.b_kmajor;
+    const uint64_t b0 = bk ? smem_desc_sw128(smem_base + A_BYTES, 16, 1024)
+                           : smem_desc_sw128(smem_base + A_BYTES, 8192, 1024);
+    const uint32_t a_step = WG ? 128u : 2u, b_step = bk ? 2u : 128u;
+    int stage = 0, acc = 0, hint = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int t = walk0; ok && t < total; t += step) {
+      int blocks = p.k_blocks, last = BK / 16;
+      if (WG) {
+        const Tile c = find_tile<WG>(p, gt, t, hint);
+        const int n = gt->off[c.e + 1] - gt->off[c.e];
+        blocks = (n + BK - 1) / BK;
+        last = ((n - 1) % BK + 16) / 16;
+      }
+      if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, fault)) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+      for (int kb = 0; kb < blocks; ++kb) {
+        const bool got = CG == 2 ? mbar_wait_acq(full_bar(stage), phase, abort_flag, fault)
+                                 : mbar_wait(full_bar(stage), phase, abort_flag, fault);
+        if (!got) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t so = (uint64_t)((stage * STAGE_BYTES) >> 4);
+        const int steps = WG && kb + 1 == blocks ? last : BK / 16;
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k)
+          if (k < steps)
+            tc_mma<CG>(d_tmem, a0 + so + a_step * k, b0 + so + b_step * k, p.idesc,
+                       (kb > 0 || k > 0) ? 1u : 0u);
+        if (CG == 2) tc_commit_pair(empty_bar(stage), 0x3);
+        else tc_commit(empty_bar(stage));
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (CG == 2) tc_commit_pair(tfull_bar(acc), 0x3);
+      else tc_commit(tfull_bar(acc));
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if (!ok) spin_ns(2000000ull);   // let MMAs already issued complete
+  } else if (WG && warp == 3) {
+    // ---------------- tail rows of a group's last block (every CTA) ----------------
+    const uint32_t leader_full0 = CG == 2 ? map_to_rank(full_bar(0), 0) : full_bar(0);
+    int stage = 0, hint = 0;
+    uint32_t used = 0;              // parity of each stage's tail barrier
+    for (int t = walk0; t < total; t += step) {
+      const Tile c = find_tile<WG>(p, gt, t, hint);
+      const int n = gt->off[c.e + 1] - gt->off[c.e];
+      const int blocks = (n + BK - 1) / BK, valid = n % BK;
+      if (blocks == 0) continue;
+      const int s = (stage + blocks - 1) % STAGES;
+      stage = (stage + blocks) % STAGES;
+      if (valid == 0) continue;
+      const bool got = mbar_wait(tail_bar(s), (used >> s) & 1u, abort_flag, fault);
+      if (!__all_sync(0xffffffffu, got)) break;
+      used ^= 1u << s;
+      const int stop = (valid + 15) & ~15;
+      const uint32_t base = smem_base + s * STAGE_BYTES;
+      for (int i = valid * 8 + lane; i < stop * 8; i += 32)
+#pragma unroll
+        for (int b = 0; b < 2 + S::B_COLS / 64; ++b)
+          sts128(base + b * 8192 + i * 16, make_uint4(0, 0, 0, 0));
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2) mbar_arrive_cluster(leader_full0 + 8u * s);
+        else mbar_arrive(full_bar(s));
+      }
+    }
+  } else if (warp >= EPI_WARP0) {
+    // ---------------- epilogue (every CTA, its own 128 rows) ----------------
+    const int q = warp & 3;
+    uint8_t* mine = epi + q * (kSegBytes + BN * 4);
+    const uint32_t seg = smem_u32(mine), bias_s = seg + kSegBytes;
+    const uint32_t leader_tempty0 = CG == 2 ? map_to_rank(tempty_bar(0), 0) : tempty_bar(0);
+    int acc = 0, hint = 0;
+    uint32_t acc_phase = 0;
+    for (int t = walk0; t < total; t += step) {
+      const Tile c = find_tile<WG>(p, gt, t, hint);
+      const int r0 = gt->off[c.e], r1 = gt->off[c.e + 1];
+      const int tile_row = c.mt * BM + (int)rank * 128 + q * 32;
+      const int n0 = c.nt * BN;
+      const int valid = min(32, (WG ? p.K : r1 - r0) - tile_row);
+      const int64_t row = WG ? (int64_t)c.e * p.K + tile_row : (int64_t)r0 + tile_row;
+      if (!WG && p.bias) {   // while the accumulator is being computed
+        for (int i = lane; i < BN; i += 32) {
+          const float b = n0 + i < p.N ? Num<T>::bias(p.bias, (int64_t)c.e * p.N + n0 + i) : 0.f;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias_s + i * 4), "f"(b) : "memory");
+        }
+        __syncwarp();
+      }
+      const bool waited = mbar_wait(tfull_bar(acc), acc_phase, abort_flag, fault);
+      if (!__all_sync(0xffffffffu, waited)) break;
+      tc_fence_after();
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2 && rank != 0) mbar_arrive_cluster(leader_tempty0 + 8u * acc);
+          else mbar_arrive(tempty_bar(acc));
+        }
+      };
+      if (valid > 0)
+        store_rows<T, BN>(tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(q * 32) << 16),
+                          static_cast<T*>(p.y) + row * p.ldy, p.ldy, valid, n0, p.N, seg,
+                          !WG && p.bias ? bias_s : 0u, WG && r1 == r0, p.aligned != 0, lane,
+                          release);
+      else
+        release();
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();   // no remote arrive or MMA of the pair still pending
+  if (threadIdx.x == 0 && p.status) {
+    if (gt->bad) atomicExch(p.status, (int32_t)BRA_ERR_INVALID);
+    else if (*abort_flag) atomicExch(p.status, (int32_t)BRA_ERR_TIMEOUT);
+  }
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc<CG>(tmem_base, S::TMEM_COLS);
+  }
+}
+
+// Clusters of the kernel that are resident at once, found on first use.
+template <typename T, int CG, int BN, bool WG>
+cudaError_t resident(int* clusters) {
+  static std::mutex mu;
+  static int known[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  int& n = known[dev & 63];
+  if (n == 0) {
+    constexpr int smem = GShape<CG, BN>::SMEM_BYTES;
+    e = cudaFuncSetAttribute(grouped_kernel<T, CG, BN, WG>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CG, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = CG;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int m = 0;
+    e = cudaOccupancyMaxActiveClusters(&m, grouped_kernel<T, CG, BN, WG>, &cfg);
+    if (e != cudaSuccess) return e;
+    n = m < 1 ? 1 : m;
+  }
+  *clusters = n;
+  return cudaSuccess;
+}
+
+template <typename T, int CG, int BN, bool WG>
+cudaError_t launch(const GroupedProblem& g, cudaStream_t st) {
+  using S = GShape<CG, BN>;
+  int clusters = 0;
+  cudaError_t e = resident<T, CG, BN, WG>(&clusters);
+  if (e != cudaSuccess) return e;
+  GroupedParams p;
+  std::memset(&p, 0, sizeof(p));
+  const CUtensorMapDataType dt =
+      g.dtype == BRA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const uint64_t K = g.K, N = g.N, R = g.R, E = g.E;
+  bool ok;
+  if (WG) {
+    ok = encode_3d(&p.ta, dt, g.x, K, R, 1, 64, BK, g.ldx) &&
+         encode_3d(&p.tb, dt, g.w, N, R, 1, 64, BK, g.ldw);
+  } else {
+    ok = encode_3d(&p.ta, dt, g.x, K, R, 1, BK, 128, g.ldx) &&
+         encode_3d(&p.ta32, dt, g.x, K, R, 1, BK, 32, g.ldx) &&
+         (g.wt ? encode_3d(&p.tb, dt, g.w, K, N, E, BK, S::B_COLS, g.ldw)
+               : encode_3d(&p.tb, dt, g.w, N, K, E, 64, BK, g.ldw));
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  p.bias = g.bias;
+  p.y = g.y;
+  p.counts = g.counts;
+  p.status = g.status;
+  p.R = g.R;
+  p.ldy = g.ldy;
+  p.E = g.E;
+  p.K = g.K;
+  p.N = g.N;
+  p.b_kmajor = g.wt;
+  p.aligned = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0 && g.N % 8 == 0;
+  p.idesc = make_idesc(g.dtype == BRA_BF16, 128 * CG, BN, !WG && g.wt) | (WG ? 1u << 15 : 0u);
+  constexpr int BM = 128 * CG;
+  p.m_tiles = (g.K + BM - 1) / BM;
+  p.n_tiles = (g.N + BN - 1) / BN;
+  p.k_blocks = (g.K + BK - 1) / BK;
+  const int64_t groups = g.R < g.E ? g.R : g.E;
+  int64_t tiles = WG ? (int64_t)g.E * p.m_tiles : g.R / BM + groups;   // at most
+  tiles *= p.n_tiles;
+  if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  const int nc = (int)(tiles < clusters ? tiles : clusters);
+  grouped_kernel<T, CG, BN, WG><<<CG * nc, THREADS, S::SMEM_BYTES, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int CG, int BN, bool WG>
+cudaError_t launch_t(const GroupedProblem& g, cudaStream_t st) {
+  return g.dtype == BRA_BF16 ? launch<__nv_bfloat16, CG, BN, WG>(g, st)
+                             : launch<__half, CG, BN, WG>(g, st);
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st) {
+  // Rows to an expert on average, and the most experts that can have rows.
+  const int64_t avg = g.R / g.E, groups = g.R < g.E ? g.R : g.E;
+  if (avg >= 128) return launch_t<2, 256, false>(g, st);
+  // Few rows: the weights' bytes bound the call, and narrow tiles spread them
+  // over the SMs.
+  const int64_t mt = g.R / 128 + groups;
+  if (mt * ((g.N + 255) / 256) >= 152) return launch_t<1, 256, false>(g, st);
+  if (mt * ((g.N + 127) / 128) >= 152) return launch_t<1, 128, false>(g, st);
+  return launch_t<1, 64, false>(g, st);
+}
+
+cudaError_t launch_grouped_wgrad(const GroupedProblem& g, cudaStream_t st) {
+  if (g.K > 128 && g.N > 128) return launch_t<2, 256, true>(g, st);
+  return launch_t<1, 128, true>(g, st);
+}
+
+cudaError_t read_grouped_fault_word(int32_t* code, int clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(code, g_bra_fault_word_grouped, sizeof(int32_t));
+  if (e != cudaSuccess) return e;
+  if (clear) {
+    const int32_t z = 0;
+    e = cudaMemcpyToSymbol(g_bra_fault_word_grouped, &z, sizeof(int32_t));
+  }
+  return e;
+}
+
+}  // namespace bra

@@ -1,0 +1,271 @@
+// Host entry points of the ragged expert operators: argument checks and
+// launches.  Every rule cited here is stated in include/bra_moe.h.
+#include <cstring>
+
+#include "moe_internal.h"
+
+namespace {
+
+using namespace bra;
+
+bool off_by(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
+
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  if (!a || !b || an <= 0 || bn <= 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
+// Bytes of `rows` rows of n elements, ld apart (the last one without padding).
+int64_t span(int64_t rows, int64_t ld, int64_t n, int64_t es) {
+  return rows > 0 ? ((rows - 1) * ld + n) * es : 0;
+}
+
+struct GroupedSizes {
+  int64_t R, E, K, N, xp, yp;
+};
+
+int check_sizes(const bra_grouped_args* a, GroupedSizes* s) {
+  if (!a) return BRA_ERR_NULLPTR;
+  constexpr int64_t kWide = int64_t(1) << 24;
+  if (a->rows < 0 || a->rows >= (int64_t(1) << 31) || a->groups < 1 ||
+      a->groups > BRA_MAX_GROUPS || a->in < 1 || a->in > kWide || a->out < 1 || a->out > kWide)
+    return BRA_ERR_INVALID;
+  if (a->dtype != BRA_FP16 && a->dtype != BRA_BF16) return BRA_ERR_INVALID;
+  *s = {a->rows, a->groups, a->in, a->out, a->x_pitch ? a->x_pitch : a->in,
+        a->y_pitch ? a->y_pitch : a->out};
+  if (s->xp < s->K || s->yp < s->N || s->xp > (int64_t(1) << 36) || s->yp > (int64_t(1) << 36))
+    return BRA_ERR_INVALID;
+  if (off_by(a->status, 3u) || off_by(a->workspace, 255u) || a->workspace_bytes < 0 ||
+      (!a->workspace && a->workspace_bytes != 0))
+    return BRA_ERR_INVALID;
+  return BRA_OK;
+}
+
+// An operand's copy: rows of n elements at a pitch of whole 128-byte lines.
+struct Copy {
+  bool need = false;
+  int64_t rows = 0, n = 0, ld = 0, pitch = 0, bytes = 0;
+};
+
+Copy copy_of(const void* p, int64_t rows, int64_t n, int64_t ld) {
+  Copy c;
+  c.rows = rows;
+  c.n = n;
+  c.ld = ld;
+  c.pitch = ld;
+  // TMA: 16-byte aligned base and pitch, pitch below 2^40 bytes
+  c.need = rows > 0 && (off_by(p, 15u) || ld % 8 != 0);
+  if (c.need) {
+    c.pitch = (n + 63) / 64 * 64;
+    c.bytes = (rows * c.pitch * 2 + 255) / 256 * 256;
+  }
+  return c;
+}
+
+// Hands out workspace and enqueues the copies.
+struct Workspace {
+  uint8_t* at;
+  int64_t left;
+  int rc = BRA_OK;
+  const void* take(const void* src, const Copy& c, cudaStream_t st) {
+    if (!c.need || rc != BRA_OK) return src;
+    if (!at) {
+      rc = BRA_ERR_UNSUPPORTED;
+      return src;
+    }
+    if (left < c.bytes) {
+      rc = BRA_ERR_INVALID;
+      return src;
+    }
+    void* dst = at;
+    at += c.bytes;
+    left -= c.bytes;
+    if (launch_pack_rows(src, c.ld, dst, c.pitch, c.rows, c.n, st) != cudaSuccess) rc = BRA_ERR_CUDA;
+    return dst;
+  }
+};
+
+// What the copies need, against what the caller gave.
+int check_workspace(const bra_grouped_args* a, int64_t need) {
+  if (need == 0) return BRA_OK;
+  if (!a->workspace) return BRA_ERR_UNSUPPORTED;
+  return a->workspace_bytes >= need ? BRA_OK : BRA_ERR_INVALID;
+}
+
+int status_of(cudaError_t e) {
+  return e == cudaSuccess ? BRA_OK : e == cudaErrorInvalidValue ? BRA_ERR_UNSUPPORTED
+                                                                : BRA_ERR_CUDA;
+}
+
+int clear_status(int32_t* status, cudaStream_t st) {
+  if (!status) return BRA_OK;
+  return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;
+}
+
+// The weight as rows: (E*K) rows of N, or (E*N) rows of K when transposed.
+Copy weight_copy(const void* w, const bra_grouped_args* a, const GroupedSizes& s) {
+  const int64_t n = a->transpose_weight ? s.K : s.N, rows = a->transpose_weight ? s.N : s.K;
+  return copy_of(w, s.E * rows, n, n);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t grouped_matmul_workspace_size(const void* x, const void* weight,
+                                      const bra_grouped_args* args) {
+  GroupedSizes s;
+  const int rc = check_sizes(args, &s);
+  if (rc != BRA_OK) return -rc;
+  if (s.R == 0) return 0;
+  return copy_of(x, s.R, s.K, s.xp).bytes + weight_copy(weight, args, s).bytes;
+}
+
+int64_t grouped_matmul_grad_workspace_size(const void* dy, const void* x, const void* weight,
+                                           int want_dx, int want_dweight,
+                                           const bra_grouped_args* args) {
+  GroupedSizes s;
+  const int rc = check_sizes(args, &s);
+  if (rc != BRA_OK) return -rc;
+  if (s.R == 0) return 0;
+  int64_t n = 0;
+  if (want_dx || want_dweight) n += copy_of(dy, s.R, s.N, s.yp).bytes;
+  if (want_dx) n += weight_copy(weight, args, s).bytes;
+  if (want_dweight) n += copy_of(x, s.R, s.K, s.xp).bytes;
+  return n;
+}
+
+int grouped_matmul(const void* x, const void* weight, const void* bias, const int64_t* counts,
+                   void* y, const bra_grouped_args* args, bra_stream_t stream) {
+  GroupedSizes s;
+  int rc = check_sizes(args, &s);
+  if (rc != BRA_OK) return rc;
+  if (!weight || !counts || (s.R > 0 && (!x || !y))) return BRA_ERR_NULLPTR;
+  const int64_t bes = args->dtype == BRA_BF16 ? 4 : 2;
+  if (off_by(x, 1u) || off_by(weight, 1u) || off_by(y, 1u) || off_by(bias, bes - 1) ||
+      off_by(counts, 7u))
+    return BRA_ERR_INVALID;
+  const Copy cx = copy_of(x, s.R, s.K, s.xp), cw = weight_copy(weight, args, s);
+  const int64_t yb = span(s.R, s.yp, s.N, 2);
+  if (overlap(y, yb, x, span(s.R, s.xp, s.K, 2)) || overlap(y, yb, weight, s.E * s.K * s.N * 2) ||
+      overlap(y, yb, bias, s.E * s.N * bes) || overlap(y, yb, counts, s.E * 8) ||
+      overlap(y, yb, args->workspace, args->workspace_bytes))
+    return BRA_ERR_INVALID;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (s.R == 0) return clear_status(args->status, st);
+  if ((rc = check_workspace(args, cx.bytes + cw.bytes)) != BRA_OK) return rc;
+  if ((rc = clear_status(args->status, st)) != BRA_OK) return rc;
+  Workspace ws{static_cast<uint8_t*>(args->workspace), args->workspace_bytes};
+  GroupedProblem g;
+  std::memset(&g, 0, sizeof(g));
+  g.x = ws.take(x, cx, st);
+  g.w = ws.take(weight, cw, st);
+  if (ws.rc != BRA_OK) return ws.rc;
+  g.bias = bias;
+  g.y = y;
+  g.counts = counts;
+  g.status = args->status;
+  g.R = s.R;
+  g.ldx = cx.pitch;
+  g.ldw = cw.pitch;
+  g.ldy = s.yp;
+  g.E = (int)s.E;
+  g.K = (int)s.K;
+  g.N = (int)s.N;
+  g.dtype = args->dtype;
+  g.wt = args->transpose_weight ? 1 : 0;
+  return status_of(launch_grouped_fwd(g, st));
+}
+
+int grouped_matmul_grad(const void* dy, const void* x, const void* weight, const int64_t* counts,
+                        void* dx, void* dweight, void* dbias, const bra_grouped_args* args,
+                        bra_stream_t stream) {
+  GroupedSizes s;
+  int rc = check_sizes(args, &s);
+  if (rc != BRA_OK) return rc;
+  if (!counts || (!dx && !dweight && !dbias) || (s.R > 0 && !dy) || (dx && !weight) ||
+      (dweight && s.R > 0 && !x))
+    return BRA_ERR_NULLPTR;
+  const int64_t bes = args->dtype == BRA_BF16 ? 4 : 2;
+  if (off_by(dy, 1u) || off_by(x, 1u) || off_by(weight, 1u) || off_by(dx, 1u) ||
+      off_by(dweight, 1u) || off_by(dbias, bes - 1) || off_by(counts, 7u))
+    return BRA_ERR_INVALID;
+  const bool wt = args->transpose_weight != 0;
+  const Copy cd = copy_of(dy, s.R, s.N, s.yp), cx = copy_of(x, s.R, s.K, s.xp),
+             cw = weight_copy(weight, args, s);
+  struct Buf {
+    const void* p;
+    int64_t n;
+  };
+  const int64_t wb = s.E * s.K * s.N * 2;
+  const Buf outs[3] = {{dx, s.R * s.K * 2}, {dweight, wb}, {dbias, s.E * s.N * bes}};
+  const Buf ins[5] = {{dy, span(s.R, s.yp, s.N, 2)},
+                      {x, span(s.R, s.xp, s.K, 2)},
+                      {weight, wb},
+                      {counts, s.E * 8},
+                      {args->workspace, args->workspace_bytes}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Buf& b : ins)
+      if (overlap(outs[i].p, outs[i].n, b.p, b.n)) return BRA_ERR_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return BRA_ERR_INVALID;
+  }
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (s.R == 0) {
+    if (dweight && cudaMemsetAsync(dweight, 0, (size_t)wb, st) != cudaSuccess) return BRA_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, (size_t)(s.E * s.N * bes), st) != cudaSuccess)
+      return BRA_ERR_CUDA;
+    return clear_status(args->status, st);
+  }
+  const int64_t need = (dx || dweight ? cd.bytes : 0) + (dx ? cw.bytes : 0) + (dweight ? cx.bytes : 0);
+  if ((rc = check_workspace(args, need)) != BRA_OK) return rc;
+  if ((rc = clear_status(args->status, st)) != BRA_OK) return rc;
+  Workspace ws{static_cast<uint8_t*>(args->workspace), args->workspace_bytes};
+  GroupedProblem g;
+  std::memset(&g, 0, sizeof(g));
+  g.counts = counts;
+  g.status = args->status;
+  g.R = s.R;
+  g.E = (int)s.E;
+  g.dtype = args->dtype;
+  const void* d = dx || dweight ? ws.take(dy, cd, st) : dy;
+  if (dx) {
+    // dx = dy W^T: the contraction runs over N, the weight's layout as stored
+    // is the other one seen from here
+    g.x = d;
+    g.w = ws.take(weight, cw, st);
+    if (ws.rc != BRA_OK) return ws.rc;
+    g.y = dx;
+    g.ldx = cd.pitch;
+    g.ldw = cw.pitch;
+    g.ldy = s.K;
+    g.K = (int)s.N;
+    g.N = (int)s.K;
+    g.wt = wt ? 0 : 1;
+    if ((rc = status_of(launch_grouped_fwd(g, st))) != BRA_OK) return rc;
+  }
+  if (dweight) {
+    const void* xs = ws.take(x, cx, st);
+    if (ws.rc != BRA_OK) return ws.rc;
+    // (E, N, K) gradients are the same product with the operands exchanged
+    g.x = wt ? d : xs;
+    g.w = wt ? xs : d;
+    g.ldx = wt ? cd.pitch : cx.pitch;
+    g.ldw = wt ? cx.pitch : cd.pitch;
+    g.y = dweight;
+    g.K = (int)(wt ? s.N : s.K);
+    g.N = (int)(wt ? s.K : s.N);
+    g.ldy = g.N;
+    g.wt = 0;
+    if ((rc = status_of(launch_grouped_wgrad(g, st))) != BRA_OK) return rc;
+  }
+  if (dbias) {
+    BiasGradProblem b = {dy, dbias, counts, args->status, s.R, s.yp, (int)s.E, (int)s.N,
+                         args->dtype};
+    if ((rc = status_of(launch_bias_grad(b, st))) != BRA_OK) return rc;
+  }
+  return BRA_OK;
+}
+
+}  // extern "C"

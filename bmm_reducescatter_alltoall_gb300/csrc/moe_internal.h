@@ -1,0 +1,47 @@
+// Internal declarations of the ragged expert operators: the grouped products,
+// the 4-bit microscaled formats, the router and the row permutation.
+// Not installed; the public ABI is include/bra_moe.h.
+#pragma once
+
+#include "bra_internal.h"
+#include "bra_moe.h"
+
+namespace bra {
+
+// Groups of one call: the table of group offsets lives in shared memory.
+constexpr int kMaxGroups = BRA_MAX_GROUPS;
+
+// y = x W_e (+ bias) over row groups, or dW_e = x_e^T dy_e.
+struct GroupedProblem {
+  const void* x;         // [R][ldx], K used
+  const void* w;         // forward: weights; wgrad: dy [R][ldw], N used
+  const void* bias;      // forward: [E][N] or nullptr
+  void* y;               // forward: [R][ldy]; wgrad: [E][K][N]
+  const int64_t* counts; // device [E]
+  int32_t* status;       // device, optional
+  int64_t R, ldx, ldw, ldy;
+  int E, K, N;
+  int dtype;             // BRA_FP16 | BRA_BF16
+  int wt;                // forward: weights stored (E, N, K)
+};
+// Operands must be TMA-ready: pointers 16-byte aligned, row pitches a
+// multiple of 8 elements.  cudaErrorInvalidValue if a map cannot be encoded.
+cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st);
+cudaError_t launch_grouped_wgrad(const GroupedProblem& g, cudaStream_t st);
+// db_e = the sum of the rows of dy_e, in fp16 (FP16) or fp32 (BF16).
+struct BiasGradProblem {
+  const void* dy;
+  void* db;
+  const int64_t* counts;
+  int32_t* status;
+  int64_t R, ld;
+  int E, N, dtype;
+};
+cudaError_t launch_bias_grad(const BiasGradProblem& g, cudaStream_t st);
+// Copies `rows` rows of `len` 16-bit elements, ld apart, to rows `pitch` apart
+// (a multiple of 8) at a 16-byte aligned dst.
+cudaError_t launch_pack_rows(const void* src, int64_t ld, void* dst, int64_t pitch, int64_t rows,
+                             int64_t len, cudaStream_t st);
+cudaError_t read_grouped_fault_word(int32_t* code, int clear);
+
+}  // namespace bra

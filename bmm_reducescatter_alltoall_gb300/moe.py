@@ -1,0 +1,252 @@
+"""Ragged expert operators: products grouped by expert, and their gradients.
+
+Bindings of include/bra_moe.h in the manner of the package's other calls: each
+function has a `_plan` form that checks its tensors once and returns a Plan,
+and the one-shot form is that plan run once.  Rows are sorted by expert and
+`counts` (CUDA int64, one per expert) says how many each has.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import bmm_reducescatter_alltoall_gb300 as _bra
+
+__all__ = ["GroupedArgs", "MAX_GROUPS", "grouped_matmul", "grouped_matmul_plan",
+           "grouped_matmul_grad", "grouped_matmul_grad_plan"]
+
+MAX_GROUPS = 512
+
+
+class GroupedArgs(ctypes.Structure):
+    """bra_grouped_args of the C header."""
+    _fields_ = [("rows", ctypes.c_int64), ("groups", ctypes.c_int64), ("in_", ctypes.c_int64),
+                ("out", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("transpose_weight", ctypes.c_int32), ("x_pitch", ctypes.c_int64),
+                ("y_pitch", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64), ("status", ctypes.c_void_p)]
+
+
+def declare(lib) -> None:
+    """Argument types of the library's functions (called once when it is loaded)."""
+    vp, i64, i32, c_int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
+    gp = ctypes.POINTER(GroupedArgs)
+    lib.grouped_matmul.argtypes = [vp, vp, vp, vp, vp, gp, vp]
+    lib.grouped_matmul.restype = c_int
+    lib.grouped_matmul_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, gp, vp]
+    lib.grouped_matmul_grad.restype = c_int
+    lib.grouped_matmul_workspace_size.argtypes = [vp, vp, gp]
+    lib.grouped_matmul_workspace_size.restype = i64
+    lib.grouped_matmul_grad_workspace_size.argtypes = [vp, vp, vp, c_int, c_int, gp]
+    lib.grouped_matmul_grad_workspace_size.restype = i64
+
+
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t, what: str, dtype=None, shape=None) -> int:
+    """Row pitch of a 2-D CUDA tensor whose rows are contiguous (0 = dense)."""
+    torch = _bra._torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor (got {t.device})")
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D (got shape {tuple(t.shape)})")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype} (got {t.dtype})")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return 0
+    r, n = t.shape
+    # strides of unit dimensions address nothing
+    pitch = t.stride(0) if r > 1 else n
+    if (n > 1 and t.stride(1) != 1) or pitch < n:
+        raise ValueError(f"{what} must have contiguous rows (got strides {t.stride()})")
+    return 0 if pitch == n else pitch
+
+
+def _dense(t, what: str, dtype, shape):
+    _bra._dev_tensor(t, what, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _counts(counts, groups: Optional[int] = None):
+    torch = _bra._torch()
+    _bra._dev_tensor(counts, "counts", torch.int64)
+    if counts.dim() != 1 or (groups is not None and counts.numel() != groups):
+        raise ValueError(f"counts must be ({groups if groups is not None else 'E'},), got "
+                         f"{tuple(counts.shape)}")
+    return counts
+
+
+def _status(status) -> Optional[int]:
+    if status is None:
+        return None
+    torch = _bra._torch()
+    _bra._dev_tensor(status, "status", torch.int32)
+    if status.numel() < 1:
+        raise ValueError("status must have at least one element")
+    return status.data_ptr()
+
+
+def _same_device(first, *others) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"every tensor must be on {first.device} (got {t.device})")
+
+
+def _take_workspace(workspace, need: int, device, args):
+    """Resolves `workspace` ("auto", None or a tensor) against `need` bytes."""
+    torch = _bra._torch()
+    if need < 0:
+        raise _bra.BraError(-need, "workspace size")
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError('workspace must be a CUDA tensor, None or "auto"')
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    if workspace is not None:
+        if not (workspace.is_cuda and workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        if workspace.numel():
+            args.workspace = workspace.data_ptr()
+            args.workspace_bytes = workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def _weight_dims(weight, transpose_weight: bool):
+    torch = _bra._torch()
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a torch.Tensor")
+    if weight.dim() != 3:
+        raise ValueError(f"weight must be 3-D (got shape {tuple(weight.shape)})")
+    E, a, b = weight.shape
+    return (E, b, a) if transpose_weight else (E, a, b)
+
+
+def _bias_dtype(dt):
+    torch = _bra._torch()
+    return torch.float16 if dt == torch.float16 else torch.float32
+
+
+def _grouped_args(R, E, K, N, dt, transpose_weight, xp, yp, status) -> GroupedArgs:
+    a = GroupedArgs()
+    a.rows, a.groups, a.in_, a.out = R, E, K, N
+    a.dtype = _bra._fused_dtype(dt)
+    a.transpose_weight = 1 if transpose_weight else 0
+    a.x_pitch, a.y_pitch = xp, yp
+    a.status = _status(status)
+    return a
+
+
+def grouped_matmul_plan(x, weight, counts, bias=None, out=None, transpose_weight: bool = False,
+                        workspace="auto", status=None):
+    """grouped_matmul prepared once (see Plan); plan.run() returns out."""
+    torch = _bra._torch()
+    E, K, N = _weight_dims(weight, transpose_weight)
+    dt = weight.dtype
+    _bra._fused_dtype(dt)
+    _dense(weight, "weight", dt, weight.shape)
+    xp = _rows(x, "x", dt)
+    if x.shape[1] != K:
+        raise ValueError(f"x has rows of {x.shape[1]}, weight takes {K}")
+    R = x.shape[0]
+    _counts(counts, E)
+    if bias is not None:
+        _dense(bias, "bias", _bias_dtype(dt), (E, N))
+    if out is None:
+        out = torch.empty((R, N), dtype=dt, device=x.device)
+    yp = _rows(out, "out", dt, (R, N))
+    _same_device(x, weight, counts, bias, out, status)
+    a = _grouped_args(R, E, K, N, dt, transpose_weight, xp, yp, status)
+    lib = _bra.library()
+    need = lib.grouped_matmul_workspace_size(_ptr(x), _ptr(weight), ctypes.byref(a))
+    workspace = _take_workspace(workspace, need, x.device, a)
+    args = (_ptr(x), _ptr(weight), _ptr(bias), _ptr(counts), _ptr(out), ctypes.byref(a))
+    return _bra.Plan(lib.grouped_matmul, args, "grouped_matmul", out,
+                     (x, weight, bias, counts, a, workspace, status))
+
+
+def grouped_matmul(x, weight, counts, bias=None, out=None, transpose_weight: bool = False,
+                   workspace="auto", status=None, stream=None):
+    """y[r] = x[r] @ weight[e] + bias[e] for the rows r of each expert e.
+
+    x: CUDA (R, K), rows sorted by expert (a row-pitched view is read in
+    place).  weight: (E, K, N), or (E, N, K) with transpose_weight; fp16 or
+    bf16, as x.  counts: CUDA int64 (E,), rows of each expert, on the device;
+    their sum may be below R: the rows after it are not written.  bias: None
+    or (E, N), fp16 for fp16 and fp32 for bf16.  workspace: scratch memory
+    for operands whose rows lack a 16-byte pitch ("auto": from torch's
+    allocator, only when needed).  status: optional CUDA int32, ERR_INVALID
+    when the counts were refused (nothing is written then).  Returns out
+    (R, N), allocated when None.  Asynchronous on `stream`."""
+    return grouped_matmul_plan(x, weight, counts, bias, out, transpose_weight, workspace,
+                               status).run(stream)
+
+
+def grouped_matmul_grad_plan(dy, x, weight, counts, bias=None, dx=None, dweight=None, dbias=None,
+                             want=("dx", "dweight", "dbias"), transpose_weight: bool = False,
+                             workspace="auto", status=None):
+    """grouped_matmul_grad prepared once (see Plan); plan.run() returns its dict."""
+    torch = _bra._torch()
+    unknown = set(want) - {"dx", "dweight", "dbias"}
+    if unknown:
+        raise ValueError(f"want takes dx, dweight and dbias (got {sorted(unknown)})")
+    E, K, N = _weight_dims(weight, transpose_weight)
+    dt = weight.dtype
+    _bra._fused_dtype(dt)
+    _dense(weight, "weight", dt, weight.shape)
+    yp = _rows(dy, "dy", dt)
+    R = dy.shape[0]
+    if dy.shape[1] != N:
+        raise ValueError(f"dy has rows of {dy.shape[1]}, weight gives {N}")
+    xp = _rows(x, "x", dt, (R, K))
+    _counts(counts, E)
+    bdt = _bias_dtype(dt)
+    if bias is not None:
+        _dense(bias, "bias", bdt, (E, N))
+    new = lambda shape, d: torch.empty(shape, dtype=d, device=dy.device)   # noqa: E731
+    if "dx" in want:
+        dx = _dense(new((R, K), dt) if dx is None else dx, "dx", dt, (R, K))
+    elif dx is not None:
+        raise ValueError("dx was given and is not wanted")
+    if "dweight" in want:
+        dweight = _dense(new(tuple(weight.shape), dt) if dweight is None else dweight, "dweight",
+                         dt, weight.shape)
+    elif dweight is not None:
+        raise ValueError("dweight was given and is not wanted")
+    if "dbias" in want and (bias is not None or dbias is not None):
+        dbias = _dense(new((E, N), bdt) if dbias is None else dbias, "dbias", bdt, (E, N))
+    elif dbias is not None:
+        raise ValueError("dbias was given and is not wanted")
+    if dx is None and dweight is None and dbias is None:
+        raise ValueError("no gradient is wanted")
+    _same_device(dy, x, weight, counts, bias, dx, dweight, dbias, status)
+    a = _grouped_args(R, E, K, N, dt, transpose_weight, xp, yp, status)
+    lib = _bra.library()
+    need = lib.grouped_matmul_grad_workspace_size(_ptr(dy), _ptr(x), _ptr(weight), dx is not None,
+                                                  dweight is not None, ctypes.byref(a))
+    workspace = _take_workspace(workspace, need, dy.device, a)
+    args = (_ptr(dy), _ptr(x), _ptr(weight), _ptr(counts), _ptr(dx), _ptr(dweight), _ptr(dbias),
+            ctypes.byref(a))
+    result = {"dx": dx, "dweight": dweight, "dbias": dbias}
+    return _bra.Plan(lib.grouped_matmul_grad, args, "grouped_matmul_grad", result,
+                     (dy, x, weight, bias, counts, a, workspace, status))
+
+
+def grouped_matmul_grad(dy, x, weight, counts, bias=None, dx=None, dweight=None, dbias=None,
+                        want=("dx", "dweight", "dbias"), transpose_weight: bool = False,
+                        workspace="auto", status=None, stream=None) -> dict:
+    """Gradients of grouped_matmul for the output's gradient dy (R, N).
+
+    Returns {'dx': (R, K), 'dweight': the weight's shape, 'dbias': (E, N)},
+    with None for what `want` leaves out and for dbias when there is no bias
+    (neither `bias` nor an output `dbias` given).  Experts without rows get
+    zero; rows of dx after the counts' sum are not written.  Results do not
+    change from run to run."""
+    return grouped_matmul_grad_plan(dy, x, weight, counts, bias, dx, dweight, dbias, want,
+                                    transpose_weight, workspace, status).run(stream)

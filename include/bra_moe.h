@@ -1,0 +1,113 @@
+/*
+ * bra_moe.h -- ragged expert operators of libbmmrsa2a.so: matrix products
+ * grouped by expert with row groups of any size, and their gradients.
+ *
+ * They work on what a variable-count exchange delivers: one matrix of rows
+ * sorted by expert, and the number of rows of each expert in device memory
+ * (int64, the type of all_to_all_v's counts).  The conventions of
+ * bmm_rs_a2a.h hold: device pointers, row-major tensors, work enqueued on
+ * `stream`, status codes, no device memory allocated, thread-safe, no state
+ * from one call to the next.
+ */
+#ifndef BRA_MOE_H
+#define BRA_MOE_H
+
+#include "bmm_rs_a2a.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Most row groups (experts) of one call. */
+#define BRA_MAX_GROUPS 512
+
+/* ------------------------------------------------------------------------ */
+/* Products grouped by expert                                                */
+/* ------------------------------------------------------------------------ */
+
+/* Sizes and options of a grouped product.  Zero-initialise. */
+typedef struct {
+  int64_t rows;        /* R: rows of x, y and dy, at most 2^31 - 1            */
+  int64_t groups;      /* E: 1 .. BRA_MAX_GROUPS                              */
+  int64_t in;          /* K: 1 .. 2^24                                        */
+  int64_t out;         /* N: 1 .. 2^24                                        */
+  int32_t dtype;       /* BRA_FP16 or BRA_BF16: x, weight, y and gradients    */
+  int32_t transpose_weight;  /* non-zero: weight (and dweight) is (E, N, K)   */
+  int64_t x_pitch;     /* elements between rows of x; 0 = K                   */
+  int64_t y_pitch;     /* elements between rows of y (forward) or dy (grad); 0 = N */
+  void* workspace;     /* 256-byte aligned, or NULL                           */
+  int64_t workspace_bytes;
+  int32_t* status;     /* device int32 of this call, or NULL (see below)      */
+} bra_grouped_args;
+
+/*
+ * grouped_matmul -- y[r, :] = x[r, :] W_e + bias[e, :] for the rows r of each
+ * expert e: rows off_e .. off_e + counts[e] - 1, off_e = sum of the counts
+ * before e.  Sums in fp32, the bias added in fp32, one rounding to dtype.
+ *
+ *   x       device (R, K), row pitch x_pitch, rows sorted by expert.
+ *   weight  device (E, K, N), or (E, N, K) with transpose_weight; dense.
+ *   bias    NULL, or device (E, N): fp16 for FP16, fp32 for BF16.
+ *   counts  device int64 (E).  Their sum R' may be below R: rows R' .. R-1 of
+ *           x are not read into any result and those of y not written.
+ *   y       device (R, N), row pitch y_pitch.
+ * A count of 0 is an expert without rows.  Counts are checked on the device:
+ * when one is negative or their sum passes R, nothing is written and
+ * *status becomes BRA_ERR_INVALID.
+ * status: set to BRA_OK on the stream before the kernels; BRA_ERR_TIMEOUT if
+ * a bounded wait of this call gave up.
+ *
+ * The kernels read operands by TMA.  An operand whose rows lack a 16-byte
+ * pitch or whose pointer is not 16-byte aligned is first copied to the
+ * workspace (grouped_matmul_workspace_size; 0 when none is).  y may have any
+ * element-aligned pointer and pitch.
+ *
+ * Errors (nothing launched):
+ *   BRA_ERR_NULLPTR      args, x, weight, counts or y is NULL (x and y may be
+ *                        NULL when rows is 0).
+ *   BRA_ERR_INVALID      a size outside the ranges above, another dtype, a
+ *                        pitch below the row length, a pointer that is not
+ *                        element-aligned (counts: 8 bytes, status: 4), a
+ *                        workspace not 256-byte aligned or smaller than
+ *                        needed, y overlapping an input or the workspace.
+ *   BRA_ERR_UNSUPPORTED  a copy is needed and there is no workspace; more
+ *                        than 2^31 - 1 output tiles.
+ *   BRA_ERR_CUDA         the launch failed.
+ */
+BRA_API int grouped_matmul(const void* x, const void* weight, const void* bias,
+                           const int64_t* counts, void* y, const bra_grouped_args* args,
+                           bra_stream_t stream);
+
+/*
+ * grouped_matmul_grad -- the gradients of grouped_matmul for the output's
+ * gradient dy; each output may be NULL (not wanted):
+ *   dx[r, :]   = dy[r, :] W_e^T           (R, K) dense; rows R' .. R-1 not written
+ *   dweight[e] = x_e^T dy_e               the weight's shape and layout; zero
+ *                                         for an expert without rows
+ *   dbias[e]   = sum of the rows of dy_e  (E, N), the bias's type
+ * Sums in fp32, one rounding; results do not change from run to run.  x is
+ * read for dweight only, weight for dx only (NULL otherwise allowed).
+ * y_pitch is dy's.  Errors, counts, status and workspace as grouped_matmul
+ * (grouped_matmul_grad_workspace_size); BRA_ERR_NULLPTR when all three
+ * outputs are NULL.
+ */
+BRA_API int grouped_matmul_grad(const void* dy, const void* x, const void* weight,
+                                const int64_t* counts, void* dx, void* dweight, void* dbias,
+                                const bra_grouped_args* args, bra_stream_t stream);
+
+/* Workspace bytes of the two calls for these pointers and sizes: 0 when every
+ * operand can be read in place.  Pointers are only inspected for alignment;
+ * the workspace fields are ignored.  A negative bra_status when the call
+ * would be rejected.  Pure host. */
+BRA_API int64_t grouped_matmul_workspace_size(const void* x, const void* weight,
+                                              const bra_grouped_args* args);
+BRA_API int64_t grouped_matmul_grad_workspace_size(const void* dy, const void* x,
+                                                   const void* weight, int want_dx,
+                                                   int want_dweight,
+                                                   const bra_grouped_args* args);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* BRA_MOE_H */

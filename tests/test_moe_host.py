@@ -1,0 +1,113 @@
+"""Host-side tests of include/bra_moe.h (no GPU needed, no kernel launched):
+exports, workspace sizes, and calls that must be refused before any launch."""
+import ctypes
+import os
+import pathlib
+import re
+
+import pytest
+
+import bmm_reducescatter_alltoall_gb300 as bra
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "bra_moe.h")
+NULLPTR, INVALID, UNSUPPORTED = bra.ERR_NULLPTR, bra.ERR_INVALID, bra.ERR_UNSUPPORTED
+
+# stand-in addresses, never dereferenced by a refused call
+X, W, B, C, Y, G, S = (0x10000000 * (i + 1) for i in range(7))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return bra.library()
+
+
+def test_every_declared_symbol_is_exported(lib):
+    names = re.findall(r"^BRA_API\s+[\w\s\*]+?\b(\w+)\s*\(", pathlib.Path(HEADER).read_text(),
+                       flags=re.M)
+    assert "grouped_matmul" in names
+    for name in names:
+        assert hasattr(lib, name), name
+
+
+def test_limits_match_the_header():
+    text = pathlib.Path(HEADER).read_text()
+    assert int(re.search(r"#define BRA_MAX_GROUPS (\d+)", text).group(1)) == bra.MAX_GROUPS
+
+
+def args(**kw):
+    a = bra.GroupedArgs()
+    base = dict(rows=16, groups=4, in_=64, out=72, dtype=bra.FP16)
+    base.update(kw)
+    for k, v in base.items():
+        setattr(a, k, v)
+    return a
+
+
+def test_grouped_struct_layout():
+    assert ctypes.sizeof(bra.GroupedArgs) == 80
+    assert bra.GroupedArgs.workspace.offset == 56 and bra.GroupedArgs.status.offset == 72
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(rows=-1), INVALID), (dict(rows=1 << 31), INVALID), (dict(groups=0), INVALID),
+    (dict(groups=513), INVALID), (dict(in_=0), INVALID), (dict(out=0), INVALID),
+    (dict(out=(1 << 24) + 1), INVALID), (dict(dtype=bra.FP32), INVALID),
+    (dict(x_pitch=63), INVALID), (dict(y_pitch=71), INVALID), (dict(status=S + 1), INVALID),
+    (dict(workspace=S + 128, workspace_bytes=1 << 20), INVALID),
+    (dict(workspace_bytes=5), INVALID), (dict(in_=65), UNSUPPORTED),
+    (dict(in_=65, workspace=S, workspace_bytes=256), INVALID),
+], ids=str)
+def test_grouped_matmul_refuses(lib, change, code):
+    assert lib.grouped_matmul(X, W, B, C, Y, ctypes.byref(args(**change)), None) == code
+    if "in_" not in change or change["in_"] == 0:
+        assert lib.grouped_matmul_grad(Y, X, W, C, G, None, None, ctypes.byref(args(**change)),
+                                       None) == code
+
+
+def test_grouped_matmul_refuses_pointers(lib):
+    a = ctypes.byref(args())
+    call = lib.grouped_matmul
+    for ptrs in ((None, W, B, C, Y), (X, None, B, C, Y), (X, W, B, None, Y), (X, W, B, C, None)):
+        assert call(*ptrs, a, None) == NULLPTR
+    assert call(X, W, B, C, Y, None, None) == NULLPTR
+    for ptrs in ((X + 1, W, B, C, Y), (X, W + 1, B, C, Y), (X, W, B + 1, C, Y),
+                 (X, W, B, C + 4, Y), (X, W, B, C, Y + 1)):
+        assert call(*ptrs, a, None) == INVALID
+    for y in (X, X + 64, W + 100, B, C):
+        assert call(X, W, B, C, y, a, None) == INVALID
+    bf = ctypes.byref(args(dtype=bra.BF16))
+    assert call(X, W, B + 2, C, Y, bf, None) == INVALID
+
+
+def test_grouped_matmul_grad_refuses_pointers(lib):
+    a = ctypes.byref(args())
+    call = lib.grouped_matmul_grad
+    assert call(Y, X, W, C, None, None, None, a, None) == NULLPTR
+    assert call(None, X, W, C, G, None, None, a, None) == NULLPTR
+    assert call(Y, X, None, C, G, None, None, a, None) == NULLPTR
+    assert call(Y, None, W, C, None, G, None, a, None) == NULLPTR
+    assert call(Y, X, W, C, Y + 64, None, None, a, None) == INVALID      # dx over dy
+    assert call(Y, X, W, C, G, G + 64, None, a, None) == INVALID         # dx over dweight
+    assert call(Y, X, W, C, None, None, W + 64, a, None) == INVALID      # dbias over weight
+
+
+def test_workspace_sizes(lib):
+    size = lambda x, w, **kw: lib.grouped_matmul_workspace_size(         # noqa: E731
+        x, w, ctypes.byref(args(**kw)))
+    assert size(X, W) == 0
+    assert size(X + 2, W) == 16 * 64 * 2
+    assert size(X, W + 2) == 4 * 64 * 128 * 2
+    assert size(X, W, in_=65) == 16 * 128 * 2                            # the weight's rows are N long
+    assert size(X, W, in_=65, transpose_weight=1) == 16 * 128 * 2 + 4 * 72 * 128 * 2
+    assert size(X, W, x_pitch=67) == 16 * 64 * 2
+    assert size(X, W, x_pitch=80) == 0
+    assert size(X + 2, W, rows=0) == 0
+    assert size(X, W, dtype=7) == -INVALID
+    grad = lambda want, **kw: lib.grouped_matmul_grad_workspace_size(    # noqa: E731
+        Y, X, W, *want, ctypes.byref(args(**kw)))
+    assert grad((1, 1)) == 0
+    assert grad((0, 0), out=75) == 0
+    assert grad((0, 1), out=75) == 16 * 128 * 2                          # dy
+    assert grad((1, 0), out=75) == 16 * 128 * 2 + 4 * 64 * 128 * 2       # dy and the weight
+    assert grad((0, 1), in_=65) == 16 * 128 * 2                          # x

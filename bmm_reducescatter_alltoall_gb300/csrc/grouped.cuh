@@ -62,14 +62,6 @@ __device__ __forceinline__ void build_table(GroupTable* t, const int64_t* counts
   }
 }
 
-// Arrive on a leader's barrier (shared::cluster address) and add the bytes
-// this CTA's copies will complete on it.
-__device__ __forceinline__ void mbar_expect_tx_cluster(uint32_t cluster_bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
-                   cluster_bar),
-               "r"(bytes)
-               : "memory");
-}
 // Wait on a barrier that CTAs of the cluster arrive on (acquire at cluster
 // scope); bounded as mbar_wait.
 __device__ __forceinline__ bool mbar_try_acq(uint32_t bar, uint32_t parity) {

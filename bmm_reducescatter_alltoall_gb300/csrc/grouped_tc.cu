@@ -116,13 +116,14 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t smem_base = smem_u32(smem);
   uint8_t* bars = smem + STAGES * STAGE_BYTES;
   const uint32_t bar_base = smem_u32(bars);
-  // barriers (8 bytes each): full, empty, tail (wgrad) per stage; tfull[2], tempty[2]
+  // barriers (8 bytes each): full, empty, tail and ptail (wgrad) per stage; tfull[2], tempty[2]
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
   auto tail_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + s); };
-  auto tfull_bar = [&](int a) { return bar_base + 8u * (3 * STAGES + a); };
-  auto tempty_bar = [&](int a) { return bar_base + 8u * (3 * STAGES + 2 + a); };
-  static_assert(8 * (3 * STAGES + 4) + 16 <= BAR_BYTES, "barrier area");
+  auto ptail_bar = [&](int s) { return bar_base + 8u * (3 * STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (4 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (4 * STAGES + 2 + a); };
+  static_assert(8 * (4 * STAGES + 4) + 16 <= BAR_BYTES, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BAR_BYTES - 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_BYTES - 8);
   GroupTable* gt = reinterpret_cast<GroupTable*>(bars + BAR_BYTES);
@@ -134,9 +135,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), CG);    // leader: one arrival per CTA of the pair
+      mbar_init(full_bar(s), 1);     // leader: its expect_tx; the bytes of both CTAs
       mbar_init(empty_bar(s), 1);
-      mbar_init(tail_bar(s), 1);
+      mbar_init(tail_bar(s), 1);     // this CTA's copies of a tail block
+      mbar_init(ptail_bar(s), 1);    // leader: the peer's tail block is ready
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
@@ -161,9 +163,13 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
   const int total = gt->bad ? 0 : (WG ? p.E * p.m_tiles : gt->tile[p.E]) * p.n_tiles;
   const int walk0 = blockIdx.x / CG, step = gridDim.x / CG;
 
-  if (warp == 0 && lane == 0) {
-    // ---------------- TMA producer (every CTA) ----------------
+  if ((warp == 0 || warp == 2) && lane == 0) {
+    // ---------------- TMA producers (every CTA): warp 0 for A, warp 2 for B ----------------
+    // One thread issuing a block's four boxes was the bound of the weight
+    // gradient (1345 against 1650 TFLOP/s with fewer instructions a box).
+    const bool is_a = warp == 0;
     const uint32_t leader_full0 = CG == 2 ? map_to_rank(full_bar(0), 0) : full_bar(0);
+    const uint32_t own_tail0 = CG == 2 ? map_to_rank(tail_bar(0), rank) : tail_bar(0);
     int stage = 0, hint = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -177,41 +183,42 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
       if (CG == 2) tma_load_3d_pair(dst, m, bar, c0, c1, c2);
       else tma_load_3d(dst, m, bar, c0, c1, c2);
     };
-    auto expect = [&](uint32_t bar, uint32_t bytes) {
-      if (CG == 2) mbar_expect_tx_cluster(bar, bytes);
-      else mbar_expect_tx(bar, bytes);
-    };
     for (int t = walk0; ok && t < total; t += step) {
       const Tile c = find_tile<WG>(p, gt, t, hint);
       const int r0 = gt->off[c.e], r1 = gt->off[c.e + 1];
+      const int a_row = c.mt * BM + (int)rank * 128;            // of the output
       const int b_col = c.nt * BN + (int)rank * S::B_COLS;
       if (WG) {
-        const int a_col = c.mt * BM + (int)rank * 128;
         for (int row = r0; row < r1; row += BK) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, fault)) {
             ok = false;
             break;
           }
           const uint32_t a_dst = smem_base + stage * STAGE_BYTES, b_dst = a_dst + A_BYTES;
-          const bool tail = r1 - row < BK;
-          const uint32_t fb = leader_full0 + 8u * stage, tb = tail_bar(stage);
-          if (tail) mbar_expect_tx(tb, STAGE_BYTES);   // warp 3 passes it on
-          else expect(fb, STAGE_BYTES);
+          const bool tail = r1 - row < BK;     // this CTA's own barrier: warp 3 passes it on
+          const uint32_t bar = (tail ? own_tail0 : leader_full0) + 8u * stage;
+          if (is_a) {
+            // only the leader arrives on a full barrier: a remote arrive of the peer for
+            // each block (release at cluster scope) held the pair to 790 TFLOP/s
+            if (tail) mbar_expect_tx(tail_bar(stage), STAGE_BYTES);
+            else if (rank == 0) mbar_expect_tx(full_bar(stage), CG * STAGE_BYTES);
 #pragma unroll
-          for (int i = 0; i < 2 + S::B_COLS / 64; ++i) {
-            const uint32_t dst = i < 2 ? a_dst + i * 8192 : b_dst + (i - 2) * 8192;
-            const CUtensorMap* m = i < 2 ? &p.ta : &p.tb;
-            const int col = i < 2 ? a_col + i * 64 : b_col + (i - 2) * 64;
-            if (tail) tma_load_3d(dst, m, tb, col, row, 0);
-            else load(dst, m, fb, col, row, 0);
+            for (int i = 0; i < 2; ++i)
+              load(a_dst + i * 8192, &p.ta, bar, a_row + i * 64, row, 0);
+          } else {
+#pragma unroll
+            for (int i = 0; i < S::B_COLS / 64; ++i)
+              load(b_dst + i * 8192, &p.tb, bar, b_col + i * 64, row, 0);
           }
           next();
         }
       } else {
-        const int row = r0 + c.mt * BM + (int)rank * 128;
-        const int valid = min(128, r1 - row);        // <= 0: nothing of A to fetch
-        const int small = valid <= 64 ? (max(valid, 0) + 31) / 32 : -1;
-        const uint32_t bytes = (small < 0 ? A_BYTES : small * (A_BYTES / 4)) + S::B_BYTES;
+        const int row = r0 + a_row;
+        // 32-row boxes of A to fetch (none past the group), or one of 128 rows
+        auto boxes = [&](int valid) { return valid <= 64 ? (max(valid, 0) + 31) / 32 : 4; };
+        const int mine = boxes(r1 - row);
+        uint32_t bytes = CG * S::B_BYTES + mine * (A_BYTES / 4);
+        if (CG == 2) bytes += boxes(r1 - row - 128) * (A_BYTES / 4);   // used by the leader
         for (int kb = 0; kb < p.k_blocks; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, fault)) {
             ok = false;
@@ -219,18 +226,19 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
           }
           const uint32_t fb = leader_full0 + 8u * stage;
           const uint32_t a_dst = smem_base + stage * STAGE_BYTES, b_dst = a_dst + A_BYTES;
-          expect(fb, bytes);
-          if (p.b_kmajor) {
+          if (is_a) {
+            if (rank == 0) mbar_expect_tx(full_bar(stage), bytes);
+            if (mine == 4) load(a_dst, &p.ta, fb, kb * BK, row, 0);
+            else
+              for (int i = 0; i < mine; ++i)
+                load(a_dst + i * (A_BYTES / 4), &p.ta32, fb, kb * BK, row + i * 32, 0);
+          } else if (p.b_kmajor) {
             load(b_dst, &p.tb, fb, kb * BK, b_col, c.e);
           } else {
 #pragma unroll
             for (int i = 0; i < S::B_COLS / 64; ++i)
               load(b_dst + i * 8192, &p.tb, fb, b_col + i * 64, kb * BK, c.e);
           }
-          if (small < 0) load(a_dst, &p.ta, fb, kb * BK, row, 0);
-          else
-            for (int i = 0; i < small; ++i)
-              load(a_dst + i * (A_BYTES / 4), &p.ta32, fb, kb * BK, row + i * 32, 0);
           next();
         }
       }
@@ -246,39 +254,55 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
                            : smem_desc_sw128(smem_base + A_BYTES, 8192, 1024);
     const uint32_t a_step = WG ? 128u : 2u, b_step = bk ? 2u : 128u;
     int stage = 0, acc = 0, hint = 0;
-    uint32_t phase = 0, acc_phase = 0;
+    uint32_t phase = 0, acc_phase = 0, pused = 0;
     bool ok = true;
+    auto next = [&] {
+      if (CG == 2) tc_commit_pair(empty_bar(stage), 0x3);
+      else tc_commit(empty_bar(stage));
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
     for (int t = walk0; ok && t < total; t += step) {
-      int blocks = p.k_blocks, last = BK / 16;
+      int full = p.k_blocks, tail = 0;     // whole blocks, rows of a last one
       if (WG) {
         const Tile c = find_tile<WG>(p, gt, t, hint);
         const int n = gt->off[c.e + 1] - gt->off[c.e];
-        blocks = (n + BK - 1) / BK;
-        last = ((n - 1) % BK + 16) / 16;
+        full = n / BK;
+        tail = n % BK;
       }
       if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, fault)) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-      for (int kb = 0; kb < blocks; ++kb) {
-        const bool got = CG == 2 ? mbar_wait_acq(full_bar(stage), phase, abort_flag, fault)
-                                 : mbar_wait(full_bar(stage), phase, abort_flag, fault);
-        if (!got) {
+      // the last block's wait and shorter MMA run are outside this loop: with
+      // them inside, the issuing thread fell behind (1650 against 1730 TFLOP/s)
+      for (int kb = 0; kb < full; ++kb) {
+        if (!mbar_wait(full_bar(stage), phase, abort_flag, fault)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint64_t so = (uint64_t)((stage * STAGE_BYTES) >> 4);
-        const int steps = WG && kb + 1 == blocks ? last : BK / 16;
 #pragma unroll
         for (int k = 0; k < BK / 16; ++k)
-          if (k < steps)
+          tc_mma<CG>(d_tmem, a0 + so + a_step * k, b0 + so + b_step * k, p.idesc,
+                     (kb > 0 || k > 0) ? 1u : 0u);
+        next();
+      }
+      if (WG && ok && tail) {
+        ok = mbar_wait(full_bar(stage), phase, abort_flag, fault);
+        if (CG == 2 && ok) {
+          ok = mbar_wait_acq(ptail_bar(stage), (pused >> stage) & 1u, abort_flag, fault);
+          pused ^= 1u << stage;
+        }
+        if (ok) {
+          tc_fence_after();
+          const uint64_t so = (uint64_t)((stage * STAGE_BYTES) >> 4);
+          for (int k = 0; k * 16 < tail; ++k)
             tc_mma<CG>(d_tmem, a0 + so + a_step * k, b0 + so + b_step * k, p.idesc,
-                       (kb > 0 || k > 0) ? 1u : 0u);
-        if (CG == 2) tc_commit_pair(empty_bar(stage), 0x3);
-        else tc_commit(empty_bar(stage));
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
+                       (full > 0 || k > 0) ? 1u : 0u);
+          next();
         }
       }
       if (!ok) break;
@@ -292,7 +316,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
     if (!ok) spin_ns(2000000ull);   // let MMAs already issued complete
   } else if (WG && warp == 3) {
     // ---------------- tail rows of a group's last block (every CTA) ----------------
-    const uint32_t leader_full0 = CG == 2 ? map_to_rank(full_bar(0), 0) : full_bar(0);
+    const uint32_t leader_ptail0 = CG == 2 ? map_to_rank(ptail_bar(0), 0) : 0u;
     int stage = 0, hint = 0;
     uint32_t used = 0;              // parity of each stage's tail barrier
     for (int t = walk0; t < total; t += step) {
@@ -315,8 +339,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2) mbar_arrive_cluster(leader_full0 + 8u * s);
-        else mbar_arrive(full_bar(s));
+        if (rank == 0) mbar_arrive(full_bar(s));
+        else mbar_arrive_cluster(leader_ptail0 + 8u * s);
       }
     }
   } else if (warp >= EPI_WARP0) {
@@ -366,6 +390,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
     }
   }
 
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync();   // no remote arrive or MMA of the pair still pending

@@ -70,6 +70,9 @@ KERNEL_SOURCES = {
     "grouped_kernel": "grouped_tc.cu",
     "bias_grad_kernel": "grouped_aux.cu",
     "pack_rows_kernel": "grouped_aux.cu",
+    "quantize_kernel": "mx_quant.cu",
+    "dequantize_kernel": "mx_quant.cu",
+    "mx_grouped_kernel": "mx_tc.cu",
 }
 
 

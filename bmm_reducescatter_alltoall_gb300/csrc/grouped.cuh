@@ -117,102 +117,121 @@ struct Num<__nv_bfloat16> {
 constexpr int kSegStride = 144;
 constexpr int kSegBytes = 32 * kSegStride;
 
+// 64 accumulator columns (fp32 bits) plus their bias (64 floats in shared
+// memory at bias_s, or 0), rounded once to packed pairs of T; zeros for an
+// empty sum.
+template <typename T>
+__device__ __forceinline__ void pack_segment(uint32_t (&v)[64], uint32_t (&o)[32], uint32_t bias_s,
+                                             bool zero) {
+  if (bias_s) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint4 b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = lds128e(bias_s + (uint32_t)(q * 16 + i * 4) * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t* w = &v[q * 16 + i * 4];
+        w[0] = __float_as_uint(__uint_as_float(w[0]) + __uint_as_float(b[i].x));
+        w[1] = __float_as_uint(__uint_as_float(w[1]) + __uint_as_float(b[i].y));
+        w[2] = __float_as_uint(__uint_as_float(w[2]) + __uint_as_float(b[i].z));
+        w[3] = __float_as_uint(__uint_as_float(w[3]) + __uint_as_float(b[i].w));
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    o[k] = zero ? 0u : Out<T>::pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+}
+
+// One warp writes a 64-column segment of its 32 rows (lane = row, packed
+// pairs in o) to rows y0, y0 + ldy, ... of which `valid` (1 .. 32) exist, at
+// columns nc .. below N.  `aligned`: every row starts on a 16-byte boundary
+// and N % 8 == 0.  between() runs after the segment is staged.
+template <typename T, typename Between>
+__device__ __forceinline__ void put_segment(const uint32_t (&o)[32], T* y0, int64_t ldy, int valid,
+                                            int nc, int N, uint32_t seg, bool aligned, int lane,
+                                            Between&& between) {
+  const uint32_t my = seg + (uint32_t)lane * kSegStride;
+  const int cols = min(64, N - nc);          // <= 0: past the matrix
+  if (aligned) {
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      sts128(my + g * 16, make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]));
+  } else {
+    // the segment shifted to its destination's place in a 16-byte chunk
+    const uint32_t d = (uint32_t)(reinterpret_cast<uintptr_t>(y0 + lane * ldy + nc) & 15u) >> 1;
+    const uint32_t at = my + (d >> 1) * 4;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const uint32_t w = (d & 1) ? __funnelshift_l(k ? o[k - 1] : 0u, o[k], 16) : o[k];
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + k * 4), "r"(w) : "memory");
+    }
+    if (d & 1) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 128), "r"(o[31] >> 16) : "memory");
+  }
+  between();
+  __syncwarp();
+  if (aligned) {
+    // 8 lanes to a row's 128 bytes, 4 rows an instruction
+    const int c8 = (lane & 7) * 8, r0 = lane >> 3;
+    if (c8 < cols) {
+      uint4 w[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) w[q] = lds128e(seg + (uint32_t)(4 * q + r0) * kSegStride + c8 * 2);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (4 * q + r0 < valid)
+          *reinterpret_cast<uint4*>(y0 + (4 * q + r0) * ldy + nc + c8) = w[q];
+    }
+  } else if (cols > 0) {
+    // (row, chunk) pairs: whole chunks as vectors, the partial ones at the
+    // segment's two ends element by element
+#pragma unroll 1
+    for (int u = lane; u < valid * 9; u += 32) {
+      const int r = u / 9, c = u - r * 9;
+      T* dst = y0 + r * ldy + nc;
+      const int d = (int)((reinterpret_cast<uintptr_t>(dst) & 15u) >> 1);
+      const int lo = max(c * 8, d), hi = min(c * 8 + 8, d + cols);   // in the shifted segment
+      if (lo >= hi) continue;
+      const uint4 w = lds128e(seg + (uint32_t)r * kSegStride + c * 16);
+      if (hi - lo == 8) {
+        *reinterpret_cast<uint4*>(dst - d + c * 8) = w;
+      } else {
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c * 8 + i >= lo && c * 8 + i < hi)
+            reinterpret_cast<uint16_t*>(dst)[c * 8 + i - d] =
+                (uint16_t)(ws[i >> 1] >> ((i & 1) * 16));
+      }
+    }
+  }
+  __syncwarp();
+}
+
 // One warp's 32 accumulator rows (TMEM address t_base, this warp's lane
-// quarter), columns n0 .. n0+BN-1, to rows y0, y0 + ldy, ... of which `valid`
-// (<= 32, > 0) are stored, columns below N.  bias_s: BN floats in shared
-// memory, or 0.  zero: the accumulator holds nothing (an empty sum).
-// `aligned`: every row starts on a 16-byte boundary and N % 8 == 0.
-// tmem_done() runs after the last TMEM load.  Each value is rounded once.
+// quarter), columns n0 .. n0+BN-1, 64 at a time: the next segment's TMEM
+// loads are issued while the staged one goes out.  bias_s: BN floats in
+// shared memory, or 0.  tmem_done() runs after the last TMEM load.
 template <typename T, int BN, typename Done>
 __device__ __forceinline__ void store_rows(uint32_t t_base, T* y0, int64_t ldy, int valid, int n0,
                                            int N, uint32_t seg, uint32_t bias_s, bool zero,
                                            bool aligned, int lane, Done&& tmem_done) {
-  const uint32_t my = seg + (uint32_t)lane * kSegStride;
   uint32_t v[64];
   tmem_ld32(t_base, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
   tmem_ld32(t_base + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
 #pragma unroll 1
   for (int ch = 0; ch < BN / 64; ++ch) {
-    const int nc = n0 + ch * 64;
-    const int cols = min(64, N - nc);          // <= 0: past the matrix
     tmem_ld_wait();
     if (ch + 1 == BN / 64) tmem_done();
-    if (bias_s) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint4 b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = lds128e(bias_s + (uint32_t)(ch * 64 + q * 16 + i * 4) * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t* w = &v[q * 16 + i * 4];
-          w[0] = __float_as_uint(__uint_as_float(w[0]) + __uint_as_float(b[i].x));
-          w[1] = __float_as_uint(__uint_as_float(w[1]) + __uint_as_float(b[i].y));
-          w[2] = __float_as_uint(__uint_as_float(w[2]) + __uint_as_float(b[i].z));
-          w[3] = __float_as_uint(__uint_as_float(w[3]) + __uint_as_float(b[i].w));
-        }
-      }
-    }
     uint32_t o[32];
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-      o[k] = zero ? 0u : Out<T>::pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-    if (aligned) {
-#pragma unroll
-      for (int g = 0; g < 8; ++g)
-        sts128(my + g * 16, make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]));
-    } else {
-      // the segment shifted to its destination's place in a 16-byte chunk
-      const uint32_t d = (uint32_t)(reinterpret_cast<uintptr_t>(y0 + lane * ldy + nc) & 15u) >> 1;
-      const uint32_t at = my + (d >> 1) * 4;
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const uint32_t w = (d & 1) ? __funnelshift_l(k ? o[k - 1] : 0u, o[k], 16) : o[k];
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + k * 4), "r"(w) : "memory");
+    pack_segment<T>(v, o, bias_s ? bias_s + ch * 256 : 0u, zero);
+    put_segment<T>(o, y0, ldy, valid, n0 + ch * 64, N, seg, aligned, lane, [&] {
+      if (ch + 1 < BN / 64) {
+        tmem_ld32(t_base + (ch + 1) * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+        tmem_ld32(t_base + (ch + 1) * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
       }
-      if (d & 1) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 128), "r"(o[31] >> 16) : "memory");
-    }
-    if (ch + 1 < BN / 64) {
-      tmem_ld32(t_base + (ch + 1) * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-      tmem_ld32(t_base + (ch + 1) * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-    }
-    __syncwarp();
-    if (aligned) {
-      // 8 lanes to a row's 128 bytes, 4 rows an instruction
-      const int c8 = (lane & 7) * 8, r0 = lane >> 3;
-      if (c8 < cols) {
-        uint4 w[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) w[q] = lds128e(seg + (uint32_t)(4 * q + r0) * kSegStride + c8 * 2);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (4 * q + r0 < valid)
-            *reinterpret_cast<uint4*>(y0 + (4 * q + r0) * ldy + nc + c8) = w[q];
-      }
-    } else if (cols > 0) {
-      // (row, chunk) pairs: whole chunks as vectors, the partial ones at the
-      // segment's two ends element by element
-#pragma unroll 1
-      for (int u = lane; u < valid * 9; u += 32) {
-        const int r = u / 9, c = u - r * 9;
-        T* dst = y0 + r * ldy + nc;
-        const int d = (int)((reinterpret_cast<uintptr_t>(dst) & 15u) >> 1);
-        const int lo = max(c * 8, d), hi = min(c * 8 + 8, d + cols);   // in the shifted segment
-        if (lo >= hi) continue;
-        const uint4 w = lds128e(seg + (uint32_t)r * kSegStride + c * 16);
-        if (hi - lo == 8) {
-          *reinterpret_cast<uint4*>(dst - d + c * 8) = w;
-        } else {
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c * 8 + i >= lo && c * 8 + i < hi)
-              reinterpret_cast<uint16_t*>(dst)[c * 8 + i - d] =
-                  (uint16_t)(ws[i >> 1] >> ((i & 1) * 16));
-        }
-      }
-    }
-    __syncwarp();
+    });
   }
 }
 

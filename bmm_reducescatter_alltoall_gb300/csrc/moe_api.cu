@@ -3,6 +3,7 @@
 #include <cstring>
 
 #include "moe_internal.h"
+#include "mx.cuh"
 
 namespace {
 
@@ -109,9 +110,119 @@ Copy weight_copy(const void* w, const bra_grouped_args* a, const GroupedSizes& s
   return copy_of(w, s.E * rows, n, n);
 }
 
+int check_mx(const bra_mx_args* a) {
+  if (!a) return BRA_ERR_NULLPTR;
+  if (a->rows < 0 || a->rows >= (int64_t(1) << 31) || a->k < 1 || a->k > (int64_t(1) << 24) ||
+      a->groups < 1 || a->groups > BRA_MAX_GROUPS || a->rows_per_group < 0 ||
+      a->rows_per_group >= (int64_t(1) << 31) || a->reserved != 0)
+    return BRA_ERR_INVALID;
+  if (a->rows_per_group > 0 && a->rows != a->groups * a->rows_per_group) return BRA_ERR_INVALID;
+  if (a->x_pitch != 0 && (a->x_pitch < a->k || a->x_pitch > (int64_t(1) << 36)))
+    return BRA_ERR_INVALID;
+  if (off_by(a->status, 3u)) return BRA_ERR_INVALID;
+  return BRA_OK;
+}
+
+// The parts of the two conversions that are the same: pointers and sizes.
+// `data` is x or y, `ld` its pitch.
+int check_mx_call(const void* data, int64_t ld, int64_t es, const int64_t* counts,
+                  const uint8_t* codes, const uint8_t* scales, const bra_mx_args* a, bool quantize) {
+  if (a->rows > 0 && (!data || !codes || !scales)) return BRA_ERR_NULLPTR;
+  if (a->rows > 0 && a->rows_per_group == 0 && !counts) return BRA_ERR_NULLPTR;
+  if (off_by(data, es - 1) || off_by(codes, 15u) || off_by(scales, 15u) || off_by(counts, 7u))
+    return BRA_ERR_INVALID;
+  const int64_t db = span(a->rows, ld, a->k, es), cb = mxfp4_code_bytes(a),
+                sb = mxfp4_scale_bytes(a), nb = a->rows_per_group == 0 ? a->groups * 8 : 0;
+  if (overlap(data, db, codes, cb) || overlap(data, db, scales, sb)) return BRA_ERR_INVALID;
+  if (quantize && (overlap(codes, cb, scales, sb) || overlap(counts, nb, codes, cb) ||
+                   overlap(counts, nb, scales, sb)))
+    return BRA_ERR_INVALID;
+  if (!quantize && overlap(counts, nb, data, db)) return BRA_ERR_INVALID;
+  return BRA_OK;
+}
+
+MxRows mx_rows(const uint8_t* codes, const uint8_t* scales, const int64_t* counts,
+               const bra_mx_args* a) {
+  return {const_cast<uint8_t*>(codes),
+          const_cast<uint8_t*>(scales),
+          a->rows_per_group == 0 ? counts : nullptr,
+          a->status,
+          a->rows,
+          a->k,
+          a->rows_per_group,
+          (int)a->groups};
+}
+
 }  // namespace
 
 extern "C" {
+
+int64_t mxfp4_code_bytes(const bra_mx_args* args) {
+  const int rc = check_mx(args);
+  return rc != BRA_OK ? -rc : args->rows * mx::code_pitch(args->k);
+}
+
+int64_t mxfp4_scale_bytes(const bra_mx_args* args) {
+  const int rc = check_mx(args);
+  if (rc != BRA_OK) return -rc;
+  return mx::blocks_of(args->rows, args->groups, args->rows_per_group) * mx::units(args->k) *
+         mx::kUnitBytes;
+}
+
+int mxfp4_quantize(const void* x, const int64_t* counts, uint8_t* codes, uint8_t* scales,
+                   const bra_mx_args* args, bra_stream_t stream) {
+  int rc = check_mx(args);
+  if (rc != BRA_OK) return rc;
+  if (args->dtype != BRA_FP16 && args->dtype != BRA_BF16) return BRA_ERR_INVALID;
+  const int64_t ld = args->x_pitch ? args->x_pitch : args->k;
+  if ((rc = check_mx_call(x, ld, 2, counts, codes, scales, args, true)) != BRA_OK) return rc;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if ((rc = clear_status(args->status, st)) != BRA_OK || args->rows == 0) return rc;
+  return status_of(launch_mx_quantize(mx_rows(codes, scales, counts, args), x, ld, args->dtype, st));
+}
+
+int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, const int64_t* counts, void* y,
+                     const bra_mx_args* args, bra_stream_t stream) {
+  int rc = check_mx(args);
+  if (rc != BRA_OK) return rc;
+  if ((args->dtype != BRA_FP16 && args->dtype != BRA_BF16 && args->dtype != BRA_FP32) ||
+      args->x_pitch != 0)
+    return BRA_ERR_INVALID;
+  const int64_t es = args->dtype == BRA_FP32 ? 4 : 2;
+  if ((rc = check_mx_call(y, args->k, es, counts, codes, scales, args, false)) != BRA_OK) return rc;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if ((rc = clear_status(args->status, st)) != BRA_OK || args->rows == 0) return rc;
+  return status_of(launch_mx_dequantize(mx_rows(codes, scales, counts, args), y, args->dtype, st));
+}
+
+int mxfp4_grouped_matmul(const uint8_t* x_codes, const uint8_t* x_scales, const uint8_t* w_codes,
+                         const uint8_t* w_scales, const void* bias, const int64_t* counts, void* y,
+                         const bra_grouped_args* args, bra_stream_t stream) {
+  GroupedSizes s;
+  int rc = check_sizes(args, &s);
+  if (rc != BRA_OK) return rc;
+  if (args->x_pitch != 0 || args->transpose_weight != 0) return BRA_ERR_INVALID;
+  if (!w_codes || !w_scales || !counts || (s.R > 0 && (!x_codes || !x_scales || !y)))
+    return BRA_ERR_NULLPTR;
+  const int64_t bes = args->dtype == BRA_BF16 ? 4 : 2;
+  if (off_by(x_codes, 15u) || off_by(x_scales, 15u) || off_by(w_codes, 15u) ||
+      off_by(w_scales, 15u) || off_by(y, 1u) || off_by(bias, bes - 1) || off_by(counts, 7u))
+    return BRA_ERR_INVALID;
+  const int64_t cp = mx::code_pitch(s.K), unit = mx::units(s.K) * mx::kUnitBytes;
+  const int64_t yb = span(s.R, s.yp, s.N, 2);
+  if (overlap(y, yb, x_codes, s.R * cp) ||
+      overlap(y, yb, x_scales, mx::blocks_of(s.R, s.E, 0) * unit) ||
+      overlap(y, yb, w_codes, s.E * s.N * cp) ||
+      overlap(y, yb, w_scales, mx::blocks_of(s.E * s.N, s.E, s.N) * unit) ||
+      overlap(y, yb, bias, s.E * s.N * bes) || overlap(y, yb, counts, s.E * 8))
+    return BRA_ERR_INVALID;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if ((rc = clear_status(args->status, st)) != BRA_OK || s.R == 0) return rc;
+  const MxProblem g = {x_codes, x_scales, w_codes,      w_scales, bias,
+                       y,       counts,   args->status, s.R,      s.yp,
+                       (int)s.E, (int)s.K, (int)s.N,     args->dtype};
+  return status_of(launch_mx_grouped(g, st));
+}
 
 int64_t grouped_matmul_workspace_size(const void* x, const void* weight,
                                       const bra_grouped_args* args) {

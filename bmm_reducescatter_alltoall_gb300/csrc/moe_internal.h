@@ -42,6 +42,33 @@ cudaError_t launch_bias_grad(const BiasGradProblem& g, cudaStream_t st);
 // (a multiple of 8) at a 16-byte aligned dst.
 cudaError_t launch_pack_rows(const void* src, int64_t ld, void* dst, int64_t pitch, int64_t rows,
                              int64_t len, cudaStream_t st);
+// Rows in the 4-bit microscaled layout (mx.cuh): row groups of `each` rows,
+// or of counts[E] rows when each is 0.
+struct MxRows {
+  uint8_t* codes;
+  uint8_t* scales;
+  const int64_t* counts;
+  int32_t* status;
+  int64_t R, K, each;
+  int E;
+};
+cudaError_t launch_mx_quantize(const MxRows& q, const void* x, int64_t ld, int dtype,
+                               cudaStream_t st);
+cudaError_t launch_mx_dequantize(const MxRows& q, void* y, int dtype, cudaStream_t st);
+struct MxProblem {
+  const uint8_t* xc;     // rows: codes and scales, grouped by counts
+  const uint8_t* xs;
+  const uint8_t* wc;     // weights: E groups of N rows
+  const uint8_t* ws;
+  const void* bias;
+  void* y;
+  const int64_t* counts;
+  int32_t* status;
+  int64_t R, ldy;
+  int E, K, N, dtype;
+};
+cudaError_t launch_mx_grouped(const MxProblem& g, cudaStream_t st);
+cudaError_t read_mx_fault_word(int32_t* code, int clear);
 cudaError_t read_grouped_fault_word(int32_t* code, int clear);
 
 }  // namespace bra

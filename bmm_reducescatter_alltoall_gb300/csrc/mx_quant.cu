@@ -1,0 +1,267 @@
+// Quantisation to 4-bit microscaled values, and back.
+//
+// Of each 32 elements, a = max |x|; the scale is 2^s with
+// s = max(floor(log2 a) - 2, -127), the largest power of two that puts a at or
+// above 4 of the format's largest magnitude 6; the code is the nearest of
+// +-{0, .5, 1, 1.5, 2, 3, 4, 6} to x / 2^s, ties to the even code, magnitudes
+// past 6 to 6.  x / 2^s is exact (a product with a power of two), so the codes
+// are a function of x alone.  A block with a NaN or an infinity has no scale:
+// byte 255, every value NaN.
+//
+// Memory bound: 16 bits read and 4.25 written to an element.  A lane holds 8
+// consecutive elements (one 16-byte load, one 4-byte store), four lanes share
+// a block, a warp takes up to 1024 elements of one row with their loads
+// issued together.
+#include "grouped.cuh"
+#include "mx.cuh"
+
+namespace bra {
+namespace {
+
+using namespace grp;
+
+constexpr int kThreads = 256;
+constexpr int kPieces = 4;                // 256-element pieces of a warp's unit
+
+template <typename T>
+__device__ __forceinline__ float2 pair_of(uint32_t w);
+template <>
+__device__ __forceinline__ float2 pair_of<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 pair_of<__nv_bfloat16>(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+
+__device__ __forceinline__ uint32_t code_pair(float lo, float hi) {
+  uint16_t r;
+  asm("{\n\t.reg .b8 t;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
+      "cvt.u16.u8 %0, t;\n\t}"
+      : "=h"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Row block and row within it of row r: groups of `each` rows, or of the
+// table's counts.
+__device__ __forceinline__ void locate(const GroupTable* gt, int E, int64_t each, int64_t r,
+                                       int64_t* blk, int* in) {
+  if (each > 0) {
+    const int64_t g = r / each, i = r - g * each;
+    *blk = g * ((each + 127) / 128) + i / 128;
+    *in = (int)(i & 127);
+    return;
+  }
+  int lo = 0, hi = E - 1;                 // the last group that starts at or before r
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (gt->off[mid] <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  const int i = (int)(r - gt->off[lo]);
+  *blk = gt->tile[lo] + (i >> 7);
+  *in = i & 127;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    quantize_kernel(const T* x, int64_t ld, int64_t R, int64_t K, const int64_t* counts, int E,
+                    int64_t each, uint8_t* codes, uint8_t* scales, int vec, int32_t* status) {
+  __shared__ GroupTable gt;
+  const int lane = threadIdx.x & 31;
+  int64_t rows = R;
+  if (counts) {
+    if (threadIdx.x < 32) build_table<128>(&gt, counts, E, R, lane);
+    __syncthreads();
+    if (gt.bad) {
+      if (blockIdx.x == 0 && threadIdx.x == 0 && status)
+        atomicExch(status, (int32_t)BRA_ERR_INVALID);
+      return;
+    }
+    rows = gt.off[E];
+  }
+  const int64_t cpitch = mx::code_pitch(K), k_units = mx::units(K);
+  const int64_t per_row = (k_units + kPieces - 1) / kPieces;
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < rows * per_row;
+       u += warps) {
+    const int64_t r = u / per_row, k0 = (u - r * per_row) * (kPieces * mx::kUnitK);
+    const T* src = x + r * ld;
+    uint32_t w[kPieces][4];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t k = k0 + i * mx::kUnitK + lane * 8;
+      w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
+      if (vec && k + 8 <= K) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src + k));
+        w[i][0] = q.x, w[i][1] = q.y, w[i][2] = q.z, w[i][3] = q.w;
+      } else if (k < K) {
+        const uint16_t* s = reinterpret_cast<const uint16_t*>(src + k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (k + j < K) w[i][j >> 1] |= (uint32_t)__ldg(s + j) << ((j & 1) * 16);
+      }
+    }
+    int64_t blk;
+    int in;
+    locate(&gt, E, each, r, &blk, &in);
+    uint8_t* crow = codes + r * cpitch;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t k = k0 + i * mx::kUnitK + lane * 8;
+      if (k0 + i * mx::kUnitK >= K) break;          // the same for the whole warp
+      float f[8];
+      uint32_t a = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 p = pair_of<T>(w[i][j]);
+        f[2 * j] = p.x;
+        f[2 * j + 1] = p.y;
+        // magnitudes ordered as integers: NaN above infinity above all else
+        a = max(a, max(__float_as_uint(p.x) & 0x7fffffffu, __float_as_uint(p.y) & 0x7fffffffu));
+      }
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      const bool none = a >= 0x7f800000u;
+      const int field = (int)(a >> 23);             // subnormals and zero: 0
+      const uint32_t byte = none ? 255u : (uint32_t)max(field - 2, 0);
+      const float inv = __uint_as_float((254u - (none ? 0u : byte)) << 23);   // 2^(127 - byte)
+      uint32_t c = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c |= code_pair(f[2 * j] * inv, f[2 * j + 1] * inv) << (8 * j);
+      if (k < cpitch * 2) *reinterpret_cast<uint32_t*>(crow + k / 2) = none ? 0u : c;
+      // a 128-element atom's four scales as one word
+      uint32_t s = byte << (8 * ((lane >> 2) & 3));
+      s |= __shfl_xor_sync(0xffffffffu, s, 4);
+      s |= __shfl_xor_sync(0xffffffffu, s, 8);
+      if ((lane & 15) == 0)
+        *reinterpret_cast<uint32_t*>(scales + mx::scale_at(blk, in, k / mx::kBlock, k_units)) = s;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T to(float v);
+template <>
+__device__ __forceinline__ __half to<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 to<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ float to<float>(float v) { return v; }
+
+// value = code * 2^(byte - 127); a lane makes the 8 values of one code word.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int64_t R, int64_t K,
+                      const int64_t* counts, int E, int64_t each, T* y, int vec, int32_t* status) {
+  __shared__ GroupTable gt;
+  const int lane = threadIdx.x & 31;
+  int64_t rows = R;
+  if (counts) {
+    if (threadIdx.x < 32) build_table<128>(&gt, counts, E, R, lane);
+    __syncthreads();
+    if (gt.bad) {
+      if (blockIdx.x == 0 && threadIdx.x == 0 && status)
+        atomicExch(status, (int32_t)BRA_ERR_INVALID);
+      return;
+    }
+    rows = gt.off[E];
+  }
+  const int64_t cpitch = mx::code_pitch(K), k_units = mx::units(K);
+  const int64_t per_row = (k_units + kPieces - 1) / kPieces;
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < rows * per_row;
+       u += warps) {
+    const int64_t r = u / per_row, k0 = (u - r * per_row) * (kPieces * mx::kUnitK);
+    int64_t blk;
+    int in;
+    locate(&gt, E, each, r, &blk, &in);
+    uint32_t c[kPieces], b[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t k = k0 + i * mx::kUnitK + lane * 8;
+      c[i] = b[i] = 0u;
+      if (k < K) {
+        c[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + r * cpitch + k / 2));
+        b[i] = __ldg(scales + mx::scale_at(blk, in, k / mx::kBlock, k_units));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t k = k0 + i * mx::kUnitK + lane * 8;
+      if (k >= K) break;
+      // 2^(b - 127): b = 0 is the subnormal 2^-127, 255 is NaN
+      const float s = __uint_as_float(b[i] == 255u ? 0x7fc00000u : b[i] ? b[i] << 23 : 1u << 22);
+      T v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t q = c[i] >> (4 * j), m = q & 7u;
+        // 0 and .5, then 1.m * 2^(e - 1)
+        const float mag = m < 2 ? 0.5f * (float)m
+                                : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
+        v[j] = to<T>(((q & 8u) ? -mag : mag) * s);
+      }
+      T* dst = y + r * K + k;
+      if (vec && k + 8 <= K) {
+#pragma unroll
+        for (int j = 0; j < (int)sizeof(T) / 2; ++j)
+          reinterpret_cast<uint4*>(dst)[j] = reinterpret_cast<const uint4*>(v)[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (k + j < K) dst[j] = v[j];
+      }
+    }
+  }
+}
+
+cudaError_t blocks_for(int64_t warps_wanted, unsigned* grid) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t want = (warps_wanted + kThreads / 32 - 1) / (kThreads / 32), full = (int64_t)sms * 8;
+  *grid = (unsigned)(want < 1 ? 1 : want < full ? want : full);
+  return cudaSuccess;
+}
+
+int64_t warps_of(int64_t R, int64_t K) { return R * ((mx::units(K) + kPieces - 1) / kPieces); }
+
+}  // namespace
+
+cudaError_t launch_mx_quantize(const MxRows& q, const void* x, int64_t ld, int dtype,
+                               cudaStream_t st) {
+  unsigned grid = 0;
+  cudaError_t e = blocks_for(warps_of(q.R, q.K), &grid);
+  if (e != cudaSuccess) return e;
+  const int vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ld % 8 == 0;
+  if (dtype == BRA_BF16)
+    quantize_kernel<<<grid, kThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(x), ld, q.R, q.K,
+                                               q.counts, q.E, q.each, q.codes, q.scales, vec,
+                                               q.status);
+  else
+    quantize_kernel<<<grid, kThreads, 0, st>>>(static_cast<const __half*>(x), ld, q.R, q.K,
+                                               q.counts, q.E, q.each, q.codes, q.scales, vec,
+                                               q.status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_mx_dequantize(const MxRows& q, void* y, int dtype, cudaStream_t st) {
+  unsigned grid = 0;
+  cudaError_t e = blocks_for(warps_of(q.R, q.K), &grid);
+  if (e != cudaSuccess) return e;
+  const int64_t es = dtype == BRA_FP32 ? 4 : 2;
+  const int vec = (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && q.K * es % 16 == 0;
+  auto run = [&](auto* out) {
+    dequantize_kernel<<<grid, kThreads, 0, st>>>(q.codes, q.scales, q.R, q.K, q.counts, q.E,
+                                                 q.each, out, vec, q.status);
+  };
+  if (dtype == BRA_BF16) run(static_cast<__nv_bfloat16*>(y));
+  else if (dtype == BRA_FP16) run(static_cast<__half*>(y));
+  else run(static_cast<float*>(y));
+  return cudaGetLastError();
+}
+
+}  // namespace bra

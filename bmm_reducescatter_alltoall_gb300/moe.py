@@ -13,7 +13,9 @@ from typing import Optional
 import bmm_reducescatter_alltoall_gb300 as _bra
 
 __all__ = ["GroupedArgs", "MAX_GROUPS", "grouped_matmul", "grouped_matmul_plan",
-           "grouped_matmul_grad", "grouped_matmul_grad_plan"]
+           "grouped_matmul_grad", "grouped_matmul_grad_plan", "MxArgs", "MxTensor",
+           "mxfp4_quantize", "mxfp4_quantize_plan", "mxfp4_dequantize", "mxfp4_dequantize_plan",
+           "mxfp4_grouped_matmul", "mxfp4_grouped_matmul_plan"]
 
 MAX_GROUPS = 512
 
@@ -25,6 +27,14 @@ class GroupedArgs(ctypes.Structure):
                 ("transpose_weight", ctypes.c_int32), ("x_pitch", ctypes.c_int64),
                 ("y_pitch", ctypes.c_int64), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_int64), ("status", ctypes.c_void_p)]
+
+
+class MxArgs(ctypes.Structure):
+    """bra_mx_args of the C header."""
+    _fields_ = [("rows", ctypes.c_int64), ("k", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("rows_per_group", ctypes.c_int64), ("x_pitch", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("status", ctypes.c_void_p)]
 
 
 def declare(lib) -> None:
@@ -39,6 +49,13 @@ def declare(lib) -> None:
     lib.grouped_matmul_workspace_size.restype = i64
     lib.grouped_matmul_grad_workspace_size.argtypes = [vp, vp, vp, c_int, c_int, gp]
     lib.grouped_matmul_grad_workspace_size.restype = i64
+    mp = ctypes.POINTER(MxArgs)
+    for fn in (lib.mxfp4_code_bytes, lib.mxfp4_scale_bytes):
+        fn.argtypes, fn.restype = [mp], i64
+    for fn in (lib.mxfp4_quantize, lib.mxfp4_dequantize):
+        fn.argtypes, fn.restype = [vp, vp, vp, vp, mp, vp], c_int
+    lib.mxfp4_grouped_matmul.argtypes = [vp, vp, vp, vp, vp, vp, vp, gp, vp]
+    lib.mxfp4_grouped_matmul.restype = c_int
 
 
 def _ptr(t) -> Optional[int]:
@@ -250,3 +267,146 @@ def grouped_matmul_grad(dy, x, weight, counts, bias=None, dx=None, dweight=None,
     change from run to run."""
     return grouped_matmul_grad_plan(dy, x, weight, counts, bias, dx, dweight, dbias, want,
                                     transpose_weight, workspace, status).run(stream)
+
+
+class MxTensor:
+    """Rows in 4-bit microscaled floating point (mxfp4_quantize).
+
+    shape: (R, K), or (E, N, K) for weights.  codes: uint8, two codes to a
+    byte, rows padded to 32 elements.  scales: uint8, one to 32 elements, in
+    the tensor core's order (include/bra_moe.h).  counts: the tensor of row
+    counts the rows were grouped with, or None: then each matrix of N rows is
+    a group."""
+
+    def __init__(self, codes, scales, shape, counts):
+        self.codes, self.scales, self.shape, self.counts = codes, scales, tuple(shape), counts
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def _args(self) -> MxArgs:
+        a = MxArgs()
+        a.k = self.shape[-1]
+        if self.counts is not None:
+            a.rows, a.groups = self.shape[0], self.counts.numel()
+        else:
+            a.groups = self.shape[0] if len(self.shape) == 3 else 1
+            a.rows_per_group = self.shape[-2]
+            a.rows = a.groups * a.rows_per_group
+            if a.rows == 0:
+                a.rows_per_group = 0
+        return a
+
+
+def mxfp4_quantize_plan(x, counts=None, out: Optional[MxTensor] = None, status=None):
+    """mxfp4_quantize prepared once (see Plan); plan.run() returns the MxTensor."""
+    torch = _bra._torch()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    code = _bra._fused_dtype(x.dtype)
+    if x.dim() == 3 and counts is None:
+        _bra._dev_tensor(x, "x")
+        pitch = 0
+    else:
+        pitch = _rows(x, "x")
+    if x.numel() == 0 and x.shape[-1] == 0:
+        raise ValueError("x has rows of no elements")
+    if counts is not None:
+        _counts(counts)
+    shape = tuple(x.shape)
+    probe = MxTensor(x, None, shape, counts)._args()
+    lib = _bra.library()
+    cb = lib.mxfp4_code_bytes(ctypes.byref(probe))
+    sb = lib.mxfp4_scale_bytes(ctypes.byref(probe))
+    if cb < 0 or sb < 0:
+        raise _bra.BraError(-min(cb, sb), "mxfp4_quantize")
+    if out is None:
+        new = lambda n: torch.empty(n, dtype=torch.uint8, device=x.device)   # noqa: E731
+        out = MxTensor(new(cb).view(shape[:-1] + (-(-shape[-1] // 32) * 16,)), new(sb), shape,
+                       counts)
+    elif out.shape != shape or out.codes.numel() < cb or out.scales.numel() < sb or \
+            out.counts is not counts:
+        raise ValueError(f"out holds {out.shape} and its own counts, expected {shape} with counts")
+    _same_device(x, out.codes, out.scales, counts, status)
+    a = probe
+    a.x_pitch, a.dtype, a.status = pitch, code, _status(status)
+    args = (_ptr(x), _ptr(counts), _ptr(out.codes), _ptr(out.scales), ctypes.byref(a))
+    return _bra.Plan(lib.mxfp4_quantize, args, "mxfp4_quantize", out, (x, counts, a, status))
+
+
+def mxfp4_quantize(x, counts=None, out: Optional[MxTensor] = None, status=None,
+                   stream=None) -> MxTensor:
+    """x (fp16 or bf16) in 4-bit microscaled floating point (MXFP4).
+
+    Each 32 elements of a row share the scale 2^s, s = floor(log2 max|x|) - 2;
+    values are the nearest multiples by {0, .5, 1, 1.5, 2, 3, 4, 6}, ties to
+    the even code.  x: (R, K) rows of any pitch, grouped by `counts` (CUDA
+    int64) if given, or (E, N, K) weights.  A block with a NaN or an infinity
+    becomes NaN."""
+    return mxfp4_quantize_plan(x, counts, out, status).run(stream)
+
+
+def mxfp4_dequantize_plan(q: MxTensor, dtype, out=None, status=None):
+    """mxfp4_dequantize prepared once (see Plan); plan.run() returns out."""
+    torch = _bra._torch()
+    codes = {torch.float16: _bra.FP16, torch.bfloat16: _bra.BF16, torch.float32: _bra.FP32}
+    if dtype not in codes:
+        raise TypeError(f"mxfp4_dequantize gives float16, bfloat16 or float32, got {dtype}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    _dense(out, "out", dtype, q.shape)
+    _same_device(q.codes, q.scales, q.counts, out, status)
+    a = q._args()
+    a.dtype, a.status = codes[dtype], _status(status)
+    args = (_ptr(q.codes), _ptr(q.scales), _ptr(q.counts), _ptr(out), ctypes.byref(a))
+    return _bra.Plan(_bra.library().mxfp4_dequantize, args, "mxfp4_dequantize", out,
+                     (q, a, status))
+
+
+def mxfp4_dequantize(q: MxTensor, dtype, out=None, status=None, stream=None):
+    """The values of an MxTensor as fp16, bf16 or fp32 (one rounding)."""
+    return mxfp4_dequantize_plan(q, dtype, out, status).run(stream)
+
+
+def mxfp4_grouped_matmul_plan(x: MxTensor, weight: MxTensor, counts, bias=None, out=None,
+                              dtype=None, status=None):
+    """mxfp4_grouped_matmul prepared once (see Plan); plan.run() returns out."""
+    torch = _bra._torch()
+    if not isinstance(x, MxTensor) or not isinstance(weight, MxTensor):
+        raise TypeError("x and weight must be MxTensors (mxfp4_quantize)")
+    if len(x.shape) != 2 or len(weight.shape) != 3 or weight.counts is not None:
+        raise ValueError("x must hold rows (R, K) and weight matrices (E, N, K)")
+    (R, K), (E, N, Kw) = x.shape, weight.shape
+    if K != Kw:
+        raise ValueError(f"x has rows of {K}, weight takes {Kw}")
+    _counts(counts, E)
+    if x.counts is None and E != 1 or \
+            x.counts is not None and x.counts.data_ptr() != counts.data_ptr():
+        raise ValueError("x has to be quantized with these counts: its scales are grouped by them")
+    dt = dtype if dtype is not None else out.dtype if out is not None else torch.bfloat16
+    code = _bra._fused_dtype(dt)
+    if bias is not None:
+        _dense(bias, "bias", _bias_dtype(dt), (E, N))
+    if out is None:
+        out = torch.empty((R, N), dtype=dt, device=x.device)
+    yp = _rows(out, "out", dt, (R, N))
+    _same_device(x.codes, weight.codes, counts, bias, out, status)
+    a = GroupedArgs()
+    a.rows, a.groups, a.in_, a.out = R, E, K, N
+    a.dtype, a.y_pitch, a.status = code, yp, _status(status)
+    args = (_ptr(x.codes), _ptr(x.scales), _ptr(weight.codes), _ptr(weight.scales), _ptr(bias),
+            _ptr(counts), _ptr(out), ctypes.byref(a))
+    return _bra.Plan(_bra.library().mxfp4_grouped_matmul, args, "mxfp4_grouped_matmul", out,
+                     (x, weight, counts, bias, a, status))
+
+
+def mxfp4_grouped_matmul(x: MxTensor, weight: MxTensor, counts, bias=None, out=None, dtype=None,
+                         status=None, stream=None):
+    """grouped_matmul on 4-bit operands: y[r] = x[r] @ weight[e].T + bias[e].
+
+    x: rows quantized with these `counts` (with one expert, also without).
+    weight: (E, N, K) quantized.  Products and sums of the dequantized values
+    in fp32, one rounding to dtype (bf16 by default, or fp16).  The rest as
+    grouped_matmul."""
+    return mxfp4_grouped_matmul_plan(x, weight, counts, bias, out, dtype, status).run(stream)

@@ -1,6 +1,7 @@
 /*
  * bra_moe.h -- ragged expert operators of libbmmrsa2a.so: matrix products
- * grouped by expert with row groups of any size, and their gradients.
+ * grouped by expert with row groups of any size, and their gradients; the
+ * same products on 4-bit microscaled weights and rows.
  *
  * They work on what a variable-count exchange delivers: one matrix of rows
  * sorted by expert, and the number of rows of each expert in device memory
@@ -105,6 +106,72 @@ BRA_API int64_t grouped_matmul_grad_workspace_size(const void* dy, const void* x
                                                    const void* weight, int want_dx,
                                                    int want_dweight,
                                                    const bra_grouped_args* args);
+
+/* ------------------------------------------------------------------------ */
+/* 4-bit microscaled floating point (MXFP4)                                  */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Rows of e2m1 codes with one power-of-two scale to 32 elements.  For a block
+ * with largest magnitude a, s = max(floor(log2 a) - 2, -127) (a = 0: -127),
+ * the scale byte is s + 127 and an element's code the nearest of
+ * +-{0, .5, 1, 1.5, 2, 3, 4, 6} to x / 2^s, ties to the even code, magnitudes
+ * past 6 to 6.  A block with a NaN or an infinity gets byte 255: every value
+ * of it is NaN.
+ *
+ * codes: mxfp4_code_bytes: rows of ceil(K/32) * 16 bytes, two codes to a byte
+ * (the even element in the low half), zeros past K.  scales:
+ * mxfp4_scale_bytes: in the tensor core's order, per 128 rows and 256
+ * elements a unit of 1024 bytes (byte (s/4)*512 + (r%32)*16 + (r/32)*4 + s%4
+ * for row r and scale s of the unit); a unit's bytes of rows that do not
+ * exist are not written.  The 128-row blocks start anew at each row group, so
+ * scales belong to the grouping they were made with.
+ */
+typedef struct {
+  int64_t rows;            /* R: 0 .. 2^31 - 1                                 */
+  int64_t k;               /* K: elements of a row, 1 .. 2^24                  */
+  int64_t groups;          /* E: 1 .. BRA_MAX_GROUPS                           */
+  int64_t rows_per_group;  /* groups of this many rows (R = E * that); 0: of   */
+                           /* counts[E] rows, device int64, sum at most R      */
+  int64_t x_pitch;         /* quantize: elements between rows of x; 0 = K      */
+  int32_t dtype;           /* x: FP16 or BF16; dequantized y: FP16, BF16, FP32 */
+  int32_t reserved;        /* 0                                                */
+  int32_t* status;         /* device int32 of this call, or NULL               */
+} bra_mx_args;
+
+/* Bytes of the two buffers (or a negative bra_status).  Pure host. */
+BRA_API int64_t mxfp4_code_bytes(const bra_mx_args* args);
+BRA_API int64_t mxfp4_scale_bytes(const bra_mx_args* args);
+
+/*
+ * mxfp4_quantize -- x (R, K) to codes and scales; mxfp4_dequantize -- back to
+ * y (R, K), dense, each value exact before its rounding to dtype.  With
+ * counts, rows past their sum are neither read nor written, and counts are
+ * checked on the device as in grouped_matmul.
+ * Errors: BRA_ERR_NULLPTR for a NULL args, or data with R > 0 (counts when
+ * rows_per_group is 0); BRA_ERR_INVALID for sizes outside the ranges, rows
+ * other than groups * rows_per_group, another dtype, a pitch below K, codes
+ * or scales not 16-byte aligned, x or y not element-aligned, an output
+ * overlapping an input or the other output; BRA_ERR_CUDA.
+ */
+BRA_API int mxfp4_quantize(const void* x, const int64_t* counts, uint8_t* codes, uint8_t* scales,
+                           const bra_mx_args* args, bra_stream_t stream);
+BRA_API int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, const int64_t* counts,
+                             void* y, const bra_mx_args* args, bra_stream_t stream);
+
+/*
+ * mxfp4_grouped_matmul -- grouped_matmul on 4-bit operands: rows quantized
+ * with the same counts, weights (E, N, K) quantized as E groups of N rows.
+ * y[r, n] = sum of the dequantized products in fp32 + bias[e, n], one
+ * rounding to args->dtype (FP16 or BF16; the bias is fp16 or fp32 as there).
+ * Of bra_grouped_args, x_pitch and transpose_weight must be 0 and no
+ * workspace is used.  Errors, counts and status as grouped_matmul; codes and
+ * scales have to be 16-byte aligned (BRA_ERR_INVALID).
+ */
+BRA_API int mxfp4_grouped_matmul(const uint8_t* x_codes, const uint8_t* x_scales,
+                                 const uint8_t* w_codes, const uint8_t* w_scales,
+                                 const void* bias, const int64_t* counts, void* y,
+                                 const bra_grouped_args* args, bra_stream_t stream);
 
 #ifdef __cplusplus
 }

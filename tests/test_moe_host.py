@@ -111,3 +111,63 @@ def test_workspace_sizes(lib):
     assert grad((0, 1), out=75) == 16 * 128 * 2                          # dy
     assert grad((1, 0), out=75) == 16 * 128 * 2 + 4 * 64 * 128 * 2       # dy and the weight
     assert grad((0, 1), in_=65) == 16 * 128 * 2                          # x
+
+
+def mx(**kw):
+    a = bra.MxArgs()
+    base = dict(rows=16, k=64, groups=4, rows_per_group=4, dtype=bra.FP16)
+    base.update(kw)
+    for k, v in base.items():
+        setattr(a, k, v)
+    return a
+
+
+def test_mx_struct_layout():
+    assert ctypes.sizeof(bra.MxArgs) == 56 and bra.MxArgs.status.offset == 48
+
+
+def test_mx_buffer_sizes(lib):
+    code = lambda **kw: lib.mxfp4_code_bytes(ctypes.byref(mx(**kw)))     # noqa: E731
+    scale = lambda **kw: lib.mxfp4_scale_bytes(ctypes.byref(mx(**kw)))   # noqa: E731
+    assert code() == 16 * 32 and code(k=65) == 16 * 48 and code(k=1) == 16 * 16
+    assert scale() == 4 * 1024                                  # four groups, one block each
+    assert scale(k=257) == 4 * 2048
+    assert scale(rows=1000, groups=4, rows_per_group=250) == 8 * 1024
+    assert scale(rows=1000, groups=4, rows_per_group=0) == (7 + 4) * 1024
+    assert scale(rows=2, groups=4, rows_per_group=0) == 2 * 1024
+    assert code(rows=15) == -INVALID and scale(k=0) == -INVALID
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(rows=15), INVALID), (dict(rows=-4), INVALID), (dict(k=0), INVALID),
+    (dict(groups=513, rows=513 * 4), INVALID), (dict(dtype=bra.INT8), INVALID),
+    (dict(dtype=bra.FP32), INVALID), (dict(x_pitch=63), INVALID), (dict(reserved=1), INVALID),
+    (dict(status=S + 2), INVALID),
+], ids=str)
+def test_mx_quantize_refuses(lib, change, code):
+    assert lib.mxfp4_quantize(X, None, W, B, ctypes.byref(mx(**change)), None) == code
+    if change != dict(dtype=bra.FP32):
+        assert lib.mxfp4_dequantize(W, B, None, X, ctypes.byref(mx(**change)), None) == code
+
+
+def test_mx_refuses_pointers(lib):
+    a = ctypes.byref(mx())
+    for ptrs in ((None, None, W, B), (X, None, None, B), (X, None, W, None)):
+        assert lib.mxfp4_quantize(*ptrs, a, None) == NULLPTR
+    assert lib.mxfp4_quantize(X, None, W, B, ctypes.byref(mx(rows_per_group=0)), None) == NULLPTR
+    for ptrs in ((X + 1, None, W, B), (X, None, W + 8, B), (X, None, W, B + 8), (X, None, X, B),
+                 (X, None, W, X), (X, None, W, W)):
+        assert lib.mxfp4_quantize(*ptrs, a, None) == INVALID
+    g = ctypes.byref(args())
+    call = lib.mxfp4_grouped_matmul
+    ok = [X, X + 0x1000000, W, W + 0x1000000, B, C, Y]
+    for i in (0, 1, 2, 3, 5, 6):
+        bad = list(ok)
+        bad[i] = None
+        assert call(*bad, g, None) == NULLPTR, i
+        bad[i] = ok[i] + 1
+        assert call(*bad, g, None) == INVALID, i
+    for i in range(6):
+        assert call(*ok[:6], ok[i], g, None) == INVALID, i          # y over an input
+    for change in (dict(transpose_weight=1), dict(x_pitch=64), dict(dtype=bra.FP32)):
+        assert call(*ok, ctypes.byref(args(**change)), None) == INVALID

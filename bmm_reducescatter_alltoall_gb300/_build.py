@@ -73,6 +73,12 @@ KERNEL_SOURCES = {
     "quantize_kernel": "mx_quant.cu",
     "dequantize_kernel": "mx_quant.cu",
     "mx_grouped_kernel": "mx_tc.cu",
+    "route_choose_kernel": "moe_route.cu",
+    "route_place_kernel": "moe_route.cu",
+    "route_grad_kernel": "moe_route.cu",
+    "dispatch_kernel": "moe_permute.cu",
+    "combine_kernel": "moe_permute.cu",
+    "combine_grad_kernel": "moe_permute.cu",
 }
 
 

@@ -153,9 +153,183 @@ MxRows mx_rows(const uint8_t* codes, const uint8_t* scales, const int64_t* count
           (int)a->groups};
 }
 
+// A range of memory of a call.
+struct Span {
+  const void* p;
+  int64_t n;
+};
+
+// Whether an output overlaps an input or another output.
+bool any_overlap(const Span* outs, int no, const Span* ins, int ni) {
+  for (int i = 0; i < no; ++i) {
+    for (int j = 0; j < ni; ++j)
+      if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return true;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
+  }
+  return false;
+}
+
+int64_t element_size(int dtype) { return dtype == BRA_FP32 ? 4 : 2; }
+
+bool row_dtype_ok(int dtype) {
+  return dtype == BRA_FP16 || dtype == BRA_BF16 || dtype == BRA_FP32;
+}
+
+int check_route(const bra_route_args* a) {
+  if (!a) return BRA_ERR_NULLPTR;
+  if (a->tokens < 0 || a->experts < 1 || a->experts > BRA_MAX_GROUPS || a->choices < 1 ||
+      a->choices > BRA_MAX_CHOICES || a->choices > a->experts ||
+      a->tokens >= (int64_t(1) << 31) || a->tokens * a->choices >= (int64_t(1) << 31) ||
+      !row_dtype_ok(a->dtype))
+    return BRA_ERR_INVALID;
+  return BRA_OK;
+}
+
+int check_permute(const bra_permute_args* a) {
+  if (!a) return BRA_ERR_NULLPTR;
+  if (a->tokens < 0 || a->tokens >= (int64_t(1) << 31) || a->rows < 0 ||
+      a->rows >= (int64_t(1) << 31) || a->choices < 1 || a->choices > BRA_MAX_CHOICES ||
+      a->width < 1 || a->width > (int64_t(1) << 24) || !row_dtype_ok(a->dtype) || a->reserved != 0)
+    return BRA_ERR_INVALID;
+  return BRA_OK;
+}
+
+PermuteCall permute_call(const void* in, void* out, const int32_t* row_tokens, const int32_t* slots,
+                         const float* weights, const bra_permute_args* a) {
+  return {in,      out,     row_tokens,      slots,         weights,  a->tokens,
+          a->rows, (int)a->choices, (int)a->width, a->dtype};
+}
+
+// dispatch_grad (weights NULL and unused) and combine.
+int run_combine(const void* rows, const int32_t* slots, const float* weights, bool weighted, void* y,
+                const bra_permute_args* args, cudaStream_t st) {
+  const int rc = check_permute(args);
+  if (rc != BRA_OK) return rc;
+  if (args->tokens == 0) return BRA_OK;
+  if (!slots || !y || (weighted && !weights) || (args->rows > 0 && !rows)) return BRA_ERR_NULLPTR;
+  const int64_t es = element_size(args->dtype), n = args->tokens * args->choices * 4;
+  if (off_by(rows, es - 1) || off_by(y, es - 1) || off_by(slots, 3u) || off_by(weights, 3u))
+    return BRA_ERR_INVALID;
+  const Span outs[1] = {{y, args->tokens * args->width * es}};
+  const Span ins[3] = {{rows, args->rows * args->width * es}, {slots, n}, {weights, n}};
+  if (any_overlap(outs, 1, ins, 3)) return BRA_ERR_INVALID;
+  return status_of(launch_combine(permute_call(rows, y, nullptr, slots, weights, args), st));
+}
+
 }  // namespace
 
 extern "C" {
+
+int64_t moe_route_workspace_size(const bra_route_args* args) {
+  const int rc = check_route(args);
+  if (rc != BRA_OK) return -rc;
+  const int64_t chunk = route_chunk(args->tokens);
+  const int64_t chunks = (args->tokens + chunk - 1) / chunk;
+  return chunks > 1 ? (chunks * args->experts * 4 + 255) / 256 * 256 : 0;
+}
+
+int moe_route(const void* logits, int32_t* ids, float* weights, int64_t* counts, int32_t* slots,
+              int32_t* tokens, void* workspace, int64_t workspace_bytes,
+              const bra_route_args* args, bra_stream_t stream) {
+  const int64_t need = moe_route_workspace_size(args);
+  if (need < 0) return (int)-need;
+  const bool some = args->tokens > 0;
+  if (!counts || (some && (!logits || !ids || !weights || !slots || !tokens)) ||
+      (need > 0 && !workspace))
+    return BRA_ERR_NULLPTR;
+  const int64_t es = element_size(args->dtype), n = args->tokens * args->choices * 4;
+  if (off_by(logits, es - 1) || off_by(ids, 3u) || off_by(weights, 3u) || off_by(counts, 7u) ||
+      off_by(slots, 3u) || off_by(tokens, 3u) || off_by(workspace, 255u) || workspace_bytes < need)
+    return BRA_ERR_INVALID;
+  const Span outs[6] = {{ids, n},   {weights, n}, {counts, args->experts * 8},
+                        {slots, n}, {tokens, n},  {workspace, need}};
+  const Span ins[1] = {{logits, args->tokens * args->experts * es}};
+  if (any_overlap(outs, 6, ins, 1)) return BRA_ERR_INVALID;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (!some)
+    return cudaMemsetAsync(counts, 0, (size_t)args->experts * 8, st) == cudaSuccess ? BRA_OK
+                                                                                    : BRA_ERR_CUDA;
+  const RouteCall r = {logits,       ids,
+                       weights,      counts,
+                       slots,        tokens,
+                       static_cast<int32_t*>(workspace),
+                       args->tokens, (int)args->experts,
+                       (int)args->choices, args->renormalize ? 1 : 0,
+                       args->dtype};
+  return status_of(launch_route(r, st));
+}
+
+int moe_route_grad(const float* dweights, const void* logits, const int32_t* ids,
+                   const float* weights, void* dlogits, const bra_route_args* args,
+                   bra_stream_t stream) {
+  const int rc = check_route(args);
+  if (rc != BRA_OK) return rc;
+  if (args->tokens == 0) return BRA_OK;
+  if (!dweights || !ids || !weights || !dlogits || (!args->renormalize && !logits))
+    return BRA_ERR_NULLPTR;
+  const int64_t es = element_size(args->dtype), n = args->tokens * args->choices * 4,
+                lb = args->tokens * args->experts * es;
+  if (off_by(logits, es - 1) || off_by(dlogits, es - 1) || off_by(dweights, 3u) || off_by(ids, 3u) ||
+      off_by(weights, 3u))
+    return BRA_ERR_INVALID;
+  const Span outs[1] = {{dlogits, lb}};
+  const Span ins[4] = {{dweights, n}, {ids, n}, {weights, n}, {logits, lb}};
+  if (any_overlap(outs, 1, ins, 4)) return BRA_ERR_INVALID;
+  const RouteGradCall r = {dweights,     logits,
+                           ids,          weights,
+                           dlogits,      args->tokens,
+                           (int)args->experts, (int)args->choices,
+                           args->renormalize ? 1 : 0, args->dtype};
+  return status_of(launch_route_grad(r, (cudaStream_t)stream));
+}
+
+int moe_dispatch(const void* x, const int32_t* tokens, void* xs, const bra_permute_args* args,
+                 bra_stream_t stream) {
+  const int rc = check_permute(args);
+  if (rc != BRA_OK) return rc;
+  if (args->rows == 0) return BRA_OK;
+  if (!tokens || !xs || (args->tokens > 0 && !x)) return BRA_ERR_NULLPTR;
+  const int64_t es = element_size(args->dtype);
+  if (off_by(x, es - 1) || off_by(xs, es - 1) || off_by(tokens, 3u)) return BRA_ERR_INVALID;
+  const Span outs[1] = {{xs, args->rows * args->width * es}};
+  const Span ins[2] = {{x, args->tokens * args->width * es}, {tokens, args->rows * 4}};
+  if (any_overlap(outs, 1, ins, 2)) return BRA_ERR_INVALID;
+  return status_of(
+      launch_dispatch(permute_call(x, xs, tokens, nullptr, nullptr, args), (cudaStream_t)stream));
+}
+
+int moe_dispatch_grad(const void* dxs, const int32_t* slots, void* dx, const bra_permute_args* args,
+                      bra_stream_t stream) {
+  return run_combine(dxs, slots, nullptr, false, dx, args, (cudaStream_t)stream);
+}
+
+int moe_combine(const void* ys, const int32_t* slots, const float* weights, void* y,
+                const bra_permute_args* args, bra_stream_t stream) {
+  return run_combine(ys, slots, weights, true, y, args, (cudaStream_t)stream);
+}
+
+int moe_combine_grad(const void* dy, const void* ys, const int32_t* slots, const float* weights,
+                     const int32_t* tokens, void* dys, float* dweights,
+                     const bra_permute_args* args, bra_stream_t stream) {
+  const int rc = check_permute(args);
+  if (rc != BRA_OK) return rc;
+  if (args->tokens == 0 && args->rows == 0) return BRA_OK;
+  if ((args->tokens > 0 && (!dy || !slots || !weights || !dweights)) ||
+      (args->rows > 0 && (!ys || !dys)))
+    return BRA_ERR_NULLPTR;
+  const int64_t es = element_size(args->dtype), n = args->tokens * args->choices * 4,
+                rb = args->rows * args->width * es;
+  if (off_by(dy, es - 1) || off_by(ys, es - 1) || off_by(dys, es - 1) || off_by(slots, 3u) ||
+      off_by(weights, 3u) || off_by(tokens, 3u) || off_by(dweights, 3u))
+    return BRA_ERR_INVALID;
+  const Span outs[2] = {{dys, rb}, {dweights, n}};
+  const Span ins[5] = {{dy, args->tokens * args->width * es}, {ys, rb}, {slots, n}, {weights, n},
+                       {tokens, tokens ? args->rows * 4 : 0}};
+  if (any_overlap(outs, 2, ins, 5)) return BRA_ERR_INVALID;
+  return status_of(launch_combine_grad(permute_call(dy, dys, tokens, slots, weights, args), ys,
+                                       dweights, (cudaStream_t)stream));
+}
 
 int64_t mxfp4_code_bytes(const bra_mx_args* args) {
   const int rc = check_mx(args);

@@ -69,6 +69,45 @@ struct MxProblem {
 };
 cudaError_t launch_mx_grouped(const MxProblem& g, cudaStream_t st);
 cudaError_t read_mx_fault_word(int32_t* code, int clear);
+
+// The router.  hist: workspace of chunks x E int32 when there are several.
+struct RouteCall {
+  const void* logits;
+  int32_t* ids;
+  float* weights;
+  int64_t* counts;
+  int32_t* slots;
+  int32_t* tokens;
+  int32_t* hist;
+  int64_t T;
+  int E, k, renorm, dtype;
+};
+int route_chunk(int64_t T);                     // tokens of a chunk
+cudaError_t launch_route(const RouteCall& r, cudaStream_t st);
+struct RouteGradCall {
+  const float* dweights;
+  const void* logits;
+  const int32_t* ids;
+  const float* weights;
+  void* dlogits;
+  int64_t T;
+  int E, k, renorm, dtype;
+};
+cudaError_t launch_route_grad(const RouteGradCall& r, cudaStream_t st);
+// Row permutation; in and out are token rows (T) or expert rows (R).
+struct PermuteCall {
+  const void* in;
+  void* out;
+  const int32_t* row_tokens;   // [R], or nullptr
+  const int32_t* slots;        // [T][k], or nullptr
+  const float* weights;        // [T][k], or nullptr: ones
+  int64_t T, R;
+  int k, H, dtype;
+};
+cudaError_t launch_dispatch(const PermuteCall& c, cudaStream_t st);
+cudaError_t launch_combine(const PermuteCall& c, cudaStream_t st);
+// in: dy, out: dys
+cudaError_t launch_combine_grad(const PermuteCall& c, const void* ys, float* dw, cudaStream_t st);
 cudaError_t read_grouped_fault_word(int32_t* code, int clear);
 
 }  // namespace bra

@@ -1,0 +1,297 @@
+// Moving token rows to their experts and back, with the gradients.
+//
+//   dispatch       xs[r] = x[tokens[r]]                     (0 for -1)
+//   combine        y[t]  = sum_j w[t,j] ys[slots[t,j]]      (-1: nothing)
+//   dispatch grad  dx[t] = sum_j dxs[slots[t,j]]            combine with w = 1
+//   combine grad   dys[slots[t,j]] = w[t,j] dy[t], dw[t,j] = <dy[t], ys[slots[t,j]]>
+//
+// All bound by memory: every row is read and written once (dispatch reads a
+// token's row once for each of its experts, from L2 where it still is).  Sums
+// are in fp32, in the order of j and of a fixed tree, so results do not
+// change from run to run; nothing is added atomically.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "moe_internal.h"
+
+namespace bra {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxK = BRA_MAX_CHOICES;
+
+// Eight elements of a row held by a lane: consecutive ones with 16-byte
+// accesses (VEC), else 32 apart so that a warp's accesses stay together.
+template <typename T, bool VEC>
+struct Eight {
+  static __device__ __forceinline__ int at(int base, int lane, int i) {
+    return VEC ? base + lane * 8 + i : base + lane + 32 * i;
+  }
+  static __device__ __forceinline__ void load(const T* row, int base, int lane, int H,
+                                              float (&f)[8]) {
+    if constexpr (VEC) {
+      constexpr int N = (int)sizeof(T) / 2;        // 16-byte loads
+      uint4 w[N];
+      const bool in = base + lane * 8 < H;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        w[i] = in ? __ldg(reinterpret_cast<const uint4*>(row + base + lane * 8) + i)
+                  : make_uint4(0, 0, 0, 0);
+      const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(e[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = base + lane + 32 * i;
+        f[i] = c < H ? static_cast<float>(row[c]) : 0.f;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(T* row, int base, int lane, int H,
+                                               const float (&f)[8]) {
+    if constexpr (VEC) {
+      constexpr int N = (int)sizeof(T) / 2;
+      if (base + lane * 8 >= H) return;
+      uint4 w[N];
+      T* e = reinterpret_cast<T*>(w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = static_cast<T>(f[i]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) reinterpret_cast<uint4*>(row + base + lane * 8)[i] = w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = base + lane + 32 * i;
+        if (c < H) row[c] = static_cast<T>(f[i]);
+      }
+    }
+  }
+};
+
+// Rows as `units` of sizeof(W) bytes; a warp copies up to 8 of its lanes' units at once.
+template <typename W>
+__global__ void __launch_bounds__(kThreads)
+    dispatch_kernel(const W* x, const int32_t* tokens, W* xs, int64_t R, int64_t T, int64_t units) {
+  constexpr int U = 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t pieces = (units + 32 * U - 1) / (32 * U), warps = (int64_t)gridDim.x * kWarps;
+  for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < R * pieces; u += warps) {
+    const int64_t r = u / pieces, c0 = (u - r * pieces) * (32 * U) + lane;
+    const int t = __ldg(tokens + r);
+    const bool have = t >= 0 && t < T;
+    const W* src = x + (int64_t)(have ? t : 0) * units;
+    W v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      v[i] = W{};
+      if (have && c0 + 32 * i < units) v[i] = __ldg(src + c0 + 32 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (c0 + 32 * i < units) xs[r * units + c0 + 32 * i] = v[i];
+  }
+}
+
+// y[t] = sum_j w[t,j] rows[slots[t,j]]; w NULL: ones.  A warp takes 256
+// elements of a token; the rows' loads are issued four at a time.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+    combine_kernel(const T* rows, const int32_t* slots, const float* w, T* y, int64_t tokens,
+                   int64_t R, int k, int H) {
+  const int lane = threadIdx.x & 31;
+  const int64_t pieces = (H + 255) / 256, warps = (int64_t)gridDim.x * kWarps;
+  for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < tokens * pieces;
+       u += warps) {
+    const int64_t t = u / pieces;
+    const int base = (int)(u - t * pieces) * 256;
+    int slot = -1;
+    float wt = 0.f;
+    if (lane < k) {
+      slot = __ldg(slots + t * k + lane);
+      if (slot < 0 || slot >= R) slot = -1;
+      wt = w ? __ldg(w + t * k + lane) : 1.f;
+    }
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < k; j0 += 4) {
+      float f[4][8];
+      int sj[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sj[j] = j0 + j < k ? __shfl_sync(0xffffffffu, slot, (j0 + j) & 31) : -1;
+        if (sj[j] >= 0) Eight<T, VEC>::load(rows + (int64_t)sj[j] * H, base, lane, H, f[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, wt, (j0 + j) & 31);
+        if (sj[j] >= 0)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] = fmaf(wj, f[j][i], s[i]);
+      }
+    }
+    Eight<T, VEC>::store(y + t * H, base, lane, H, s);
+  }
+}
+
+// One token to WPT warps: dys rows and the k dot products.  The block also
+// zeroes its share of the rows that no token has.
+template <typename T, bool VEC, int WPT>
+__global__ void __launch_bounds__(kThreads)
+    combine_grad_kernel(const T* dy, const T* ys, const int32_t* slots, const float* w,
+                        const int32_t* row_tokens, T* dys, float* dw, int64_t tokens, int64_t R,
+                        int k, int H) {
+  __shared__ float part[kWarps][kMaxK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int TPB = kWarps / WPT;              // tokens of a block
+  const int sub = warp % WPT;
+  for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < tokens; t0 += (int64_t)gridDim.x * TPB) {
+    const int64_t t = t0 + warp / WPT;
+    float dot[kMaxK];
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) dot[j] = 0.f;
+    if (t < tokens) {
+      int slot = -1;
+      float wt = 0.f;
+      if (lane < k) {
+        slot = __ldg(slots + t * k + lane);
+        if (slot < 0 || slot >= R) slot = -1;
+        wt = __ldg(w + t * k + lane);
+      }
+      for (int base = sub * 256; base < H; base += WPT * 256) {
+        float d[8];
+        Eight<T, VEC>::load(dy + t * H, base, lane, H, d);
+#pragma unroll
+        for (int j = 0; j < kMaxK; ++j) {
+          if (j >= k) break;
+          const int s = __shfl_sync(0xffffffffu, slot, j);
+          const float wj = __shfl_sync(0xffffffffu, wt, j);
+          if (s < 0) continue;
+          float f[8], o[8];
+          Eight<T, VEC>::load(ys + (int64_t)s * H, base, lane, H, f);
+          float a = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            a = fmaf(d[i], f[i], a);
+            o[i] = wj * d[i];
+          }
+          dot[j] += a;
+          Eight<T, VEC>::store(dys + (int64_t)s * H, base, lane, H, o);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kMaxK; ++j) {
+        if (j >= k) break;
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], m);
+        if (lane == 0) part[warp][j] = dot[j];
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < TPB * k; i += kThreads) {
+      const int tok = i / k, j = i - tok * k;
+      if (t0 + tok < tokens) {
+        float a = 0.f;
+#pragma unroll
+        for (int q = 0; q < WPT; ++q) a += part[tok * WPT + q][j];
+        dw[(t0 + tok) * k + j] = a;
+      }
+    }
+    __syncthreads();
+  }
+  if (row_tokens) {
+    // rows without a token: a warp looks at 32 rows at once
+    const int64_t warps = (int64_t)gridDim.x * kWarps;
+    const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int64_t r0 = ((int64_t)blockIdx.x * kWarps + warp) * 32; r0 < R; r0 += warps * 32) {
+      uint32_t idle = __ballot_sync(0xffffffffu, r0 + lane < R && __ldg(row_tokens + r0 + lane) < 0);
+      for (; idle; idle &= idle - 1) {
+        T* row = dys + (r0 + __ffs(idle) - 1) * H;
+        for (int base = 0; base < H; base += 256) Eight<T, VEC>::store(row, base, lane, H, z);
+      }
+    }
+  }
+}
+
+cudaError_t grid_of(int64_t blocks, int per_sm, unsigned* grid) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t full = (int64_t)sms * per_sm;
+  *grid = (unsigned)(blocks < 1 ? 1 : blocks < full ? blocks : full);
+  return cudaSuccess;
+}
+
+bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <typename F>
+cudaError_t by_type(int dtype, bool vec, F&& f) {
+  auto go = [&](auto* type) {
+    return vec ? f(type, std::true_type{}) : f(type, std::false_type{});
+  };
+  if (dtype == BRA_FP32) return go((float*)nullptr);
+  if (dtype == BRA_BF16) return go((__nv_bfloat16*)nullptr);
+  return go((__half*)nullptr);
+}
+
+}  // namespace
+
+cudaError_t launch_dispatch(const PermuteCall& c, cudaStream_t st) {
+  const int64_t bytes = (int64_t)c.H * (c.dtype == BRA_FP32 ? 4 : 2);
+  auto run = [&](auto* type) {
+    using W = std::remove_pointer_t<decltype(type)>;
+    const int64_t units = bytes / (int64_t)sizeof(W);
+    unsigned grid = 0;
+    const int64_t warps = c.R * ((units + 255) / 256);
+    cudaError_t e = grid_of((warps + kWarps - 1) / kWarps, 16, &grid);
+    if (e != cudaSuccess) return e;
+    dispatch_kernel<<<grid, kThreads, 0, st>>>(static_cast<const W*>(c.in), c.row_tokens,
+                                               static_cast<W*>(c.out), c.R, c.T, units);
+    return cudaGetLastError();
+  };
+  auto fits = [&](uintptr_t n) {
+    return bytes % (int64_t)n == 0 && (reinterpret_cast<uintptr_t>(c.in) & (n - 1)) == 0 &&
+           (reinterpret_cast<uintptr_t>(c.out) & (n - 1)) == 0;
+  };
+  if (fits(16)) return run((uint4*)nullptr);
+  if (fits(4)) return run((uint32_t*)nullptr);
+  return run((unsigned short*)nullptr);
+}
+
+cudaError_t launch_combine(const PermuteCall& c, cudaStream_t st) {
+  const bool vec = c.H % 8 == 0 && aligned(c.in) && aligned(c.out);
+  unsigned grid = 0;
+  const int64_t warps = c.T * ((c.H + 255) / 256);
+  cudaError_t e = grid_of((warps + kWarps - 1) / kWarps, 16, &grid);
+  if (e != cudaSuccess) return e;
+  return by_type(c.dtype, vec, [&](auto* type, auto v) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    combine_kernel<T, decltype(v)::value><<<grid, kThreads, 0, st>>>(
+        static_cast<const T*>(c.in), c.slots, c.weights, static_cast<T*>(c.out), c.T, c.R, c.k,
+        c.H);
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_combine_grad(const PermuteCall& c, const void* ys, float* dw, cudaStream_t st) {
+  const bool vec = c.H % 8 == 0 && aligned(c.in) && aligned(c.out) && aligned(ys);
+  return by_type(c.dtype, vec, [&](auto* type, auto v) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    constexpr bool V = decltype(v)::value;
+    auto run = [&](auto kernel, int tpb) {
+      unsigned grid = 0;
+      cudaError_t e = grid_of((c.T + tpb - 1) / tpb, 16, &grid);
+      if (e != cudaSuccess) return e;
+      kernel<<<grid, kThreads, 0, st>>>(static_cast<const T*>(c.in), static_cast<const T*>(ys),
+                                        c.slots, c.weights, c.row_tokens, static_cast<T*>(c.out),
+                                        dw, c.T, c.R, c.k, c.H);
+      return cudaGetLastError();
+    };
+    return c.H >= 1024 ? run(combine_grad_kernel<T, V, 4>, 1) : run(combine_grad_kernel<T, V, 1>, 4);
+  });
+}
+
+}  // namespace bra

@@ -15,9 +15,13 @@ import bmm_reducescatter_alltoall_gb300 as _bra
 __all__ = ["GroupedArgs", "MAX_GROUPS", "grouped_matmul", "grouped_matmul_plan",
            "grouped_matmul_grad", "grouped_matmul_grad_plan", "MxArgs", "MxTensor",
            "mxfp4_quantize", "mxfp4_quantize_plan", "mxfp4_dequantize", "mxfp4_dequantize_plan",
-           "mxfp4_grouped_matmul", "mxfp4_grouped_matmul_plan"]
+           "mxfp4_grouped_matmul", "mxfp4_grouped_matmul_plan", "MAX_CHOICES", "RouteArgs",
+           "PermuteArgs", "moe_route", "moe_route_plan", "moe_route_grad", "moe_route_grad_plan",
+           "moe_dispatch", "moe_dispatch_plan", "moe_dispatch_grad", "moe_dispatch_grad_plan",
+           "moe_combine", "moe_combine_plan", "moe_combine_grad", "moe_combine_grad_plan"]
 
 MAX_GROUPS = 512
+MAX_CHOICES = 16
 
 
 class GroupedArgs(ctypes.Structure):
@@ -35,6 +39,20 @@ class MxArgs(ctypes.Structure):
                 ("rows_per_group", ctypes.c_int64), ("x_pitch", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("status", ctypes.c_void_p)]
+
+
+class RouteArgs(ctypes.Structure):
+    """bra_route_args of the C header."""
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64),
+                ("choices", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32)]
+
+
+class PermuteArgs(ctypes.Structure):
+    """bra_permute_args of the C header."""
+    _fields_ = [("tokens", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("choices", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def declare(lib) -> None:
@@ -56,6 +74,18 @@ def declare(lib) -> None:
         fn.argtypes, fn.restype = [vp, vp, vp, vp, mp, vp], c_int
     lib.mxfp4_grouped_matmul.argtypes = [vp, vp, vp, vp, vp, vp, vp, gp, vp]
     lib.mxfp4_grouped_matmul.restype = c_int
+    rp, pp = ctypes.POINTER(RouteArgs), ctypes.POINTER(PermuteArgs)
+    lib.moe_route.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, rp, vp]
+    lib.moe_route_workspace_size.argtypes = [rp]
+    lib.moe_route_workspace_size.restype = i64
+    lib.moe_route_grad.argtypes = [vp, vp, vp, vp, vp, rp, vp]
+    lib.moe_dispatch.argtypes = [vp, vp, vp, pp, vp]
+    lib.moe_dispatch_grad.argtypes = [vp, vp, vp, pp, vp]
+    lib.moe_combine.argtypes = [vp, vp, vp, vp, pp, vp]
+    lib.moe_combine_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, pp, vp]
+    for fn in (lib.moe_route, lib.moe_route_grad, lib.moe_dispatch, lib.moe_dispatch_grad,
+               lib.moe_combine, lib.moe_combine_grad):
+        fn.restype = c_int
 
 
 def _ptr(t) -> Optional[int]:
@@ -410,3 +440,198 @@ def mxfp4_grouped_matmul(x: MxTensor, weight: MxTensor, counts, bias=None, out=N
     in fp32, one rounding to dtype (bf16 by default, or fp16).  The rest as
     grouped_matmul."""
     return mxfp4_grouped_matmul_plan(x, weight, counts, bias, out, dtype, status).run(stream)
+
+
+def _row_dtype(dt, what: str) -> int:
+    torch = _bra._torch()
+    codes = {torch.float16: _bra.FP16, torch.bfloat16: _bra.BF16, torch.float32: _bra.FP32}
+    if dt not in codes:
+        raise TypeError(f"{what} takes float16, bfloat16 or float32, got {dt}")
+    return codes[dt]
+
+
+def _matrix(t, what: str, dtype=None, shape=None):
+    """A dense 2-D CUDA tensor."""
+    _bra._dev_tensor(t, what, dtype)
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D (got shape {tuple(t.shape)})")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _route_args(logits, k: int, renormalize: bool) -> RouteArgs:
+    a = RouteArgs()
+    a.tokens, a.experts = logits.shape
+    a.choices = int(k)
+    a.dtype = _row_dtype(logits.dtype, "moe_route")
+    a.renormalize = 1 if renormalize else 0
+    return a
+
+
+def moe_route_plan(logits, k: int, renormalize: bool = True, ids=None, weights=None, counts=None,
+                   slots=None, tokens=None, workspace="auto"):
+    """moe_route prepared once (see Plan); plan.run() returns its dict."""
+    torch = _bra._torch()
+    _matrix(logits, "logits")
+    a = _route_args(logits, k, renormalize)
+    T, E = logits.shape
+    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=logits.device)   # noqa: E731
+    i32 = torch.int32
+    ids = _dense(new((T, k), i32) if ids is None else ids, "ids", i32, (T, k))
+    weights = _dense(new((T, k), torch.float32) if weights is None else weights, "weights",
+                     torch.float32, (T, k))
+    counts = _counts(new((E,), torch.int64) if counts is None else counts, E)
+    slots = _dense(new((T, k), i32) if slots is None else slots, "slots", i32, (T, k))
+    tokens = _dense(new((T * k,), i32) if tokens is None else tokens, "tokens", i32, (T * k,))
+    _same_device(logits, ids, weights, counts, slots, tokens)
+    lib = _bra.library()
+    box = GroupedArgs()                                   # holds the workspace's address
+    workspace = _take_workspace(workspace, lib.moe_route_workspace_size(ctypes.byref(a)),
+                                logits.device, box)
+    result = {"ids": ids, "weights": weights, "counts": counts, "slots": slots, "tokens": tokens}
+    args = (_ptr(logits), _ptr(ids), _ptr(weights), _ptr(counts), _ptr(slots), _ptr(tokens),
+            box.workspace, box.workspace_bytes, ctypes.byref(a))
+    return _bra.Plan(lib.moe_route, args, "moe_route", result, (logits, a, workspace))
+
+
+def moe_route(logits, k: int, renormalize: bool = True, ids=None, weights=None, counts=None,
+              slots=None, tokens=None, workspace="auto", stream=None) -> dict:
+    """Each token's k experts, and the order that sorts the pairs by expert.
+
+    logits: CUDA (T, E), fp16, bf16 or fp32; -inf or NaN closes an expert to
+    a token.  Returns {'ids' (T, k) int32, 'weights' (T, k) fp32, 'counts'
+    (E,) int64, 'slots' (T, k) int32, 'tokens' (T*k,) int32}: the chosen
+    experts, largest logit first (ties: the lowest index), their softmax
+    weights (renormalised over the chosen by default), rows of each expert,
+    the row of each pair when sorted by expert, and the token of each row.  A
+    token with fewer than k open experts has -1, weight 0 and slot -1 for the
+    rest; rows past the last pair have token -1."""
+    return moe_route_plan(logits, k, renormalize, ids, weights, counts, slots, tokens,
+                          workspace).run(stream)
+
+
+def moe_route_grad_plan(dweights, logits, ids, weights, renormalize: bool = True, out=None):
+    """moe_route_grad prepared once (see Plan); plan.run() returns out."""
+    torch = _bra._torch()
+    _matrix(logits, "logits")
+    _matrix(ids, "ids", torch.int32)
+    T, k = ids.shape
+    a = _route_args(logits, k, renormalize)
+    if logits.shape[0] != T:
+        raise ValueError(f"logits have {logits.shape[0]} tokens, ids {T}")
+    _matrix(dweights, "dweights", torch.float32, (T, k))
+    _matrix(weights, "weights", torch.float32, (T, k))
+    if out is None:
+        out = torch.empty_like(logits)
+    _matrix(out, "out", logits.dtype, logits.shape)
+    _same_device(logits, dweights, ids, weights, out)
+    args = (_ptr(dweights), _ptr(logits), _ptr(ids), _ptr(weights), _ptr(out), ctypes.byref(a))
+    return _bra.Plan(_bra.library().moe_route_grad, args, "moe_route_grad", out,
+                     (dweights, logits, ids, weights, a))
+
+
+def moe_route_grad(dweights, logits, ids, weights, renormalize: bool = True, out=None,
+                   stream=None):
+    """Gradient of the logits for the gradient of moe_route's weights."""
+    return moe_route_grad_plan(dweights, logits, ids, weights, renormalize, out).run(stream)
+
+
+def _permute_args(T: int, R: int, k: int, rows, what: str) -> PermuteArgs:
+    a = PermuteArgs()
+    a.tokens, a.rows, a.choices, a.width = T, R, k, rows.shape[1]
+    a.dtype = _row_dtype(rows.dtype, what)
+    return a
+
+
+def moe_dispatch_plan(x, tokens, out=None):
+    """moe_dispatch prepared once (see Plan); plan.run() returns out."""
+    torch = _bra._torch()
+    _matrix(x, "x")
+    _bra._dev_tensor(tokens, "tokens", torch.int32)
+    R = tokens.numel()
+    if out is None:
+        out = torch.empty((R, x.shape[1]), dtype=x.dtype, device=x.device)
+    _matrix(out, "out", x.dtype, (R, x.shape[1]))
+    _same_device(x, tokens, out)
+    a = _permute_args(x.shape[0], R, 1, x, "moe_dispatch")
+    args = (_ptr(x), _ptr(tokens), _ptr(out), ctypes.byref(a))
+    return _bra.Plan(_bra.library().moe_dispatch, args, "moe_dispatch", out, (x, tokens, a))
+
+
+def moe_dispatch(x, tokens, out=None, stream=None):
+    """Token rows in expert order: out[r] = x[tokens[r]], zeros for -1."""
+    return moe_dispatch_plan(x, tokens, out).run(stream)
+
+
+def _to_tokens_plan(rows, slots, weights, out, name: str, what: str):
+    torch = _bra._torch()
+    _matrix(rows, what)
+    _matrix(slots, "slots", torch.int32)
+    T, k = slots.shape
+    if weights is not None:
+        _matrix(weights, "weights", torch.float32, (T, k))
+    if out is None:
+        out = torch.empty((T, rows.shape[1]), dtype=rows.dtype, device=rows.device)
+    _matrix(out, "out", rows.dtype, (T, rows.shape[1]))
+    _same_device(rows, slots, weights, out)
+    a = _permute_args(T, rows.shape[0], k, rows, name)
+    args = (_ptr(rows), _ptr(slots)) + (() if weights is None else (_ptr(weights),)) + \
+        (_ptr(out), ctypes.byref(a))
+    return _bra.Plan(getattr(_bra.library(), name), args, name, out, (rows, slots, weights, a))
+
+
+def moe_dispatch_grad_plan(dxs, slots, out=None):
+    """moe_dispatch_grad prepared once (see Plan); plan.run() returns out."""
+    return _to_tokens_plan(dxs, slots, None, out, "moe_dispatch_grad", "dxs")
+
+
+def moe_dispatch_grad(dxs, slots, out=None, stream=None):
+    """Gradient of moe_dispatch: out[t] = sum of dxs[slots[t, j]] over j."""
+    return moe_dispatch_grad_plan(dxs, slots, out).run(stream)
+
+
+def moe_combine_plan(ys, slots, weights, out=None):
+    """moe_combine prepared once (see Plan); plan.run() returns out."""
+    if weights is None:
+        raise TypeError("weights must be a torch.Tensor")
+    return _to_tokens_plan(ys, slots, weights, out, "moe_combine", "ys")
+
+
+def moe_combine(ys, slots, weights, out=None, stream=None):
+    """Expert rows back to tokens: out[t] = sum of weights[t, j] * ys[slots[t, j]]
+    over j (fp32, one rounding); slots of -1 are left out."""
+    return moe_combine_plan(ys, slots, weights, out).run(stream)
+
+
+def moe_combine_grad_plan(dy, ys, slots, weights, tokens=None, dys=None, dweights=None):
+    """moe_combine_grad prepared once (see Plan); plan.run() returns its dict."""
+    torch = _bra._torch()
+    _matrix(dy, "dy")
+    _matrix(ys, "ys", dy.dtype)
+    _matrix(slots, "slots", torch.int32)
+    T, k = slots.shape
+    R, H = ys.shape
+    if tuple(dy.shape) != (T, H):
+        raise ValueError(f"dy has shape {tuple(dy.shape)}, expected {(T, H)}")
+    _matrix(weights, "weights", torch.float32, (T, k))
+    if tokens is not None:
+        _dense(tokens, "tokens", torch.int32, (R,))
+    dys = _matrix(torch.empty_like(ys) if dys is None else dys, "dys", ys.dtype, (R, H))
+    dweights = _matrix(torch.empty_like(weights) if dweights is None else dweights, "dweights",
+                       torch.float32, (T, k))
+    _same_device(dy, ys, slots, weights, tokens, dys, dweights)
+    a = _permute_args(T, R, k, ys, "moe_combine_grad")
+    args = (_ptr(dy), _ptr(ys), _ptr(slots), _ptr(weights), _ptr(tokens), _ptr(dys),
+            _ptr(dweights), ctypes.byref(a))
+    return _bra.Plan(_bra.library().moe_combine_grad, args, "moe_combine_grad",
+                     {"dys": dys, "dweights": dweights}, (dy, ys, slots, weights, tokens, a))
+
+
+def moe_combine_grad(dy, ys, slots, weights, tokens=None, dys=None, dweights=None,
+                     stream=None) -> dict:
+    """Gradients of moe_combine: {'dys': (R, H), 'dweights': (T, k) fp32}.
+
+    tokens (of moe_route): rows without a token get zeros; without it those
+    rows of dys are not written."""
+    return moe_combine_grad_plan(dy, ys, slots, weights, tokens, dys, dweights).run(stream)

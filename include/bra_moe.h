@@ -1,7 +1,8 @@
 /*
  * bra_moe.h -- ragged expert operators of libbmmrsa2a.so: matrix products
  * grouped by expert with row groups of any size, and their gradients; the
- * same products on 4-bit microscaled weights and rows.
+ * same products on 4-bit microscaled weights and rows; the router that makes
+ * the groups, and the moves of token rows to their experts and back.
  *
  * They work on what a variable-count exchange delivers: one matrix of rows
  * sorted by expert, and the number of rows of each expert in device memory
@@ -19,8 +20,9 @@
 extern "C" {
 #endif
 
-/* Most row groups (experts) of one call. */
+/* Most row groups (experts) of one call, and most experts of one token. */
 #define BRA_MAX_GROUPS 512
+#define BRA_MAX_CHOICES 16
 
 /* ------------------------------------------------------------------------ */
 /* Products grouped by expert                                                */
@@ -172,6 +174,98 @@ BRA_API int mxfp4_grouped_matmul(const uint8_t* x_codes, const uint8_t* x_scales
                                  const uint8_t* w_codes, const uint8_t* w_scales,
                                  const void* bias, const int64_t* counts, void* y,
                                  const bra_grouped_args* args, bra_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Router                                                                    */
+/* ------------------------------------------------------------------------ */
+
+typedef struct {
+  int64_t tokens;      /* T: 0 .. 2^31 - 1, T * k below 2^31                  */
+  int64_t experts;     /* E: 1 .. BRA_MAX_GROUPS                              */
+  int64_t choices;     /* k: 1 .. min(E, BRA_MAX_CHOICES)                     */
+  int32_t dtype;       /* logits: BRA_FP16, BRA_BF16 or BRA_FP32              */
+  int32_t renormalize; /* non-zero: weights add up to 1 over the chosen       */
+} bra_route_args;
+
+/*
+ * moe_route -- each token's k experts from its logits (T, E), and the order
+ * that sorts the (token, choice) pairs by expert.
+ *   A logit of -inf or NaN closes an expert to a token; +inf counts as the
+ *   largest float.  The k largest open logits are chosen, largest first, ties
+ *   to the lowest expert.  With fewer than k open ones the choices left have
+ *   id -1, weight 0 and slot -1.
+ *   ids     (T, k) int32.
+ *   weights (T, k) fp32: the softmax over the token's open experts at the
+ *           chosen ones; with renormalize divided by their sum.
+ *   counts  (E) int64: pairs of each expert: grouped_matmul's and, as a row
+ *           of its matrix, all_to_all_v's counts.
+ *   slots   (T, k) int32: the pair's row among the R = T * k rows sorted by
+ *           expert, within an expert by token.
+ *   tokens  (R) int32: the token of each row; -1 for the rows past the last
+ *           pair.
+ * workspace: moe_route_workspace_size bytes (0 for a few tokens), 256-byte
+ * aligned.
+ * Errors: BRA_ERR_NULLPTR (args or counts; with tokens > 0 any pointer, or a
+ * workspace where one is needed); BRA_ERR_INVALID: sizes outside the ranges,
+ * another dtype, pointers not element-aligned, a workspace too small or
+ * misaligned, an output overlapping the logits or another output;
+ * BRA_ERR_CUDA.
+ */
+BRA_API int moe_route(const void* logits, int32_t* ids, float* weights, int64_t* counts,
+                      int32_t* slots, int32_t* tokens, void* workspace, int64_t workspace_bytes,
+                      const bra_route_args* args, bra_stream_t stream);
+BRA_API int64_t moe_route_workspace_size(const bra_route_args* args);
+
+/*
+ * moe_route_grad -- the gradient of the logits (T, E, their type) for the
+ * gradient dweights (T, k) fp32 of moe_route's weights, with its ids and
+ * weights: the softmax's, closed experts and missing choices get 0.  logits
+ * are read without renormalize only (NULL otherwise allowed).  ids outside
+ * [0, E) count as missing.  Errors as moe_route.
+ */
+BRA_API int moe_route_grad(const float* dweights, const void* logits, const int32_t* ids,
+                           const float* weights, void* dlogits, const bra_route_args* args,
+                           bra_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Token rows to their experts and back                                      */
+/* ------------------------------------------------------------------------ */
+
+typedef struct {
+  int64_t tokens;      /* T: 0 .. 2^31 - 1                                    */
+  int64_t rows;        /* R: 0 .. 2^31 - 1                                    */
+  int64_t choices;     /* k: 1 .. BRA_MAX_CHOICES                             */
+  int64_t width;       /* H: elements of a row, 1 .. 2^24                     */
+  int32_t dtype;       /* rows: BRA_FP16, BRA_BF16 or BRA_FP32                */
+  int32_t reserved;    /* 0                                                   */
+} bra_permute_args;
+
+/*
+ * Token rows are (T, H), expert rows (R, H), dense; tokens (R) and slots
+ * (T, k) int32 as moe_route writes them, weights (T, k) fp32.  Sums in fp32
+ * in the order of the choices, one rounding; results do not change from run
+ * to run.  Entries outside their range count as -1 and are never followed.
+ *   moe_dispatch       xs[r] = x[tokens[r]]; zeros for -1.  (choices unused)
+ *   moe_dispatch_grad  dx[t] = sum of dxs[slots[t, j]] over j, -1 left out.
+ *   moe_combine        y[t] = sum of weights[t, j] * ys[slots[t, j]].
+ *   moe_combine_grad   dys[slots[t, j]] = weights[t, j] * dy[t];
+ *                      dweights[t, j] = <dy[t], ys[slots[t, j]]>, 0 for -1.
+ *                      Rows whose token is -1 get zeros (tokens NULL: they
+ *                      are not written).  No two slots may be the same.
+ * Errors: BRA_ERR_NULLPTR for a NULL args, or pointer to data there is;
+ * BRA_ERR_INVALID: sizes outside the ranges, another dtype, pointers not
+ * element-aligned, an output overlapping an input or the other output;
+ * BRA_ERR_CUDA.
+ */
+BRA_API int moe_dispatch(const void* x, const int32_t* tokens, void* xs,
+                         const bra_permute_args* args, bra_stream_t stream);
+BRA_API int moe_dispatch_grad(const void* dxs, const int32_t* slots, void* dx,
+                              const bra_permute_args* args, bra_stream_t stream);
+BRA_API int moe_combine(const void* ys, const int32_t* slots, const float* weights, void* y,
+                        const bra_permute_args* args, bra_stream_t stream);
+BRA_API int moe_combine_grad(const void* dy, const void* ys, const int32_t* slots,
+                             const float* weights, const int32_t* tokens, void* dys,
+                             float* dweights, const bra_permute_args* args, bra_stream_t stream);
 
 #ifdef __cplusplus
 }

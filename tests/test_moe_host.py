@@ -171,3 +171,94 @@ def test_mx_refuses_pointers(lib):
         assert call(*ok[:6], ok[i], g, None) == INVALID, i          # y over an input
     for change in (dict(transpose_weight=1), dict(x_pitch=64), dict(dtype=bra.FP32)):
         assert call(*ok, ctypes.byref(args(**change)), None) == INVALID
+
+
+def route(**kw):
+    a = bra.RouteArgs()
+    base = dict(tokens=100, experts=16, choices=4, dtype=bra.FP32)
+    base.update(kw)
+    for k, v in base.items():
+        setattr(a, k, v)
+    return a
+
+
+def permute(**kw):
+    a = bra.PermuteArgs()
+    base = dict(tokens=16, rows=64, choices=4, width=72, dtype=bra.FP16)
+    base.update(kw)
+    for k, v in base.items():
+        setattr(a, k, v)
+    return a
+
+
+def test_route_limits_and_workspace(lib):
+    text = pathlib.Path(HEADER).read_text()
+    assert int(re.search(r"#define BRA_MAX_CHOICES (\d+)", text).group(1)) == bra.MAX_CHOICES
+    assert ctypes.sizeof(bra.RouteArgs) == 32 and ctypes.sizeof(bra.PermuteArgs) == 40
+    size = lambda **kw: lib.moe_route_workspace_size(ctypes.byref(route(**kw)))   # noqa: E731
+    assert size(tokens=0) == 0 and size(tokens=64) == 0
+    assert size(tokens=65) == 256                        # three chunks of 32 tokens, 16 experts
+    assert size(tokens=65536, experts=128) == 128 * 128 * 4
+    assert size(experts=513) == -INVALID
+
+
+@pytest.mark.parametrize("change", [
+    dict(tokens=-1), dict(tokens=1 << 31), dict(tokens=1 << 30, choices=2), dict(experts=0),
+    dict(experts=513), dict(choices=0), dict(choices=17), dict(experts=3), dict(dtype=bra.INT8),
+], ids=str)
+def test_route_refuses_sizes(lib, change):
+    a = ctypes.byref(route(**change))
+    assert lib.moe_route(X, W, B, C, Y, G, S, 1 << 40, a, None) == INVALID
+    assert lib.moe_route_grad(B, X, W, C, G, a, None) == INVALID
+
+
+def test_route_refuses_pointers(lib):
+    a = ctypes.byref(route())
+    ok = [X, W, B, C, Y, G, S]
+    for i in range(7):
+        bad = list(ok)
+        bad[i] = None
+        assert lib.moe_route(*bad, 1 << 20, a, None) == NULLPTR, i
+        bad[i] = ok[i] + 2
+        assert lib.moe_route(*bad, 1 << 20, a, None) == INVALID, i
+    assert lib.moe_route(*ok, 128, a, None) == INVALID                  # workspace too small
+    assert lib.moe_route(X, X, B, C, Y, G, S, 1 << 20, a, None) == INVALID
+    assert lib.moe_route(X, W, B, C, Y, Y + 64, S, 1 << 20, a, None) == INVALID
+    g = [B, X, W, C, G]
+    for i in (0, 2, 3, 4):
+        bad = list(g)
+        bad[i] = None
+        assert lib.moe_route_grad(*bad, a, None) == NULLPTR, i
+    assert lib.moe_route_grad(B, None, W, C, G, a, None) == NULLPTR     # needed: not renormalised
+    assert lib.moe_route_grad(B, X, W, C, X, a, None) == INVALID
+    assert lib.moe_route(X, W, B, C, Y, G, S, 1 << 20, None, None) == NULLPTR
+
+
+@pytest.mark.parametrize("change", [
+    dict(tokens=-1), dict(rows=1 << 31), dict(choices=0), dict(choices=17), dict(width=0),
+    dict(width=(1 << 24) + 1), dict(dtype=bra.INT8), dict(reserved=1),
+], ids=str)
+def test_permute_refuses_sizes(lib, change):
+    a = ctypes.byref(permute(**change))
+    assert lib.moe_dispatch(X, W, Y, a, None) == INVALID
+    assert lib.moe_dispatch_grad(X, W, Y, a, None) == INVALID
+    assert lib.moe_combine(X, W, B, Y, a, None) == INVALID
+    assert lib.moe_combine_grad(X, W, B, C, None, Y, G, a, None) == INVALID
+
+
+def test_permute_refuses_pointers(lib):
+    a = ctypes.byref(permute())
+    calls = [(lib.moe_dispatch, [X, W, Y]), (lib.moe_dispatch_grad, [X, W, Y]),
+             (lib.moe_combine, [X, W, B, Y]), (lib.moe_combine_grad, [X, W, B, C, S, Y, G])]
+    for fn, ok in calls:
+        for i in range(len(ok)):
+            bad = list(ok)
+            bad[i] = None
+            if not (fn is lib.moe_combine_grad and i == 4):             # its tokens may be left out
+                assert fn(*bad, a, None) == NULLPTR, (fn, i)
+            bad[i] = ok[i] + 1
+            assert fn(*bad, a, None) == INVALID, (fn, i)
+        bad = list(ok)
+        bad[-1] = ok[0]
+        assert fn(*bad, a, None) == INVALID                             # an output over an input
+        assert fn(*ok, None, None) == NULLPTR

@@ -184,25 +184,54 @@ __device__ __forceinline__ void put_segment(const uint32_t (&o)[32], T* y0, int6
           *reinterpret_cast<uint4*>(y0 + (4 * q + r0) * ldy + nc + c8) = w[q];
     }
   } else if (cols > 0) {
-    // (row, chunk) pairs: whole chunks as vectors, the partial ones at the
-    // segment's two ends element by element
-#pragma unroll 1
-    for (int u = lane; u < valid * 9; u += 32) {
-      const int r = u / 9, c = u - r * 9;
+    // The run of a row lies at [d, d + cols) of its shifted segment.  Whole
+    // 16-byte chunks first, as above; then each lane its own row's partial
+    // chunks at the two ends, in aligned pieces of 8, 4 and 2 bytes.
+    const int c8 = (lane & 7) * 8, r0 = lane >> 3;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int r = 4 * q + r0;
       T* dst = y0 + r * ldy + nc;
       const int d = (int)((reinterpret_cast<uintptr_t>(dst) & 15u) >> 1);
-      const int lo = max(c * 8, d), hi = min(c * 8 + 8, d + cols);   // in the shifted segment
-      if (lo >= hi) continue;
-      const uint4 w = lds128e(seg + (uint32_t)r * kSegStride + c * 16);
-      if (hi - lo == 8) {
-        *reinterpret_cast<uint4*>(dst - d + c * 8) = w;
-      } else {
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c * 8 + i >= lo && c * 8 + i < hi)
-            reinterpret_cast<uint16_t*>(dst)[c * 8 + i - d] =
-                (uint16_t)(ws[i >> 1] >> ((i & 1) * 16));
+      if (r < valid && c8 >= d && c8 + 8 <= d + cols)
+        *reinterpret_cast<uint4*>(dst + (c8 - d)) = lds128e(seg + (uint32_t)r * kSegStride + c8 * 2);
+    }
+    if (lane < valid) {
+      T* dst = y0 + lane * ldy + nc;
+      const int d = (int)((reinterpret_cast<uintptr_t>(dst) & 15u) >> 1), end = d + cols;
+      uint16_t* out = reinterpret_cast<uint16_t*>(dst) - d;        // by place in the segment
+      auto put2 = [&](int i) {
+        uint16_t w;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w) : "r"(my + i * 2) : "memory");
+        out[i] = w;
+      };
+      auto put4 = [&](int i) {
+        uint32_t w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(my + i * 2) : "memory");
+        *reinterpret_cast<uint32_t*>(out + i) = w;
+      };
+      auto put8 = [&](int i) {
+        uint2 w;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(w.x), "=r"(w.y)
+                     : "r"(my + i * 2)
+                     : "memory");
+        *reinterpret_cast<uint2*>(out + i) = w;
+      };
+      if (d > 0) {
+        const int stop = min(8, end);
+        int i = d;
+        if ((i & 1) && i < stop) put2(i++);
+        if ((i & 2) && i + 2 <= stop) put4(i), i += 2;
+        if ((i & 4) && i + 4 <= stop) put8(i), i += 4;
+        for (; i < stop; ++i) put2(i);                             // a run within one chunk
+      }
+      const int last = end & ~7;
+      if ((end & 7) && (last > 0 || d == 0)) {
+        int i = last;
+        if (end & 4) put8(i), i += 4;
+        if (end & 2) put4(i), i += 2;
+        if (end & 1) put2(i);
       }
     }
   }

@@ -64,26 +64,19 @@ Copy copy_of(const void* p, int64_t rows, int64_t n, int64_t ld) {
   return c;
 }
 
-// Hands out workspace and enqueues the copies.
+// Hands out workspace; copy() enqueues what was taken, before the products.
 struct Workspace {
   uint8_t* at;
-  int64_t left;
-  int rc = BRA_OK;
-  const void* take(const void* src, const Copy& c, cudaStream_t st) {
-    if (!c.need || rc != BRA_OK) return src;
-    if (!at) {
-      rc = BRA_ERR_UNSUPPORTED;
-      return src;
-    }
-    if (left < c.bytes) {
-      rc = BRA_ERR_INVALID;
-      return src;
-    }
+  PackJobs jobs = {};
+  const void* take(const void* src, const Copy& c) {
+    if (!c.need) return src;
     void* dst = at;
     at += c.bytes;
-    left -= c.bytes;
-    if (launch_pack_rows(src, c.ld, dst, c.pitch, c.rows, c.n, st) != cudaSuccess) rc = BRA_ERR_CUDA;
+    jobs.job[jobs.n++] = {src, dst, c.ld, c.pitch, c.rows, c.n};
     return dst;
+  }
+  int copy(cudaStream_t st) {
+    return launch_pack_rows(jobs, st) == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;
   }
 };
 
@@ -441,12 +434,12 @@ int grouped_matmul(const void* x, const void* weight, const void* bias, const in
   if (s.R == 0) return clear_status(args->status, st);
   if ((rc = check_workspace(args, cx.bytes + cw.bytes)) != BRA_OK) return rc;
   if ((rc = clear_status(args->status, st)) != BRA_OK) return rc;
-  Workspace ws{static_cast<uint8_t*>(args->workspace), args->workspace_bytes};
+  Workspace ws{static_cast<uint8_t*>(args->workspace)};
   GroupedProblem g;
   std::memset(&g, 0, sizeof(g));
-  g.x = ws.take(x, cx, st);
-  g.w = ws.take(weight, cw, st);
-  if (ws.rc != BRA_OK) return ws.rc;
+  g.x = ws.take(x, cx);
+  g.w = ws.take(weight, cw);
+  if ((rc = ws.copy(st)) != BRA_OK) return rc;
   g.bias = bias;
   g.y = y;
   g.counts = counts;
@@ -506,7 +499,7 @@ int grouped_matmul_grad(const void* dy, const void* x, const void* weight, const
   const int64_t need = (dx || dweight ? cd.bytes : 0) + (dx ? cw.bytes : 0) + (dweight ? cx.bytes : 0);
   if ((rc = check_workspace(args, need)) != BRA_OK) return rc;
   if ((rc = clear_status(args->status, st)) != BRA_OK) return rc;
-  Workspace ws{static_cast<uint8_t*>(args->workspace), args->workspace_bytes};
+  Workspace ws{static_cast<uint8_t*>(args->workspace)};
   GroupedProblem g;
   std::memset(&g, 0, sizeof(g));
   g.counts = counts;
@@ -514,13 +507,15 @@ int grouped_matmul_grad(const void* dy, const void* x, const void* weight, const
   g.R = s.R;
   g.E = (int)s.E;
   g.dtype = args->dtype;
-  const void* d = dx || dweight ? ws.take(dy, cd, st) : dy;
+  const void* d = dx || dweight ? ws.take(dy, cd) : dy;
+  const void* w = dx ? ws.take(weight, cw) : weight;
+  const void* xs = dweight ? ws.take(x, cx) : x;
+  if ((rc = ws.copy(st)) != BRA_OK) return rc;
   if (dx) {
     // dx = dy W^T: the contraction runs over N, the weight's layout as stored
     // is the other one seen from here
     g.x = d;
-    g.w = ws.take(weight, cw, st);
-    if (ws.rc != BRA_OK) return ws.rc;
+    g.w = w;
     g.y = dx;
     g.ldx = cd.pitch;
     g.ldw = cw.pitch;
@@ -531,8 +526,6 @@ int grouped_matmul_grad(const void* dy, const void* x, const void* weight, const
     if ((rc = status_of(launch_grouped_fwd(g, st))) != BRA_OK) return rc;
   }
   if (dweight) {
-    const void* xs = ws.take(x, cx, st);
-    if (ws.rc != BRA_OK) return ws.rc;
     // (E, N, K) gradients are the same product with the operands exchanged
     g.x = wt ? d : xs;
     g.w = wt ? xs : d;

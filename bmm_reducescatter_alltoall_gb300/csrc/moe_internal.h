@@ -38,10 +38,18 @@ struct BiasGradProblem {
   int E, N, dtype;
 };
 cudaError_t launch_bias_grad(const BiasGradProblem& g, cudaStream_t st);
-// Copies `rows` rows of `len` 16-bit elements, ld apart, to rows `pitch` apart
-// (a multiple of 8) at a 16-byte aligned dst.
-cudaError_t launch_pack_rows(const void* src, int64_t ld, void* dst, int64_t pitch, int64_t rows,
-                             int64_t len, cudaStream_t st);
+// Copies rows of `len` 16-bit elements, ld apart, to rows `pitch` apart (a
+// multiple of 8) at a 16-byte aligned dst; a call's copies in one launch.
+struct PackJob {
+  const void* src;
+  void* dst;
+  int64_t ld, pitch, rows, len;
+};
+struct PackJobs {
+  PackJob job[3];
+  int n;
+};
+cudaError_t launch_pack_rows(const PackJobs& jobs, cudaStream_t st);
 // Rows in the 4-bit microscaled layout (mx.cuh): row groups of `each` rows,
 // or of counts[E] rows when each is 0.
 struct MxRows {

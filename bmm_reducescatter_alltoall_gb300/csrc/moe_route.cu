@@ -7,14 +7,17 @@
 //             chosen) of exp(l - m), m the largest logit
 //   row of (t, j) = rows of lower experts + earlier tokens with this expert
 //
-// One warp takes a token: lane l holds logits l, l + 32, ...  A choice is two
-// warp reductions, of the logit as an ordered integer and of the lowest index
-// that has it.  Tokens are dealt to CTAs in chunks.  In a chunk each expert
-// has a bit per token, set by whoever chose it: a population count below a
-// token's bit is its place among the chunk's rows of that expert, in token
-// order and without any order of the setting.  The chunks' counts go to a
-// small matrix; a second kernel sums the chunks before its own and the lower
-// experts and writes the rows.  A single chunk does both in one launch.
+// A group of L lanes takes a token, 16 logits a lane (L = 4 to 32 by E), so a
+// warp has 32 / L tokens in hand: the scan of a lane's 16 logits after each
+// choice and the log2(L) exchange steps serve all of them.  (With a warp to a
+// token and the hardware's warp reductions, two to a choice, 65536 tokens of
+// 128 experts took 55 us; the reductions, about 32 cycles each, were the
+// bound.)  Tokens are dealt to CTAs in chunks.  In a chunk each expert has a
+// bit per token, set by whoever chose it: a population count below a token's
+// bit is its place among the chunk's rows of that expert, in token order and
+// without any order of the setting.  The chunks' counts go to a small matrix;
+// a second kernel adds to each place the rows of the chunks before and of the
+// lower experts.  A single chunk does both in one launch.
 // Bound by reading the logits once (4 bytes x E a token) and, for few tokens,
 // by latency.
 #include <cuda_bf16.h>
@@ -45,12 +48,6 @@ __device__ __forceinline__ uint32_t key_of(float v) {
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
-}
-
 struct RouteParams {
   const void* logits;
   int32_t* ids;        // [T][k]
@@ -61,57 +58,113 @@ struct RouteParams {
   int32_t* hist;       // [chunks][E], unless there is one chunk
   int T, E, k, renorm;
   int chunk, chunks;   // tokens of a chunk (a multiple of 32)
+  int vec;             // logits' rows are read four at a time
 };
 
-// One token's choice: lane j < k gets the j-th expert (-1: none) and weight.
-template <typename T, int V>
-__device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, int* id, float* w) {
+__device__ __forceinline__ float group_sum(float v, int L) {
+  for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// The experts of one token to each group of L lanes (t < 0: none): lane l of
+// the group holds logits (i / 4) * 4L + 4l + i % 4, i < 16, so that four of
+// them are one 16-byte load.  Writes ids and weights and sets the chunk's
+// bits (word `word`, bit `bit` of each expert's `words`).  Whole warps.
+template <typename T, int L>
+__device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, uint32_t* bits,
+                                       int words, int word, uint32_t bit) {
+  constexpr int V = 16, OWN = (BRA_MAX_CHOICES + L - 1) / L;   // choices a lane keeps
+  const int gl = lane % L;
   const T* row = static_cast<const T*>(p.logits) + (int64_t)t * p.E;
   float v[V];
   uint32_t key[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const bool in = lane + 32 * i < p.E;
-    v[i] = in ? logit(row + lane + 32 * i) : 0.f;
-    key[i] = in ? key_of(v[i]) : 0u;
+  for (int i = 0; i < V; i += 4) {
+    const int at = i * L + 4 * gl;
+    T raw[4];
+    if (t >= 0 && p.vec && at + 4 <= p.E) {
+      if constexpr (sizeof(T) == 4) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + at));
+        *reinterpret_cast<uint4*>(raw) = q;
+      } else {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + at));
+        *reinterpret_cast<uint2*>(raw) = q;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) raw[c] = t >= 0 && at + c < p.E ? row[at + c] : T(-INFINITY);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v[i + c] = logit(&raw[c]);
+      key[i + c] = at + c < p.E ? key_of(v[i + c]) : 0u;
+    }
   }
-  int my_id = -1;
-  uint32_t my_key = 0u, top = 0u;
-  for (int j = 0; j < p.k; ++j) {
-    uint32_t best = key[0];
+  uint32_t best = key[0];
+  int rel = 0;                                  // index of `best` less 4 gl
 #pragma unroll
-    for (int i = 1; i < V; ++i) best = max(best, key[i]);
-    const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-    if (most == 0u) break;                       // no valid expert is left
-    if (j == 0) top = most;
-    uint32_t at = 0xffffffffu;
+  for (int i = 1; i < V; ++i)
+    if (key[i] > best) {
+      best = key[i];
+      rel = (i / 4) * 4 * L + i % 4;
+    }
+  uint32_t my_key[OWN], top = 0u;
+  int64_t out = (int64_t)t * p.k;
 #pragma unroll
-    for (int i = V - 1; i >= 0; --i)
-      if (key[i] == most) at = lane + 32 * i;
-    at = __reduce_min_sync(0xffffffffu, at);
+  for (int o = 0; o < OWN; ++o) {
+    my_key[o] = 0u;
+    for (int j = o * L; j < min(p.k, (o + 1) * L); ++j) {
+      uint32_t most = best;
+      int at = rel + 4 * gl;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (at == (uint32_t)(lane + 32 * i)) key[i] = 0u;
-    if (lane == j) {
-      my_id = (int)at;
-      my_key = most;
+      for (int d = L / 2; d > 0; d >>= 1) {
+        const uint32_t mk = __shfl_xor_sync(0xffffffffu, most, d);
+        const int mi = __shfl_xor_sync(0xffffffffu, at, d);
+        if (mk > most || (mk == most && mi < at)) {
+          most = mk;
+          at = mi;
+        }
+      }
+      if (j == 0) top = most;
+      if (gl == j - o * L) {
+        my_key[o] = most;
+        if (t >= 0) {
+          p.ids[out + j] = most ? at : -1;
+          if (most) atomicOr(&bits[at * words + word], bit);
+        }
+      }
+      // strike it out and find the lane's best again
+      const int gone = most ? at - 4 * gl : -1;
+      best = 0u;
+      rel = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = (i / 4) * 4 * L + i % 4;
+        if (gone == c) key[i] = 0u;
+        if (key[i] > best) {
+          best = key[i];
+          rel = c;
+        }
+      }
     }
   }
   const float m = value_of(top);
-  const float e = my_id >= 0 ? expf(value_of(my_key) - m) : 0.f;
-  float s;
-  if (p.renorm) {
-    s = warp_sum(e);
-  } else {
-    // all valid logits: those still marked, and the chosen ones
-    s = e;
+  float e[OWN], s = 0.f;
+#pragma unroll
+  for (int o = 0; o < OWN; ++o) {
+    e[o] = my_key[o] ? expf(value_of(my_key[o]) - m) : 0.f;
+    s += e[o];
+  }
+  if (!p.renorm) {
+    // all open logits: those not struck out, and the chosen ones
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (key[i]) s += expf(v[i] - m);
-    s = warp_sum(s);
   }
-  *id = my_id;
-  *w = my_id >= 0 ? e / s : 0.f;
+  s = group_sum(s, L);
+#pragma unroll
+  for (int o = 0; o < OWN; ++o)
+    if (t >= 0 && o * L + gl < p.k) p.weights[out + o * L + gl] = my_key[o] ? e[o] / s : 0.f;
 }
 
 // The chunk's experts as bits: words (chunk / 32) to an expert.
@@ -149,33 +202,17 @@ __device__ __forceinline__ void scan_experts(const RouteParams& p, const int* to
   }
 }
 
-// Slots and tokens of the chunk's pairs, whose bits and bases are known, and
-// this chunk's share of the rows that no pair has.
-__device__ __forceinline__ void place(const RouteParams& p, int c, const uint32_t* bits,
-                                      const int* base, int used) {
-  const int words = p.chunk / 32, t0 = c * p.chunk, n = min(p.chunk, p.T - t0);
-  for (int i = threadIdx.x; i < n * p.k; i += kThreads) {
-    const int local = i / p.k;
-    const int64_t at = (int64_t)t0 * p.k + i;
-    const int e = p.ids[at];
-    int slot = -1;
-    if (e >= 0) {
-      const uint32_t* b = bits + e * words;
-      int rank = __popc(b[local >> 5] & ((1u << (local & 31)) - 1u));
-      for (int w = 0; w < (local >> 5); ++w) rank += __popc(b[w]);
-      slot = base[e] + rank;
-      p.tokens[slot] = t0 + local;
-    }
-    p.slots[at] = slot;
-  }
+// This chunk's share of the rows that no pair has.
+__device__ __forceinline__ void mark_unused(const RouteParams& p, int c, int used) {
   const int64_t R = (int64_t)p.T * p.k;
   for (int64_t r = used + (int64_t)c * kThreads + threadIdx.x; r < R;
        r += (int64_t)p.chunks * kThreads)
     p.tokens[r] = -1;
 }
 
-// Choices of one chunk; with a single chunk, everything.
-template <typename T, int V>
+// Choices of one chunk, and each pair's place among the chunk's rows of its
+// expert in `slots`; with a single chunk, everything.
+template <typename T, int L>
 __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParams p) {
   extern __shared__ uint32_t bits[];                    // [E][chunk / 32]
   __shared__ int total[kMaxGroups], base[kMaxGroups], zero[kMaxGroups];
@@ -185,16 +222,10 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParam
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   clear_bits(bits, p.E * words);
   __syncthreads();
-  for (int i = warp; i < n; i += kWarps) {
-    int id;
-    float w;
-    choose<T, V>(p, t0 + i, lane, &id, &w);
-    if (lane < p.k) {
-      const int64_t at = (int64_t)(t0 + i) * p.k + lane;
-      p.ids[at] = id;
-      p.weights[at] = w;
-      if (id >= 0) atomicOr(&bits[id * words + (i >> 5)], 1u << (i & 31));
-    }
+  constexpr int G = 32 / L;                             // tokens of a warp
+  for (int i0 = warp * G; i0 < n; i0 += kWarps * G) {
+    const int i = i0 + lane / L;
+    choose<T, L>(p, i < n ? t0 + i : -1, lane, bits, words, i >> 5, 1u << (i & 31));
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
@@ -208,29 +239,45 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParam
       p.counts[e] = s;
     }
   }
-  if (p.chunks > 1) return;
-  __syncthreads();
-  scan_experts(p, total, zero, base, &used);
-  __syncthreads();
-  place(p, 0, bits, base, used);
+  if (p.chunks == 1) {
+    __syncthreads();
+    scan_experts(p, total, zero, base, &used);
+    __syncthreads();
+    mark_unused(p, 0, used);
+  }
+  for (int i = threadIdx.x; i < n * p.k; i += kThreads) {
+    const int local = i / p.k;
+    const int64_t at = (int64_t)t0 * p.k + i;
+    const int e = p.ids[at];
+    int slot = -1;
+    if (e >= 0) {
+      const uint32_t* b = bits + e * words;
+      slot = __popc(b[local >> 5] & ((1u << (local & 31)) - 1u));
+      for (int w = 0; w < (local >> 5); ++w) slot += __popc(b[w]);
+      if (p.chunks == 1) {
+        slot += base[e];
+        p.tokens[slot] = local;
+      }
+    }
+    p.slots[at] = slot;
+  }
 }
 
 // Rows of one chunk, from the counts of all of them.
 __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams p) {
-  extern __shared__ uint32_t bits[];
   __shared__ int total[kMaxGroups], before[kMaxGroups], base[kMaxGroups];
   __shared__ int used;
-  const int words = p.chunk / 32, c = blockIdx.x, t0 = c * p.chunk;
+  const int c = blockIdx.x, t0 = c * p.chunk;
   const int n = min(p.chunk, p.T - t0);
-  clear_bits(bits, p.E * words);
   for (int e = threadIdx.x; e < p.E; e += kThreads) total[e] = before[e] = 0;
   __syncthreads();
+  cudaGridDependencySynchronize();                      // the choices are written
   // threads of a row of the matrix side by side, rows dealt over the rest
   const int width = (p.E + 31) / 32 * 32, rows = kThreads / width;
   const int e = threadIdx.x % width, r0 = threadIdx.x / width;
   if (e < p.E && r0 < rows) {
     int all = 0, old = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int r = r0; r < p.chunks; r += rows) {
       const int h = p.hist[(int64_t)r * p.E + e];
       all += h;
@@ -239,16 +286,22 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams
     atomicAdd(&total[e], all);
     atomicAdd(&before[e], old);
   }
-  for (int i = threadIdx.x; i < n * p.k; i += kThreads) {
-    const int id = p.ids[(int64_t)t0 * p.k + i], local = i / p.k;
-    if (id >= 0) atomicOr(&bits[id * words + (local >> 5)], 1u << (local & 31));
-  }
   __syncthreads();
   scan_experts(p, total, before, base, &used);
   if (c == 0)
     for (int i = threadIdx.x; i < p.E; i += kThreads) p.counts[i] = total[i];
   __syncthreads();
-  place(p, c, bits, base, used);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n * p.k; i += kThreads) {
+    const int64_t at = (int64_t)t0 * p.k + i;
+    const int id = p.ids[at];
+    if (id >= 0) {
+      const int slot = p.slots[at] + base[id];
+      p.slots[at] = slot;
+      p.tokens[slot] = t0 + i / p.k;
+    }
+  }
+  mark_unused(p, c, used);
 }
 
 // --------------------------------------------------------------------------
@@ -263,6 +316,7 @@ struct RouteGradParams {
   const float* weights;
   void* dlogits;
   int T, E, k, renorm;
+  int vec;             // rows are written four at a time
 };
 
 template <typename T>
@@ -270,85 +324,107 @@ __device__ __forceinline__ T rounded(float v) {
   return static_cast<T>(v);
 }
 
-template <typename T, int V>
+// A group of L lanes takes a token, with choose()'s places for 16 logits a
+// lane: rows are read and written 16 (8) bytes at a time.
+template <typename T, int L>
 __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p) {
-  const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * 8;
-  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < p.T; t += warps) {
-    int id = -1;
-    float w = 0.f, g = 0.f;
-    if (lane < p.k) {
-      const int64_t at = (int64_t)t * p.k + lane;
-      id = p.ids[at];
-      if (id >= 0) {
-        w = p.weights[at];
-        g = p.dweights[at];
-      }
+  constexpr int V = 16, G = 32 / L, OWN = (BRA_MAX_CHOICES + L - 1) / L;
+  const int lane = threadIdx.x & 31, gl = lane % L;
+  const int64_t step = (int64_t)gridDim.x * 8 * G;
+  for (int64_t t0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * G; t0 < p.T; t0 += step) {
+    const int64_t t = t0 + lane / L;
+    const bool in = t < p.T;
+    int id[OWN];
+    float w[OWN], g[OWN], s = 0.f;
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      const int j = o * L + gl;
+      const int64_t at = t * p.k + j;
+      id[o] = in && j < p.k ? p.ids[at] : -1;
+      w[o] = id[o] >= 0 ? p.weights[at] : 0.f;
+      g[o] = id[o] >= 0 ? p.dweights[at] : 0.f;
+      s += w[o] * g[o];
     }
-    const float s = warp_sum(w * g);
-    float d[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = 0.f;
-    if (p.renorm) {
-      const float mine = w * (g - s);
-      for (int j = 0; j < p.k; ++j) {
-        const int at = __shfl_sync(0xffffffffu, id, j);
-        const float dj = __shfl_sync(0xffffffffu, mine, j);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (at == lane + 32 * i) d[i] = dj;
-      }
-    } else {
-      const T* row = static_cast<const T*>(p.logits) + (int64_t)t * p.E;
+    s = group_sum(s, L);
+    const T* row = static_cast<const T*>(p.logits) + t * p.E;
+    float d[V], q[V];
+    if (!p.renorm) {
       float v[V];
       uint32_t best = 0u;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        v[i] = lane + 32 * i < p.E ? logit(row + lane + 32 * i) : -INFINITY;
+        const int c = (i / 4) * 4 * L + 4 * gl + i % 4;
+        v[i] = in && c < p.E ? logit(row + c) : -INFINITY;
         best = max(best, key_of(v[i]));
       }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      const float m = value_of(top);
+#pragma unroll
+      for (int m = L / 2; m > 0; m >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, m));
+      const float m = value_of(best);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        v[i] = key_of(v[i]) ? expf(v[i] - m) : 0.f;
-        sum += v[i];
+        q[i] = key_of(v[i]) ? expf(v[i] - m) : 0.f;
+        sum += q[i];
       }
-      sum = warp_sum(sum);
+      sum = group_sum(sum, L);
       const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = -s;
-      for (int j = 0; j < p.k; ++j) {
-        const int at = __shfl_sync(0xffffffffu, id, j);
-        const float gj = __shfl_sync(0xffffffffu, g, j);
+      for (int i = 0; i < V; ++i) {
+        q[i] *= inv;
+        d[i] = -s * q[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] = 0.f;
+    }
+#pragma unroll
+    for (int o = 0; o < OWN; ++o)
+      for (int j = o * L; j < min(p.k, (o + 1) * L); ++j) {
+        const int from = (lane & ~(L - 1)) + j - o * L;
+        const int at = __shfl_sync(0xffffffffu, id[o], from) - 4 * gl;
+        const float gj = __shfl_sync(0xffffffffu, g[o], from) - s;
+        const float wj = __shfl_sync(0xffffffffu, w[o], from);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (at == lane + 32 * i) d[i] = gj - s;
+          if (at == (i / 4) * 4 * L + i % 4) d[i] = (p.renorm ? wj : q[i]) * gj;
       }
+    if (!in) continue;
+    T* out = static_cast<T*>(p.dlogits) + t * p.E;
 #pragma unroll
-      for (int i = 0; i < V; ++i) d[i] *= v[i] * inv;
+    for (int i = 0; i < V; i += 4) {
+      const int at = i * L + 4 * gl;
+      T r[4] = {rounded<T>(d[i]), rounded<T>(d[i + 1]), rounded<T>(d[i + 2]), rounded<T>(d[i + 3])};
+      if (p.vec && at + 4 <= p.E) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(r);
+        else
+          *reinterpret_cast<uint2*>(out + at) = *reinterpret_cast<const uint2*>(r);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (at + c < p.E) out[at + c] = r[c];
+      }
     }
-    T* out = static_cast<T*>(p.dlogits) + (int64_t)t * p.E;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < p.E) out[lane + 32 * i] = rounded<T>(d[i]);
   }
 }
 
-// Calls f.template operator()<T, V>() for the logits' type and E.
+// f for the logits' type and the lanes of a token: 16 logits a lane.
 template <typename F>
 cudaError_t by_type(int dtype, int E, F&& f) {
-  auto by_width = [&](auto* type) {
-    if (E <= 32) return f(type, std::integral_constant<int, 1>{});
-    if (E <= 64) return f(type, std::integral_constant<int, 2>{});
-    if (E <= 128) return f(type, std::integral_constant<int, 4>{});
-    if (E <= 256) return f(type, std::integral_constant<int, 8>{});
-    return f(type, std::integral_constant<int, 16>{});
+  auto by_lanes = [&](auto* type) {
+    if (E <= 64) return f(type, std::integral_constant<int, 4>{});
+    if (E <= 128) return f(type, std::integral_constant<int, 8>{});
+    if (E <= 256) return f(type, std::integral_constant<int, 16>{});
+    return f(type, std::integral_constant<int, 32>{});
   };
-  if (dtype == BRA_FP32) return by_width((float*)nullptr);
-  if (dtype == BRA_BF16) return by_width((__nv_bfloat16*)nullptr);
-  return by_width((__half*)nullptr);
+  if (dtype == BRA_FP32) return by_lanes((float*)nullptr);
+  if (dtype == BRA_BF16) return by_lanes((__nv_bfloat16*)nullptr);
+  return by_lanes((__half*)nullptr);
+}
+
+// Whether rows of E elements can be read four at a time.
+int rows_vec(const void* p, int E, int dtype) {
+  return E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & (dtype == BRA_FP32 ? 15u : 7u)) == 0;
 }
 
 }  // namespace
@@ -363,42 +439,49 @@ int route_chunk(int64_t T) {
 
 cudaError_t launch_route(const RouteCall& r, cudaStream_t st) {
   RouteParams p = {r.logits, r.ids,   r.weights, r.counts, r.slots, r.tokens, r.hist, (int)r.T,
-                   r.E,      r.k,     r.renorm,  route_chunk(r.T), 0};
+                   r.E,      r.k,     r.renorm,  route_chunk(r.T), 0,
+                   rows_vec(r.logits, r.E, r.dtype)};
   p.chunks = (int)((r.T + p.chunk - 1) / p.chunk);
   const int smem = r.E * (p.chunk / 32) * 4;
-  const cudaError_t e = by_type(r.dtype, r.E, [&](auto* type, auto v) {
+  const cudaError_t e = by_type(r.dtype, r.E, [&](auto* type, auto l) {
     using T = std::remove_pointer_t<decltype(type)>;
     if (smem > 32768) {
       const cudaError_t a =
-          cudaFuncSetAttribute(route_choose_kernel<T, decltype(v)::value>,
+          cudaFuncSetAttribute(route_choose_kernel<T, decltype(l)::value>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (a != cudaSuccess) return a;
     }
-    route_choose_kernel<T, decltype(v)::value><<<p.chunks, kThreads, smem, st>>>(p);
+    route_choose_kernel<T, decltype(l)::value><<<p.chunks, kThreads, smem, st>>>(p);
     return cudaGetLastError();
   });
   if (e != cudaSuccess || p.chunks == 1) return e;
-  if (smem > 32768) {
-    const cudaError_t a = cudaFuncSetAttribute(
-        route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (a != cudaSuccess) return a;
-  }
-  route_place_kernel<<<p.chunks, kThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  // launched while the choices are still being made; it waits for them itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.chunks, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, route_place_kernel, p);
 }
 
 cudaError_t launch_route_grad(const RouteGradCall& r, cudaStream_t st) {
   const RouteGradParams p = {r.dweights, r.logits, r.ids, r.weights, r.dlogits,
-                             (int)r.T,   r.E,      r.k,   r.renorm};
+                             (int)r.T,   r.E,      r.k,   r.renorm,
+                             rows_vec(r.dlogits, r.E, r.dtype)};
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t want = (r.T + 7) / 8, full = (int64_t)sms * 8;
-  const unsigned grid = (unsigned)(want < full ? want : full);
-  return by_type(r.dtype, r.E, [&](auto* type, auto v) {
+  return by_type(r.dtype, r.E, [&](auto* type, auto l) {
     using T = std::remove_pointer_t<decltype(type)>;
-    route_grad_kernel<T, decltype(v)::value><<<grid, 256, 0, st>>>(p);
+    constexpr int tokens = 8 * 32 / decltype(l)::value;           // of a block
+    const int64_t want = (r.T + tokens - 1) / tokens, full = (int64_t)sms * 8;
+    route_grad_kernel<T, decltype(l)::value>
+        <<<(unsigned)(want < full ? want : full), 256, 0, st>>>(p);
     return cudaGetLastError();
   });
 }

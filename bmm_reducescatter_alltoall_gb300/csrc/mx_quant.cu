@@ -34,23 +34,60 @@ __device__ __forceinline__ float2 pair_of<__nv_bfloat16>(uint32_t w) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
 
-__device__ __forceinline__ uint32_t code_pair(float lo, float hi) {
-  uint16_t r;
-  asm("{\n\t.reg .b8 t;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-      "cvt.u16.u8 %0, t;\n\t}"
-      : "=h"(r)
-      : "f"(hi), "f"(lo));
+// Eight codes, the first in the lowest four bits.
+__device__ __forceinline__ uint32_t code_word(const float (&f)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return r;
 }
+// Two codes (the low byte of w) as a pair of halves, which hold them exactly.
+__device__ __forceinline__ float2 values_of(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+      : "=r"(h)
+      : "r"(w));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// A warp's walk over (row, unit of kPieces pieces): units are dealt to the
+// grid's warps in order, and the next one is found by adding, not dividing.
+struct Walk {
+  uint32_t row, part, per_row, d_row, d_part;
+  __device__ __forceinline__ Walk(uint32_t k_units, int pieces) {
+    per_row = (k_units + pieces - 1) / pieces;
+    const uint32_t warps = gridDim.x * (blockDim.x / 32);
+    const uint32_t w = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+    row = w / per_row;
+    part = w - row * per_row;
+    d_row = warps / per_row;
+    d_part = warps - d_row * per_row;
+  }
+  __device__ __forceinline__ void next() {
+    row += d_row;
+    part += d_part;
+    if (part >= per_row) {
+      part -= per_row;
+      ++row;
+    }
+  }
+};
 
 // Row block and row within it of row r: groups of `each` rows, or of the
 // table's counts.
 __device__ __forceinline__ void locate(const GroupTable* gt, int E, int64_t each, int64_t r,
                                        int64_t* blk, int* in) {
   if (each > 0) {
-    const int64_t g = r / each, i = r - g * each;
-    *blk = g * ((each + 127) / 128) + i / 128;
+    const uint32_t n = (uint32_t)each, g = (uint32_t)r / n, i = (uint32_t)r - g * n;
+    *blk = (int64_t)g * ((n + 127) / 128) + (i >> 7);
     *in = (int)(i & 127);
     return;
   }
@@ -83,16 +120,14 @@ __global__ void __launch_bounds__(kThreads)
     rows = gt.off[E];
   }
   const int64_t cpitch = mx::code_pitch(K), k_units = mx::units(K);
-  const int64_t per_row = (k_units + kPieces - 1) / kPieces;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < rows * per_row;
-       u += warps) {
-    const int64_t r = u / per_row, k0 = (u - r * per_row) * (kPieces * mx::kUnitK);
+  for (Walk at((uint32_t)k_units, kPieces); at.row < rows; at.next()) {
+    const int64_t r = at.row;
+    const int k0 = (int)at.part * (kPieces * mx::kUnitK);
     const T* src = x + r * ld;
     uint32_t w[kPieces][4];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int64_t k = k0 + i * mx::kUnitK + lane * 8;
+      const int k = k0 + i * mx::kUnitK + lane * 8;
       w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
       if (vec && k + 8 <= K) {
         const uint4 q = __ldg(reinterpret_cast<const uint4*>(src + k));
@@ -110,27 +145,28 @@ __global__ void __launch_bounds__(kThreads)
     uint8_t* crow = codes + r * cpitch;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int64_t k = k0 + i * mx::kUnitK + lane * 8;
+      const int k = k0 + i * mx::kUnitK + lane * 8;
       if (k0 + i * mx::kUnitK >= K) break;          // the same for the whole warp
-      float f[8];
+      // magnitudes ordered as 16-bit integers: NaN above infinity above all else
       uint32_t a = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a = __vmaxu2(a, w[i][j] & 0x7fff7fffu);
+      a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      const float2 top = pair_of<T>(__vmaxu2(a, a >> 16));
+      const uint32_t bits = __float_as_uint(top.x);
+      const bool none = bits >= 0x7f800000u;
+      const int field = (int)(bits >> 23);          // subnormals and zero: 0
+      const uint32_t byte = none ? 255u : (uint32_t)max(field - 2, 0);
+      const float inv = __uint_as_float((254u - (none ? 0u : byte)) << 23);   // 2^(127 - byte)
+      float f[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 p = pair_of<T>(w[i][j]);
-        f[2 * j] = p.x;
-        f[2 * j + 1] = p.y;
-        // magnitudes ordered as integers: NaN above infinity above all else
-        a = max(a, max(__float_as_uint(p.x) & 0x7fffffffu, __float_as_uint(p.y) & 0x7fffffffu));
+        f[2 * j] = p.x * inv;
+        f[2 * j + 1] = p.y * inv;
       }
-      a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-      const bool none = a >= 0x7f800000u;
-      const int field = (int)(a >> 23);             // subnormals and zero: 0
-      const uint32_t byte = none ? 255u : (uint32_t)max(field - 2, 0);
-      const float inv = __uint_as_float((254u - (none ? 0u : byte)) << 23);   // 2^(127 - byte)
-      uint32_t c = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c |= code_pair(f[2 * j] * inv, f[2 * j + 1] * inv) << (8 * j);
+      const uint32_t c = code_word(f);
       if (k < cpitch * 2) *reinterpret_cast<uint32_t*>(crow + k / 2) = none ? 0u : c;
       // a 128-element atom's four scales as one word
       uint32_t s = byte << (8 * ((lane >> 2) & 3));
@@ -170,18 +206,16 @@ __global__ void __launch_bounds__(kThreads)
     rows = gt.off[E];
   }
   const int64_t cpitch = mx::code_pitch(K), k_units = mx::units(K);
-  const int64_t per_row = (k_units + kPieces - 1) / kPieces;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < rows * per_row;
-       u += warps) {
-    const int64_t r = u / per_row, k0 = (u - r * per_row) * (kPieces * mx::kUnitK);
+  for (Walk at((uint32_t)k_units, kPieces); at.row < rows; at.next()) {
+    const int64_t r = at.row;
+    const int k0 = (int)at.part * (kPieces * mx::kUnitK);
     int64_t blk;
     int in;
     locate(&gt, E, each, r, &blk, &in);
     uint32_t c[kPieces], b[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int64_t k = k0 + i * mx::kUnitK + lane * 8;
+      const int k = k0 + i * mx::kUnitK + lane * 8;
       c[i] = b[i] = 0u;
       if (k < K) {
         c[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + r * cpitch + k / 2));
@@ -190,18 +224,16 @@ __global__ void __launch_bounds__(kThreads)
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int64_t k = k0 + i * mx::kUnitK + lane * 8;
+      const int k = k0 + i * mx::kUnitK + lane * 8;
       if (k >= K) break;
       // 2^(b - 127): b = 0 is the subnormal 2^-127, 255 is NaN
       const float s = __uint_as_float(b[i] == 255u ? 0x7fc00000u : b[i] ? b[i] << 23 : 1u << 22);
       T v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t q = c[i] >> (4 * j), m = q & 7u;
-        // 0 and .5, then 1.m * 2^(e - 1)
-        const float mag = m < 2 ? 0.5f * (float)m
-                                : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
-        v[j] = to<T>(((q & 8u) ? -mag : mag) * s);
+      for (int j = 0; j < 4; ++j) {
+        const float2 m = values_of(c[i] >> (8 * j));
+        v[2 * j] = to<T>(m.x * s);
+        v[2 * j + 1] = to<T>(m.y * s);
       }
       T* dst = y + r * K + k;
       if (vec && k + 8 <= K) {

@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "moe_internal.h"
+#include "walk.cuh"
 
 namespace bra {
 namespace {
@@ -25,36 +26,35 @@ constexpr int kMaxK = BRA_MAX_CHOICES;
 
 // Eight elements of a row held by a lane: consecutive ones with 16-byte
 // accesses (VEC), else 32 apart so that a warp's accesses stay together.
+// `load` only issues the loads; `get` converts what has come.
 template <typename T, bool VEC>
 struct Eight {
-  static __device__ __forceinline__ int at(int base, int lane, int i) {
-    return VEC ? base + lane * 8 + i : base + lane + 32 * i;
-  }
-  static __device__ __forceinline__ void load(const T* row, int base, int lane, int H,
-                                              float (&f)[8]) {
+  static constexpr int N = (int)sizeof(T) / 2;      // 16-byte accesses
+  uint4 raw[N];
+  __device__ __forceinline__ void load(const T* row, int base, int lane, int H) {
     if constexpr (VEC) {
-      constexpr int N = (int)sizeof(T) / 2;        // 16-byte loads
-      uint4 w[N];
       const bool in = base + lane * 8 < H;
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        w[i] = in ? __ldg(reinterpret_cast<const uint4*>(row + base + lane * 8) + i)
-                  : make_uint4(0, 0, 0, 0);
-      const T* e = reinterpret_cast<const T*>(w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(e[i]);
+        raw[i] = in ? __ldg(reinterpret_cast<const uint4*>(row + base + lane * 8) + i)
+                    : make_uint4(0, 0, 0, 0);
     } else {
+      T* e = reinterpret_cast<T*>(raw);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int c = base + lane + 32 * i;
-        f[i] = c < H ? static_cast<float>(row[c]) : 0.f;
+        e[i] = c < H ? row[c] : T(0.f);
       }
     }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const T* e = reinterpret_cast<const T*>(raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(e[i]);
   }
   static __device__ __forceinline__ void store(T* row, int base, int lane, int H,
                                                const float (&f)[8]) {
     if constexpr (VEC) {
-      constexpr int N = (int)sizeof(T) / 2;
       if (base + lane * 8 >= H) return;
       uint4 w[N];
       T* e = reinterpret_cast<T*>(w);
@@ -72,16 +72,18 @@ struct Eight {
   }
 };
 
-// Rows as `units` of sizeof(W) bytes; a warp copies up to 8 of its lanes' units at once.
+// Rows as `units` of sizeof(W) bytes; a warp copies 8 of its lanes' units at
+// once.  The next rows' tokens are fetched meanwhile.
 template <typename W>
 __global__ void __launch_bounds__(kThreads)
-    dispatch_kernel(const W* x, const int32_t* tokens, W* xs, int64_t R, int64_t T, int64_t units) {
+    dispatch_kernel(const W* x, const int32_t* tokens, W* xs, uint32_t R, int64_t T, int units) {
   constexpr int U = 8;
   const int lane = threadIdx.x & 31;
-  const int64_t pieces = (units + 32 * U - 1) / (32 * U), warps = (int64_t)gridDim.x * kWarps;
-  for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < R * pieces; u += warps) {
-    const int64_t r = u / pieces, c0 = (u - r * pieces) * (32 * U) + lane;
-    const int t = __ldg(tokens + r);
+  Walk at((uint32_t)(units + 32 * U - 1) / (32 * U));
+  int t = at.row < R ? __ldg(tokens + at.row) : -1;
+  while (at.row < R) {
+    const uint32_t r = at.row;
+    const int c0 = (int)at.part * (32 * U) + lane;
     const bool have = t >= 0 && t < T;
     const W* src = x + (int64_t)(have ? t : 0) * units;
     W v[U];
@@ -90,46 +92,62 @@ __global__ void __launch_bounds__(kThreads)
       v[i] = W{};
       if (have && c0 + 32 * i < units) v[i] = __ldg(src + c0 + 32 * i);
     }
+    at.next();
+    t = at.row < R ? __ldg(tokens + at.row) : -1;
+    W* dst = xs + (int64_t)r * units;
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (c0 + 32 * i < units) xs[r * units + c0 + 32 * i] = v[i];
+      if (c0 + 32 * i < units) __stcs(dst + c0 + 32 * i, v[i]);
   }
 }
 
 // y[t] = sum_j w[t,j] rows[slots[t,j]]; w NULL: ones.  A warp takes 256
-// elements of a token; the rows' loads are issued four at a time.
+// elements of a token; the rows' loads are issued eight (fp32: four) at a
+// time, and the next token's slots before this one's sums.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads)
-    combine_kernel(const T* rows, const int32_t* slots, const float* w, T* y, int64_t tokens,
+    combine_kernel(const T* rows, const int32_t* slots, const float* w, T* y, uint32_t tokens,
                    int64_t R, int k, int H) {
+  constexpr int U = sizeof(T) == 4 ? 4 : 8;
   const int lane = threadIdx.x & 31;
-  const int64_t pieces = (H + 255) / 256, warps = (int64_t)gridDim.x * kWarps;
-  for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < tokens * pieces;
-       u += warps) {
-    const int64_t t = u / pieces;
-    const int base = (int)(u - t * pieces) * 256;
-    int slot = -1;
-    float wt = 0.f;
-    if (lane < k) {
-      slot = __ldg(slots + t * k + lane);
-      if (slot < 0 || slot >= R) slot = -1;
-      wt = w ? __ldg(w + t * k + lane) : 1.f;
+  Walk at((uint32_t)(H + 255) / 256);
+  int slot = -1;
+  float wt = 0.f;
+  auto fetch = [&] {
+    slot = -1;
+    wt = 0.f;
+    if (at.row < tokens && lane < k) {
+      const int64_t i = (int64_t)at.row * k + lane;
+      slot = __ldg(slots + i);
+      wt = w ? __ldg(w + i) : 1.f;
     }
+  };
+  fetch();
+  while (at.row < tokens) {
+    const int64_t t = at.row;
+    const int base = (int)at.part * 256;
+    const int my_slot = slot >= 0 && slot < R ? slot : -1;
+    const float my_w = wt;
+    at.next();
+    fetch();
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < k; j0 += 4) {
-      float f[4][8];
-      int sj[4];
+    for (int j0 = 0; j0 < k; j0 += U) {
+      Eight<T, VEC> e[U];
+      int sj[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sj[j] = j0 + j < k ? __shfl_sync(0xffffffffu, slot, (j0 + j) & 31) : -1;
-        if (sj[j] >= 0) Eight<T, VEC>::load(rows + (int64_t)sj[j] * H, base, lane, H, f[j]);
+      for (int j = 0; j < U; ++j) {
+        sj[j] = j0 + j < k ? __shfl_sync(0xffffffffu, my_slot, (j0 + j) & 31) : -1;
+        if (sj[j] >= 0) e[j].load(rows + (int64_t)sj[j] * H, base, lane, H);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, wt, (j0 + j) & 31);
-        if (sj[j] >= 0)
+      for (int j = 0; j < U; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, my_w, (j0 + j) & 31);
+        if (sj[j] >= 0) {
+          float f[8];
+          e[j].get(f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[i] = fmaf(wj, f[j][i], s[i]);
+          for (int i = 0; i < 8; ++i) s[i] = fmaf(wj, f[i], s[i]);
+        }
       }
     }
     Eight<T, VEC>::store(y + t * H, base, lane, H, s);
@@ -146,12 +164,10 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ float part[kWarps][kMaxK];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int TPB = kWarps / WPT;              // tokens of a block
+  constexpr int U = 4;                           // rows in flight
   const int sub = warp % WPT;
   for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < tokens; t0 += (int64_t)gridDim.x * TPB) {
     const int64_t t = t0 + warp / WPT;
-    float dot[kMaxK];
-#pragma unroll
-    for (int j = 0; j < kMaxK; ++j) dot[j] = 0.f;
     if (t < tokens) {
       int slot = -1;
       float wt = 0.f;
@@ -160,33 +176,43 @@ __global__ void __launch_bounds__(kThreads)
         if (slot < 0 || slot >= R) slot = -1;
         wt = __ldg(w + t * k + lane);
       }
-      for (int base = sub * 256; base < H; base += WPT * 256) {
-        float d[8];
-        Eight<T, VEC>::load(dy + t * H, base, lane, H, d);
+#pragma unroll 1
+      for (int j0 = 0; j0 < k; j0 += U) {
+        float dot[U] = {0.f, 0.f, 0.f, 0.f}, wj[U];
+        int sj[U];
 #pragma unroll
-        for (int j = 0; j < kMaxK; ++j) {
-          if (j >= k) break;
-          const int s = __shfl_sync(0xffffffffu, slot, j);
-          const float wj = __shfl_sync(0xffffffffu, wt, j);
-          if (s < 0) continue;
-          float f[8], o[8];
-          Eight<T, VEC>::load(ys + (int64_t)s * H, base, lane, H, f);
-          float a = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            a = fmaf(d[i], f[i], a);
-            o[i] = wj * d[i];
-          }
-          dot[j] += a;
-          Eight<T, VEC>::store(dys + (int64_t)s * H, base, lane, H, o);
+        for (int j = 0; j < U; ++j) {
+          sj[j] = j0 + j < k ? __shfl_sync(0xffffffffu, slot, (j0 + j) & 31) : -1;
+          wj[j] = __shfl_sync(0xffffffffu, wt, (j0 + j) & 31);
         }
-      }
+        for (int base = sub * 256; base < H; base += WPT * 256) {
+          Eight<T, VEC> d, e[U];
+          d.load(dy + t * H, base, lane, H);       // again for the next four, from L1 or L2
 #pragma unroll
-      for (int j = 0; j < kMaxK; ++j) {
-        if (j >= k) break;
+          for (int j = 0; j < U; ++j)
+            if (sj[j] >= 0) e[j].load(ys + (int64_t)sj[j] * H, base, lane, H);
+          float dv[8];
+          d.get(dv);
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], m);
-        if (lane == 0) part[warp][j] = dot[j];
+          for (int j = 0; j < U; ++j)
+            if (sj[j] >= 0) {
+              float f[8], o[8], a = 0.f;
+              e[j].get(f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                a = fmaf(dv[i], f[i], a);
+                o[i] = wj[j] * dv[i];
+              }
+              dot[j] += a;
+              Eight<T, VEC>::store(dys + (int64_t)sj[j] * H, base, lane, H, o);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+#pragma unroll
+          for (int m = 16; m > 0; m >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], m);
+          if (lane == 0 && j0 + j < k) part[warp][j0 + j] = dot[j];
+        }
       }
     }
     __syncthreads();
@@ -249,7 +275,8 @@ cudaError_t launch_dispatch(const PermuteCall& c, cudaStream_t st) {
     cudaError_t e = grid_of((warps + kWarps - 1) / kWarps, 16, &grid);
     if (e != cudaSuccess) return e;
     dispatch_kernel<<<grid, kThreads, 0, st>>>(static_cast<const W*>(c.in), c.row_tokens,
-                                               static_cast<W*>(c.out), c.R, c.T, units);
+                                               static_cast<W*>(c.out), (uint32_t)c.R, c.T,
+                                               (int)units);
     return cudaGetLastError();
   };
   auto fits = [&](uintptr_t n) {
@@ -270,8 +297,8 @@ cudaError_t launch_combine(const PermuteCall& c, cudaStream_t st) {
   return by_type(c.dtype, vec, [&](auto* type, auto v) {
     using T = std::remove_pointer_t<decltype(type)>;
     combine_kernel<T, decltype(v)::value><<<grid, kThreads, 0, st>>>(
-        static_cast<const T*>(c.in), c.slots, c.weights, static_cast<T*>(c.out), c.T, c.R, c.k,
-        c.H);
+        static_cast<const T*>(c.in), c.slots, c.weights, static_cast<T*>(c.out),
+        (uint32_t)c.T, c.R, c.k, c.H);
     return cudaGetLastError();
   });
 }

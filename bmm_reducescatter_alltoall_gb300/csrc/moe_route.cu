@@ -7,19 +7,18 @@
 //             chosen) of exp(l - m), m the largest logit
 //   row of (t, j) = rows of lower experts + earlier tokens with this expert
 //
-// A group of L lanes takes a token, 16 logits a lane (L = 4 to 32 by E), so a
-// warp has 32 / L tokens in hand: the scan of a lane's 16 logits after each
-// choice and the log2(L) exchange steps serve all of them.  (With a warp to a
-// token and the hardware's warp reductions, two to a choice, 65536 tokens of
-// 128 experts took 55 us; the reductions, about 32 cycles each, were the
-// bound.)  Tokens are dealt to CTAs in chunks.  In a chunk each expert has a
-// bit per token, set by whoever chose it: a population count below a token's
-// bit is its place among the chunk's rows of that expert, in token order and
-// without any order of the setting.  The chunks' counts go to a small matrix;
-// a second kernel adds to each place the rows of the chunks before and of the
+// A group of L lanes takes a token, V = 8 or 16 consecutive logits a lane
+// (L = 4 to 32 by E).  Each lane sorts its own once; a choice is then the
+// largest of the lanes' heads, found in log2(L) exchanges, and the lane that
+// has it (the lowest of equals: lanes hold rising indices) drops its head.
+// Tokens are dealt to CTAs in chunks.  In a chunk each expert has a bit per
+// token, set by whoever chose it: a population count below a token's bit is
+// its place among the chunk's rows of that expert, in token order and without
+// any order of the setting.  The chunks' counts go to a small matrix; a
+// second kernel adds to each place the rows of the chunks before and of the
 // lower experts.  A single chunk does both in one launch.
-// Bound by reading the logits once (4 bytes x E a token) and, for few tokens,
-// by latency.
+// The logits are read once (4 bytes x E a token), but the choices' compares
+// and selects bound it; for few tokens, latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -66,85 +65,86 @@ __device__ __forceinline__ float group_sum(float v, int L) {
   return v;
 }
 
-// The experts of one token to each group of L lanes (t < 0: none): lane l of
-// the group holds logits (i / 4) * 4L + 4l + i % 4, i < 16, so that four of
-// them are one 16-byte load.  Writes ids and weights and sets the chunk's
-// bits (word `word`, bit `bit` of each expert's `words`).  Whole warps.
-template <typename T, int L>
+// Sorts V (key, index) pairs, largest key first, equal keys by index: Batcher's
+// odd-even merge sort, all places known when compiled.
+template <int V>
+__device__ __forceinline__ void sort_lane(uint32_t (&key)[V], int (&idx)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i) {
+          const int a = i + j, b = i + j + q;
+          if (b < V && a / (2 * p) == b / (2 * p)) {
+            const bool swap = key[b] > key[a] || (key[b] == key[a] && idx[b] < idx[a]);
+            const uint32_t ka = swap ? key[b] : key[a], kb = swap ? key[a] : key[b];
+            const int ia = swap ? idx[b] : idx[a], ib = swap ? idx[a] : idx[b];
+            key[a] = ka, key[b] = kb, idx[a] = ia, idx[b] = ib;
+          }
+        }
+}
+
+// The experts of one token to each group of L lanes (t < 0: none); lane l of
+// the group holds logits l * V ..  Writes ids and weights and sets the
+// chunk's bits (word `word`, bit `bit` of each expert's `words`).  Whole warps.
+template <typename T, int L, int V>
 __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, uint32_t* bits,
                                        int words, int word, uint32_t bit) {
-  constexpr int V = 16, OWN = (BRA_MAX_CHOICES + L - 1) / L;   // choices a lane keeps
+  constexpr int OWN = (BRA_MAX_CHOICES + L - 1) / L;   // choices a lane keeps
   const int gl = lane % L;
+  const uint32_t group = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
   const T* row = static_cast<const T*>(p.logits) + (int64_t)t * p.E;
-  float v[V];
   uint32_t key[V];
+  int idx[V];
 #pragma unroll
   for (int i = 0; i < V; i += 4) {
-    const int at = i * L + 4 * gl;
+    const int at = gl * V + i;
     T raw[4];
     if (t >= 0 && p.vec && at + 4 <= p.E) {
-      if constexpr (sizeof(T) == 4) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + at));
-        *reinterpret_cast<uint4*>(raw) = q;
-      } else {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + at));
-        *reinterpret_cast<uint2*>(raw) = q;
-      }
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<uint4*>(raw) = __ldg(reinterpret_cast<const uint4*>(row + at));
+      else
+        *reinterpret_cast<uint2*>(raw) = __ldg(reinterpret_cast<const uint2*>(row + at));
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c) raw[c] = t >= 0 && at + c < p.E ? row[at + c] : T(-INFINITY);
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      v[i + c] = logit(&raw[c]);
-      key[i + c] = at + c < p.E ? key_of(v[i + c]) : 0u;
+      key[i + c] = key_of(logit(&raw[c]));
+      idx[i + c] = i + c;
     }
   }
-  uint32_t best = key[0];
-  int rel = 0;                                  // index of `best` less 4 gl
+  sort_lane<V>(key, idx);
+  uint64_t order = 0;                           // the sorted places, four bits each
 #pragma unroll
-  for (int i = 1; i < V; ++i)
-    if (key[i] > best) {
-      best = key[i];
-      rel = (i / 4) * 4 * L + i % 4;
-    }
+  for (int i = 0; i < V; ++i) order |= (uint64_t)idx[i] << (4 * i);
   uint32_t my_key[OWN], top = 0u;
-  int64_t out = (int64_t)t * p.k;
+  const int64_t out = (int64_t)t * p.k;
 #pragma unroll
   for (int o = 0; o < OWN; ++o) {
     my_key[o] = 0u;
     for (int j = o * L; j < min(p.k, (o + 1) * L); ++j) {
-      uint32_t most = best;
-      int at = rel + 4 * gl;
+      uint32_t most = key[0];
 #pragma unroll
-      for (int d = L / 2; d > 0; d >>= 1) {
-        const uint32_t mk = __shfl_xor_sync(0xffffffffu, most, d);
-        const int mi = __shfl_xor_sync(0xffffffffu, at, d);
-        if (mk > most || (mk == most && mi < at)) {
-          most = mk;
-          at = mi;
-        }
-      }
+      for (int d = L / 2; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+      const uint32_t has = __ballot_sync(0xffffffffu, key[0] == most) & group;
       if (j == 0) top = most;
       if (gl == j - o * L) {
         my_key[o] = most;
-        if (t >= 0) {
-          p.ids[out + j] = most ? at : -1;
-          if (most) atomicOr(&bits[at * words + word], bit);
-        }
+        if (t >= 0 && most == 0u) p.ids[out + j] = -1;
       }
-      // strike it out and find the lane's best again
-      const int gone = most ? at - 4 * gl : -1;
-      best = 0u;
-      rel = 0;
+      if (most != 0u && lane == __ffs(has) - 1) {
+        const int at = gl * V + (int)(order & 15u);
+        p.ids[out + j] = at;
+        atomicOr(&bits[at * words + word], bit);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = (i / 4) * 4 * L + i % 4;
-        if (gone == c) key[i] = 0u;
-        if (key[i] > best) {
-          best = key[i];
-          rel = c;
-        }
+        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+        key[V - 1] = 0u;
+        order >>= 4;
       }
     }
   }
@@ -156,10 +156,10 @@ __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, ui
     s += e[o];
   }
   if (!p.renorm) {
-    // all open logits: those not struck out, and the chosen ones
+    // all open logits: the ones left, and the chosen
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (key[i]) s += expf(v[i] - m);
+      if (key[i]) s += expf(value_of(key[i]) - m);
   }
   s = group_sum(s, L);
 #pragma unroll
@@ -212,7 +212,7 @@ __device__ __forceinline__ void mark_unused(const RouteParams& p, int c, int use
 
 // Choices of one chunk, and each pair's place among the chunk's rows of its
 // expert in `slots`; with a single chunk, everything.
-template <typename T, int L>
+template <typename T, int L, int V>
 __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParams p) {
   extern __shared__ uint32_t bits[];                    // [E][chunk / 32]
   __shared__ int total[kMaxGroups], base[kMaxGroups], zero[kMaxGroups];
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParam
   constexpr int G = 32 / L;                             // tokens of a warp
   for (int i0 = warp * G; i0 < n; i0 += kWarps * G) {
     const int i = i0 + lane / L;
-    choose<T, L>(p, i < n ? t0 + i : -1, lane, bits, words, i >> 5, 1u << (i & 31));
+    choose<T, L, V>(p, i < n ? t0 + i : -1, lane, bits, words, i >> 5, 1u << (i & 31));
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
@@ -272,12 +272,22 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams
   for (int e = threadIdx.x; e < p.E; e += kThreads) total[e] = before[e] = 0;
   __syncthreads();
   cudaGridDependencySynchronize();                      // the choices are written
+  // the first pairs' loads go out before the matrix is summed
+  constexpr int AHEAD = 4;
+  int id[AHEAD], place[AHEAD];
+#pragma unroll
+  for (int a = 0; a < AHEAD; ++a) {
+    const int i = threadIdx.x + a * kThreads;
+    const bool in = i < n * p.k;
+    id[a] = in ? p.ids[(int64_t)t0 * p.k + i] : -1;
+    place[a] = in ? p.slots[(int64_t)t0 * p.k + i] : -1;
+  }
   // threads of a row of the matrix side by side, rows dealt over the rest
   const int width = (p.E + 31) / 32 * 32, rows = kThreads / width;
   const int e = threadIdx.x % width, r0 = threadIdx.x / width;
   if (e < p.E && r0 < rows) {
     int all = 0, old = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int r = r0; r < p.chunks; r += rows) {
       const int h = p.hist[(int64_t)r * p.E + e];
       all += h;
@@ -291,16 +301,17 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams
   if (c == 0)
     for (int i = threadIdx.x; i < p.E; i += kThreads) p.counts[i] = total[i];
   __syncthreads();
-#pragma unroll 4
-  for (int i = threadIdx.x; i < n * p.k; i += kThreads) {
-    const int64_t at = (int64_t)t0 * p.k + i;
-    const int id = p.ids[at];
-    if (id >= 0) {
-      const int slot = p.slots[at] + base[id];
-      p.slots[at] = slot;
+  auto put = [&](int i, int e1, int at) {
+    if (e1 >= 0) {
+      const int slot = at + base[e1];
+      p.slots[(int64_t)t0 * p.k + i] = slot;
       p.tokens[slot] = t0 + i / p.k;
     }
-  }
+  };
+#pragma unroll
+  for (int a = 0; a < AHEAD; ++a) put(threadIdx.x + a * kThreads, id[a], place[a]);
+  for (int i = threadIdx.x + AHEAD * kThreads; i < n * p.k; i += kThreads)
+    put(i, p.ids[(int64_t)t0 * p.k + i], p.slots[(int64_t)t0 * p.k + i]);
   mark_unused(p, c, used);
 }
 
@@ -324,11 +335,12 @@ __device__ __forceinline__ T rounded(float v) {
   return static_cast<T>(v);
 }
 
-// A group of L lanes takes a token, with choose()'s places for 16 logits a
-// lane: rows are read and written 16 (8) bytes at a time.
-template <typename T, int L>
+// A group of L lanes takes a token: the row is written whole as if nothing
+// were chosen, four elements a store, then the chosen ones over it (p_i is
+// w_j there).
+template <typename T, int L, int V>
 __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p) {
-  constexpr int V = 16, G = 32 / L, OWN = (BRA_MAX_CHOICES + L - 1) / L;
+  constexpr int G = 32 / L, OWN = (BRA_MAX_CHOICES + L - 1) / L;
   const int lane = threadIdx.x & 31, gl = lane % L;
   const int64_t step = (int64_t)gridDim.x * 8 * G;
   for (int64_t t0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * G; t0 < p.T; t0 += step) {
@@ -339,23 +351,24 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
       const int j = o * L + gl;
-      const int64_t at = t * p.k + j;
-      id[o] = in && j < p.k ? p.ids[at] : -1;
-      w[o] = id[o] >= 0 ? p.weights[at] : 0.f;
-      g[o] = id[o] >= 0 ? p.dweights[at] : 0.f;
+      const bool have = in && j < p.k;
+      id[o] = have ? __ldg(p.ids + t * p.k + j) : -1;
+      w[o] = have ? __ldg(p.weights + t * p.k + j) : 0.f;
+      g[o] = have ? __ldg(p.dweights + t * p.k + j) : 0.f;
+      if (id[o] < 0 || id[o] >= p.E) id[o] = -1, w[o] = 0.f, g[o] = 0.f;
       s += w[o] * g[o];
     }
     s = group_sum(s, L);
-    const T* row = static_cast<const T*>(p.logits) + t * p.E;
-    float d[V], q[V];
+    float d[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = 0.f;
     if (!p.renorm) {
-      float v[V];
+      const T* row = static_cast<const T*>(p.logits) + t * p.E;
       uint32_t best = 0u;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = (i / 4) * 4 * L + 4 * gl + i % 4;
-        v[i] = in && c < p.E ? logit(row + c) : -INFINITY;
-        best = max(best, key_of(v[i]));
+        d[i] = in && gl * V + i < p.E ? logit(row + gl * V + i) : -INFINITY;
+        best = max(best, key_of(d[i]));
       }
 #pragma unroll
       for (int m = L / 2; m > 0; m >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, m));
@@ -363,59 +376,48 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        q[i] = key_of(v[i]) ? expf(v[i] - m) : 0.f;
-        sum += q[i];
+        d[i] = key_of(d[i]) ? expf(d[i] - m) : 0.f;
+        sum += d[i];
       }
       sum = group_sum(sum, L);
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float f = sum > 0.f ? -s / sum : 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        q[i] *= inv;
-        d[i] = -s * q[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = 0.f;
+      for (int i = 0; i < V; ++i) d[i] *= f;
     }
-#pragma unroll
-    for (int o = 0; o < OWN; ++o)
-      for (int j = o * L; j < min(p.k, (o + 1) * L); ++j) {
-        const int from = (lane & ~(L - 1)) + j - o * L;
-        const int at = __shfl_sync(0xffffffffu, id[o], from) - 4 * gl;
-        const float gj = __shfl_sync(0xffffffffu, g[o], from) - s;
-        const float wj = __shfl_sync(0xffffffffu, w[o], from);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (at == (i / 4) * 4 * L + i % 4) d[i] = (p.renorm ? wj : q[i]) * gj;
-      }
-    if (!in) continue;
     T* out = static_cast<T*>(p.dlogits) + t * p.E;
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
-      const int at = i * L + 4 * gl;
+      const int at = gl * V + i;
       T r[4] = {rounded<T>(d[i]), rounded<T>(d[i + 1]), rounded<T>(d[i + 2]), rounded<T>(d[i + 3])};
-      if (p.vec && at + 4 <= p.E) {
+      if (in && p.vec && at + 4 <= p.E) {
         if constexpr (sizeof(T) == 4)
           *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(r);
         else
           *reinterpret_cast<uint2*>(out + at) = *reinterpret_cast<const uint2*>(r);
-      } else {
+      } else if (in) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           if (at + c < p.E) out[at + c] = r[c];
       }
     }
+    __syncwarp();                    // the row lies before its chosen elements are written
+#pragma unroll
+    for (int o = 0; o < OWN; ++o)
+      if (id[o] >= 0) out[id[o]] = rounded<T>(w[o] * (g[o] - s));
+    __syncwarp();
   }
 }
 
-// f for the logits' type and the lanes of a token: 16 logits a lane.
+// f for the logits' type, the lanes of a token and the logits of a lane.
 template <typename F>
 cudaError_t by_type(int dtype, int E, F&& f) {
   auto by_lanes = [&](auto* type) {
-    if (E <= 64) return f(type, std::integral_constant<int, 4>{});
-    if (E <= 128) return f(type, std::integral_constant<int, 8>{});
-    if (E <= 256) return f(type, std::integral_constant<int, 16>{});
-    return f(type, std::integral_constant<int, 32>{});
+    using std::integral_constant;
+    if (E <= 32) return f(type, integral_constant<int, 4>{}, integral_constant<int, 8>{});
+    if (E <= 64) return f(type, integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    if (E <= 128) return f(type, integral_constant<int, 16>{}, integral_constant<int, 8>{});
+    if (E <= 256) return f(type, integral_constant<int, 32>{}, integral_constant<int, 8>{});
+    return f(type, integral_constant<int, 32>{}, integral_constant<int, 16>{});
   };
   if (dtype == BRA_FP32) return by_lanes((float*)nullptr);
   if (dtype == BRA_BF16) return by_lanes((__nv_bfloat16*)nullptr);
@@ -443,15 +445,15 @@ cudaError_t launch_route(const RouteCall& r, cudaStream_t st) {
                    rows_vec(r.logits, r.E, r.dtype)};
   p.chunks = (int)((r.T + p.chunk - 1) / p.chunk);
   const int smem = r.E * (p.chunk / 32) * 4;
-  const cudaError_t e = by_type(r.dtype, r.E, [&](auto* type, auto l) {
+  const cudaError_t e = by_type(r.dtype, r.E, [&](auto* type, auto l, auto v) {
     using T = std::remove_pointer_t<decltype(type)>;
     if (smem > 32768) {
       const cudaError_t a =
-          cudaFuncSetAttribute(route_choose_kernel<T, decltype(l)::value>,
+          cudaFuncSetAttribute(route_choose_kernel<T, decltype(l)::value, decltype(v)::value>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (a != cudaSuccess) return a;
     }
-    route_choose_kernel<T, decltype(l)::value><<<p.chunks, kThreads, smem, st>>>(p);
+    route_choose_kernel<T, decltype(l)::value, decltype(v)::value><<<p.chunks, kThreads, smem, st>>>(p);
     return cudaGetLastError();
   });
   if (e != cudaSuccess || p.chunks == 1) return e;
@@ -476,11 +478,11 @@ cudaError_t launch_route_grad(const RouteGradCall& r, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  return by_type(r.dtype, r.E, [&](auto* type, auto l) {
+  return by_type(r.dtype, r.E, [&](auto* type, auto l, auto v) {
     using T = std::remove_pointer_t<decltype(type)>;
     constexpr int tokens = 8 * 32 / decltype(l)::value;           // of a block
     const int64_t want = (r.T + tokens - 1) / tokens, full = (int64_t)sms * 8;
-    route_grad_kernel<T, decltype(l)::value>
+    route_grad_kernel<T, decltype(l)::value, decltype(v)::value>
         <<<(unsigned)(want < full ? want : full), 256, 0, st>>>(p);
     return cudaGetLastError();
   });

@@ -14,6 +14,7 @@
 // issued together.
 #include "grouped.cuh"
 #include "mx.cuh"
+#include "walk.cuh"
 
 namespace bra {
 namespace {
@@ -58,29 +59,6 @@ __device__ __forceinline__ float2 values_of(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// A warp's walk over (row, unit of kPieces pieces): units are dealt to the
-// grid's warps in order, and the next one is found by adding, not dividing.
-struct Walk {
-  uint32_t row, part, per_row, d_row, d_part;
-  __device__ __forceinline__ Walk(uint32_t k_units, int pieces) {
-    per_row = (k_units + pieces - 1) / pieces;
-    const uint32_t warps = gridDim.x * (blockDim.x / 32);
-    const uint32_t w = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
-    row = w / per_row;
-    part = w - row * per_row;
-    d_row = warps / per_row;
-    d_part = warps - d_row * per_row;
-  }
-  __device__ __forceinline__ void next() {
-    row += d_row;
-    part += d_part;
-    if (part >= per_row) {
-      part -= per_row;
-      ++row;
-    }
-  }
-};
-
 // Row block and row within it of row r: groups of `each` rows, or of the
 // table's counts.
 __device__ __forceinline__ void locate(const GroupTable* gt, int E, int64_t each, int64_t r,
@@ -120,7 +98,7 @@ __global__ void __launch_bounds__(kThreads)
     rows = gt.off[E];
   }
   const int64_t cpitch = mx::code_pitch(K), k_units = mx::units(K);
-  for (Walk at((uint32_t)k_units, kPieces); at.row < rows; at.next()) {
+  for (Walk at((uint32_t)((k_units + kPieces - 1) / kPieces)); at.row < rows; at.next()) {
     const int64_t r = at.row;
     const int k0 = (int)at.part * (kPieces * mx::kUnitK);
     const T* src = x + r * ld;
@@ -206,7 +184,7 @@ __global__ void __launch_bounds__(kThreads)
     rows = gt.off[E];
   }
   const int64_t cpitch = mx::code_pitch(K), k_units = mx::units(K);
-  for (Walk at((uint32_t)k_units, kPieces); at.row < rows; at.next()) {
+  for (Walk at((uint32_t)((k_units + kPieces - 1) / kPieces)); at.row < rows; at.next()) {
     const int64_t r = at.row;
     const int k0 = (int)at.part * (kPieces * mx::kUnitK);
     int64_t blk;

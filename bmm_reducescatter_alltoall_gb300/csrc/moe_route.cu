@@ -119,33 +119,34 @@ __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, ui
     }
   }
   sort_lane<V>(key, idx);
-  uint64_t order = 0;                           // the sorted places, four bits each
+  using Order = std::conditional_t<V == 8, uint32_t, uint64_t>;
+  Order order = 0;                              // the sorted places, four bits each
 #pragma unroll
-  for (int i = 0; i < V; ++i) order |= (uint64_t)idx[i] << (4 * i);
+  for (int i = 0; i < V; ++i) order |= (Order)idx[i] << (4 * i);
   uint32_t my_key[OWN], top = 0u;
-  const int64_t out = (int64_t)t * p.k;
+  int my_id[OWN];
 #pragma unroll
   for (int o = 0; o < OWN; ++o) {
     my_key[o] = 0u;
+    my_id[o] = -1;
     for (int j = o * L; j < min(p.k, (o + 1) * L); ++j) {
       uint32_t most = key[0];
 #pragma unroll
       for (int d = L / 2; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
       const uint32_t has = __ballot_sync(0xffffffffu, key[0] == most) & group;
+      const int win = __ffs(has) - 1;
+      const int at = __shfl_sync(0xffffffffu, gl * V + (int)(order & 15u), win);
       if (j == 0) top = most;
-      if (gl == j - o * L) {
+      if (gl == j - o * L && most) {
         my_key[o] = most;
-        if (t >= 0 && most == 0u) p.ids[out + j] = -1;
+        my_id[o] = at;
       }
-      if (most != 0u && lane == __ffs(has) - 1) {
-        const int at = gl * V + (int)(order & 15u);
-        p.ids[out + j] = at;
-        atomicOr(&bits[at * words + word], bit);
+      // the winner drops its head (with most = 0 there is nothing to drop)
+      const bool drop = lane == win;
 #pragma unroll
-        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-        key[V - 1] = 0u;
-        order >>= 4;
-      }
+      for (int i = 0; i + 1 < V; ++i) key[i] = drop ? key[i + 1] : key[i];
+      key[V - 1] = drop ? 0u : key[V - 1];
+      order = drop ? order >> 4 : order;
     }
   }
   const float m = value_of(top);
@@ -162,9 +163,14 @@ __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, ui
       if (key[i]) s += expf(value_of(key[i]) - m);
   }
   s = group_sum(s, L);
+  const int64_t out = (int64_t)t * p.k;
 #pragma unroll
   for (int o = 0; o < OWN; ++o)
-    if (t >= 0 && o * L + gl < p.k) p.weights[out + o * L + gl] = my_key[o] ? e[o] / s : 0.f;
+    if (t >= 0 && o * L + gl < p.k) {
+      p.ids[out + o * L + gl] = my_id[o];
+      p.weights[out + o * L + gl] = my_key[o] ? e[o] / s : 0.f;
+      if (my_id[o] >= 0) atomicOr(&bits[my_id[o] * words + word], bit);
+    }
 }
 
 // The chunk's experts as bits: words (chunk / 32) to an expert.
@@ -343,21 +349,33 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
   constexpr int G = 32 / L, OWN = (BRA_MAX_CHOICES + L - 1) / L;
   const int lane = threadIdx.x & 31, gl = lane % L;
   const int64_t step = (int64_t)gridDim.x * 8 * G;
-  for (int64_t t0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * G; t0 < p.T; t0 += step) {
-    const int64_t t = t0 + lane / L;
-    const bool in = t < p.T;
-    int id[OWN];
-    float w[OWN], g[OWN], s = 0.f;
+  const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * G;
+  int id[OWN], id_next[OWN];
+  float w[OWN], g[OWN], w_next[OWN], g_next[OWN];
+  auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
       const int j = o * L + gl;
-      const bool have = in && j < p.k;
-      id[o] = have ? __ldg(p.ids + t * p.k + j) : -1;
-      w[o] = have ? __ldg(p.weights + t * p.k + j) : 0.f;
-      g[o] = have ? __ldg(p.dweights + t * p.k + j) : 0.f;
-      if (id[o] < 0 || id[o] >= p.E) id[o] = -1, w[o] = 0.f, g[o] = 0.f;
+      const bool have = t < p.T && j < p.k;
+      id_next[o] = have ? __ldg(p.ids + t * p.k + j) : -1;
+      w_next[o] = have ? __ldg(p.weights + t * p.k + j) : 0.f;
+      g_next[o] = have ? __ldg(p.dweights + t * p.k + j) : 0.f;
+    }
+  };
+  fetch(first + lane / L);
+  for (int64_t t0 = first; t0 < p.T; t0 += step) {
+    const int64_t t = t0 + lane / L;
+    const bool in = t < p.T;
+    float s = 0.f;
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+      const bool open = id_next[o] >= 0 && id_next[o] < p.E;
+      id[o] = open ? id_next[o] : -1;
+      w[o] = open ? w_next[o] : 0.f;
+      g[o] = open ? g_next[o] : 0.f;
       s += w[o] * g[o];
     }
+    fetch(t + step);
     s = group_sum(s, L);
     float d[V];
 #pragma unroll

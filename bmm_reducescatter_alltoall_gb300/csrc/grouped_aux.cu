@@ -27,6 +27,8 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
   __shared__ float part[kBgRows][64];
   __shared__ float sum[64];
   const int tid = threadIdx.x;
+  grid_wait();
+  grid_go();
   if (tid < 32) build_table<1>(&gt, counts, E, R, tid);
   __syncthreads();
   const uint32_t rank = SPLIT > 1 ? cluster_rank() : 0u;
@@ -116,6 +118,8 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
 // elements are not read.
 // --------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) pack_rows_kernel(const __grid_constant__ PackJobs jobs) {
+  grid_wait();
+  grid_go();
   const int64_t step = (int64_t)gridDim.x * 256;
   int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
   for (int j = 0; j < jobs.n; ++j) {
@@ -169,9 +173,8 @@ cudaError_t launch_bias_grad(const BiasGradProblem& g, cudaStream_t st) {
   auto run = [&](auto kernel, auto* dy, auto* db) {
     using T = std::remove_pointer_t<decltype(dy)>;
     using B = std::remove_pointer_t<decltype(db)>;
-    kernel<<<grid, kBgThreads, 0, st>>>(static_cast<const T*>(g.dy), static_cast<B*>(g.db),
-                                        g.counts, g.status, g.R, g.ld, g.E, g.N, vec);
-    return cudaGetLastError();
+    return launch_overlapped(kernel, grid, kBgThreads, 0, st, static_cast<const T*>(g.dy),
+                             static_cast<B*>(g.db), g.counts, g.status, g.R, g.ld, g.E, g.N, vec);
   };
   __nv_bfloat16* b = nullptr;
   __half* h = nullptr;
@@ -192,8 +195,7 @@ cudaError_t launch_pack_rows(const PackJobs& jobs, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int64_t want = (total + 255) / 256, full = (int64_t)sms * 8;
-  pack_rows_kernel<<<(unsigned)(want < full ? want : full), 256, 0, st>>>(jobs);
-  return cudaGetLastError();
+  return launch_overlapped(pack_rows_kernel, (unsigned)(want < full ? want : full), 256, 0, st, jobs);
 }
 
 }  // namespace bra

@@ -154,6 +154,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
     tmem_alloc<CG>(smem_u32(tmem_slot), S::TMEM_COLS);
     tmem_relinquish<CG>();
   }
+  grid_wait();
+  grid_go();
   if (warp == 3) build_table<BM>(gt, p.counts, p.E, p.R, lane);
   tc_fence_before();
   __syncthreads();
@@ -482,8 +484,7 @@ cudaError_t launch(const GroupedProblem& g, cudaStream_t st) {
   tiles *= p.n_tiles;
   if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   const int nc = (int)(tiles < clusters ? tiles : clusters);
-  grouped_kernel<T, CG, BN, WG><<<CG * nc, THREADS, S::SMEM_BYTES, st>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(grouped_kernel<T, CG, BN, WG>, CG * nc, THREADS, S::SMEM_BYTES, st, p);
 }
 
 template <int CG, int BN, bool WG>

@@ -5,6 +5,7 @@
 
 #include "bra_internal.h"
 #include "bra_moe.h"
+#include "launch.cuh"
 
 namespace bra {
 

@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int U = 8;
   const int lane = threadIdx.x & 31;
   Walk at((uint32_t)(units + 32 * U - 1) / (32 * U));
+  grid_wait();
+  grid_go();
   int t = at.row < R ? __ldg(tokens + at.row) : -1;
   while (at.row < R) {
     const uint32_t r = at.row;
@@ -111,6 +113,8 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int U = sizeof(T) == 4 ? 4 : 8;
   const int lane = threadIdx.x & 31;
   Walk at((uint32_t)(H + 255) / 256);
+  grid_wait();
+  grid_go();
   int slot = -1;
   float wt = 0.f;
   auto fetch = [&] {
@@ -166,6 +170,8 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int TPB = kWarps / WPT;              // tokens of a block
   constexpr int U = 4;                           // rows in flight
   const int sub = warp % WPT;
+  grid_wait();
+  grid_go();
   for (int64_t t0 = (int64_t)blockIdx.x * TPB; t0 < tokens; t0 += (int64_t)gridDim.x * TPB) {
     const int64_t t = t0 + warp / WPT;
     if (t < tokens) {
@@ -274,10 +280,9 @@ cudaError_t launch_dispatch(const PermuteCall& c, cudaStream_t st) {
     const int64_t warps = c.R * ((units + 255) / 256);
     cudaError_t e = grid_of((warps + kWarps - 1) / kWarps, 16, &grid);
     if (e != cudaSuccess) return e;
-    dispatch_kernel<<<grid, kThreads, 0, st>>>(static_cast<const W*>(c.in), c.row_tokens,
-                                               static_cast<W*>(c.out), (uint32_t)c.R, c.T,
-                                               (int)units);
-    return cudaGetLastError();
+    return launch_overlapped(dispatch_kernel<W>, grid, kThreads, 0, st,
+                             static_cast<const W*>(c.in), c.row_tokens, static_cast<W*>(c.out),
+                             (uint32_t)c.R, c.T, (int)units);
   };
   auto fits = [&](uintptr_t n) {
     return bytes % (int64_t)n == 0 && (reinterpret_cast<uintptr_t>(c.in) & (n - 1)) == 0 &&
@@ -296,10 +301,9 @@ cudaError_t launch_combine(const PermuteCall& c, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   return by_type(c.dtype, vec, [&](auto* type, auto v) {
     using T = std::remove_pointer_t<decltype(type)>;
-    combine_kernel<T, decltype(v)::value><<<grid, kThreads, 0, st>>>(
-        static_cast<const T*>(c.in), c.slots, c.weights, static_cast<T*>(c.out),
-        (uint32_t)c.T, c.R, c.k, c.H);
-    return cudaGetLastError();
+    return launch_overlapped(combine_kernel<T, decltype(v)::value>, grid, kThreads, 0, st,
+                             static_cast<const T*>(c.in), c.slots, c.weights,
+                             static_cast<T*>(c.out), (uint32_t)c.T, c.R, c.k, c.H);
   });
 }
 
@@ -312,10 +316,9 @@ cudaError_t launch_combine_grad(const PermuteCall& c, const void* ys, float* dw,
       unsigned grid = 0;
       cudaError_t e = grid_of((c.T + tpb - 1) / tpb, 16, &grid);
       if (e != cudaSuccess) return e;
-      kernel<<<grid, kThreads, 0, st>>>(static_cast<const T*>(c.in), static_cast<const T*>(ys),
-                                        c.slots, c.weights, c.row_tokens, static_cast<T*>(c.out),
-                                        dw, c.T, c.R, c.k, c.H);
-      return cudaGetLastError();
+      return launch_overlapped(kernel, grid, kThreads, 0, st, static_cast<const T*>(c.in),
+                               static_cast<const T*>(ys), c.slots, c.weights, c.row_tokens,
+                               static_cast<T*>(c.out), dw, c.T, c.R, c.k, c.H);
     };
     return c.H >= 1024 ? run(combine_grad_kernel<T, V, 4>, 1) : run(combine_grad_kernel<T, V, 1>, 4);
   });

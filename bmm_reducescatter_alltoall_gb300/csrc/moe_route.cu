@@ -228,6 +228,8 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParam
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   clear_bits(bits, p.E * words);
   __syncthreads();
+  grid_wait();
+  grid_go();
   constexpr int G = 32 / L;                             // tokens of a warp
   for (int i0 = warp * G; i0 < n; i0 += kWarps * G) {
     const int i = i0 + lane / L;
@@ -277,7 +279,8 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams
   const int n = min(p.chunk, p.T - t0);
   for (int e = threadIdx.x; e < p.E; e += kThreads) total[e] = before[e] = 0;
   __syncthreads();
-  cudaGridDependencySynchronize();                      // the choices are written
+  grid_wait();                                          // the choices are written
+  grid_go();
   // the first pairs' loads go out before the matrix is summed
   constexpr int AHEAD = 4;
   int id[AHEAD], place[AHEAD];
@@ -348,6 +351,8 @@ template <typename T, int L, int V>
 __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p) {
   constexpr int G = 32 / L, OWN = (BRA_MAX_CHOICES + L - 1) / L;
   const int lane = threadIdx.x & 31, gl = lane % L;
+  grid_wait();
+  grid_go();
   const int64_t step = (int64_t)gridDim.x * 8 * G;
   const int64_t first = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * G;
   int id[OWN], id_next[OWN];
@@ -471,21 +476,11 @@ cudaError_t launch_route(const RouteCall& r, cudaStream_t st) {
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (a != cudaSuccess) return a;
     }
-    route_choose_kernel<T, decltype(l)::value, decltype(v)::value><<<p.chunks, kThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(route_choose_kernel<T, decltype(l)::value, decltype(v)::value>,
+                             (unsigned)p.chunks, kThreads, smem, st, p);
   });
   if (e != cudaSuccess || p.chunks == 1) return e;
-  // launched while the choices are still being made; it waits for them itself
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.chunks, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, route_place_kernel, p);
+  return launch_overlapped(route_place_kernel, (unsigned)p.chunks, kThreads, 0, st, p);
 }
 
 cudaError_t launch_route_grad(const RouteGradCall& r, cudaStream_t st) {
@@ -500,9 +495,8 @@ cudaError_t launch_route_grad(const RouteGradCall& r, cudaStream_t st) {
     using T = std::remove_pointer_t<decltype(type)>;
     constexpr int tokens = 8 * 32 / decltype(l)::value;           // of a block
     const int64_t want = (r.T + tokens - 1) / tokens, full = (int64_t)sms * 8;
-    route_grad_kernel<T, decltype(l)::value, decltype(v)::value>
-        <<<(unsigned)(want < full ? want : full), 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(route_grad_kernel<T, decltype(l)::value, decltype(v)::value>,
+                             (unsigned)(want < full ? want : full), 256, 0, st, p);
   });
 }
 

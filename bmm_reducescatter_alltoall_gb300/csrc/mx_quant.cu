@@ -12,6 +12,8 @@
 // consecutive elements (one 16-byte load, one 4-byte store), four lanes share
 // a block, a warp takes up to 1024 elements of one row with their loads
 // issued together.
+#include <type_traits>
+
 #include "grouped.cuh"
 #include "mx.cuh"
 #include "walk.cuh"
@@ -87,6 +89,8 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ GroupTable gt;
   const int lane = threadIdx.x & 31;
   int64_t rows = R;
+  grid_wait();
+  grid_go();
   if (counts) {
     if (threadIdx.x < 32) build_table<128>(&gt, counts, E, R, lane);
     __syncthreads();
@@ -173,6 +177,8 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ GroupTable gt;
   const int lane = threadIdx.x & 31;
   int64_t rows = R;
+  grid_wait();
+  grid_go();
   if (counts) {
     if (threadIdx.x < 32) build_table<128>(&gt, counts, E, R, lane);
     __syncthreads();
@@ -247,15 +253,12 @@ cudaError_t launch_mx_quantize(const MxRows& q, const void* x, int64_t ld, int d
   cudaError_t e = blocks_for(warps_of(q.R, q.K), &grid);
   if (e != cudaSuccess) return e;
   const int vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ld % 8 == 0;
-  if (dtype == BRA_BF16)
-    quantize_kernel<<<grid, kThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(x), ld, q.R, q.K,
-                                               q.counts, q.E, q.each, q.codes, q.scales, vec,
-                                               q.status);
-  else
-    quantize_kernel<<<grid, kThreads, 0, st>>>(static_cast<const __half*>(x), ld, q.R, q.K,
-                                               q.counts, q.E, q.each, q.codes, q.scales, vec,
-                                               q.status);
-  return cudaGetLastError();
+  auto run = [&](auto* in) {
+    using T = std::remove_pointer_t<decltype(in)>;
+    return launch_overlapped(quantize_kernel<T>, grid, kThreads, 0, st, static_cast<const T*>(x),
+                             ld, q.R, q.K, q.counts, q.E, q.each, q.codes, q.scales, vec, q.status);
+  };
+  return dtype == BRA_BF16 ? run((__nv_bfloat16*)nullptr) : run((__half*)nullptr);
 }
 
 cudaError_t launch_mx_dequantize(const MxRows& q, void* y, int dtype, cudaStream_t st) {
@@ -265,13 +268,13 @@ cudaError_t launch_mx_dequantize(const MxRows& q, void* y, int dtype, cudaStream
   const int64_t es = dtype == BRA_FP32 ? 4 : 2;
   const int vec = (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && q.K * es % 16 == 0;
   auto run = [&](auto* out) {
-    dequantize_kernel<<<grid, kThreads, 0, st>>>(q.codes, q.scales, q.R, q.K, q.counts, q.E,
-                                                 q.each, out, vec, q.status);
+    using T = std::remove_pointer_t<decltype(out)>;
+    return launch_overlapped(dequantize_kernel<T>, grid, kThreads, 0, st, q.codes, q.scales, q.R,
+                             q.K, q.counts, q.E, q.each, static_cast<T*>(y), vec, q.status);
   };
-  if (dtype == BRA_BF16) run(static_cast<__nv_bfloat16*>(y));
-  else if (dtype == BRA_FP16) run(static_cast<__half*>(y));
-  else run(static_cast<float*>(y));
-  return cudaGetLastError();
+  if (dtype == BRA_BF16) return run((__nv_bfloat16*)nullptr);
+  if (dtype == BRA_FP16) return run((__half*)nullptr);
+  return run((float*)nullptr);
 }
 
 }  // namespace bra

@@ -163,6 +163,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
     tmem_alloc<CG>(smem_u32(tmem_slot), 512);
     tmem_relinquish<CG>();
   }
+  grid_wait();
+  grid_go();
   if (warp == 3) build_table<BM>(gt, p.counts, p.E, p.R, lane);
   if (warp == 1) build_table<128>(gb, p.counts, p.E, p.R, lane);
   tc_fence_before();
@@ -455,8 +457,7 @@ cudaError_t launch(const MxProblem& g, cudaStream_t st) {
   const int64_t tiles = (g.R / (128 * CG) + groups) * p.n_tiles;         // at most
   if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   const int nc = (int)(tiles < clusters ? tiles : clusters);
-  mx_grouped_kernel<T, CG, BN><<<CG * nc, S::THREADS, S::SMEM_BYTES, st>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(mx_grouped_kernel<T, CG, BN>, CG * nc, S::THREADS, S::SMEM_BYTES, st, p);
 }
 
 }  // namespace

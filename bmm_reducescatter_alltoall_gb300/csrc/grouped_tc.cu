@@ -24,6 +24,10 @@
 //     times another group's infinity would: warp 3 zeroes them in both
 //     operands (a box row is 128 bytes of shared memory, whatever the
 //     swizzle), up to the next multiple of 16, where the block's MMAs stop.
+//     Its tiles cost as many blocks as the group has rows, so the groups are
+//     walked largest first: a long tile begun last would be waited for alone
+//     (32 experts of 1300 to 13000 rows, K = N = 1024: 134 us in the groups'
+//     own order, 92 for equal ones).
 // Every wait is bounded (about 4 s) and reports through the fault word.
 #include <cstring>
 #include <mutex>
@@ -67,7 +71,8 @@ struct GShape {
   static constexpr int B_BYTES = B_COLS * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int EPI_BYTES = 4 * (kSegBytes + BN * 4);
-  static constexpr int FIXED = BAR_BYTES + EPI_BYTES + (int)sizeof(GroupTable) + 1024;
+  static constexpr int FIXED =
+      BAR_BYTES + EPI_BYTES + (int)sizeof(GroupTable) + kMaxGroups * 2 + 16 + 1024;
   static constexpr int FIT = (232448 - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + FIXED;
@@ -81,12 +86,12 @@ struct Tile {
 };
 
 template <bool WG>
-__device__ __forceinline__ Tile find_tile(const GroupedParams& p, const GroupTable* gt, int t,
-                                          int& e_hint) {
+__device__ __forceinline__ Tile find_tile(const GroupedParams& p, const GroupTable* gt,
+                                          const uint16_t* order, int t, int& e_hint) {
   Tile r;
   if (WG) {
     const TileCoord c = tile_coord(t, p.m_tiles, p.n_tiles, kGroupM);
-    r.e = c.g;
+    r.e = order[c.g];
     r.mt = c.mt;
     r.nt = c.nt;
   } else {
@@ -127,7 +132,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BAR_BYTES - 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_BYTES - 8);
   GroupTable* gt = reinterpret_cast<GroupTable*>(bars + BAR_BYTES);
-  uint8_t* epi = bars + BAR_BYTES + ((sizeof(GroupTable) + 15) & ~15);
+  uint16_t* order = reinterpret_cast<uint16_t*>(gt + 1);       // wgrad: groups, largest first
+  uint8_t* epi = bars + BAR_BYTES + ((sizeof(GroupTable) + kMaxGroups * 2 + 15) & ~15);
   int32_t* fault = &g_bra_fault_word_grouped;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -159,11 +165,30 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp == 3) build_table<BM>(gt, p.counts, p.E, p.R, lane);
   tc_fence_before();
   __syncthreads();
+  if (WG) {
+    for (int e = threadIdx.x; e < p.E; e += THREADS) {
+      const int n = gt->off[e + 1] - gt->off[e];
+      int at = 0;
+      for (int i = 0; i < p.E; ++i) {
+        const int m = gt->off[i + 1] - gt->off[i];
+        at += m > n || (m == n && i < e);
+      }
+      order[at] = (uint16_t)e;
+    }
+    __syncthreads();
+  }
   if (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int total = gt->bad ? 0 : (WG ? p.E * p.m_tiles : gt->tile[p.E]) * p.n_tiles;
+  // This cluster's tile of each round over the clusters.  wgrad: largest first,
+  // every second round backwards, so that who began with a long tile goes on
+  // with a short one.
   const int walk0 = blockIdx.x / CG, step = gridDim.x / CG;
+  const int rounds = (total + step - 1) / step;
+  auto tile_at = [&](int round) {
+    return round * step + (WG && (round & 1) ? step - 1 - walk0 : walk0);
+  };
 
   if ((warp == 0 || warp == 2) && lane == 0) {
     // ---------------- TMA producers (every CTA): warp 0 for A, warp 2 for B ----------------
@@ -185,8 +210,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
       if (CG == 2) tma_load_3d_pair(dst, m, bar, c0, c1, c2);
       else tma_load_3d(dst, m, bar, c0, c1, c2);
     };
-    for (int t = walk0; ok && t < total; t += step) {
-      const Tile c = find_tile<WG>(p, gt, t, hint);
+    for (int round = 0; ok && round < rounds; ++round) {
+      const int t = tile_at(round);
+      if (t >= total) break;
+      const Tile c = find_tile<WG>(p, gt, order, t, hint);
       const int r0 = gt->off[c.e], r1 = gt->off[c.e + 1];
       const int a_row = c.mt * BM + (int)rank * 128;            // of the output
       const int b_col = c.nt * BN + (int)rank * S::B_COLS;
@@ -266,10 +293,12 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
         phase ^= 1u;
       }
     };
-    for (int t = walk0; ok && t < total; t += step) {
+    for (int round = 0; ok && round < rounds; ++round) {
+      const int t = tile_at(round);
+      if (t >= total) break;
       int full = p.k_blocks, tail = 0;     // whole blocks, rows of a last one
       if (WG) {
-        const Tile c = find_tile<WG>(p, gt, t, hint);
+        const Tile c = find_tile<WG>(p, gt, order, t, hint);
         const int n = gt->off[c.e + 1] - gt->off[c.e];
         full = n / BK;
         tail = n % BK;
@@ -321,8 +350,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t leader_ptail0 = CG == 2 ? map_to_rank(ptail_bar(0), 0) : 0u;
     int stage = 0, hint = 0;
     uint32_t used = 0;              // parity of each stage's tail barrier
-    for (int t = walk0; t < total; t += step) {
-      const Tile c = find_tile<WG>(p, gt, t, hint);
+    for (int round = 0; round < rounds; ++round) {
+      const int t = tile_at(round);
+      if (t >= total) break;
+      const Tile c = find_tile<WG>(p, gt, order, t, hint);
       const int n = gt->off[c.e + 1] - gt->off[c.e];
       const int blocks = (n + BK - 1) / BK, valid = n % BK;
       if (blocks == 0) continue;
@@ -353,8 +384,10 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t leader_tempty0 = CG == 2 ? map_to_rank(tempty_bar(0), 0) : tempty_bar(0);
     int acc = 0, hint = 0;
     uint32_t acc_phase = 0;
-    for (int t = walk0; t < total; t += step) {
-      const Tile c = find_tile<WG>(p, gt, t, hint);
+    for (int round = 0; round < rounds; ++round) {
+      const int t = tile_at(round);
+      if (t >= total) break;
+      const Tile c = find_tile<WG>(p, gt, order, t, hint);
       const int r0 = gt->off[c.e], r1 = gt->off[c.e + 1];
       const int tile_row = c.mt * BM + (int)rank * 128 + q * 32;
       const int n0 = c.nt * BN;
@@ -495,21 +528,36 @@ cudaError_t launch_t(const GroupedProblem& g, cudaStream_t st) {
 
 }  // namespace
 
+// The CTA pair moves a third less through shared memory per product, but has
+// half as many, twice as large tiles.  bf16, pair against one CTA, us (rows an
+// expert x experts, K, N):
+//   forward                           wgrad
+//   128 x  8, 1024, 1024  11 / 10     128 x 64, 2048, 4096  310 / 222
+//   256 x  8, 2048, 4096  38 / 36     256 x 64, 4096, 2048  374 / 324
+//   512 x 16, 1024, 1024  22 / 17     512 x 64, 2048, 4096  586 / 547
+//   128 x 64, 2048, 4096 159 / 171   1024 x 64, 2048, 4096  832 / 839
+//   512 x 64, 2048, 4096 434 / 483   1024 x 32, 1024, 1024   63 /  66
+//  2048 x  8, 2048, 4096 163 / 177   2048 x 64, 2048, 4096 1407 / 1511
+// So forward takes the pair from 128 rows an expert and four waves of tiles
+// on, the weight gradient (whose K loop is the rows) from 1024 rows on.
 cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st) {
-  // Rows to an expert on average, and the most experts that can have rows.
+  // rows to an expert on average, and the most experts that can have rows
   const int64_t avg = g.R / g.E, groups = g.R < g.E ? g.R : g.E;
-  if (avg >= 128) return launch_t<2, 256, false>(g, st);
-  // Few rows: the weights' bytes bound the call, and narrow tiles spread them
-  // over the SMs.
+  const int64_t nt = (g.N + 255) / 256;
+  if (avg >= 128 && (2 * (g.R / 256) + groups) * nt >= 2 * 304) return launch_t<2, 256, false>(g, st);
+  // One CTA a tile.  256 columns, unless that leaves SMs without a tile (128
+  // rows x 8, 1024, 1024: 10.0 us with 256, 8.9 with 128); with few rows to
+  // an expert the weights' bytes bound the call, and narrower tiles still
+  // spread them (a token's two experts, 2048, 4096: 64 columns, 128 tiles).
   const int64_t mt = g.R / 128 + groups;
-  if (mt * ((g.N + 255) / 256) >= 152) return launch_t<1, 256, false>(g, st);
-  if (mt * ((g.N + 127) / 128) >= 152) return launch_t<1, 128, false>(g, st);
+  if (mt * nt >= 100) return launch_t<1, 256, false>(g, st);
+  if (avg >= 16 || mt * ((g.N + 127) / 128) >= 152) return launch_t<1, 128, false>(g, st);
   return launch_t<1, 64, false>(g, st);
 }
 
 cudaError_t launch_grouped_wgrad(const GroupedProblem& g, cudaStream_t st) {
-  if (g.K > 128 && g.N > 128) return launch_t<2, 256, true>(g, st);
-  return launch_t<1, 128, true>(g, st);
+  if (g.R / g.E >= 1024 && g.K > 128 && g.N > 128) return launch_t<2, 256, true>(g, st);
+  return g.N > 128 ? launch_t<1, 256, true>(g, st) : launch_t<1, 128, true>(g, st);
 }
 
 cudaError_t read_grouped_fault_word(int32_t* code, int clear) {

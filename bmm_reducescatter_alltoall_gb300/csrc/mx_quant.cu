@@ -8,10 +8,14 @@
 // are a function of x alone.  A block with a NaN or an infinity has no scale:
 // byte 255, every value NaN.
 //
-// Memory bound: 16 bits read and 4.25 written to an element.  A lane holds 8
-// consecutive elements (one 16-byte load, one 4-byte store), four lanes share
-// a block, a warp takes up to 1024 elements of one row with their loads
-// issued together.
+// 16 bits are read and 4.25 written to an element, but at those rates the
+// instructions of a warp count as much as the bytes.  Quantising, a lane takes
+// a whole block: no exchange for the maximum, one 16-byte store of codes, and
+// the block's scale once (with 8 elements a lane, four lanes to a block, the
+// same work took 112 instructions an 8 elements and 34 us for 64 Mi values
+// where the bytes take 25).  Going back, a lane makes 8 elements, one 16-byte
+// store.  A warp takes up to 1024 elements of a row with their loads issued
+// together.
 #include <type_traits>
 
 #include "grouped.cuh"
@@ -102,61 +106,63 @@ __global__ void __launch_bounds__(kThreads)
     rows = gt.off[E];
   }
   const int64_t cpitch = mx::code_pitch(K), k_units = mx::units(K);
+  const int nblocks = (int)((K + mx::kBlock - 1) / mx::kBlock), nscales = (int)k_units * 8;
   for (Walk at((uint32_t)((k_units + kPieces - 1) / kPieces)); at.row < rows; at.next()) {
     const int64_t r = at.row;
-    const int k0 = (int)at.part * (kPieces * mx::kUnitK);
-    const T* src = x + r * ld;
-    uint32_t w[kPieces][4];
+    const int b = (int)at.part * 32 + lane;         // this lane's block of the row
+    const T* src = x + r * ld + (int64_t)b * mx::kBlock;
+    uint32_t w[16];
+    if (vec && (b + 1) * mx::kBlock <= K) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int k = k0 + i * mx::kUnitK + lane * 8;
-      w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0u;
-      if (vec && k + 8 <= K) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src + k));
-        w[i][0] = q.x, w[i][1] = q.y, w[i][2] = q.z, w[i][3] = q.w;
-      } else if (k < K) {
-        const uint16_t* s = reinterpret_cast<const uint16_t*>(src + k);
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+      }
+    } else {
+      const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
+      const int64_t left = K - (int64_t)b * mx::kBlock;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (k + j < K) w[i][j >> 1] |= (uint32_t)__ldg(s + j) << ((j & 1) * 16);
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t lo = 2 * i < left ? __ldg(e + 2 * i) : 0u;
+        const uint32_t hi = 2 * i + 1 < left ? __ldg(e + 2 * i + 1) : 0u;
+        w[i] = lo | hi << 16;
       }
     }
     int64_t blk;
     int in;
     locate(&gt, E, each, r, &blk, &in);
-    uint8_t* crow = codes + r * cpitch;
+    // magnitudes ordered as 16-bit integers: NaN above infinity above all else
+    uint32_t a = 0;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int k = k0 + i * mx::kUnitK + lane * 8;
-      if (k0 + i * mx::kUnitK >= K) break;          // the same for the whole warp
-      // magnitudes ordered as 16-bit integers: NaN above infinity above all else
-      uint32_t a = 0;
+    for (int i = 0; i < 16; ++i) a = __vmaxu2(a, w[i] & 0x7fff7fffu);
+    const float2 top = pair_of<T>(__vmaxu2(a, a >> 16));
+    const uint32_t bits = __float_as_uint(top.x);
+    const bool none = bits >= 0x7f800000u;
+    const int field = (int)(bits >> 23);            // subnormals and zero: 0
+    const uint32_t byte = none ? 255u : (uint32_t)max(field - 2, 0);
+    const float inv = __uint_as_float((254u - (none ? 0u : byte)) << 23);   // 2^(127 - byte)
+    if (b < nblocks) {
+      uint32_t c[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a = __vmaxu2(a, w[i][j] & 0x7fff7fffu);
-      a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 2));
-      const float2 top = pair_of<T>(__vmaxu2(a, a >> 16));
-      const uint32_t bits = __float_as_uint(top.x);
-      const bool none = bits >= 0x7f800000u;
-      const int field = (int)(bits >> 23);          // subnormals and zero: 0
-      const uint32_t byte = none ? 255u : (uint32_t)max(field - 2, 0);
-      const float inv = __uint_as_float((254u - (none ? 0u : byte)) << 23);   // 2^(127 - byte)
-      float f[8];
+      for (int i = 0; i < 4; ++i) {
+        float f[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 p = pair_of<T>(w[i][j]);
-        f[2 * j] = p.x * inv;
-        f[2 * j + 1] = p.y * inv;
+        for (int j = 0; j < 4; ++j) {
+          const float2 p = pair_of<T>(w[4 * i + j]);
+          f[2 * j] = p.x * inv;
+          f[2 * j + 1] = p.y * inv;
+        }
+        c[i] = none ? 0u : code_word(f);
       }
-      const uint32_t c = code_word(f);
-      if (k < cpitch * 2) *reinterpret_cast<uint32_t*>(crow + k / 2) = none ? 0u : c;
-      // a 128-element atom's four scales as one word
-      uint32_t s = byte << (8 * ((lane >> 2) & 3));
-      s |= __shfl_xor_sync(0xffffffffu, s, 4);
-      s |= __shfl_xor_sync(0xffffffffu, s, 8);
-      if ((lane & 15) == 0)
-        *reinterpret_cast<uint32_t*>(scales + mx::scale_at(blk, in, k / mx::kBlock, k_units)) = s;
+      *reinterpret_cast<uint4*>(codes + r * cpitch + (int64_t)b * 16) =
+          make_uint4(c[0], c[1], c[2], c[3]);
     }
+    // a 128-element atom's four scales as one word
+    uint32_t s = byte << (8 * (lane & 3));
+    s |= __shfl_xor_sync(0xffffffffu, s, 1);
+    s |= __shfl_xor_sync(0xffffffffu, s, 2);
+    if ((lane & 3) == 0 && b < nscales)
+      *reinterpret_cast<uint32_t*>(scales + mx::scale_at(blk, in, b, k_units)) = s;
   }
 }
 
@@ -192,24 +198,26 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t cpitch = mx::code_pitch(K), k_units = mx::units(K);
   for (Walk at((uint32_t)((k_units + kPieces - 1) / kPieces)); at.row < rows; at.next()) {
     const int64_t r = at.row;
-    const int k0 = (int)at.part * (kPieces * mx::kUnitK);
+    const int k0 = (int)at.part * (kPieces * mx::kUnitK) + lane * 8;
     int64_t blk;
     int in;
     locate(&gt, E, each, r, &blk, &in);
+    const uint8_t* code = codes + r * cpitch + k0 / 2;
+    const uint8_t* scale = scales + mx::scale_at(blk, in, k0 / mx::kBlock, k_units);
+    T* dst = y + r * K + k0;
     uint32_t c[kPieces], b[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int k = k0 + i * mx::kUnitK + lane * 8;
       c[i] = b[i] = 0u;
-      if (k < K) {
-        c[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + r * cpitch + k / 2));
-        b[i] = __ldg(scales + mx::scale_at(blk, in, k / mx::kBlock, k_units));
+      if (k0 + i * mx::kUnitK < K) {
+        c[i] = __ldg(reinterpret_cast<const uint32_t*>(code + i * (mx::kUnitK / 2)));
+        b[i] = __ldg(scale + i * mx::kUnitBytes);     // a unit's scales are a unit's bytes on
       }
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int k = k0 + i * mx::kUnitK + lane * 8;
-      if (k >= K) break;
+      const int left = (int)K - (k0 + i * mx::kUnitK);
+      if (left <= 0) break;
       // 2^(b - 127): b = 0 is the subnormal 2^-127, 255 is NaN
       const float s = __uint_as_float(b[i] == 255u ? 0x7fc00000u : b[i] ? b[i] << 23 : 1u << 22);
       T v[8];
@@ -219,15 +227,15 @@ __global__ void __launch_bounds__(kThreads)
         v[2 * j] = to<T>(m.x * s);
         v[2 * j + 1] = to<T>(m.y * s);
       }
-      T* dst = y + r * K + k;
-      if (vec && k + 8 <= K) {
+      T* out = dst + i * mx::kUnitK;
+      if (vec && left >= 8) {
 #pragma unroll
         for (int j = 0; j < (int)sizeof(T) / 2; ++j)
-          reinterpret_cast<uint4*>(dst)[j] = reinterpret_cast<const uint4*>(v)[j];
+          reinterpret_cast<uint4*>(out)[j] = reinterpret_cast<const uint4*>(v)[j];
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (k + j < K) dst[j] = v[j];
+          if (j < left) out[j] = v[j];
       }
     }
   }

@@ -5,25 +5,34 @@
 // The walk over ragged row groups is grouped_tc.cu's.  A K block is 256
 // elements (128 bytes of codes to a row, one 128-byte swizzle row) and four
 // MMAs of K = 64; their scales, one byte to 32 elements of each row and
-// weight column, have to be in tensor memory.  They are stored in memory in
-// the order tcgen05.cp wants (mx.cuh), so one TMA box of 1 KiB (2 KiB for two
-// weight blocks) brings the scales of 128 rows and 256 elements to shared
-// memory (a tensor copy, which in a pair may complete on the leader's barrier,
-// as an untiled one may not) and two tcgen05.cp
-// (32 lanes x 128 bits, broadcast to the four lane quarters) to 8 columns of
-// tensor memory; an MMA picks its two bytes of a column by the scale ids of
-// its instruction descriptor.  Each ring stage has its own scale columns, so
-// a stage's commit also frees them.
-//   CG = 2, BN = 256: 256 x 256 tile of a CTA pair.  Accumulator (256
-//     columns) and scales (5 x 24) fit tensor memory once, so the epilogue
-//     first drains the accumulator into registers (eight warps, 128 columns
-//     each, rounded and packed), hands it back, and stores while the next
-//     tile is computed.
+// weight column, have to be in tensor memory, the same in all four lane
+// quarters.  They are stored in memory in atoms (mx.cuh) in which a lane's
+// four words are 16 bytes, so one TMA box brings a unit to shared memory and
+// each of four writer warps, one to a lane quarter, passes it on with a few
+// 16-byte loads and tcgen05.st.  An MMA picks its two bytes of a column by the
+// scale ids of its instruction descriptor.
+//   Writers and not tcgen05.cp: a copy takes its 55 cycles of the tensor pipe
+//   itself, and a 256 x 256 pair tile needs six to a K block, next to 512
+//   cycles of MMAs; 8 x 2048 rows, K = 16384, N = 4096 took 442 us with
+//   copies and 316 with stores beside the MMAs.
+//   The writers' word to the MMA issuer carries no memory of theirs, only
+//   that their tcgen05.st have completed (tcgen05.wait::st, and the tcgen05
+//   fences on both sides of the barrier): the arrival is relaxed.  With a
+//   release at cluster scope the remote one took 1400 cycles a K block.
+//   CG = 2, BN = 256: 256 x 256 tile of a CTA pair.  What feeds the tensor
+//     cores bounds it: some 58 bytes a clock and SM from L2, 35 KiB a K block
+//     and CTA, 600 cycles where the MMAs take 512 (with a quarter of the MMAs
+//     left out the time hardly changed).  256 x 192 tiles, whose two
+//     accumulators fit beside the scales, need 15% more of it: 452 us against
+//     316 on the sizes above.  With one accumulator the epilogue first drains
+//     it into registers (eight warps, 128 columns each, rounded and packed),
+//     hands it back, and stores while the next tile is computed.
 //   CG = 1, BN = 128: 128 x 128 tile, two accumulators, for few rows to an
 //     expert (the weights' bytes bound the call).
 // Every wait is bounded (about 4 s) and reports through the fault word.
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "grouped.cuh"
 #include "mx.cuh"
@@ -39,8 +48,9 @@ using namespace grp;
 
 constexpr int BKB = 128;                    // bytes of codes of a K block (256 elements)
 constexpr int kGroupM = 8;
-constexpr int EPI_WARP0 = 4;
-constexpr int BAR_BYTES = 256;
+constexpr int WRITE_WARP0 = 4;
+constexpr int EPI_WARP0 = 8;
+constexpr int BAR_BYTES = 512;
 
 struct MxParams {
   CUtensorMap ta, ta32;                     // row codes, boxes of 128 and 32 rows
@@ -62,19 +72,26 @@ struct MShape {
   static constexpr int B_ROWS = BN / CG;                  // weight rows held by one CTA
   static constexpr int B_BYTES = B_ROWS * BKB;
   static constexpr int NSB = BN / 128;                    // weight scale blocks of a tile
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  // The scales' way to tensor memory has a ring of its own, so that it runs
+  // ahead of the codes.
   static constexpr int SF_BYTES = (1 + NSB) * mx::kUnitBytes;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
+  static constexpr int SF_STAGES = 4;
   static constexpr int EPI_WARPS = BN / 32;               // 128 columns each
-  static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
+  static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;   // 4 role and 4 writer warps
   static constexpr int NACC = BN == 128 ? 2 : 1;
   static constexpr int EPI_BYTES = EPI_WARPS * (kSegBytes + 512);
-  static constexpr int FIXED = BAR_BYTES + EPI_BYTES + 2 * (int)sizeof(GroupTable) + 64 + 1024;
+  static constexpr int FIXED = BAR_BYTES + EPI_BYTES + 2 * (int)sizeof(GroupTable) + 16 + 1024 +
+                               SF_STAGES * SF_BYTES;
   static constexpr int FIT = (232448 - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + FIXED;
-  static constexpr int SF_COLS = 8 + 8 * NSB;             // scale columns of a stage
+  // scale columns of a K block: 8 of the rows, 8 for each half's weights
+  static constexpr int SF_COLS = 24;
   static constexpr uint32_t SF0 = NACC * BN;
-  static_assert(SF0 + STAGES * SF_COLS <= 512 && STAGES >= 4, "tensor memory, ring");
+  static constexpr int SF_FIT = (512 - NACC * BN) / SF_COLS;
+  static constexpr int SLOTS = SF_FIT > STAGES ? STAGES : SF_FIT;   // K blocks of scales
+  static_assert(SLOTS >= 4 && STAGES >= 4, "tensor memory, ring");
   static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms");
 };
 
@@ -99,22 +116,24 @@ __device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sa), "r"(sb)
         : "memory");
 }
-// 32 lanes x 16 bytes (512 contiguous bytes) to four columns, repeated in the
-// four lane quarters; with CG == 2 in both CTAs, each from its own memory.
-template <int CG>
-__device__ __forceinline__ void scale_copy(uint32_t taddr, uint64_t desc) {
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
+// N words a lane to N columns of this warp's lane quarter.
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
 }
-// Descriptor of a scale atom: no swizzle, groups of 8 rows 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 |
-         (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+
+// Arrive on a barrier of another CTA of the cluster without ordering this
+// thread's memory accesses.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
 template <typename T, int CG, int BN>
 __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THREADS, 1)
     mx_grouped_kernel(const __grid_constant__ MxParams p) {
@@ -124,14 +143,22 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   const uint32_t smem_base = smem_u32(smem);
-  uint8_t* bars = smem + STAGES * STAGE_BYTES;
+  const uint32_t sf_base = smem_base + STAGES * STAGE_BYTES;
+  uint8_t* bars = smem + STAGES * STAGE_BYTES + S::SF_STAGES * S::SF_BYTES;
   const uint32_t bar_base = smem_u32(bars);
-  // barriers (8 bytes each): full, empty per stage; tfull[2], tempty[2]
+  // barriers (8 bytes each): per stage full, empty; per scale stage sfull
+  // (this CTA's scales have come) and sempty (they have been passed on); per
+  // slot of scale columns sready (leader: both CTAs' are in tensor memory);
+  // tfull[2], tempty[2]
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
-  auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * STAGES + a); };
-  auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * STAGES + 2 + a); };
-  static_assert(8 * (2 * STAGES + 4) + 16 <= BAR_BYTES, "barrier area");
+  constexpr int SFS = S::SF_STAGES;
+  auto sfull_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + s); };
+  auto sempty_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + SFS + s); };
+  auto sready_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + 2 * SFS + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * STAGES + 2 * SFS + S::SLOTS + a); };
+  auto tempty_bar = [&](int a) { return tfull_bar(2 + a); };
+  static_assert(8 * (2 * STAGES + 2 * SFS + S::SLOTS + 4) + 16 <= BAR_BYTES, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BAR_BYTES - 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_BYTES - 8);
   GroupTable* gt = reinterpret_cast<GroupTable*>(bars + BAR_BYTES);      // row tiles
@@ -147,6 +174,11 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
       mbar_init(full_bar(s), 1);     // leader: its expect_tx; the bytes of both CTAs
       mbar_init(empty_bar(s), 1);
     }
+    for (int s = 0; s < SFS; ++s) {
+      mbar_init(sfull_bar(s), 1);
+      mbar_init(sempty_bar(s), 4);
+    }
+    for (int s = 0; s < S::SLOTS; ++s) mbar_init(sready_bar(s), 4 * CG);
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), S::EPI_WARPS * CG);
@@ -200,12 +232,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
       const int row = r0 + c.mt * BM + (int)rank * 128;
       auto boxes = [&](int valid) { return valid <= 64 ? (max(valid, 0) + 31) / 32 : 4; };
       const int mine = boxes(r1 - row);
-      uint32_t bytes = CG * (S::B_BYTES + S::SF_BYTES) + mine * (S::A_BYTES / 4);
+      uint32_t bytes = CG * S::B_BYTES + mine * (S::A_BYTES / 4);
       if (CG == 2) bytes += boxes(r1 - row - 128) * (S::A_BYTES / 4);   // used by the leader
-      // scale blocks; those past the group's or the weight's last belong to
-      // rows and columns that are not stored
-      const int ablk = gb->tile[c.g] + c.mt * CG + (int)rank;
-      const int bblk = c.g * p.nb + c.nt * S::NSB;
       const int b_row = c.nt * BN + (int)rank * S::B_ROWS;
       for (int kb = 0; kb < p.k_blocks; ++kb) {
         if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, fault)) {
@@ -214,19 +242,43 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
         }
         const uint32_t fb = leader_full0 + 8u * stage;
         const uint32_t a_dst = smem_base + stage * STAGE_BYTES, b_dst = a_dst + S::A_BYTES;
-        const uint32_t s_dst = b_dst + S::B_BYTES;
         if (is_a) {
           if (rank == 0) mbar_expect_tx(full_bar(stage), bytes);
-          load(s_dst, &p.tsa, fb, 0, kb, ablk);
           if (mine == 4) load(a_dst, &p.ta, fb, kb * BKB, row, 0);
           else
             for (int i = 0; i < mine; ++i)
               load(a_dst + i * (S::A_BYTES / 4), &p.ta32, fb, kb * BKB, row + i * 32, 0);
         } else {
           load(b_dst, &p.tb, fb, kb * BKB, b_row, c.g);
-          load(s_dst + mx::kUnitBytes, &p.tsb, fb, 0, kb, bblk);
         }
         if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) spin_ns(2000000ull);   // let copies already issued land
+  } else if (warp == 3 && lane == 0) {
+    // ---------------- scale loads (every CTA, onto its own barriers) ----------------
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = walk0; ok && t < total; t += step) {
+      const TileCoord c = find(t);
+      // scale blocks; those past the group's or the weight's last belong to
+      // rows and columns that are not stored
+      const int ablk = gb->tile[c.g] + c.mt * CG + (int)rank;
+      const int bblk = c.g * p.nb + c.nt * BN / 128;
+      for (int kb = 0; kb < p.k_blocks; ++kb) {
+        if (!mbar_wait(sempty_bar(stage), phase ^ 1u, abort_flag, fault)) {
+          ok = false;
+          break;
+        }
+        const uint32_t dst = sf_base + stage * S::SF_BYTES;
+        mbar_expect_tx(sfull_bar(stage), S::SF_BYTES);
+        tma_load_3d(dst, &p.tsa, sfull_bar(stage), 0, kb, ablk);
+        tma_load_3d(dst + mx::kUnitBytes, &p.tsb, sfull_bar(stage), 0, kb, bblk);
+        if (++stage == SFS) {
           stage = 0;
           phase ^= 1u;
         }
@@ -237,38 +289,34 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
     // ---------------- MMA issuer (leader only) ----------------
     const uint64_t a0 = smem_desc_sw128(smem_base, 16, 1024);
     const uint64_t b0 = smem_desc_sw128(smem_base + S::A_BYTES, 16, 1024);
-    const uint64_t s0 = scale_desc(smem_base + S::A_BYTES + S::B_BYTES);
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
+    int stage = 0, acc = 0, slot = 0;
+    uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
     bool ok = true;
     for (int t = walk0; ok && t < total; t += step) {
       if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, fault)) break;
       tc_fence_after();
       const uint32_t d = tmem_base + (uint32_t)(acc * BN);
       for (int kb = 0; kb < p.k_blocks; ++kb) {
-        if (!mbar_wait(full_bar(stage), phase, abort_flag, fault)) {
+        if (!mbar_wait(full_bar(stage), phase, abort_flag, fault) ||
+            !mbar_wait(sready_bar(slot), slot_phase, abort_flag, fault)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint64_t so = (uint64_t)((stage * STAGE_BYTES) >> 4);
-        const uint32_t sfa = tmem_base + S::SF0 + (uint32_t)(stage * S::SF_COLS), sfb = sfa + 8;
-        // atom h (128 elements) of the rows to columns 4h, of weight block i
-        // to columns 4 (NSB h + i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          scale_copy<CG>(sfa + 4 * h, s0 + so + 32 * h);
-#pragma unroll
-          for (int i = 0; i < S::NSB; ++i)
-            scale_copy<CG>(sfb + 4 * (S::NSB * h + i), s0 + so + 64 * (1 + i) + 32 * h);
-        }
+        // half h (128 elements): rows' columns 4h, weights' 8 + 8h
+        const uint32_t sf = tmem_base + S::SF0 + (uint32_t)(slot * S::SF_COLS);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mx_mma<CG>(d, a0 + so + 2 * k, b0 + so + 2 * k,
-                     p.idesc | ((k & 1) ? (2u << 4 | 2u << 29) : 0u), sfa + 4 * (k >> 1),
-                     sfb + 4 * S::NSB * (k >> 1), (kb > 0 || k > 0) ? 1u : 0u);
+                     p.idesc | ((k & 1) ? (2u << 4 | 2u << 29) : 0u), sf + 4 * (k >> 1),
+                     sf + 8 + 8 * (k >> 1), (kb > 0 || k > 0) ? 1u : 0u);
         if (CG == 2) tc_commit_pair(empty_bar(stage), 0x3);
         else tc_commit(empty_bar(stage));
+        if (++slot == S::SLOTS) {
+          slot = 0;
+          slot_phase ^= 1u;
+        }
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -283,6 +331,84 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
       }
     }
     if (!ok) spin_ns(2000000ull);   // let MMAs already issued complete
+  } else if (warp >= WRITE_WARP0 && warp < EPI_WARP0) {
+    // ---------------- scale writers: lane quarter q, every CTA ----------------
+    const int q = warp & 3;
+    const uint32_t leader_sready0 = CG == 2 ? map_to_rank(sready_bar(0), 0) : sready_bar(0);
+    int stage = 0, slot = 0, old_stage = 0;
+    uint32_t phase = 0, old_phase = 0;   // old: the K block whose slot is written again
+    int ahead = 0;                       // K blocks so far, up to SLOTS
+    bool ok = true;
+    auto step_ring = [](int& at, uint32_t& ph, int size) {
+      if (++at == size) {
+        at = 0;
+        ph ^= 1u;
+      }
+    };
+    // One K block, or two at once: a block's waits, loads and stores are a
+    // chain of some 700 cycles, longer than its MMAs.
+    auto pass_on = [&](auto count) -> bool {
+      constexpr int C = decltype(count)::value;
+      int st = stage, slots[C];
+      uint32_t ph = phase;
+      uint32_t va[C][8], vb[C][2][8];
+#pragma unroll
+      for (int n = 0; n < C; ++n) {
+        if (!__all_sync(0xffffffffu, mbar_wait(sfull_bar(st), ph, abort_flag, fault))) return false;
+        const uint32_t at = sf_base + st * S::SF_BYTES + (uint32_t)lane * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 x = lds128e(at + h * 512);
+          va[n][4 * h] = x.x, va[n][4 * h + 1] = x.y, va[n][4 * h + 2] = x.z, va[n][4 * h + 3] = x.w;
+          uint32_t* w = vb[n][h];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 y = i < S::NSB ? lds128e(at + (1 + i) * mx::kUnitBytes + h * 512)
+                                       : make_uint4(0, 0, 0, 0);
+            w[4 * i] = y.x, w[4 * i + 1] = y.y, w[4 * i + 2] = y.z, w[4 * i + 3] = y.w;
+          }
+        }
+        step_ring(st, ph, SFS);
+        // the MMAs that read this slot have completed
+        if (ahead == S::SLOTS) {
+          if (!__all_sync(0xffffffffu,
+                          mbar_wait(empty_bar(old_stage), old_phase, abort_flag, fault)))
+            return false;
+          step_ring(old_stage, old_phase, STAGES);
+        } else {
+          ++ahead;
+        }
+        slots[n] = slot;
+        if (++slot == S::SLOTS) slot = 0;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int n = 0; n < C; ++n) {
+        const uint32_t sf =
+            tmem_base + S::SF0 + (uint32_t)(slots[n] * S::SF_COLS) + ((uint32_t)(q * 32) << 16);
+        tmem_st8(sf, va[n]);
+        tmem_st8(sf + 8, vb[n][0]);
+        tmem_st8(sf + 16, vb[n][1]);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+#pragma unroll
+      for (int n = 0; n < C; ++n) {
+        if (lane == 0) {
+          mbar_arrive(sempty_bar(stage));
+          if (rank == 0) mbar_arrive(sready_bar(slots[n]));
+          else arrive_relaxed(leader_sready0 + 8u * slots[n]);
+        }
+        step_ring(stage, phase, SFS);
+      }
+      return true;
+    };
+    for (int t = walk0; ok && t < total; t += step) {
+      int kb = 0;
+      for (; ok && kb + 2 <= p.k_blocks; kb += 2) ok = pass_on(std::integral_constant<int, 2>{});
+      if (ok && kb < p.k_blocks) ok = pass_on(std::integral_constant<int, 1>{});
+    }
   } else if (warp >= EPI_WARP0) {
     // ---------------- epilogue: lane quarter q, columns h*128 .. +128 ----------------
     const int q = warp & 3, h = (warp - EPI_WARP0) >> 2;
@@ -316,12 +442,23 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
       uint32_t o[2][32];
       if (any) {
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          uint32_t v[64];
-          tmem_ld32(t_base + ch * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-          tmem_ld32(t_base + ch * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+        for (int part = 0; part < 4; ++part) {       // 32 columns at a time: few registers
+          uint32_t v[32];
+          tmem_ld32(t_base + part * 32, v);
           tmem_ld_wait();
-          pack_segment<T>(v, o[ch], p.bias ? bias_s + ch * 256 : 0u, false);
+          if (p.bias)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 b = lds128e(bias_s + part * 128 + i * 16);
+              v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + __uint_as_float(b.x));
+              v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + __uint_as_float(b.y));
+              v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + __uint_as_float(b.z));
+              v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + __uint_as_float(b.w));
+            }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[part / 2][(part % 2) * 16 + i] =
+                Out<T>::pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
         }
       }
       tc_fence_before();

@@ -22,18 +22,19 @@ constexpr int kBgRows = kBgThreads / 8;
 template <typename T, typename B, int SPLIT>
 __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
     bias_grad_kernel(const T* dy, B* db, const int64_t* counts, int32_t* status, int64_t R,
-                     int64_t ld, int E, int N, int vec) {
+                     int64_t ld, int E, int N, int vec, int late) {
   __shared__ GroupTable gt;
   __shared__ float part[kBgRows][64];
   __shared__ float sum[64];
   const int tid = threadIdx.x;
-  grid_wait();
+  if (!late) grid_wait();
   grid_go();
   if (tid < 32) build_table<1>(&gt, counts, E, R, tid);
   __syncthreads();
   const uint32_t rank = SPLIT > 1 ? cluster_rank() : 0u;
   if (gt.bad) {   // the same for every CTA
     if (tid == 0 && blockIdx.x == 0 && status) atomicExch(status, (int32_t)BRA_ERR_INVALID);
+    if (late) grid_wait();
     return;
   }
   const int col_tiles = (N + 63) / 64;
@@ -93,7 +94,10 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
     if (SPLIT > 1) sum[tid] = t;
     else if (n0 + tid < N) db[(int64_t)e * N + n0 + tid] = static_cast<B>(t);
   }
-  if (SPLIT == 1) return;
+  if (SPLIT == 1) {
+    if (late) grid_wait();
+    return;
+  }
   cluster_sync();
   if (rank == 0 && tid < 64 && n0 + tid < N) {
     float t = 0.f;
@@ -109,6 +113,7 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
     db[(int64_t)e * N + n0 + tid] = static_cast<B>(t);
   }
   cluster_sync();   // the peers' sums have been read
+  if (late) grid_wait();
 }
 
 // --------------------------------------------------------------------------
@@ -174,7 +179,8 @@ cudaError_t launch_bias_grad(const BiasGradProblem& g, cudaStream_t st) {
     using T = std::remove_pointer_t<decltype(dy)>;
     using B = std::remove_pointer_t<decltype(db)>;
     return launch_overlapped(kernel, grid, kBgThreads, 0, st, static_cast<const T*>(g.dy),
-                             static_cast<B*>(g.db), g.counts, g.status, g.R, g.ld, g.E, g.N, vec);
+                             static_cast<B*>(g.db), g.counts, g.status, g.R, g.ld, g.E, g.N, vec,
+                             g.late);
   };
   __nv_bfloat16* b = nullptr;
   __half* h = nullptr;

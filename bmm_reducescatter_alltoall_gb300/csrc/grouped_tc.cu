@@ -60,7 +60,7 @@ struct GroupedParams {
   int64_t R, ldy;
   int E, K, N;
   int m_tiles, n_tiles, k_blocks;   // wgrad: row tiles of K; forward: K blocks
-  int b_kmajor, aligned;
+  int b_kmajor, aligned, late;
   uint32_t idesc;
 };
 
@@ -160,7 +160,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
     tmem_alloc<CG>(smem_u32(tmem_slot), S::TMEM_COLS);
     tmem_relinquish<CG>();
   }
-  grid_wait();
+  if (!p.late) grid_wait();
   grid_go();
   if (warp == 3) build_table<BM>(gt, p.counts, p.E, p.R, lane);
   tc_fence_before();
@@ -437,6 +437,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
     tc_fence_after();
     tmem_dealloc<CG>(tmem_base, S::TMEM_COLS);
   }
+  if (p.late) grid_wait();
 }
 
 // Clusters of the kernel that are resident at once, found on first use.
@@ -506,6 +507,7 @@ cudaError_t launch(const GroupedProblem& g, cudaStream_t st) {
   p.K = g.K;
   p.N = g.N;
   p.b_kmajor = g.wt;
+  p.late = g.late;
   p.aligned = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0 && g.N % 8 == 0;
   p.idesc = make_idesc(g.dtype == BRA_BF16, 128 * CG, BN, !WG && g.wt) | (WG ? 1u << 15 : 0u);
   constexpr int BM = 128 * CG;

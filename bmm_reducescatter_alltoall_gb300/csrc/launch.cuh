@@ -6,6 +6,11 @@
 // short call.  grid_go() lets the next kernel in the stream begin its own
 // set-up; what that one reads is still only valid after its grid_wait(), which
 // returns when this kernel has ended and its writes are visible.
+//
+// A kernel may wait late, before it ends instead of before it begins, when it
+// needs nothing of the kernel before it and that one (or the first of a chain
+// of such) waited early: what lies before the chain is then complete, and the
+// two run beside each other.  A later kernel's wait still covers both.
 #pragma once
 
 #include <cuda_runtime.h>

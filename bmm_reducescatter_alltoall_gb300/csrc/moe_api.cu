@@ -536,11 +536,12 @@ int grouped_matmul_grad(const void* dy, const void* x, const void* weight, const
     g.N = (int)(wt ? s.K : s.N);
     g.ldy = g.N;
     g.wt = 0;
+    g.late = dx != nullptr;      // the gradients do not need each other
     if ((rc = status_of(launch_grouped_wgrad(g, st))) != BRA_OK) return rc;
   }
   if (dbias) {
-    BiasGradProblem b = {dy, dbias, counts, args->status, s.R, s.yp, (int)s.E, (int)s.N,
-                         args->dtype};
+    BiasGradProblem b = {dy,        dbias,    counts,      args->status,     s.R, s.yp,
+                         (int)s.E, (int)s.N, args->dtype, dx || dweight};
     if ((rc = status_of(launch_bias_grad(b, st))) != BRA_OK) return rc;
   }
   return BRA_OK;

@@ -24,6 +24,7 @@ struct GroupedProblem {
   int E, K, N;
   int dtype;             // BRA_FP16 | BRA_BF16
   int wt;                // forward: weights stored (E, N, K)
+  int late;              // needs nothing of the kernel launched before it
 };
 // Operands must be TMA-ready: pointers 16-byte aligned, row pitches a
 // multiple of 8 elements.  cudaErrorInvalidValue if a map cannot be encoded.
@@ -37,6 +38,7 @@ struct BiasGradProblem {
   int32_t* status;
   int64_t R, ld;
   int E, N, dtype;
+  int late;              // as above
 };
 cudaError_t launch_bias_grad(const BiasGradProblem& g, cudaStream_t st);
 // Copies rows of `len` 16-bit elements, ld apart, to rows `pitch` apart (a

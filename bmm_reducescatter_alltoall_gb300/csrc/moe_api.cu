@@ -9,6 +9,9 @@ namespace {
 
 using namespace bra;
 
+// Rows of a call: a tile's last row index stays in 32 bits.
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - (int64_t(1) << 16);
+
 bool off_by(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
 
 bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
@@ -29,7 +32,7 @@ struct GroupedSizes {
 int check_sizes(const bra_grouped_args* a, GroupedSizes* s) {
   if (!a) return BRA_ERR_NULLPTR;
   constexpr int64_t kWide = int64_t(1) << 24;
-  if (a->rows < 0 || a->rows >= (int64_t(1) << 31) || a->groups < 1 ||
+  if (a->rows < 0 || a->rows > kMaxRows || a->groups < 1 ||
       a->groups > BRA_MAX_GROUPS || a->in < 1 || a->in > kWide || a->out < 1 || a->out > kWide)
     return BRA_ERR_INVALID;
   if (a->dtype != BRA_FP16 && a->dtype != BRA_BF16) return BRA_ERR_INVALID;
@@ -105,9 +108,9 @@ Copy weight_copy(const void* w, const bra_grouped_args* a, const GroupedSizes& s
 
 int check_mx(const bra_mx_args* a) {
   if (!a) return BRA_ERR_NULLPTR;
-  if (a->rows < 0 || a->rows >= (int64_t(1) << 31) || a->k < 1 || a->k > (int64_t(1) << 24) ||
+  if (a->rows < 0 || a->rows > kMaxRows || a->k < 1 || a->k > (int64_t(1) << 24) ||
       a->groups < 1 || a->groups > BRA_MAX_GROUPS || a->rows_per_group < 0 ||
-      a->rows_per_group >= (int64_t(1) << 31) || a->reserved != 0)
+      a->rows_per_group > kMaxRows || a->reserved != 0)
     return BRA_ERR_INVALID;
   if (a->rows_per_group > 0 && a->rows != a->groups * a->rows_per_group) return BRA_ERR_INVALID;
   if (a->x_pitch != 0 && (a->x_pitch < a->k || a->x_pitch > (int64_t(1) << 36)))

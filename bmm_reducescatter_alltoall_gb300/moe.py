@@ -1,12 +1,19 @@
-"""Ragged expert operators: products grouped by expert, and their gradients.
+"""Ragged expert operators: products grouped by expert with their gradients,
+the same on 4-bit weights, the router, and the moves of token rows.
 
 Bindings of include/bra_moe.h in the manner of the package's other calls: each
 function has a `_plan` form that checks its tensors once and returns a Plan,
 and the one-shot form is that plan run once.  Rows are sorted by expert and
 `counts` (CUDA int64, one per expert) says how many each has.
+
+Streams: a one-shot call given a `stream` allocates what it allocates (outputs
+and scratch memory) for that stream.  A plan's buffers belong to the stream
+that was current when it was made; run on another one, the two have to be
+ordered, as with any tensor.  Ordering the inputs is the caller's part.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -86,6 +93,16 @@ def declare(lib) -> None:
     for fn in (lib.moe_route, lib.moe_route_grad, lib.moe_dispatch, lib.moe_dispatch_grad,
                lib.moe_combine, lib.moe_combine_grad):
         fn.restype = c_int
+
+
+def _on(stream):
+    """A context in which `stream` (torch's, a raw handle or None) is current."""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _bra._torch()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t) -> Optional[int]:
@@ -231,8 +248,9 @@ def grouped_matmul(x, weight, counts, bias=None, out=None, transpose_weight: boo
     allocator, only when needed).  status: optional CUDA int32, ERR_INVALID
     when the counts were refused (nothing is written then).  Returns out
     (R, N), allocated when None.  Asynchronous on `stream`."""
-    return grouped_matmul_plan(x, weight, counts, bias, out, transpose_weight, workspace,
-                               status).run(stream)
+    with _on(stream):
+        return grouped_matmul_plan(x, weight, counts, bias, out, transpose_weight, workspace,
+                                   status).run()
 
 
 def grouped_matmul_grad_plan(dy, x, weight, counts, bias=None, dx=None, dweight=None, dbias=None,
@@ -295,8 +313,9 @@ def grouped_matmul_grad(dy, x, weight, counts, bias=None, dx=None, dweight=None,
     (neither `bias` nor an output `dbias` given).  Experts without rows get
     zero; rows of dx after the counts' sum are not written.  Results do not
     change from run to run."""
-    return grouped_matmul_grad_plan(dy, x, weight, counts, bias, dx, dweight, dbias, want,
-                                    transpose_weight, workspace, status).run(stream)
+    with _on(stream):
+        return grouped_matmul_grad_plan(dy, x, weight, counts, bias, dx, dweight, dbias, want,
+                                        transpose_weight, workspace, status).run()
 
 
 class MxTensor:
@@ -374,7 +393,8 @@ def mxfp4_quantize(x, counts=None, out: Optional[MxTensor] = None, status=None,
     the even code.  x: (R, K) rows of any pitch, grouped by `counts` (CUDA
     int64) if given, or (E, N, K) weights.  A block with a NaN or an infinity
     becomes NaN."""
-    return mxfp4_quantize_plan(x, counts, out, status).run(stream)
+    with _on(stream):
+        return mxfp4_quantize_plan(x, counts, out, status).run()
 
 
 def mxfp4_dequantize_plan(q: MxTensor, dtype, out=None, status=None):
@@ -396,7 +416,8 @@ def mxfp4_dequantize_plan(q: MxTensor, dtype, out=None, status=None):
 
 def mxfp4_dequantize(q: MxTensor, dtype, out=None, status=None, stream=None):
     """The values of an MxTensor as fp16, bf16 or fp32 (one rounding)."""
-    return mxfp4_dequantize_plan(q, dtype, out, status).run(stream)
+    with _on(stream):
+        return mxfp4_dequantize_plan(q, dtype, out, status).run()
 
 
 def mxfp4_grouped_matmul_plan(x: MxTensor, weight: MxTensor, counts, bias=None, out=None,
@@ -439,7 +460,8 @@ def mxfp4_grouped_matmul(x: MxTensor, weight: MxTensor, counts, bias=None, out=N
     weight: (E, N, K) quantized.  Products and sums of the dequantized values
     in fp32, one rounding to dtype (bf16 by default, or fp16).  The rest as
     grouped_matmul."""
-    return mxfp4_grouped_matmul_plan(x, weight, counts, bias, out, dtype, status).run(stream)
+    with _on(stream):
+        return mxfp4_grouped_matmul_plan(x, weight, counts, bias, out, dtype, status).run()
 
 
 def _row_dtype(dt, what: str) -> int:
@@ -507,8 +529,9 @@ def moe_route(logits, k: int, renormalize: bool = True, ids=None, weights=None, 
     the row of each pair when sorted by expert, and the token of each row.  A
     token with fewer than k open experts has -1, weight 0 and slot -1 for the
     rest; rows past the last pair have token -1."""
-    return moe_route_plan(logits, k, renormalize, ids, weights, counts, slots, tokens,
-                          workspace).run(stream)
+    with _on(stream):
+        return moe_route_plan(logits, k, renormalize, ids, weights, counts, slots, tokens,
+                              workspace).run()
 
 
 def moe_route_grad_plan(dweights, logits, ids, weights, renormalize: bool = True, out=None):
@@ -534,7 +557,8 @@ def moe_route_grad_plan(dweights, logits, ids, weights, renormalize: bool = True
 def moe_route_grad(dweights, logits, ids, weights, renormalize: bool = True, out=None,
                    stream=None):
     """Gradient of the logits for the gradient of moe_route's weights."""
-    return moe_route_grad_plan(dweights, logits, ids, weights, renormalize, out).run(stream)
+    with _on(stream):
+        return moe_route_grad_plan(dweights, logits, ids, weights, renormalize, out).run()
 
 
 def _permute_args(T: int, R: int, k: int, rows, what: str) -> PermuteArgs:
@@ -561,7 +585,8 @@ def moe_dispatch_plan(x, tokens, out=None):
 
 def moe_dispatch(x, tokens, out=None, stream=None):
     """Token rows in expert order: out[r] = x[tokens[r]], zeros for -1."""
-    return moe_dispatch_plan(x, tokens, out).run(stream)
+    with _on(stream):
+        return moe_dispatch_plan(x, tokens, out).run()
 
 
 def _to_tokens_plan(rows, slots, weights, out, name: str, what: str):
@@ -588,7 +613,8 @@ def moe_dispatch_grad_plan(dxs, slots, out=None):
 
 def moe_dispatch_grad(dxs, slots, out=None, stream=None):
     """Gradient of moe_dispatch: out[t] = sum of dxs[slots[t, j]] over j."""
-    return moe_dispatch_grad_plan(dxs, slots, out).run(stream)
+    with _on(stream):
+        return moe_dispatch_grad_plan(dxs, slots, out).run()
 
 
 def moe_combine_plan(ys, slots, weights, out=None):
@@ -601,7 +627,8 @@ def moe_combine_plan(ys, slots, weights, out=None):
 def moe_combine(ys, slots, weights, out=None, stream=None):
     """Expert rows back to tokens: out[t] = sum of weights[t, j] * ys[slots[t, j]]
     over j (fp32, one rounding); slots of -1 are left out."""
-    return moe_combine_plan(ys, slots, weights, out).run(stream)
+    with _on(stream):
+        return moe_combine_plan(ys, slots, weights, out).run()
 
 
 def moe_combine_grad_plan(dy, ys, slots, weights, tokens=None, dys=None, dweights=None):
@@ -634,4 +661,5 @@ def moe_combine_grad(dy, ys, slots, weights, tokens=None, dys=None, dweights=Non
 
     tokens (of moe_route): rows without a token get zeros; without it those
     rows of dys are not written."""
-    return moe_combine_grad_plan(dy, ys, slots, weights, tokens, dys, dweights).run(stream)
+    with _on(stream):
+        return moe_combine_grad_plan(dy, ys, slots, weights, tokens, dys, dweights).run()

@@ -478,7 +478,7 @@ BRA_API int bra_l2_flush(void* buf, size_t bytes, bra_stream_t stream);
 
 /*
  * bra_fault_status -- the watchdog words of the current device: 0, or the
- * BRA_ERR_TIMEOUT code a kernel (a tensor-core fused kernel or all_to_all_v) recorded
+ * BRA_ERR_TIMEOUT code a kernel (a tensor-core kernel or all_to_all_v) recorded
  * when one of its bounded waits gave up (the kernel then stops early and its
  * output is incomplete).  The words belong to the device, not to a call:
  * every call on the device, on any stream, writes the same words, so a set

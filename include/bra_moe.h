@@ -30,7 +30,7 @@ extern "C" {
 
 /* Sizes and options of a grouped product.  Zero-initialise. */
 typedef struct {
-  int64_t rows;        /* R: rows of x, y and dy, at most 2^31 - 1            */
+  int64_t rows;        /* R: rows of x, y and dy, at most 2^31 - 2^16         */
   int64_t groups;      /* E: 1 .. BRA_MAX_GROUPS                              */
   int64_t in;          /* K: 1 .. 2^24                                        */
   int64_t out;         /* N: 1 .. 2^24                                        */
@@ -130,7 +130,7 @@ BRA_API int64_t grouped_matmul_grad_workspace_size(const void* dy, const void* x
  * scales belong to the grouping they were made with.
  */
 typedef struct {
-  int64_t rows;            /* R: 0 .. 2^31 - 1                                 */
+  int64_t rows;            /* R: 0 .. 2^31 - 2^16                              */
   int64_t k;               /* K: elements of a row, 1 .. 2^24                  */
   int64_t groups;          /* E: 1 .. BRA_MAX_GROUPS                           */
   int64_t rows_per_group;  /* groups of this many rows (R = E * that); 0: of   */

@@ -50,7 +50,7 @@ def test_grouped_struct_layout():
 
 
 @pytest.mark.parametrize("change,code", [
-    (dict(rows=-1), INVALID), (dict(rows=1 << 31), INVALID), (dict(groups=0), INVALID),
+    (dict(rows=-1), INVALID), (dict(rows=(1 << 31) - 65535), INVALID), (dict(groups=0), INVALID),
     (dict(groups=513), INVALID), (dict(in_=0), INVALID), (dict(out=0), INVALID),
     (dict(out=(1 << 24) + 1), INVALID), (dict(dtype=bra.FP32), INVALID),
     (dict(x_pitch=63), INVALID), (dict(y_pitch=71), INVALID), (dict(status=S + 1), INVALID),

@@ -77,6 +77,8 @@ KERNEL_SOURCES = {
     "route_place_kernel": "moe_route.cu",
     "route_grad_kernel": "moe_route.cu",
     "dispatch_kernel": "moe_permute.cu",
+    "list_rows_kernel": "moe_permute.cu",
+    "spread_kernel": "moe_permute.cu",
     "combine_kernel": "moe_permute.cu",
     "combine_grad_kernel": "moe_permute.cu",
 }

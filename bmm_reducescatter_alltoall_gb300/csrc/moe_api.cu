@@ -280,19 +280,29 @@ int moe_route_grad(const float* dweights, const void* logits, const int32_t* ids
   return status_of(launch_route_grad(r, (cudaStream_t)stream));
 }
 
-int moe_dispatch(const void* x, const int32_t* tokens, void* xs, const bra_permute_args* args,
-                 bra_stream_t stream) {
+int64_t moe_dispatch_workspace_size(const bra_permute_args* args) {
   const int rc = check_permute(args);
-  if (rc != BRA_OK) return rc;
+  if (rc != BRA_OK) return -rc;
+  if (!dispatch_lists(args->tokens, args->rows, args->width * element_size(args->dtype))) return 0;
+  return (args->tokens * (BRA_MAX_CHOICES + 1) * 4 + 255) / 256 * 256;
+}
+
+int moe_dispatch(const void* x, const int32_t* tokens, void* xs, void* workspace,
+                 int64_t workspace_bytes, const bra_permute_args* args, bra_stream_t stream) {
+  const int64_t need = moe_dispatch_workspace_size(args);
+  if (need < 0) return (int)-need;
   if (args->rows == 0) return BRA_OK;
-  if (!tokens || !xs || (args->tokens > 0 && !x)) return BRA_ERR_NULLPTR;
+  if (!tokens || !xs || (args->tokens > 0 && !x) || (need > 0 && !workspace))
+    return BRA_ERR_NULLPTR;
   const int64_t es = element_size(args->dtype);
-  if (off_by(x, es - 1) || off_by(xs, es - 1) || off_by(tokens, 3u)) return BRA_ERR_INVALID;
-  const Span outs[1] = {{xs, args->rows * args->width * es}};
+  if (off_by(x, es - 1) || off_by(xs, es - 1) || off_by(tokens, 3u) || off_by(workspace, 255u) ||
+      workspace_bytes < need)
+    return BRA_ERR_INVALID;
+  const Span outs[2] = {{xs, args->rows * args->width * es}, {workspace, need}};
   const Span ins[2] = {{x, args->tokens * args->width * es}, {tokens, args->rows * 4}};
-  if (any_overlap(outs, 1, ins, 2)) return BRA_ERR_INVALID;
-  return status_of(
-      launch_dispatch(permute_call(x, xs, tokens, nullptr, nullptr, args), (cudaStream_t)stream));
+  if (any_overlap(outs, 2, ins, 2)) return BRA_ERR_INVALID;
+  return status_of(launch_dispatch(permute_call(x, xs, tokens, nullptr, nullptr, args), workspace,
+                                   (cudaStream_t)stream));
 }
 
 int moe_dispatch_grad(const void* dxs, const int32_t* slots, void* dx, const bra_permute_args* args,

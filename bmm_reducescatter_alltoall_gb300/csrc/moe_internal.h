@@ -115,7 +115,9 @@ struct PermuteCall {
   int64_t T, R;
   int k, H, dtype;
 };
-cudaError_t launch_dispatch(const PermuteCall& c, cudaStream_t st);
+// With dispatch_lists, `workspace` holds T * (BRA_MAX_CHOICES + 1) int32.
+bool dispatch_lists(int64_t T, int64_t R, int64_t row_bytes);
+cudaError_t launch_dispatch(const PermuteCall& c, void* workspace, cudaStream_t st);
 cudaError_t launch_combine(const PermuteCall& c, cudaStream_t st);
 // in: dy, out: dys
 cudaError_t launch_combine_grad(const PermuteCall& c, const void* ys, float* dw, cudaStream_t st);

@@ -454,11 +454,11 @@ int rows_vec(const void* p, int E, int dtype) {
 
 }  // namespace
 
-// Tokens of a chunk: one chunk up to 64 tokens (one launch); else about 128
-// chunks, of at most 1024 tokens.
+// Tokens of a chunk: one chunk up to 64 tokens (one launch); else a chunk for
+// each of 152 SMs, of at most 1024 tokens.
 int route_chunk(int64_t T) {
   if (T <= 64) return 64;
-  const int64_t c = ((T + 127) / 128 + 31) / 32 * 32;
+  const int64_t c = ((T + 151) / 152 + 31) / 32 * 32;
   return (int)(c > 1024 ? 1024 : c);
 }
 

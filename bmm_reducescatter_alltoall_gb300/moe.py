@@ -86,7 +86,9 @@ def declare(lib) -> None:
     lib.moe_route_workspace_size.argtypes = [rp]
     lib.moe_route_workspace_size.restype = i64
     lib.moe_route_grad.argtypes = [vp, vp, vp, vp, vp, rp, vp]
-    lib.moe_dispatch.argtypes = [vp, vp, vp, pp, vp]
+    lib.moe_dispatch.argtypes = [vp, vp, vp, vp, i64, pp, vp]
+    lib.moe_dispatch_workspace_size.argtypes = [pp]
+    lib.moe_dispatch_workspace_size.restype = i64
     lib.moe_dispatch_grad.argtypes = [vp, vp, vp, pp, vp]
     lib.moe_combine.argtypes = [vp, vp, vp, vp, pp, vp]
     lib.moe_combine_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, pp, vp]
@@ -568,7 +570,7 @@ def _permute_args(T: int, R: int, k: int, rows, what: str) -> PermuteArgs:
     return a
 
 
-def moe_dispatch_plan(x, tokens, out=None):
+def moe_dispatch_plan(x, tokens, out=None, workspace="auto"):
     """moe_dispatch prepared once (see Plan); plan.run() returns out."""
     torch = _bra._torch()
     _matrix(x, "x")
@@ -579,14 +581,21 @@ def moe_dispatch_plan(x, tokens, out=None):
     _matrix(out, "out", x.dtype, (R, x.shape[1]))
     _same_device(x, tokens, out)
     a = _permute_args(x.shape[0], R, 1, x, "moe_dispatch")
-    args = (_ptr(x), _ptr(tokens), _ptr(out), ctypes.byref(a))
-    return _bra.Plan(_bra.library().moe_dispatch, args, "moe_dispatch", out, (x, tokens, a))
+    lib = _bra.library()
+    box = GroupedArgs()                                   # holds the workspace's address
+    workspace = _take_workspace(workspace, lib.moe_dispatch_workspace_size(ctypes.byref(a)),
+                                x.device, box)
+    args = (_ptr(x), _ptr(tokens), _ptr(out), box.workspace, box.workspace_bytes, ctypes.byref(a))
+    return _bra.Plan(lib.moe_dispatch, args, "moe_dispatch", out, (x, tokens, a, workspace))
 
 
-def moe_dispatch(x, tokens, out=None, stream=None):
-    """Token rows in expert order: out[r] = x[tokens[r]], zeros for -1."""
+def moe_dispatch(x, tokens, out=None, workspace="auto", stream=None):
+    """Token rows in expert order: out[r] = x[tokens[r]], zeros for -1.
+
+    workspace: scratch memory for the lists of each token's rows, used when
+    there are many ("auto": from torch's allocator)."""
     with _on(stream):
-        return moe_dispatch_plan(x, tokens, out).run()
+        return moe_dispatch_plan(x, tokens, out, workspace).run()
 
 
 def _to_tokens_plan(rows, slots, weights, out, name: str, what: str):

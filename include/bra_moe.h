@@ -246,6 +246,9 @@ typedef struct {
  * in the order of the choices, one rounding; results do not change from run
  * to run.  Entries outside their range count as -1 and are never followed.
  *   moe_dispatch       xs[r] = x[tokens[r]]; zeros for -1.  (choices unused)
+ *                      tokens may be in any order.  workspace: 256-byte
+ *                      aligned, moe_dispatch_workspace_size bytes (0 unless
+ *                      there are many long token rows with several rows each).
  *   moe_dispatch_grad  dx[t] = sum of dxs[slots[t, j]] over j, -1 left out.
  *   moe_combine        y[t] = sum of weights[t, j] * ys[slots[t, j]].
  *   moe_combine_grad   dys[slots[t, j]] = weights[t, j] * dy[t];
@@ -257,8 +260,10 @@ typedef struct {
  * element-aligned, an output overlapping an input or the other output;
  * BRA_ERR_CUDA.
  */
-BRA_API int moe_dispatch(const void* x, const int32_t* tokens, void* xs,
-                         const bra_permute_args* args, bra_stream_t stream);
+BRA_API int moe_dispatch(const void* x, const int32_t* tokens, void* xs, void* workspace,
+                         int64_t workspace_bytes, const bra_permute_args* args,
+                         bra_stream_t stream);
+BRA_API int64_t moe_dispatch_workspace_size(const bra_permute_args* args);
 BRA_API int moe_dispatch_grad(const void* dxs, const int32_t* slots, void* dx,
                               const bra_permute_args* args, bra_stream_t stream);
 BRA_API int moe_combine(const void* ys, const int32_t* slots, const float* weights, void* y,

@@ -236,6 +236,26 @@ def test_permutation_over_tokens(T, E, k, H):
     check_permute(T, E, k, H, torch.bfloat16, closed=0.3)
 
 
+@pytest.mark.parametrize("dt,H", [(torch.bfloat16, 4096), (torch.float32, 2050),
+                                  (torch.float16, 4001)])
+def test_dispatch_of_many_long_rows(dt, H):
+    """Token rows past L2, whose rows are listed first: tokens in any order, some with more rows
+    than a list holds, some without, entries out of range."""
+    T = 8000
+    g = torch.Generator(device="cuda").manual_seed(H)
+    x = torch.randn((T, H), generator=g, device="cuda").to(dt)
+    assert x.numel() * x.element_size() >= 48 << 20
+    tokens = torch.randint(-1, T, (2 * T + 777,), generator=g, device="cuda", dtype=torch.int32)
+    tokens[100:140] = 17                                  # 40 rows of one token
+    tokens[5000:5003] = torch.tensor([T, -5, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    want = torch.where(((tokens >= 0) & (tokens < T))[:, None], x[tokens.long().clamp(0, T - 1)],
+                       torch.zeros((), dtype=dt, device="cuda"))
+    plan = bra.moe_dispatch_plan(x, tokens)
+    for _ in range(2):
+        plan.result.fill_(7.0)
+        assert torch.equal(plan.run(), want)
+
+
 def test_entries_out_of_range_are_left_out():
     x = torch.randn((4, 64), device="cuda")
     tokens = torch.tensor([0, 4, -7, 3, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
@@ -327,6 +347,10 @@ def test_refused_arguments():
     ys = torch.zeros((8, 64), device="cuda")
     with pytest.raises(TypeError):
         bra.moe_dispatch(x, r["tokens"].long())
+    with pytest.raises(bra.BraError) as err:                          # needs lists
+        bra.moe_dispatch(torch.empty((8192, 4096), device="cuda"),
+                         torch.zeros(16384, dtype=torch.int32, device="cuda"), workspace=None)
+    assert err.value.code == bra.ERR_NULLPTR
     with pytest.raises(TypeError):
         bra.moe_combine(ys, r["slots"], r["weights"].half())
     with pytest.raises(ValueError):

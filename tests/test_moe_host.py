@@ -198,7 +198,7 @@ def test_route_limits_and_workspace(lib):
     size = lambda **kw: lib.moe_route_workspace_size(ctypes.byref(route(**kw)))   # noqa: E731
     assert size(tokens=0) == 0 and size(tokens=64) == 0
     assert size(tokens=65) == 256                        # three chunks of 32 tokens, 16 experts
-    assert size(tokens=65536, experts=128) == 128 * 128 * 4
+    assert size(tokens=65536, experts=128) == (147 * 128 * 4 + 255) // 256 * 256
     assert size(experts=513) == -INVALID
 
 
@@ -240,7 +240,7 @@ def test_route_refuses_pointers(lib):
 ], ids=str)
 def test_permute_refuses_sizes(lib, change):
     a = ctypes.byref(permute(**change))
-    assert lib.moe_dispatch(X, W, Y, a, None) == INVALID
+    assert lib.moe_dispatch(X, W, Y, None, 0, a, None) == INVALID
     assert lib.moe_dispatch_grad(X, W, Y, a, None) == INVALID
     assert lib.moe_combine(X, W, B, Y, a, None) == INVALID
     assert lib.moe_combine_grad(X, W, B, C, None, Y, G, a, None) == INVALID
@@ -248,7 +248,8 @@ def test_permute_refuses_sizes(lib, change):
 
 def test_permute_refuses_pointers(lib):
     a = ctypes.byref(permute())
-    calls = [(lib.moe_dispatch, [X, W, Y]), (lib.moe_dispatch_grad, [X, W, Y]),
+    dispatch = lambda x, tokens, xs, a, s: lib.moe_dispatch(x, tokens, xs, None, 0, a, s)  # noqa: E731
+    calls = [(dispatch, [X, W, Y]), (lib.moe_dispatch_grad, [X, W, Y]),
              (lib.moe_combine, [X, W, B, Y]), (lib.moe_combine_grad, [X, W, B, C, S, Y, G])]
     for fn, ok in calls:
         for i in range(len(ok)):
@@ -262,3 +263,17 @@ def test_permute_refuses_pointers(lib):
         bad[-1] = ok[0]
         assert fn(*bad, a, None) == INVALID                             # an output over an input
         assert fn(*ok, None, None) == NULLPTR
+
+
+def test_dispatch_workspace(lib):
+    size = lambda **kw: lib.moe_dispatch_workspace_size(ctypes.byref(permute(**kw)))      # noqa: E731
+    big = dict(tokens=16384, rows=131072, width=4096)
+    assert size() == 0 and size(tokens=16384, rows=16384, width=4096) == 0
+    assert size(**big) == 16384 * 17 * 4
+    assert size(tokens=-1) == -INVALID
+    a = ctypes.byref(permute(**big))
+    x, t, y, w = 1 << 34, 1 << 35, 1 << 36, 1 << 37
+    assert lib.moe_dispatch(x, t, y, None, 0, a, None) == NULLPTR
+    assert lib.moe_dispatch(x, t, y, w, 16384 * 17 * 4 - 1, a, None) == INVALID
+    assert lib.moe_dispatch(x, t, y, w + 128, 1 << 30, a, None) == INVALID
+    assert lib.moe_dispatch(x, t, y, y + 256, 1 << 30, a, None) == INVALID

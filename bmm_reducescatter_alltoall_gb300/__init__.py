@@ -1,7 +1,9 @@
 """GB300-native fused MoE BMM -> TP ReduceScatter -> bias Add -> EP AllToAll,
-all_to_all_v and its indexed form over virtual ranks on one GPU.
+all_to_all_v and its indexed form over virtual ranks on one GPU, and the ragged
+expert operators around them (moe.py).
 
-Thin Python binding over libbmmrsa2a.so (the C ABI in include/bmm_rs_a2a.h):
+Thin Python binding over libbmmrsa2a.so (the C ABI in include/bmm_rs_a2a.h and
+include/bra_moe.h):
 it checks tensors (device, dtype, contiguity), passes their data pointers and
 the current CUDA stream, and raises on a non-zero status.  Every step of the
 computation runs in the library's CUDA kernels; there is no other code path.

@@ -28,6 +28,10 @@
 //     walked largest first: a long tile begun last would be waited for alone
 //     (32 experts of 1300 to 13000 rows, K = N = 1024: 134 us in the groups'
 //     own order, 92 for equal ones).
+// With many rows the tensor cores bound it: bf16, 8 x 2048 rows, K = 2048, N =
+// 4096, 151 us forward and for the weight gradient (1820 TFLOP/s; cuBLAS's
+// batched product of equal groups 1945).  With few, the weights' bytes: 128
+// rows over 64 experts, 140 us for 949 MB, the rate of a copy.
 // Every wait is bounded (about 4 s) and reports through the fault word.
 #include <cstring>
 #include <mutex>

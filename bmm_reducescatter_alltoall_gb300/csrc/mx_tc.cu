@@ -14,7 +14,7 @@
 //   Writers and not tcgen05.cp: a copy takes its 55 cycles of the tensor pipe
 //   itself, and a 256 x 256 pair tile needs six to a K block, next to 512
 //   cycles of MMAs; 8 x 2048 rows, K = 16384, N = 4096 took 442 us with
-//   copies and 316 with stores beside the MMAs.
+//   copies and 346 (6350 TFLOP/s) with stores beside the MMAs.
 //   The writers' word to the MMA issuer carries no memory of theirs, only
 //   that their tcgen05.st have completed (tcgen05.wait::st, and the tcgen05
 //   fences on both sides of the barrier): the arrival is relaxed.  With a
@@ -24,7 +24,7 @@
 //     and CTA, 600 cycles where the MMAs take 512 (with a quarter of the MMAs
 //     left out the time hardly changed).  256 x 192 tiles, whose two
 //     accumulators fit beside the scales, need 15% more of it: 452 us against
-//     316 on the sizes above.  With one accumulator the epilogue first drains
+//     346 on the sizes above.  With one accumulator the epilogue first drains
 //     it into registers (eight warps, 128 columns each, rounded and packed),
 //     hands it back, and stores while the next tile is computed.
 //   CG = 1, BN = 128: 128 x 128 tile, two accumulators, for few rows to an

@@ -93,3 +93,40 @@ def test_one_shot_calls_on_another_stream_own_their_buffers():
     got = bra.grouped_matmul(x, w, c, stream=s.cuda_stream)     # a raw handle
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_a_training_step_in_a_graph():
+    """The step's kernels overlap each other's ends; a replay gives the bits of the step run
+    call by call, with each call waited for."""
+    w = moe_layer.init(8, 264, 96)
+    x = torch.randn((700, 264), device="cuda").bfloat16()
+    dy = torch.randn((700, 264), device="cuda").bfloat16()
+    r = bra.moe_route(x.float() @ w["router"], 2)
+    xs = bra.moe_dispatch(x, r["tokens"])
+    b = torch.randn((8, 192), device="cuda")
+    plans = [bra.grouped_matmul_plan(xs, w["up"], r["counts"], bias=b)]
+    plans += [bra.grouped_matmul_grad_plan(plans[0].result, xs, w["up"], r["counts"], bias=b)]
+    plans += [bra.moe_dispatch_grad_plan(plans[1].result["dx"], r["slots"])]
+    plans += [bra.mxfp4_quantize_plan(plans[1].result["dx"], r["counts"])]
+    flat = lambda: [plans[0].result, *plans[1].result.values(), plans[2].result,     # noqa: E731
+                    plans[3].result.codes]
+    for p in plans:
+        p.run()
+        torch.cuda.synchronize()
+    want = [t.clone() for t in flat()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for p in plans:
+            p.run()
+    for _ in range(20):
+        for t in flat():
+            t.zero_()
+        graph.replay()
+        for a, z in zip(flat(), want):
+            assert torch.equal(a, z)
+        for t in flat():
+            t.zero_()
+        for p in plans:
+            p.run()
+        for a, z in zip(flat(), want):
+            assert torch.equal(a, z)

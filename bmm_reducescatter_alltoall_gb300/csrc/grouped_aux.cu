@@ -137,6 +137,9 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const __grid_constant__ 
       if (total <= 0xffffffffll) r = (uint32_t)u / (uint32_t)chunks;
       else r = u / chunks;
       const int64_t c = u - r * chunks;
+      if (job.per_group > 0 &&
+          __ldg(reinterpret_cast<const long long*>(jobs.counts) + r / job.per_group) == 0)
+        continue;
       const uint16_t* s = src + r * ld + c * 8;
       const int n = (int)min((int64_t)8, len - c * 8);
       uint32_t w[4] = {0, 0, 0, 0};

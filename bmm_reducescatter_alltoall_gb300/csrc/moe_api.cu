@@ -68,17 +68,19 @@ Copy copy_of(const void* p, int64_t rows, int64_t n, int64_t ld) {
 }
 
 // Hands out workspace; copy() enqueues what was taken, before the products.
+// A weight's copy leaves out the experts without rows.
 struct Workspace {
   uint8_t* at;
   PackJobs jobs = {};
-  const void* take(const void* src, const Copy& c) {
+  const void* take(const void* src, const Copy& c, int64_t per_group = 0) {
     if (!c.need) return src;
     void* dst = at;
     at += c.bytes;
-    jobs.job[jobs.n++] = {src, dst, c.ld, c.pitch, c.rows, c.n};
+    jobs.job[jobs.n++] = {src, dst, c.ld, c.pitch, c.rows, c.n, per_group};
     return dst;
   }
-  int copy(cudaStream_t st) {
+  int copy(const int64_t* counts, cudaStream_t st) {
+    jobs.counts = counts;
     return launch_pack_rows(jobs, st) == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;
   }
 };
@@ -451,8 +453,8 @@ int grouped_matmul(const void* x, const void* weight, const void* bias, const in
   GroupedProblem g;
   std::memset(&g, 0, sizeof(g));
   g.x = ws.take(x, cx);
-  g.w = ws.take(weight, cw);
-  if ((rc = ws.copy(st)) != BRA_OK) return rc;
+  g.w = ws.take(weight, cw, cw.rows / s.E);
+  if ((rc = ws.copy(counts, st)) != BRA_OK) return rc;
   g.bias = bias;
   g.y = y;
   g.counts = counts;
@@ -521,9 +523,9 @@ int grouped_matmul_grad(const void* dy, const void* x, const void* weight, const
   g.E = (int)s.E;
   g.dtype = args->dtype;
   const void* d = dx || dweight ? ws.take(dy, cd) : dy;
-  const void* w = dx ? ws.take(weight, cw) : weight;
+  const void* w = dx ? ws.take(weight, cw, cw.rows / s.E) : weight;
   const void* xs = dweight ? ws.take(x, cx) : x;
-  if ((rc = ws.copy(st)) != BRA_OK) return rc;
+  if ((rc = ws.copy(counts, st)) != BRA_OK) return rc;
   if (dx) {
     // dx = dy W^T: the contraction runs over N, the weight's layout as stored
     // is the other one seen from here

@@ -47,9 +47,11 @@ struct PackJob {
   const void* src;
   void* dst;
   int64_t ld, pitch, rows, len;
+  int64_t per_group;       // 0, or: rows of a group, left out where its count is 0
 };
 struct PackJobs {
   PackJob job[3];
+  const int64_t* counts;
   int n;
 };
 cudaError_t launch_pack_rows(const PackJobs& jobs, cudaStream_t st);

@@ -8,7 +8,8 @@
 //   row of (t, j) = rows of lower experts + earlier tokens with this expert
 //
 // A group of L lanes takes a token, V = 8 or 16 consecutive logits a lane
-// (L = 4 to 32 by E).  Each lane sorts its own once; a choice is then the
+// (L = 4 to 32 by E).  Each lane sorts its own once, by eights (sixteen at once
+// went to local memory: 70 us for 11000 tokens of 280); a choice is then the
 // largest of the lanes' heads, found in log2(L) exchanges, and the lane that
 // has it (the lowest of equals: lanes hold rising indices) drops its head.
 // Tokens are dealt to CTAs in chunks.  In a chunk each expert has a bit per
@@ -67,26 +68,21 @@ __device__ __forceinline__ float group_sum(float v, int L) {
   return v;
 }
 
-// Sorts V (key, index) pairs, largest key first, equal keys by index: Batcher's
-// odd-even merge sort, all places known when compiled.
-template <int V>
-__device__ __forceinline__ void sort_lane(uint32_t (&key)[V], int (&idx)[V]) {
-#pragma unroll
-  for (int p = 1; p < V; p *= 2)
-#pragma unroll
-    for (int q = p; q >= 1; q /= 2)
-#pragma unroll
-      for (int j = q % p; j + q < V; j += 2 * q)
-#pragma unroll
-        for (int i = 0; i < q; ++i) {
-          const int a = i + j, b = i + j + q;
-          if (b < V && a / (2 * p) == b / (2 * p)) {
-            const bool swap = key[b] > key[a] || (key[b] == key[a] && idx[b] < idx[a]);
-            const uint32_t ka = swap ? key[b] : key[a], kb = swap ? key[a] : key[b];
-            const int ia = swap ? idx[b] : idx[a], ib = swap ? idx[a] : idx[b];
-            key[a] = ka, key[b] = kb, idx[a] = ia, idx[b] = ib;
-          }
-        }
+// Sorts eight (key, index) pairs, largest key first, equal keys by index:
+// Batcher's odd-even merge sort, 19 exchanges.
+__device__ __forceinline__ void sort_eight(uint32_t (&key)[8], int (&idx)[8]) {
+  auto put = [&](int a, int b) {
+    const bool swap = key[b] > key[a] || (key[b] == key[a] && idx[b] < idx[a]);
+    const uint32_t ka = swap ? key[b] : key[a], kb = swap ? key[a] : key[b];
+    const int ia = swap ? idx[b] : idx[a], ib = swap ? idx[a] : idx[b];
+    key[a] = ka, key[b] = kb, idx[a] = ia, idx[b] = ib;
+  };
+  put(0, 1), put(2, 3), put(4, 5), put(6, 7);
+  put(0, 2), put(1, 3), put(4, 6), put(5, 7);
+  put(1, 2), put(5, 6);
+  put(0, 4), put(1, 5), put(2, 6), put(3, 7);
+  put(2, 4), put(3, 5);
+  put(1, 2), put(3, 4), put(5, 6);
 }
 
 // The experts of one token to each group of L lanes (t < 0: none); lane l of
@@ -99,32 +95,36 @@ __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, ui
   const int gl = lane % L;
   const uint32_t group = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
   const T* row = static_cast<const T*>(p.logits) + (int64_t)t * p.E;
-  uint32_t key[V];
-  int idx[V];
+  // lists of eight, so that sorting stays short: the lower indices first
+  constexpr int NL = V / 8;
+  uint32_t key[NL][8], order[NL];               // order: sorted places, four bits each
 #pragma unroll
-  for (int i = 0; i < V; i += 4) {
-    const int at = gl * V + i;
-    T raw[4];
-    if (t >= 0 && p.vec && at + 4 <= p.E) {
-      if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<uint4*>(raw) = __ldg(reinterpret_cast<const uint4*>(row + at));
-      else
-        *reinterpret_cast<uint2*>(raw) = __ldg(reinterpret_cast<const uint2*>(row + at));
-    } else {
+  for (int l = 0; l < NL; ++l) {
+    int idx[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) raw[c] = t >= 0 && at + c < p.E ? row[at + c] : T(-INFINITY);
+    for (int i = 0; i < 8; i += 4) {
+      const int at = gl * V + l * 8 + i;
+      T raw[4];
+      if (t >= 0 && p.vec && at + 4 <= p.E) {
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<uint4*>(raw) = __ldg(reinterpret_cast<const uint4*>(row + at));
+        else
+          *reinterpret_cast<uint2*>(raw) = __ldg(reinterpret_cast<const uint2*>(row + at));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) raw[c] = t >= 0 && at + c < p.E ? row[at + c] : T(-INFINITY);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        key[l][i + c] = key_of(logit(&raw[c]));
+        idx[i + c] = i + c;
+      }
     }
+    sort_eight(key[l], idx);
+    order[l] = 0;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      key[i + c] = key_of(logit(&raw[c]));
-      idx[i + c] = i + c;
-    }
+    for (int i = 0; i < 8; ++i) order[l] |= (uint32_t)idx[i] << (4 * i);
   }
-  sort_lane<V>(key, idx);
-  using Order = std::conditional_t<V == 8, uint32_t, uint64_t>;
-  Order order = 0;                              // the sorted places, four bits each
-#pragma unroll
-  for (int i = 0; i < V; ++i) order |= (Order)idx[i] << (4 * i);
   uint32_t my_key[OWN], top = 0u;
   int my_id[OWN];
 #pragma unroll
@@ -132,23 +132,33 @@ __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, ui
     my_key[o] = 0u;
     my_id[o] = -1;
     for (int j = o * L; j < min(p.k, (o + 1) * L); ++j) {
-      uint32_t most = key[0];
+      uint32_t head = key[0][0];
+      int from = 0, place = (int)(order[0] & 15u);
+      if (NL == 2 && key[NL - 1][0] > head) {
+        head = key[NL - 1][0];
+        from = 1;
+        place = 8 + (int)(order[NL - 1] & 15u);
+      }
+      uint32_t most = head;
 #pragma unroll
       for (int d = L / 2; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-      const uint32_t has = __ballot_sync(0xffffffffu, key[0] == most) & group;
+      const uint32_t has = __ballot_sync(0xffffffffu, head == most) & group;
       const int win = __ffs(has) - 1;
-      const int at = __shfl_sync(0xffffffffu, gl * V + (int)(order & 15u), win);
+      const int at = __shfl_sync(0xffffffffu, gl * V + place, win);
       if (j == 0) top = most;
       if (gl == j - o * L && most) {
         my_key[o] = most;
         my_id[o] = at;
       }
       // the winner drops its head (with most = 0 there is nothing to drop)
-      const bool drop = lane == win;
 #pragma unroll
-      for (int i = 0; i + 1 < V; ++i) key[i] = drop ? key[i + 1] : key[i];
-      key[V - 1] = drop ? 0u : key[V - 1];
-      order = drop ? order >> 4 : order;
+      for (int l = 0; l < NL; ++l) {
+        const bool drop = lane == win && from == l;
+#pragma unroll
+        for (int i = 0; i + 1 < 8; ++i) key[l][i] = drop ? key[l][i + 1] : key[l][i];
+        key[l][7] = drop ? 0u : key[l][7];
+        order[l] = drop ? order[l] >> 4 : order[l];
+      }
     }
   }
   const float m = value_of(top);
@@ -162,7 +172,7 @@ __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, ui
     // all open logits: the ones left, and the chosen
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (key[i]) s += expf(value_of(key[i]) - m);
+      if (key[i / 8][i % 8]) s += expf(value_of(key[i / 8][i % 8]) - m);
   }
   s = group_sum(s, L);
   const int64_t out = (int64_t)t * p.k;
@@ -181,33 +191,31 @@ __device__ __forceinline__ void clear_bits(uint32_t* bits, int n) {
 }
 
 // Rows before each expert's in this chunk: base[e], from the counts of the
-// chunks before (before[e]) and of all chunks (total[e]).  Every thread.
+// chunks before (before[e]) and of all chunks (total[e]).  Every thread; ends
+// with a barrier.
 __device__ __forceinline__ void scan_experts(const RouteParams& p, const int* total,
                                              const int* before, int* base, int* used) {
-  // one warp: 16 experts a lane at most, in order
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x, per = (p.E + 31) / 32;
-    int s = 0;
-    for (int i = 0; i < per; ++i) {
-      const int e = lane * per + i;
-      if (e < p.E) s += total[e];
-    }
-    int inc = s;
+  __shared__ int sums[kMaxGroups / 32];
+  const int e = threadIdx.x, lane = e & 31;
+  int n = 0, inc = 0;
+  if (e < kMaxGroups) {
+    n = e < p.E ? total[e] : 0;
+    inc = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int a = __shfl_up_sync(0xffffffffu, inc, d);
       if (lane >= d) inc += a;
     }
-    int at = inc - s;
-    for (int i = 0; i < per; ++i) {
-      const int e = lane * per + i;
-      if (e < p.E) {
-        base[e] = at + before[e];
-        at += total[e];
-      }
-    }
-    if (lane == 31) *used = inc;
+    if (lane == 31) sums[e >> 5] = inc;
   }
+  __syncthreads();
+  if (e < kMaxGroups) {
+    int at = inc - n;
+    for (int w = 0; w < (e >> 5); ++w) at += sums[w];
+    if (e < p.E) base[e] = at + before[e];
+    if (e == kMaxGroups - 1) *used = at + n;
+  }
+  __syncthreads();
 }
 
 // This chunk's share of the rows that no pair has.
@@ -252,7 +260,6 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParam
   if (p.chunks == 1) {
     __syncthreads();
     scan_experts(p, total, zero, base, &used);
-    __syncthreads();
     mark_unused(p, 0, used);
   }
   for (int i = threadIdx.x; i < n * p.k; i += kThreads) {
@@ -311,7 +318,6 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams
   scan_experts(p, total, before, base, &used);
   if (c == 0)
     for (int i = threadIdx.x; i < p.E; i += kThreads) p.counts[i] = total[i];
-  __syncthreads();
   auto put = [&](int i, int e1, int at) {
     if (e1 >= 0) {
       const int slot = at + base[e1];

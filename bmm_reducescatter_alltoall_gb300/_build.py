@@ -68,6 +68,7 @@ KERNEL_SOURCES = {
     "mma_probe_kernel": "mma_probe.cu",
     "gather_probe_kernel": "gather_probe.cu",
     "grouped_kernel": "grouped_tc.cu",
+    "grouped_split_kernel": "grouped_split.cu",
     "bias_grad_kernel": "grouped_aux.cu",
     "pack_rows_kernel": "grouped_aux.cu",
     "quantize_kernel": "mx_quant.cu",

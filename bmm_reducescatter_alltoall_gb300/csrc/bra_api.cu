@@ -609,7 +609,7 @@ int bra_l2_flush(void* buf, size_t bytes, bra_stream_t stream) {
 
 int bra_fault_status(int32_t* code, int clear) {
   if (!code) return BRA_ERR_NULLPTR;
-  int32_t a = 0, b = 0, c = 0, d = 0, g = 0, h = 0, k = 0;
+  int32_t a = 0, b = 0, c = 0, d = 0, g = 0, h = 0, k = 0, l = 0;
   if (bra::read_fault_word(&a, clear) != cudaSuccess) return BRA_ERR_CUDA;
   if (bra::read_fault_word2(&c, clear) != cudaSuccess) return BRA_ERR_CUDA;
   if (bra::read_fault_word3(&d, clear) != cudaSuccess) return BRA_ERR_CUDA;
@@ -617,7 +617,8 @@ int bra_fault_status(int32_t* code, int clear) {
   if (bra::read_a2av_fault_word(&b, clear) != cudaSuccess) return BRA_ERR_CUDA;
   if (bra::read_grouped_fault_word(&h, clear) != cudaSuccess) return BRA_ERR_CUDA;
   if (bra::read_mx_fault_word(&k, clear) != cudaSuccess) return BRA_ERR_CUDA;
-  *code = a ? a : c ? c : d ? d : g ? g : h ? h : k ? k : b;
+  if (bra::read_split_fault_word(&l, clear) != cudaSuccess) return BRA_ERR_CUDA;
+  *code = a ? a : c ? c : d ? d : g ? g : h ? h : k ? k : l ? l : b;
   return BRA_OK;
 }
 

@@ -551,6 +551,9 @@ cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st) {
   const int64_t avg = g.R / g.E, groups = g.R < g.E ? g.R : g.E;
   const int64_t nt = (g.N + 255) / 256;
   if (avg >= 128 && (2 * (g.R / 256) + groups) * nt >= 2 * 304) return launch_t<2, 256, false>(g, st);
+  int64_t tiles = 0;
+  const int split = grouped_split(g, false, &tiles);
+  if (split > 1) return launch_grouped_split(g, false, split, tiles, st);
   // One CTA a tile.  256 columns, unless that leaves SMs without a tile (128
   // rows x 8, 1024, 1024: 10.0 us with 256, 8.9 with 128); with few rows to
   // an expert the weights' bytes bound the call, and narrower tiles still
@@ -562,6 +565,9 @@ cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st) {
 }
 
 cudaError_t launch_grouped_wgrad(const GroupedProblem& g, cudaStream_t st) {
+  int64_t tiles = 0;
+  const int split = grouped_split(g, true, &tiles);
+  if (split > 1) return launch_grouped_split(g, true, split, tiles, st);
   if (g.R / g.E >= 1024 && g.K > 128 && g.N > 128) return launch_t<2, 256, true>(g, st);
   return g.N > 128 ? launch_t<1, 256, true>(g, st) : launch_t<1, 128, true>(g, st);
 }

@@ -30,6 +30,12 @@ struct GroupedProblem {
 // multiple of 8 elements.  cudaErrorInvalidValue if a map cannot be encoded.
 cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st);
 cudaError_t launch_grouped_wgrad(const GroupedProblem& g, cudaStream_t st);
+// The same with each output tile's contraction split over a cluster: by how
+// much (1: not at all), the most tiles there can be, and the launch.
+int grouped_split(const GroupedProblem& g, bool wgrad, int64_t* tiles);
+cudaError_t launch_grouped_split(const GroupedProblem& g, bool wgrad, int split, int64_t tiles,
+                                 cudaStream_t st);
+cudaError_t read_split_fault_word(int32_t* code, int clear);
 // db_e = the sum of the rows of dy_e, in fp16 (FP16) or fp32 (BF16).
 struct BiasGradProblem {
   const void* dy;

@@ -126,6 +126,29 @@ def test_gradients_over_group_sizes(counts, K, N, wt, dt):
     check_grad(counts, K, N, dt, wt)
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("counts,K,N,wt", [
+    ([1, 0, 2], 4096, 64, False), ([1], 2048, 200, True), ([5, 90], 1032, 264, False),
+    ([3], 4090, 33, True), ([300], 2000, 130, False),
+], ids=str)
+def test_forward_with_the_contraction_split(counts, K, N, wt, dt):
+    """Few tiles, long sums: a cluster shares each tile."""
+    check_forward(counts, K, N, dt, wt, bias=True)
+    check_forward(counts, K, N, dt, wt, bias=False)
+    check_grad(counts, K, N, dt, wt)
+
+
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("counts,K,N,wt", [
+    ([3000], 64, 64, False), ([2049, 0, 1, 4000], 101, 64, True), ([700, 900], 200, 136, False),
+    ([513, 511], 129, 257, True), ([0, 9000, 0], 8, 8, False), ([1024], 40, 33, False),
+], ids=str)
+def test_gradients_with_the_rows_split(counts, K, N, wt, dt):
+    """Few tiles, many rows: a cluster shares each tile of the weight's gradient."""
+    check_grad(counts, K, N, dt, wt)
+    check_forward(counts, K, N, dt, wt, bias=True)
+
+
 @pytest.mark.parametrize("sizes", [[1], [15], [16], [17], [63], [64], [65], [0], [128]], ids=str)
 def test_weight_gradient_at_the_ends_of_a_row_block(sizes):
     for K, N in ((64, 72), (264, 264)):

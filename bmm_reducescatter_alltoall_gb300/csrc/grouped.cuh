@@ -144,36 +144,61 @@ __device__ __forceinline__ void pack_segment(uint32_t (&v)[64], uint32_t (&o)[32
     o[k] = zero ? 0u : Out<T>::pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
 }
 
+// What a lane keeps between the segments of its row when rows are not 16-byte
+// aligned: the last elements, which share a 16-byte chunk with the next ones.
+struct Carry {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+};
+
 // One warp writes a 64-column segment of its 32 rows (lane = row, packed
 // pairs in o) to rows y0, y0 + ldy, ... of which `valid` (1 .. 32) exist, at
-// columns nc .. below N.  `aligned`: every row starts on a 16-byte boundary
-// and N % 8 == 0.  between() runs after the segment is staged.
+// columns nc .. below N (nc < N).  `aligned`: every row starts on a 16-byte
+// boundary and N % 8 == 0.  Otherwise a row's segments go out in order, from
+// the one marked `first` to the one marked `last`: each lane shifts its
+// segment to the row's place in 16-byte chunks, whole chunks are stored as
+// vectors, and the elements past the last whole one are carried to the next
+// segment, so that only a run's two ends are stored in smaller pieces.  (With
+// both ends of every segment stored so, a 128 x 256 tile of odd rows took 5 us
+// to store: 4000 rows x 2257 gradient, 161 us.)  between() runs after the
+// segment is staged.
 template <typename T, typename Between>
-__device__ __forceinline__ void put_segment(const uint32_t (&o)[32], T* y0, int64_t ldy, int valid,
-                                            int nc, int N, uint32_t seg, bool aligned, int lane,
+__device__ __forceinline__ void put_segment(const uint32_t (&o)[32], Carry& carry, bool first,
+                                            bool last, T* y0, int64_t ldy, int valid, int nc, int N,
+                                            uint32_t seg, bool aligned, int lane,
                                             Between&& between) {
   const uint32_t my = seg + (uint32_t)lane * kSegStride;
-  const int cols = min(64, N - nc);          // <= 0: past the matrix
+  const int cols = min(64, N - nc);
   if (aligned) {
 #pragma unroll
     for (int g = 0; g < 8; ++g)
       sts128(my + g * 16, make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]));
   } else {
-    // the segment shifted to its destination's place in a 16-byte chunk
+    // element shift d = 4 b2 + 2 b1 + b0: by one half word, one word, two words
     const uint32_t d = (uint32_t)(reinterpret_cast<uintptr_t>(y0 + lane * ldy + nc) & 15u) >> 1;
-    const uint32_t at = my + (d >> 1) * 4;
+    uint32_t z[36];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const uint32_t w = (d & 1) ? __funnelshift_l(k ? o[k - 1] : 0u, o[k], 16) : o[k];
-      asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + k * 4), "r"(w) : "memory");
+    for (int k = 0; k < 32; ++k)
+      z[k] = (d & 1) ? __funnelshift_l(k ? o[k - 1] : 0u, o[k], 16) : o[k];
+    z[32] = (d & 1) ? o[31] >> 16 : 0u;
+    z[33] = z[34] = z[35] = 0u;
+#pragma unroll
+    for (int k = 33; k >= 0; --k) z[k] = (d & 2) ? (k >= 1 ? z[k - 1] : 0u) : z[k];
+#pragma unroll
+    for (int k = 35; k >= 0; --k) z[k] = (d & 4) ? (k >= 2 ? z[k - 2] : 0u) : z[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      z[k] |= carry.w[k];
+      carry.w[k] = z[32 + k];
     }
-    if (d & 1) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 128), "r"(o[31] >> 16) : "memory");
+#pragma unroll
+    for (int g = 0; g < 9; ++g)
+      sts128(my + g * 16, make_uint4(z[4 * g], z[4 * g + 1], z[4 * g + 2], z[4 * g + 3]));
   }
   between();
   __syncwarp();
+  // 8 lanes to a row's 128 bytes, 4 rows an instruction
+  const int c8 = (lane & 7) * 8, r0 = lane >> 3;
   if (aligned) {
-    // 8 lanes to a row's 128 bytes, 4 rows an instruction
-    const int c8 = (lane & 7) * 8, r0 = lane >> 3;
     if (c8 < cols) {
       uint4 w[8];
 #pragma unroll
@@ -183,20 +208,17 @@ __device__ __forceinline__ void put_segment(const uint32_t (&o)[32], T* y0, int6
         if (4 * q + r0 < valid)
           *reinterpret_cast<uint4*>(y0 + (4 * q + r0) * ldy + nc + c8) = w[q];
     }
-  } else if (cols > 0) {
-    // The run of a row lies at [d, d + cols) of its shifted segment.  Whole
-    // 16-byte chunks first, as above; then each lane its own row's partial
-    // chunks at the two ends, in aligned pieces of 8, 4 and 2 bytes.
-    const int c8 = (lane & 7) * 8, r0 = lane >> 3;
+  } else {
+    // the run lies at [d, d + cols) of the segment, after d carried elements
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const int r = 4 * q + r0;
       T* dst = y0 + r * ldy + nc;
       const int d = (int)((reinterpret_cast<uintptr_t>(dst) & 15u) >> 1);
-      if (r < valid && c8 >= d && c8 + 8 <= d + cols)
+      if (r < valid && c8 + 8 <= d + cols && (c8 >= d || !first))
         *reinterpret_cast<uint4*>(dst + (c8 - d)) = lds128e(seg + (uint32_t)r * kSegStride + c8 * 2);
     }
-    if (lane < valid) {
+    if ((first || last) && lane < valid) {
       T* dst = y0 + lane * ldy + nc;
       const int d = (int)((reinterpret_cast<uintptr_t>(dst) & 15u) >> 1), end = d + cols;
       uint16_t* out = reinterpret_cast<uint16_t*>(dst) - d;        // by place in the segment
@@ -218,7 +240,7 @@ __device__ __forceinline__ void put_segment(const uint32_t (&o)[32], T* y0, int6
                      : "memory");
         *reinterpret_cast<uint2*>(out + i) = w;
       };
-      if (d > 0) {
+      if (first && d > 0) {
         const int stop = min(8, end);
         int i = d;
         if ((i & 1) && i < stop) put2(i++);
@@ -226,9 +248,9 @@ __device__ __forceinline__ void put_segment(const uint32_t (&o)[32], T* y0, int6
         if ((i & 4) && i + 4 <= stop) put8(i), i += 4;
         for (; i < stop; ++i) put2(i);                             // a run within one chunk
       }
-      const int last = end & ~7;
-      if ((end & 7) && (last > 0 || d == 0)) {
-        int i = last;
+      const int from = end & ~7;
+      if (last && (end & 7) && (from > 0 || !first || d == 0)) {
+        int i = from;
         if (end & 4) put8(i), i += 4;
         if (end & 2) put4(i), i += 2;
         if (end & 1) put2(i);
@@ -249,14 +271,17 @@ __device__ __forceinline__ void store_rows(uint32_t t_base, T* y0, int64_t ldy, 
   uint32_t v[64];
   tmem_ld32(t_base, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
   tmem_ld32(t_base + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+  const int segs = min(BN / 64, (N - n0 + 63) / 64);        // the others lie past the matrix
+  Carry carry;
 #pragma unroll 1
-  for (int ch = 0; ch < BN / 64; ++ch) {
+  for (int ch = 0; ch < segs; ++ch) {
     tmem_ld_wait();
-    if (ch + 1 == BN / 64) tmem_done();
+    if (ch + 1 == segs) tmem_done();
     uint32_t o[32];
     pack_segment<T>(v, o, bias_s ? bias_s + ch * 256 : 0u, zero);
-    put_segment<T>(o, y0, ldy, valid, n0 + ch * 64, N, seg, aligned, lane, [&] {
-      if (ch + 1 < BN / 64) {
+    put_segment<T>(o, carry, ch == 0, ch + 1 == segs, y0, ldy, valid, n0 + ch * 64, N, seg, aligned,
+                   lane, [&] {
+      if (ch + 1 < segs) {
         tmem_ld32(t_base + (ch + 1) * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
         tmem_ld32(t_base + (ch + 1) * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
       }

@@ -11,8 +11,9 @@ using namespace grp;
 
 // --------------------------------------------------------------------------
 // dbias: column sums of each group's rows.  A unit is 64 columns of one
-// group; a thread sums 8 columns of every 64th row in fp32 and the CTA adds
-// its 64 partial rows, always in the same order: no atomics.  With few units a
+// group; a thread sums 8 columns of every 64th row (rows without 16-byte
+// alignment: one column of every 8th) in fp32 and the CTA adds its partial
+// rows, always in the same order: no atomics.  With few units a
 // cluster of 8 CTAs splits a unit's rows and its first CTA adds their sums.
 // Memory bound: dy is read once (16384 x 4096, 8 groups: 27 us, 4.9 TB/s).
 // --------------------------------------------------------------------------
@@ -44,10 +45,9 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
   const int64_t rows = r1 - r0;
   const int64_t a = r0 + rows * rank / SPLIT, b = r0 + rows * (rank + 1) / SPLIT;
   const int c = (tid & 7) * 8, rl = tid >> 3;
-  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const int n = min(8, N - n0 - c);
-  if (vec && n == 8) {
+  if (vec && n0 + 64 <= N) {
     constexpr int U = 8;                       // rows in flight
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const T* p = dy + n0 + c;
     int64_t r = a + rl;
     for (; r + (U - 1) * kBgRows < b; r += U * kBgRows) {
@@ -68,22 +68,25 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] += static_cast<float>(h[i]);
     }
-  } else {
-    for (int64_t r = a + rl; r < b; r += kBgRows)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) s[i] += static_cast<float>(dy[r * ld + n0 + c + i]);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) part[rl][c + i] = s[i];
-  __syncthreads();
-  // eight threads to a column, then their sums
-  {
+    for (int i = 0; i < 8; ++i) part[rl][c + i] = s[i];
+    __syncthreads();
+    // eight threads to a column, then their sums
     const int col = tid & 63, q = tid >> 6;
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < kBgRows / 8; ++i) t += part[q * (kBgRows / 8) + i][col];
     __syncthreads();
+    part[q][col] = t;
+  } else {
+    // rows of any alignment, or the last columns: a column to a thread
+    const int col = tid & 63, q = tid >> 6;
+    float t = 0.f;
+    if (n0 + col < N) {
+      const T* p = dy + n0 + col;
+#pragma unroll 8
+      for (int64_t r = a + q; r < b; r += 8) t += static_cast<float>(p[r * ld]);
+    }
     part[q][col] = t;
   }
   __syncthreads();

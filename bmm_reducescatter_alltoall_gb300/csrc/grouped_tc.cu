@@ -534,34 +534,44 @@ cudaError_t launch_t(const GroupedProblem& g, cudaStream_t st) {
 
 }  // namespace
 
-// The CTA pair moves a third less through shared memory per product, but has
-// half as many, twice as large tiles.  bf16, pair against one CTA, us (rows an
-// expert x experts, K, N):
-//   forward                           wgrad
-//   128 x  8, 1024, 1024  11 / 10     128 x 64, 2048, 4096  310 / 222
-//   256 x  8, 2048, 4096  38 / 36     256 x 64, 4096, 2048  374 / 324
-//   512 x 16, 1024, 1024  22 / 17     512 x 64, 2048, 4096  586 / 547
-//   128 x 64, 2048, 4096 159 / 171   1024 x 64, 2048, 4096  832 / 839
-//   512 x 64, 2048, 4096 434 / 483   1024 x 32, 1024, 1024   63 /  66
-//  2048 x  8, 2048, 4096 163 / 177   2048 x 64, 2048, 4096 1407 / 1511
-// So forward takes the pair from 128 rows an expert and four waves of tiles
-// on, the weight gradient (whose K loop is the rows) from 1024 rows on.
+// Tile shape, forward.  What feeds a tile's K block from L2 bounds it, about
+// 58 bytes a clock and SM: 560 cycles for a pair's 256 x 256 tile (32 KiB a
+// CTA), 850 for one CTA's 128 x 256 (48 KiB), 565 for its 128 x 128; the pair
+// starts some 4 us later.  The waves of tiles over the SMs then decide.
+// Measured, bf16, pair / 256 / 128 columns, us (rows an expert x experts, K, N):
+//   128 x  8, 1024, 1024   11 /  10 /  9      512 x  8, 2048, 4096   59 /  59 /  -
+//   256 x  8, 2048, 4096   38 /  36 / 43      128 x 64, 2048, 4096  159 / 171 / 189
+//  2048 x  4,  256,  512    8 /   7 /  7     1024 x 32, 1024, 1024   61 /  71 /  -
+//   620 x 17, 3176,  296    - /  61 / 44     2048 x  8, 2048, 4096  163 / 177 /  -
+//
+// The weight gradient's K loop is the rows; with few the stores of its large
+// output bound it, and twice as many CTAs store more at once.  Pair / one CTA:
+//   128 x 64, 2048, 4096  310 / 222          1024 x 64, 2048, 4096  832 / 839
+//   512 x 64, 2048, 4096  586 / 547          2048 x 64, 2048, 4096 1407 / 1511
+// It takes the pair from 1024 rows an expert on.
 cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st) {
-  // rows to an expert on average, and the most experts that can have rows
-  const int64_t avg = g.R / g.E, groups = g.R < g.E ? g.R : g.E;
-  const int64_t nt = (g.N + 255) / 256;
-  if (avg >= 128 && (2 * (g.R / 256) + groups) * nt >= 2 * 304) return launch_t<2, 256, false>(g, st);
   int64_t tiles = 0;
   const int split = grouped_split(g, false, &tiles);
   if (split > 1) return launch_grouped_split(g, false, split, tiles, st);
-  // One CTA a tile.  256 columns, unless that leaves SMs without a tile (128
-  // rows x 8, 1024, 1024: 10.0 us with 256, 8.9 with 128); with few rows to
-  // an expert the weights' bytes bound the call, and narrower tiles still
-  // spread them (a token's two experts, 2048, 4096: 64 columns, 128 tiles).
-  const int64_t mt = g.R / 128 + groups;
-  if (mt * nt >= 100) return launch_t<1, 256, false>(g, st);
-  if (avg >= 16 || mt * ((g.N + 127) / 128) >= 152) return launch_t<1, 128, false>(g, st);
-  return launch_t<1, 64, false>(g, st);
+  // rows to an expert on average, and the most experts that can have rows
+  const int64_t avg = g.R / g.E, groups = g.R < g.E ? g.R : g.E;
+  if (avg < 16) {
+    // the weights' bytes bound the call: the widest tiles that still occupy
+    // the SMs (a token's two experts, 2048 x 4096: 64 columns, 128 tiles)
+    const int64_t mt = g.R / 128 + groups;
+    if (mt * ((g.N + 255) / 256) >= 100) return launch_t<1, 256, false>(g, st);
+    if (mt * ((g.N + 127) / 128) >= 152) return launch_t<1, 128, false>(g, st);
+    return launch_t<1, 64, false>(g, st);
+  }
+  const int64_t kb = (g.K + BK - 1) / BK;
+  auto cycles = [&](int64_t bm, int64_t bn, int64_t slots, int64_t block, int64_t start) {
+    const int64_t n = (2 * (g.R / bm) + groups) * ((g.N + bn - 1) / bn) / 2;   // half filled ends
+    return (n + slots - 1) / slots * kb * block + start;
+  };
+  const int64_t pair = cycles(256, 256, 76, 560, 10000), wide = cycles(128, 256, 152, 850, 3000),
+                narrow = cycles(128, 128, 152, 565, 3000);
+  if (pair <= wide && pair <= narrow) return launch_t<2, 256, false>(g, st);
+  return wide <= narrow ? launch_t<1, 256, false>(g, st) : launch_t<1, 128, false>(g, st);
 }
 
 cudaError_t launch_grouped_wgrad(const GroupedProblem& g, cudaStream_t st) {

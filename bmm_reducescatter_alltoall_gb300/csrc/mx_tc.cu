@@ -469,10 +469,13 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
       }
       if (any) {
         T* y0 = static_cast<T*>(p.y) + ((int64_t)r0 + tile_row) * p.ldy;
+        const int segs = min(2, (p.N - n0 + 63) / 64);
+        Carry carry;
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch)
-          put_segment<T>(o[ch], y0, p.ldy, valid, n0 + ch * 64, p.N, seg, p.aligned != 0, lane,
-                         [] {});
+          if (ch < segs)
+            put_segment<T>(o[ch], carry, ch == 0, ch + 1 == segs, y0, p.ldy, valid, n0 + ch * 64,
+                           p.N, seg, p.aligned != 0, lane, [] {});
       }
       if (++acc == S::NACC) {
         acc = 0;

@@ -95,6 +95,13 @@ __device__ __forceinline__ bool mbar_wait_acq(uint32_t bar, uint32_t parity,
   return mbar_try_acq(bar, parity) || mbar_wait_acq_slow(bar, parity, abort_flag, fault);
 }
 
+// Arrive on a barrier of another CTA of the cluster without ordering this
+// thread's memory accesses.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
 // 16-bit element access of the two output types, and their bias type.
 template <typename T>
 struct Num;

@@ -411,7 +411,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (CG == 2 && rank != 0) mbar_arrive_cluster(leader_tempty0 + 8u * acc);
+          // tensor memory alone is handed back; a release would wait for the
+          // stores of the segments before
+          if (CG == 2 && rank != 0) arrive_relaxed(leader_tempty0 + 8u * acc);
           else mbar_arrive(tempty_bar(acc));
         }
       };

@@ -127,13 +127,6 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Arrive on a barrier of another CTA of the cluster without ordering this
-// thread's memory accesses.
-__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
-               : "memory");
-}
-
 template <typename T, int CG, int BN>
 __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THREADS, 1)
     mx_grouped_kernel(const __grid_constant__ MxParams p) {
@@ -442,29 +435,19 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
       uint32_t o[2][32];
       if (any) {
 #pragma unroll
-        for (int part = 0; part < 4; ++part) {       // 32 columns at a time: few registers
-          uint32_t v[32];
-          tmem_ld32(t_base + part * 32, v);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[64];
+          tmem_ld32(t_base + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+          tmem_ld32(t_base + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
           tmem_ld_wait();
-          if (p.bias)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 b = lds128e(bias_s + part * 128 + i * 16);
-              v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + __uint_as_float(b.x));
-              v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + __uint_as_float(b.y));
-              v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + __uint_as_float(b.z));
-              v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + __uint_as_float(b.w));
-            }
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            o[part / 2][(part % 2) * 16 + i] =
-                Out<T>::pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          pack_segment<T>(v, o[half], p.bias ? bias_s + half * 256 : 0u, false);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2 && rank != 0) mbar_arrive_cluster(leader_tempty0 + 8u * acc);
+        // tensor memory alone is handed back: no memory of this thread to order
+        if (CG == 2 && rank != 0) arrive_relaxed(leader_tempty0 + 8u * acc);
         else mbar_arrive(tempty_bar(acc));
       }
       if (any) {

@@ -24,24 +24,49 @@ template <typename T, typename B, int SPLIT>
 __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
     bias_grad_kernel(const T* dy, B* db, const int64_t* counts, int32_t* status, int64_t R,
                      int64_t ld, int E, int N, int vec, int late) {
-  __shared__ GroupTable gt;
+  __shared__ int32_t first, past, bad;           // the group's rows
   __shared__ float part[kBgRows][64];
   __shared__ float sum[64];
   const int tid = threadIdx.x;
   if (!late) grid_wait();
   grid_go();
-  if (tid < 32) build_table<1>(&gt, counts, E, R, tid);
+  const int col_tiles = (N + 63) / 64;
+  const int unit = blockIdx.x / SPLIT;
+  const int e = unit / col_tiles, n0 = (unit - e * col_tiles) * 64;
+  if (tid < 32) {
+    // one group's offset needs no table
+    int64_t before = 0, mine = 0, total = 0;
+    bool wrong = false;
+#pragma unroll
+    for (int i = 0; i < kMaxGroups / 32; ++i) {
+      const int g = i * 32 + tid;
+      const int64_t n = g < E ? __ldg(reinterpret_cast<const long long*>(counts) + g) : 0;
+      wrong = wrong || n < 0 || n > R;
+      total += n;
+      before += g < e ? n : 0;
+      mine += g == e ? n : 0;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, d);
+      mine += __shfl_xor_sync(0xffffffffu, mine, d);
+      total += __shfl_xor_sync(0xffffffffu, total, d);
+    }
+    wrong = __any_sync(0xffffffffu, wrong) || total > R;
+    if (tid == 0) {
+      bad = wrong ? 1 : 0;
+      first = wrong ? 0 : (int32_t)before;
+      past = wrong ? 0 : (int32_t)(before + mine);
+    }
+  }
   __syncthreads();
   const uint32_t rank = SPLIT > 1 ? cluster_rank() : 0u;
-  if (gt.bad) {   // the same for every CTA
+  if (bad) {   // the same for every CTA
     if (tid == 0 && blockIdx.x == 0 && status) atomicExch(status, (int32_t)BRA_ERR_INVALID);
     if (late) grid_wait();
     return;
   }
-  const int col_tiles = (N + 63) / 64;
-  const int unit = blockIdx.x / SPLIT;
-  const int e = unit / col_tiles, n0 = (unit - e * col_tiles) * 64;
-  const int r0 = gt.off[e], r1 = gt.off[e + 1];
+  const int r0 = first, r1 = past;
   const int64_t rows = r1 - r0;
   const int64_t a = r0 + rows * rank / SPLIT, b = r0 + rows * (rank + 1) / SPLIT;
   const int c = (tid & 7) * 8, rl = tid >> 3;
@@ -84,7 +109,7 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
     float t = 0.f;
     if (n0 + col < N) {
       const T* p = dy + n0 + col;
-#pragma unroll 8
+#pragma unroll 16
       for (int64_t r = a + q; r < b; r += 8) t += static_cast<float>(p[r * ld]);
     }
     part[q][col] = t;
@@ -176,7 +201,10 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const __grid_constant__ 
 
 cudaError_t launch_bias_grad(const BiasGradProblem& g, cudaStream_t st) {
   const int64_t units = (int64_t)g.E * ((g.N + 63) / 64);
-  // under one unit to an SM the rows are split as well
+  // Under one unit to an SM the rows are split as well; with more, the
+  // clusters' barriers cost more than the balance gives (12 groups, 3063 rows,
+  // N = 775, 156 units: 22 us split; 8 groups x 2048 rows x 4096, 512 units:
+  // 50 split, 27 unsplit).
   const int split = units < 152 ? 8 : 1;
   if (units * split >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)(units * split);

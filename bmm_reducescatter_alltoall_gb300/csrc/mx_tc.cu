@@ -14,19 +14,22 @@
 //   Writers and not tcgen05.cp: a copy takes its 55 cycles of the tensor pipe
 //   itself, and a 256 x 256 pair tile needs six to a K block, next to 512
 //   cycles of MMAs; 8 x 2048 rows, K = 16384, N = 4096 took 442 us with
-//   copies and 346 (6350 TFLOP/s) with stores beside the MMAs.
+//   copies and 346 with stores beside the MMAs.
 //   The writers' word to the MMA issuer carries no memory of theirs, only
 //   that their tcgen05.st have completed (tcgen05.wait::st, and the tcgen05
 //   fences on both sides of the barrier): the arrival is relaxed.  With a
-//   release at cluster scope the remote one took 1400 cycles a K block.
-//   CG = 2, BN = 256: 256 x 256 tile of a CTA pair.  What feeds the tensor
-//     cores bounds it: some 58 bytes a clock and SM from L2, 35 KiB a K block
-//     and CTA, 600 cycles where the MMAs take 512 (with a quarter of the MMAs
-//     left out the time hardly changed).  256 x 192 tiles, whose two
-//     accumulators fit beside the scales, need 15% more of it: 452 us against
-//     346 on the sizes above.  With one accumulator the epilogue first drains
-//     it into registers (eight warps, 128 columns each, rounded and packed),
-//     hands it back, and stores while the next tile is computed.
+//   release at cluster scope the remote one took 1400 cycles a K block.  It
+//   goes to the barrier that the codes complete: a second barrier to wait for
+//   cost the issuer 70 cycles a K block (344 us in place of 314).
+//   CG = 2, BN = 256: 256 x 256 tile of a CTA pair, 314 us (7000 TFLOP/s) on
+//     the sizes above, 95 us at K = 4096.  The MMAs and a commit a K block
+//     alone, without codes, scales or their waits, take 274 and 83 us: 512
+//     cycles and some 55 of the commit.  Codes without scales: 285 and 90.
+//     With one accumulator the epilogue first drains it into registers (eight
+//     warps, 128 columns each, rounded and packed), hands it back, and stores
+//     while the next tile is computed.  256 x 192 tiles, whose two
+//     accumulators fit beside the scales, took a third longer; two
+//     accumulators of 256 columns that share 128 of them, 4 to 5%.
 //   CG = 1, BN = 128: 128 x 128 tile, two accumulators, for few rows to an
 //     expert (the weights' bytes bound the call).
 // Every wait is bounded (about 4 s) and reports through the fault word.
@@ -89,9 +92,7 @@ struct MShape {
   // scale columns of a K block: 8 of the rows, 8 for each half's weights
   static constexpr int SF_COLS = 24;
   static constexpr uint32_t SF0 = NACC * BN;
-  static constexpr int SF_FIT = (512 - NACC * BN) / SF_COLS;
-  static constexpr int SLOTS = SF_FIT > STAGES ? STAGES : SF_FIT;   // K blocks of scales
-  static_assert(SLOTS >= 4 && STAGES >= 4, "tensor memory, ring");
+  static_assert(STAGES >= 4 && SF0 + STAGES * SF_COLS <= 512, "ring, tensor memory");
   static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms");
 };
 
@@ -126,6 +127,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&v)[8]) {
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// The four writer warps meet; whether `ok` holds for every thread of theirs.
+__device__ __forceinline__ bool join_writers(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return all != 0;
+}
 
 template <typename T, int CG, int BN>
 __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THREADS, 1)
@@ -139,19 +153,18 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
   const uint32_t sf_base = smem_base + STAGES * STAGE_BYTES;
   uint8_t* bars = smem + STAGES * STAGE_BYTES + S::SF_STAGES * S::SF_BYTES;
   const uint32_t bar_base = smem_u32(bars);
-  // barriers (8 bytes each): per stage full, empty; per scale stage sfull
-  // (this CTA's scales have come) and sempty (they have been passed on); per
-  // slot of scale columns sready (leader: both CTAs' are in tensor memory);
+  // barriers (8 bytes each): per stage full (leader: both CTAs' codes have
+  // come, and their scales are in tensor memory), empty; per scale stage sfull
+  // (this CTA's scales have come) and sempty (they have been passed on);
   // tfull[2], tempty[2]
   auto full_bar = [&](int s) { return bar_base + 8u * s; };
   auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
   constexpr int SFS = S::SF_STAGES;
   auto sfull_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + s); };
   auto sempty_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + SFS + s); };
-  auto sready_bar = [&](int s) { return bar_base + 8u * (2 * STAGES + 2 * SFS + s); };
-  auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * STAGES + 2 * SFS + S::SLOTS + a); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * STAGES + 2 * SFS + a); };
   auto tempty_bar = [&](int a) { return tfull_bar(2 + a); };
-  static_assert(8 * (2 * STAGES + 2 * SFS + S::SLOTS + 4) + 16 <= BAR_BYTES, "barrier area");
+  static_assert(8 * (2 * STAGES + 2 * SFS + 4) + 16 <= BAR_BYTES, "barrier area");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BAR_BYTES - 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_BYTES - 8);
   GroupTable* gt = reinterpret_cast<GroupTable*>(bars + BAR_BYTES);      // row tiles
@@ -164,14 +177,14 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1);     // leader: its expect_tx; the bytes of both CTAs
+      // leader: its expect_tx, the bytes of both CTAs, their scale writers
+      mbar_init(full_bar(s), 1 + CG);
       mbar_init(empty_bar(s), 1);
     }
     for (int s = 0; s < SFS; ++s) {
       mbar_init(sfull_bar(s), 1);
-      mbar_init(sempty_bar(s), 4);
+      mbar_init(sempty_bar(s), 1);
     }
-    for (int s = 0; s < S::SLOTS; ++s) mbar_init(sready_bar(s), 4 * CG);
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), S::EPI_WARPS * CG);
@@ -278,46 +291,50 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
       }
     }
     if (!ok) spin_ns(2000000ull);   // let copies already issued land
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issuer (leader only) ----------------
+    // the whole warp walks and waits, so that addresses stay warp-uniform; one
+    // lane issues (one lane for everything: 60 us in place of 58 at K = 2048)
     const uint64_t a0 = smem_desc_sw128(smem_base, 16, 1024);
     const uint64_t b0 = smem_desc_sw128(smem_base + S::A_BYTES, 16, 1024);
-    int stage = 0, acc = 0, slot = 0;
-    uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     for (int t = walk0; ok && t < total; t += step) {
-      if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, fault)) break;
+      const bool drained = mbar_wait(tempty_bar(acc), acc_phase ^ 1u, abort_flag, fault);
+      ok = __all_sync(0xffffffffu, drained);
+      if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem_base + (uint32_t)(acc * BN);
       for (int kb = 0; kb < p.k_blocks; ++kb) {
-        if (!mbar_wait(full_bar(stage), phase, abort_flag, fault) ||
-            !mbar_wait(sready_bar(slot), slot_phase, abort_flag, fault)) {
-          ok = false;
-          break;
-        }
+        const bool here = mbar_wait(full_bar(stage), phase, abort_flag, fault);
+        ok = __all_sync(0xffffffffu, here);
+        if (!ok) break;
         tc_fence_after();
         const uint64_t so = (uint64_t)((stage * STAGE_BYTES) >> 4);
         // half h (128 elements): rows' columns 4h, weights' 8 + 8h
-        const uint32_t sf = tmem_base + S::SF0 + (uint32_t)(slot * S::SF_COLS);
+        const uint32_t sf = tmem_base + S::SF0 + (uint32_t)(stage * S::SF_COLS);
+        if (lane == 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mx_mma<CG>(d, a0 + so + 2 * k, b0 + so + 2 * k,
-                     p.idesc | ((k & 1) ? (2u << 4 | 2u << 29) : 0u), sf + 4 * (k >> 1),
-                     sf + 8 + 8 * (k >> 1), (kb > 0 || k > 0) ? 1u : 0u);
-        if (CG == 2) tc_commit_pair(empty_bar(stage), 0x3);
-        else tc_commit(empty_bar(stage));
-        if (++slot == S::SLOTS) {
-          slot = 0;
-          slot_phase ^= 1u;
+          for (int k = 0; k < 4; ++k)
+            mx_mma<CG>(d, a0 + so + 2 * k, b0 + so + 2 * k,
+                       p.idesc | ((k & 1) ? (2u << 4 | 2u << 29) : 0u), sf + 4 * (k >> 1),
+                       sf + 8 + 8 * (k >> 1), (kb > 0 || k > 0) ? 1u : 0u);
+          if (CG == 2) tc_commit_pair(empty_bar(stage), 0x3);
+          else tc_commit(empty_bar(stage));
         }
+        __syncwarp();
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
         }
       }
       if (!ok) break;
-      if (CG == 2) tc_commit_pair(tfull_bar(acc), 0x3);
-      else tc_commit(tfull_bar(acc));
+      if (lane == 0) {
+        if (CG == 2) tc_commit_pair(tfull_bar(acc), 0x3);
+        else tc_commit(tfull_bar(acc));
+      }
+      __syncwarp();
       if (++acc == S::NACC) {
         acc = 0;
         acc_phase ^= 1u;
@@ -327,10 +344,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
   } else if (warp >= WRITE_WARP0 && warp < EPI_WARP0) {
     // ---------------- scale writers: lane quarter q, every CTA ----------------
     const int q = warp & 3;
-    const uint32_t leader_sready0 = CG == 2 ? map_to_rank(sready_bar(0), 0) : sready_bar(0);
-    int stage = 0, slot = 0, old_stage = 0;
-    uint32_t phase = 0, old_phase = 0;   // old: the K block whose slot is written again
-    int ahead = 0;                       // K blocks so far, up to SLOTS
+    const uint32_t leader_full0 = CG == 2 ? map_to_rank(full_bar(0), 0) : full_bar(0);
+    int from = 0, stage = 0;             // in the scales' ring, in the codes'
+    uint32_t from_phase = 0, phase = 0;
     bool ok = true;
     auto step_ring = [](int& at, uint32_t& ph, int size) {
       if (++at == size) {
@@ -339,16 +355,20 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
       }
     };
     // One K block, or two at once: a block's waits, loads and stores are a
-    // chain of some 700 cycles, longer than its MMAs.
+    // chain of some 700 cycles, longer than its MMAs.  The four warps join
+    // before one of them arrives (eight arrivals a K block, half of them
+    // remote, in place of two: 39 against 36 us at 8 x 2048 rows, K = 512,
+    // N = 4096), and leave together when a wait of any has run out.
     auto pass_on = [&](auto count) -> bool {
       constexpr int C = decltype(count)::value;
-      int st = stage, slots[C];
-      uint32_t ph = phase;
+      int at_from = from, to[C];
+      uint32_t at_phase = from_phase;
       uint32_t va[C][8], vb[C][2][8];
+      bool got = true;
 #pragma unroll
       for (int n = 0; n < C; ++n) {
-        if (!__all_sync(0xffffffffu, mbar_wait(sfull_bar(st), ph, abort_flag, fault))) return false;
-        const uint32_t at = sf_base + st * S::SF_BYTES + (uint32_t)lane * 16;
+        got = got && mbar_wait(sfull_bar(at_from), at_phase, abort_flag, fault);
+        const uint32_t at = sf_base + at_from * S::SF_BYTES + (uint32_t)lane * 16;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint4 x = lds128e(at + h * 512);
@@ -361,39 +381,34 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(MShape<CG, BN>::THR
             w[4 * i] = y.x, w[4 * i + 1] = y.y, w[4 * i + 2] = y.z, w[4 * i + 3] = y.w;
           }
         }
-        step_ring(st, ph, SFS);
-        // the MMAs that read this slot have completed
-        if (ahead == S::SLOTS) {
-          if (!__all_sync(0xffffffffu,
-                          mbar_wait(empty_bar(old_stage), old_phase, abort_flag, fault)))
-            return false;
-          step_ring(old_stage, old_phase, STAGES);
-        } else {
-          ++ahead;
-        }
-        slots[n] = slot;
-        if (++slot == S::SLOTS) slot = 0;
+        step_ring(at_from, at_phase, SFS);
+        // the MMAs that read this stage's columns have completed
+        got = got && mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, fault);
+        to[n] = stage;
+        step_ring(stage, phase, STAGES);
       }
-      tc_fence_after();
+      if (__all_sync(0xffffffffu, got)) {
+        tc_fence_after();
+#pragma unroll
+        for (int n = 0; n < C; ++n) {
+          const uint32_t sf =
+              tmem_base + S::SF0 + (uint32_t)(to[n] * S::SF_COLS) + ((uint32_t)(q * 32) << 16);
+          tmem_st8(sf, va[n]);
+          tmem_st8(sf + 8, vb[n][0]);
+          tmem_st8(sf + 16, vb[n][1]);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+      }
+      if (!join_writers(got)) return false;
 #pragma unroll
       for (int n = 0; n < C; ++n) {
-        const uint32_t sf =
-            tmem_base + S::SF0 + (uint32_t)(slots[n] * S::SF_COLS) + ((uint32_t)(q * 32) << 16);
-        tmem_st8(sf, va[n]);
-        tmem_st8(sf + 8, vb[n][0]);
-        tmem_st8(sf + 16, vb[n][1]);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-#pragma unroll
-      for (int n = 0; n < C; ++n) {
-        if (lane == 0) {
-          mbar_arrive(sempty_bar(stage));
-          if (rank == 0) mbar_arrive(sready_bar(slots[n]));
-          else arrive_relaxed(leader_sready0 + 8u * slots[n]);
+        if (warp == WRITE_WARP0 && lane == 0) {
+          if (rank == 0) mbar_arrive(full_bar(to[n]));
+          else arrive_relaxed(leader_full0 + 8u * to[n]);
+          mbar_arrive(sempty_bar(from));
         }
-        step_ring(stage, phase, SFS);
+        step_ring(from, from_phase, SFS);
       }
       return true;
     };

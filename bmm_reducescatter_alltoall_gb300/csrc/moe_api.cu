@@ -20,6 +20,11 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
   return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
 }
 
+// Whether `rows` rows `pitch` elements apart (of at most 8 bytes) count in 64 bits.
+bool counts_in_64_bits(int64_t rows, int64_t pitch) {
+  return rows <= 0 || pitch <= (int64_t(1) << 59) / rows;
+}
+
 // Bytes of `rows` rows of n elements, ld apart (the last one without padding).
 int64_t span(int64_t rows, int64_t ld, int64_t n, int64_t es) {
   return rows > 0 ? ((rows - 1) * ld + n) * es : 0;
@@ -38,7 +43,8 @@ int check_sizes(const bra_grouped_args* a, GroupedSizes* s) {
   if (a->dtype != BRA_FP16 && a->dtype != BRA_BF16) return BRA_ERR_INVALID;
   *s = {a->rows, a->groups, a->in, a->out, a->x_pitch ? a->x_pitch : a->in,
         a->y_pitch ? a->y_pitch : a->out};
-  if (s->xp < s->K || s->yp < s->N || s->xp > (int64_t(1) << 36) || s->yp > (int64_t(1) << 36))
+  if (s->xp < s->K || s->yp < s->N || s->xp > (int64_t(1) << 36) || s->yp > (int64_t(1) << 36) ||
+      !counts_in_64_bits(s->R, s->xp) || !counts_in_64_bits(s->R, s->yp))
     return BRA_ERR_INVALID;
   if (off_by(a->status, 3u) || off_by(a->workspace, 255u) || a->workspace_bytes < 0 ||
       (!a->workspace && a->workspace_bytes != 0))
@@ -115,7 +121,8 @@ int check_mx(const bra_mx_args* a) {
       a->rows_per_group > kMaxRows || a->reserved != 0)
     return BRA_ERR_INVALID;
   if (a->rows_per_group > 0 && a->rows != a->groups * a->rows_per_group) return BRA_ERR_INVALID;
-  if (a->x_pitch != 0 && (a->x_pitch < a->k || a->x_pitch > (int64_t(1) << 36)))
+  if (a->x_pitch != 0 && (a->x_pitch < a->k || a->x_pitch > (int64_t(1) << 36) ||
+                          !counts_in_64_bits(a->rows, a->x_pitch)))
     return BRA_ERR_INVALID;
   if (off_by(a->status, 3u)) return BRA_ERR_INVALID;
   return BRA_OK;
@@ -447,7 +454,14 @@ int grouped_matmul(const void* x, const void* weight, const void* bias, const in
     return BRA_ERR_INVALID;
   const cudaStream_t st = (cudaStream_t)stream;
   if (s.R == 0) return clear_status(args->status, st);
-  if ((rc = check_workspace(args, cx.bytes + cw.bytes)) != BRA_OK) return rc;
+  const int64_t need = cx.bytes + cw.bytes;
+  if ((rc = check_workspace(args, need)) != BRA_OK) return rc;
+  const Span ins[4] = {{x, span(s.R, s.xp, s.K, 2)},
+                       {weight, s.E * s.K * s.N * 2},
+                       {bias, s.E * s.N * bes},
+                       {counts, s.E * 8}};
+  const Span ws_used[1] = {{args->workspace, need}};
+  if (any_overlap(ws_used, 1, ins, 4)) return BRA_ERR_INVALID;
   if ((rc = clear_status(args->status, st)) != BRA_OK) return rc;
   Workspace ws{static_cast<uint8_t*>(args->workspace)};
   GroupedProblem g;
@@ -487,23 +501,14 @@ int grouped_matmul_grad(const void* dy, const void* x, const void* weight, const
   const bool wt = args->transpose_weight != 0;
   const Copy cd = copy_of(dy, s.R, s.N, s.yp), cx = copy_of(x, s.R, s.K, s.xp),
              cw = weight_copy(weight, args, s);
-  struct Buf {
-    const void* p;
-    int64_t n;
-  };
   const int64_t wb = s.E * s.K * s.N * 2;
-  const Buf outs[3] = {{dx, s.R * s.K * 2}, {dweight, wb}, {dbias, s.E * s.N * bes}};
-  const Buf ins[5] = {{dy, span(s.R, s.yp, s.N, 2)},
-                      {x, span(s.R, s.xp, s.K, 2)},
-                      {weight, wb},
-                      {counts, s.E * 8},
-                      {args->workspace, args->workspace_bytes}};
-  for (int i = 0; i < 3; ++i) {
-    for (const Buf& b : ins)
-      if (overlap(outs[i].p, outs[i].n, b.p, b.n)) return BRA_ERR_INVALID;
-    for (int j = 0; j < i; ++j)
-      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return BRA_ERR_INVALID;
-  }
+  const Span outs[3] = {{dx, s.R * s.K * 2}, {dweight, wb}, {dbias, s.E * s.N * bes}};
+  const Span ins[5] = {{dy, span(s.R, s.yp, s.N, 2)},
+                       {x, span(s.R, s.xp, s.K, 2)},
+                       {weight, wb},
+                       {counts, s.E * 8},
+                       {args->workspace, args->workspace_bytes}};
+  if (any_overlap(outs, 3, ins, 5)) return BRA_ERR_INVALID;
   const cudaStream_t st = (cudaStream_t)stream;
   if (s.R == 0) {
     if (dweight && cudaMemsetAsync(dweight, 0, (size_t)wb, st) != cudaSuccess) return BRA_ERR_CUDA;
@@ -513,6 +518,8 @@ int grouped_matmul_grad(const void* dy, const void* x, const void* weight, const
   }
   const int64_t need = (dx || dweight ? cd.bytes : 0) + (dx ? cw.bytes : 0) + (dweight ? cx.bytes : 0);
   if ((rc = check_workspace(args, need)) != BRA_OK) return rc;
+  const Span ws_used[1] = {{args->workspace, need}};
+  if (any_overlap(ws_used, 1, ins, 4)) return BRA_ERR_INVALID;
   if ((rc = clear_status(args->status, st)) != BRA_OK) return rc;
   Workspace ws{static_cast<uint8_t*>(args->workspace)};
   GroupedProblem g;

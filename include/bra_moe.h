@@ -36,7 +36,8 @@ typedef struct {
   int64_t out;         /* N: 1 .. 2^24                                        */
   int32_t dtype;       /* BRA_FP16 or BRA_BF16: x, weight, y and gradients    */
   int32_t transpose_weight;  /* non-zero: weight (and dweight) is (E, N, K)   */
-  int64_t x_pitch;     /* elements between rows of x; 0 = K                   */
+  int64_t x_pitch;     /* elements between rows of x; 0 = K.  A pitch is at   */
+                       /* most 2^36, and rows times it 2^59                   */
   int64_t y_pitch;     /* elements between rows of y (forward) or dy (grad); 0 = N */
   void* workspace;     /* 256-byte aligned, or NULL                           */
   int64_t workspace_bytes;
@@ -72,7 +73,8 @@ typedef struct {
  *                        pitch below the row length, a pointer that is not
  *                        element-aligned (counts: 8 bytes, status: 4), a
  *                        workspace not 256-byte aligned or smaller than
- *                        needed, y overlapping an input or the workspace.
+ *                        needed, y overlapping an input or the workspace,
+ *                        the part of the workspace in use an input.
  *   BRA_ERR_UNSUPPORTED  a copy is needed and there is no workspace; more
  *                        than 2^31 - 1 output tiles.
  *   BRA_ERR_CUDA         the launch failed.
@@ -135,7 +137,8 @@ typedef struct {
   int64_t groups;          /* E: 1 .. BRA_MAX_GROUPS                           */
   int64_t rows_per_group;  /* groups of this many rows (R = E * that); 0: of   */
                            /* counts[E] rows, device int64, sum at most R      */
-  int64_t x_pitch;         /* quantize: elements between rows of x; 0 = K      */
+  int64_t x_pitch;         /* quantize: elements between rows of x; 0 = K; at  */
+                           /* most 2^36, and rows times it 2^59                */
   int32_t dtype;           /* x: FP16 or BF16; dequantized y: FP16, BF16, FP32 */
   int32_t reserved;        /* 0                                                */
   int32_t* status;         /* device int32 of this call, or NULL               */

@@ -92,6 +92,31 @@ def test_grouped_matmul_grad_refuses_pointers(lib):
     assert call(Y, X, W, C, None, None, W + 64, a, None) == INVALID      # dbias over weight
 
 
+def test_pitches_past_64_bits_are_refused(lib):
+    """Rows times pitch is an address range: it has to stay in 64 bits."""
+    rows, wide = (1 << 31) - (1 << 16), 1 << 36
+    for change in (dict(x_pitch=wide), dict(y_pitch=wide)):
+        a = ctypes.byref(args(rows=rows, **change))
+        assert lib.grouped_matmul(X, W, None, C, Y, a, None) == INVALID
+        assert lib.grouped_matmul_grad(Y, X, W, C, G, None, None, a, None) == INVALID
+        assert lib.grouped_matmul_workspace_size(X, W, a) == -INVALID
+    m = ctypes.byref(mx(rows=rows, rows_per_group=0, x_pitch=wide))
+    assert lib.mxfp4_quantize(X, C, W, B, m, None) == INVALID
+    assert lib.grouped_matmul_workspace_size(X + 2, W, ctypes.byref(args(x_pitch=wide))) == 16 * 64 * 2
+
+
+def test_workspace_over_an_input_is_refused(lib):
+    """The copies would overwrite what they are made from."""
+    def a(at, size):
+        return ctypes.byref(args(in_=65, transpose_weight=1, workspace=at, workspace_bytes=size))
+    size = lib.grouped_matmul_workspace_size(X, W, a(S, 1 << 20))
+    for at in (X, W, B, C, X - size + 256):
+        assert lib.grouped_matmul(X, W, B, C, Y, a(at, size), None) == INVALID
+    size = lib.grouped_matmul_grad_workspace_size(Y, X, W, 1, 0, a(S, 1 << 20))
+    for at in (X, W, C, Y, W - size + 256):                              # dx alone: the weight's copy
+        assert lib.grouped_matmul_grad(Y, X, W, C, G, None, None, a(at, size), None) == INVALID
+
+
 def test_workspace_sizes(lib):
     size = lambda x, w, **kw: lib.grouped_matmul_workspace_size(         # noqa: E731
         x, w, ctypes.byref(args(**kw)))

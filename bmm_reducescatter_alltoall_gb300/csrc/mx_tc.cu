@@ -600,16 +600,20 @@ cudaError_t launch(const MxProblem& g, cudaStream_t st) {
 
 }  // namespace
 
-// The pair from 160 rows an expert on, with a tile for each pair of SMs.
+// The pair from 128 rows an expert on, with a tile for each pair of SMs.
 // bf16, one CTA against pair, us (rows an expert x experts, K, N):
-//   128 x  8, 2048, 4096   11 / 15     128 x 64, 2048, 4096   60 / 79
-//   192 x  8, 2048, 4096   19 / 16     192 x 64, 2048, 4096  100 / 86
-//   512 x 16, 2048, 4096   49 / 41     256 x  8, 4096, 1024   11 / 13
-//  1024 x 16, 2048, 4096   88 / 71     512 x  8, 4096, 1024   17 / 14
+//   equal groups                           groups drawn at random
+//    96 x  8, 2048, 4096   10 / 13         112 x  8, 2048, 4096   10 / 13
+//   160 x  8, 2048, 4096   17 / 13         128 x  8, 2048, 4096   13 / 13
+//   128 x 64, 2048, 4096   60 / 66         120 x 64, 2048, 4096   65 / 66
+//   160 x 64, 2048, 4096   91 / 69         128 x 64, 2048, 4096   71 / 67
+//   512 x 16, 2048, 4096   47 / 36         140 x 64, 2048, 4096   84 / 68
+//  1024 x 16, 2048, 4096   82 / 59
+//   256 x  8, 4096, 1024   10 / 12 (96 tiles)   512 x 8, 4096, 1024   15 / 13 (160)
 cudaError_t launch_mx_grouped(const MxProblem& g, cudaStream_t st) {
   const bool bf16 = g.dtype == BRA_BF16;
   const int64_t groups = g.R < g.E ? g.R : g.E;
-  if (g.R / g.E >= 160 && (2 * (g.R / 256) + groups) * ((g.N + 255) / 256) >= 2 * 76)
+  if (g.R / g.E >= 128 && (2 * (g.R / 256) + groups) * ((g.N + 255) / 256) >= 2 * 76)
     return bf16 ? launch<__nv_bfloat16, 2, 256>(g, st) : launch<__half, 2, 256>(g, st);
   return bf16 ? launch<__nv_bfloat16, 1, 128>(g, st) : launch<__half, 1, 128>(g, st);
 }

@@ -29,7 +29,7 @@
 //     warps, 128 columns each, rounded and packed), hands it back, and stores
 //     while the next tile is computed.  256 x 192 tiles, whose two
 //     accumulators fit beside the scales, took a third longer; two
-//     accumulators of 256 columns that share 128 of them, 4 to 5%.
+//     accumulators of 256 columns that share 128 of them, 6%.
 //   CG = 1, BN = 128: 128 x 128 tile, two accumulators, for few rows to an
 //     expert (the weights' bytes bound the call).
 // Every wait is bounded (about 4 s) and reports through the fault word.

@@ -75,6 +75,7 @@ KERNEL_SOURCES = {
     "dequantize_kernel": "mx_quant.cu",
     "mx_grouped_kernel": "mx_tc.cu",
     "route_choose_kernel": "moe_route.cu",
+    "route_scan_kernel": "moe_route.cu",
     "route_place_kernel": "moe_route.cu",
     "route_grad_kernel": "moe_route.cu",
     "dispatch_kernel": "moe_permute.cu",

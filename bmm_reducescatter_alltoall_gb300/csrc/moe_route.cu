@@ -17,11 +17,13 @@
 // its place among the chunk's rows of that expert, in token order and without
 // any order of the setting.  The chunks' counts go to a small matrix; a
 // second kernel adds to each place the rows of the chunks before and of the
-// lower experts.  A single chunk does both in one launch.
+// lower experts; when there are more chunks than SMs a kernel between the two
+// sums the matrix once.  A single chunk does all in one launch.
 // The logits are read once (4 bytes x E a token), but the choices' compares
 // and selects bound it: 65536 tokens, 8 of 128 experts, 29 us for the choices
 // where the logits' 34 MB take 5, 12 for the rows, 13 for the gradient.  For
-// few tokens it is one launch (64 tokens, 8 of 64: 4.7 us).
+// few tokens it is one launch (64 tokens, 8 of 64: 4.7 us); a million tokens,
+// 8 of 128, take 504 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -61,6 +63,7 @@ struct RouteParams {
   int T, E, k, renorm;
   int chunk, chunks;   // tokens of a chunk (a multiple of 32)
   int vec;             // logits' rows are read four at a time
+  int scanned;         // hist holds sums over the chunks up to each one
 };
 
 __device__ __forceinline__ float group_sum(float v, int L) {
@@ -87,10 +90,10 @@ __device__ __forceinline__ void sort_eight(uint32_t (&key)[8], int (&idx)[8]) {
 
 // The experts of one token to each group of L lanes (t < 0: none); lane l of
 // the group holds logits l * V ..  Writes ids and weights and sets the
-// chunk's bits (word `word`, bit `bit` of each expert's `words`).  Whole warps.
+// chunk's bits (word `word`, bit `bit` of each expert's `stride`).  Whole warps.
 template <typename T, int L, int V>
 __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, uint32_t* bits,
-                                       int words, int word, uint32_t bit) {
+                                       int stride, int word, uint32_t bit) {
   constexpr int OWN = (BRA_MAX_CHOICES + L - 1) / L;   // choices a lane keeps
   const int gl = lane % L;
   const uint32_t group = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (lane & ~(L - 1));
@@ -181,11 +184,16 @@ __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, ui
     if (t >= 0 && o * L + gl < p.k) {
       p.ids[out + o * L + gl] = my_id[o];
       p.weights[out + o * L + gl] = my_key[o] ? e[o] / s : 0.f;
-      if (my_id[o] >= 0) atomicOr(&bits[my_id[o] * words + word], bit);
+      if (my_id[o] >= 0) atomicOr(&bits[my_id[o] * stride + word], bit);
     }
 }
 
-// The chunk's experts as bits: words (chunk / 32) to an expert.
+// Words from one expert's bits to the next: odd, so that the same word of
+// different experts lies in different banks (1024 tokens a chunk, 32 words
+// apart: 262144 tokens, 8 of 128, 257 us in place of 130).
+__host__ __device__ constexpr int bit_stride(int chunk) { return (chunk / 32) | 1; }
+
+// The chunk's experts as bits: chunk / 32 words to an expert.
 __device__ __forceinline__ void clear_bits(uint32_t* bits, int n) {
   for (int i = threadIdx.x; i < n; i += kThreads) bits[i] = 0u;
 }
@@ -230,25 +238,25 @@ __device__ __forceinline__ void mark_unused(const RouteParams& p, int c, int use
 // expert in `slots`; with a single chunk, everything.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParams p) {
-  extern __shared__ uint32_t bits[];                    // [E][chunk / 32]
+  extern __shared__ uint32_t bits[];                    // [E][stride]
   __shared__ int total[kMaxGroups], base[kMaxGroups], zero[kMaxGroups];
   __shared__ int used;
-  const int words = p.chunk / 32, c = blockIdx.x, t0 = c * p.chunk;
+  const int words = p.chunk / 32, stride = bit_stride(p.chunk), c = blockIdx.x, t0 = c * p.chunk;
   const int n = min(p.chunk, p.T - t0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  clear_bits(bits, p.E * words);
+  clear_bits(bits, p.E * stride);
   __syncthreads();
   grid_wait();
   grid_go();
   constexpr int G = 32 / L;                             // tokens of a warp
   for (int i0 = warp * G; i0 < n; i0 += kWarps * G) {
     const int i = i0 + lane / L;
-    choose<T, L, V>(p, i < n ? t0 + i : -1, lane, bits, words, i >> 5, 1u << (i & 31));
+    choose<T, L, V>(p, i < n ? t0 + i : -1, lane, bits, stride, i >> 5, 1u << (i & 31));
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
     int s = 0;
-    for (int w = 0; w < words; ++w) s += __popc(bits[e * words + w]);
+    for (int w = 0; w < words; ++w) s += __popc(bits[e * stride + w]);
     if (p.chunks > 1) {
       p.hist[(int64_t)c * p.E + e] = s;
     } else {
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParam
     const int e = p.ids[at];
     int slot = -1;
     if (e >= 0) {
-      const uint32_t* b = bits + e * words;
+      const uint32_t* b = bits + e * stride;
       slot = __popc(b[local >> 5] & ((1u << (local & 31)) - 1u));
       for (int w = 0; w < (local >> 5); ++w) slot += __popc(b[w]);
       if (p.chunks == 1) {
@@ -280,7 +288,38 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParam
   }
 }
 
-// Rows of one chunk, from the counts of all of them.
+// The matrix of counts, summed down its columns in place: a CTA to 32 experts,
+// 32 chunks at a time, each expert's by one warp.
+__global__ void __launch_bounds__(kThreads) route_scan_kernel(const RouteParams p) {
+  __shared__ int tile[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane;
+  auto load = [&](int r) {
+    return e < p.E && r < p.chunks ? p.hist[(int64_t)r * p.E + e] : 0;
+  };
+  grid_wait();
+  grid_go();
+  int carry = 0, next = load(warp);
+  for (int r0 = 0; r0 < p.chunks; r0 += 32) {
+    tile[warp][lane] = next;                 // a warp holds a chunk, a lane an expert
+    next = load(r0 + 32 + warp);
+    __syncthreads();
+    int v = tile[lane][warp];                // the other way round
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += a;
+    }
+    v += carry;
+    carry = __shfl_sync(0xffffffffu, v, 31);
+    tile[lane][warp] = v;                    // read by this thread alone until here
+    __syncthreads();
+    if (e < p.E && r0 + warp < p.chunks) p.hist[(int64_t)(r0 + warp) * p.E + e] = tile[warp][lane];
+    // the next round's write goes to the element this thread has just read
+  }
+}
+
+// Rows of one chunk, from the counts of all of them, or from their sums.
 __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams p) {
   __shared__ int total[kMaxGroups], before[kMaxGroups], base[kMaxGroups];
   __shared__ int used;
@@ -303,7 +342,12 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams
   // threads of a row of the matrix side by side, rows dealt over the rest
   const int width = (p.E + 31) / 32 * 32, rows = kThreads / width;
   const int e = threadIdx.x % width, r0 = threadIdx.x / width;
-  if (e < p.E && r0 < rows) {
+  if (p.scanned) {
+    for (int i = threadIdx.x; i < p.E; i += kThreads) {
+      total[i] = p.hist[(int64_t)(p.chunks - 1) * p.E + i];
+      before[i] = c ? p.hist[(int64_t)(c - 1) * p.E + i] : 0;
+    }
+  } else if (e < p.E && r0 < rows) {
     int all = 0, old = 0;
 #pragma unroll 16
     for (int r = r0; r < p.chunks; r += rows) {
@@ -462,20 +506,28 @@ int rows_vec(const void* p, int E, int dtype) {
 
 }  // namespace
 
-// Tokens of a chunk: one chunk up to 64 tokens (one launch); else a chunk for
-// each of 152 SMs, of at most 1024 tokens.
+// Tokens of a chunk: one chunk up to 64 tokens (one launch); else chunks of at
+// most 1024 tokens, as many for each of 152 SMs.
 int route_chunk(int64_t T) {
   if (T <= 64) return 64;
-  const int64_t c = ((T + 151) / 152 + 31) / 32 * 32;
-  return (int)(c > 1024 ? 1024 : c);
+  const int64_t chunks = (T + 152 * 1024 - 1) / (152 * 1024) * 152;
+  return (int)(((T + chunks - 1) / chunks + 31) / 32 * 32);
 }
+
+// Chunks from which the counts are summed by a launch of their own.  Below,
+// each CTA of the last kernel sums the matrix itself, in all the square of the
+// chunks.  8 of 128 experts, us, by each CTA / by the launch: 65536 tokens (147
+// chunks) 35.1 / 35.8, 262144 (304) 132 / 129, 1048576 (1064) 576 / 504,
+// 4194304 (4256) 3045 / 1982.
+constexpr int kScanChunks = 160;
 
 cudaError_t launch_route(const RouteCall& r, cudaStream_t st) {
   RouteParams p = {r.logits, r.ids,   r.weights, r.counts, r.slots, r.tokens, r.hist, (int)r.T,
                    r.E,      r.k,     r.renorm,  route_chunk(r.T), 0,
-                   rows_vec(r.logits, r.E, r.dtype)};
+                   rows_vec(r.logits, r.E, r.dtype), 0};
   p.chunks = (int)((r.T + p.chunk - 1) / p.chunk);
-  const int smem = r.E * (p.chunk / 32) * 4;
+  p.scanned = p.chunks >= kScanChunks;
+  const int smem = r.E * bit_stride(p.chunk) * 4;
   const cudaError_t e = by_type(r.dtype, r.E, [&](auto* type, auto l, auto v) {
     using T = std::remove_pointer_t<decltype(type)>;
     if (smem > 32768) {
@@ -488,6 +540,11 @@ cudaError_t launch_route(const RouteCall& r, cudaStream_t st) {
                              (unsigned)p.chunks, kThreads, smem, st, p);
   });
   if (e != cudaSuccess || p.chunks == 1) return e;
+  if (p.scanned) {
+    const cudaError_t a =
+        launch_overlapped(route_scan_kernel, (unsigned)(r.E + 31) / 32, kThreads, 0, st, p);
+    if (a != cudaSuccess) return a;
+  }
   return launch_overlapped(route_place_kernel, (unsigned)p.chunks, kThreads, 0, st, p);
 }
 

@@ -146,6 +146,20 @@ def test_many_tokens(T):
     assert r["counts"].tolist() == [T if e in (3, 20) else 0 for e in range(24)]
 
 
+@pytest.mark.parametrize("T,E", [(155648, 16), (155649, 40), (400003, 40), (1300001, 9)])
+def test_more_chunks_than_processors(T, E):
+    """From 152 * 1024 tokens on there are several chunks to an SM, of even and odd numbers of
+    words, and the counts of all chunks are summed in between (32 experts a block)."""
+    check_route(logits_of(T, E, torch.float16, seed=T), 2, True)
+    l = torch.full((T, E), float("-inf"), device="cuda")
+    l[T - 1, E - 1] = l[7, 0] = l[T // 2, 0] = 1.0
+    r = bra.moe_route(l, 2)
+    assert r["counts"].tolist() == [2] + [0] * (E - 2) + [1]
+    assert r["tokens"][:3].tolist() == [7, T // 2, T - 1] and (r["tokens"][3:] == -1).all()
+    assert [r["slots"][t, 0].item() for t in (7, T // 2, T - 1)] == [0, 1, 2]
+    assert (r["slots"] >= 0).sum().item() == 3
+
+
 def test_the_gradient_is_that_of_differences():
     """Central differences of the weights in fp32: with steps of 2^-7 the third derivative's term
     is below 2^-14 * |g| and the rounding of a weight 2^-22 / 2^-7."""

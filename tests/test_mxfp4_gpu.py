@@ -212,6 +212,23 @@ def test_one_expert_without_counts_and_no_rows():
     assert bra.mxfp4_dequantize(bra.mxfp4_quantize(x[:0]), torch.float32).shape == (0, 96)
 
 
+@pytest.mark.parametrize("K,N", [(4096, 64), (64, 4104)])
+def test_matrices_that_pass_32_bit_offsets(K, N):
+    """Rows (of x, or of y) whose element offsets pass 2^32, in the last two groups."""
+    R = (1 << 32) // max(K, N) + 300
+    x = torch.zeros((R, K), dtype=torch.bfloat16, device="cuda")
+    x[-200:] = randn(200, K)
+    w = (randn(2, N, K, seed=1) * K ** -0.5).bfloat16()
+    c = torch.tensor([R - 150, 150], device="cuda")
+    q = bra.mxfp4_quantize(x, c)
+    y = bra.mxfp4_grouped_matmul(q, bra.mxfp4_quantize(w), c)
+    last = bra.mxfp4_dequantize(q, torch.bfloat16)[-201:]
+    assert not last[0].any() and np.array_equal(last[1:].double().cpu().numpy(), quantized(x[-200:]))
+    assert not y[0].any() and not y[-300:-200].any()
+    for e, a, z in ((0, R - 200, R - 150), (1, R - 150, R)):
+        assert_close(y[a:z], *reference(x[a:z], w[e:e + 1], None, [z - a]), K)
+
+
 def test_refused_counts_write_nothing():
     x, w, b, _ = case([20, 0, 0], 64, 72)
     wq = bra.mxfp4_quantize(w)

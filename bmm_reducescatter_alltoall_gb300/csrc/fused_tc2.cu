@@ -27,7 +27,7 @@
 //   * TMEM: 512 columns allocated by the pair (tcgen05.alloc.cta_group::2 in
 //     both CTAs; both get the same column range): two 256-column
 //     accumulators, or one 512-column accumulator for the wide tile.
-//   * Optionally two pairs per cluster share each weight box (see CL below).
+//   * Optionally two pairs per cluster (see CL below).
 // Every wait is bounded (about 4 s by %globaltimer) and reports through the
 // device fault word; both CTAs always reach the closing cluster barrier and
 // free their tensor memory.
@@ -94,9 +94,10 @@ struct Shape {
 };
 
 // CL pairs per cluster.  CL = 2: the two pairs compute m tiles 2i and 2i+1
-// of the same n tile and load each weight box once, multicast to the CTA of
-// either pair that holds it (half of the weight's L2 reads); a stage is free
-// again once both pairs' MMAs have read it.
+// of the same n tile side by side, so that they fetch the same weight boxes
+// at about the same time and share them in L2.  Each pair has its own ring
+// and loads every box of its tile itself: no load writes another pair's
+// shared memory.
 template <typename T, int NSUB, int CL>
 __global__ void __cluster_dims__(2 * CL, 1, 1) __launch_bounds__(Shape<NSUB>::THREADS, 1)
     fused_tc2_kernel(const __grid_constant__ TcParams p) {
@@ -132,12 +133,12 @@ __global__ void __cluster_dims__(2 * CL, 1, 1) __launch_bounds__(Shape<NSUB>::TH
   const int m_super = (p.m_tiles + CL - 1) / CL;
   const int num_super = p.num_tiles / (p.m_tiles * p.n_tiles) * m_super * p.n_tiles;
   constexpr int kGroupS = kGroupM / CL > 0 ? kGroupM / CL : 1;
-  constexpr uint16_t kAllCtas = (uint16_t)((1u << (2 * CL)) - 1u);
+  const uint16_t pair_ctas = (uint16_t)(0x3u << (2 * pc));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);     // leader: its expect_tx; both halves' bytes
-      mbar_init(empty_bar(s), CL);   // one multicast commit per pair and use
+      mbar_init(empty_bar(s), 1);    // one multicast commit per use
     }
     for (int a = 0; a < NACC; ++a) {
       mbar_init(tfull_bar(a), 1);    // one multicast commit per tile
@@ -165,7 +166,6 @@ __global__ void __cluster_dims__(2 * CL, 1, 1) __launch_bounds__(Shape<NSUB>::TH
   if (warp == 0 && lane == 0) {
     // ---------------- TMA producer (both CTAs) ----------------
     const uint32_t leader_full0 = map_to_rank(full_bar(0), lead);
-    const uint16_t share = (uint16_t)((1u << rank) | (1u << (rank ^ 2u)));   // CL = 2
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -192,20 +192,11 @@ __global__ void __cluster_dims__(2 * CL, 1, 1) __launch_bounds__(Shape<NSUB>::TH
             const int b_col = tc.nt * BN + sub * 256 + (int)r2 * 128;
             const uint32_t bs = b_dst + sub * B_SUB_BYTES;
             if (p.b_kmajor) {
-              // 128 rows x 128 B; shared: the pair whose index is sub % 2 loads it
-              if (CL == 1)
-                tma_load_3d_pair(bs, &p.tw[r], fb, kb * BK, b_col, e);
-              else if (sub % 2 == pc)
-                tma_load_3d_pair_mc(bs, &p.tw[r], fb, kb * BK, b_col, e, share);
+              tma_load_3d_pair(bs, &p.tw[r], fb, kb * BK, b_col, e);   // 128 rows x 128 B
             } else {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                if (CL == 1)
-                  tma_load_3d_pair(bs + c * B_BOX_BYTES, &p.tw[r], fb, b_col + c * 64, kb * BK, e);
-                else if ((sub * 2 + c) % 2 == pc)   // boxes dealt over the two pairs
-                  tma_load_3d_pair_mc(bs + c * B_BOX_BYTES, &p.tw[r], fb, b_col + c * 64,
-                                      kb * BK, e, share);
-              }
+              for (int c = 0; c < 2; ++c)
+                tma_load_3d_pair(bs + c * B_BOX_BYTES, &p.tw[r], fb, b_col + c * 64, kb * BK, e);
             }
           }
           if (++stage == STAGES) {
@@ -244,14 +235,14 @@ __global__ void __cluster_dims__(2 * CL, 1, 1) __launch_bounds__(Shape<NSUB>::TH
                       rd.b0 + so + (uint64_t)((sub * B_SUB_BYTES) >> 4) + rd.b_kstep * k, p.idesc,
                       (kk > 0 || k > 0) ? 1u : 0u);
         }
-        tc_commit_pair(empty_bar(stage), kAllCtas);
+        tc_commit_pair(empty_bar(stage), pair_ctas);
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1u;
         }
       }
       if (!ok) break;
-      tc_commit_pair(tfull_bar(acc), (uint16_t)(0x3u << (2 * pc)));
+      tc_commit_pair(tfull_bar(acc), pair_ctas);
       if (++acc == NACC) {
         acc = 0;
         acc_phase ^= 1u;
@@ -366,7 +357,7 @@ int fused_tc2_tile_n(const FusedProblem& f) {
   return K >= 8192 && f.H >= 1024 && tiles >= 38 ? 512 : 256;
 }
 
-// Whether two pairs share each weight box (clusters of four CTAs).
+// Whether two pairs that read the same weight boxes form a cluster (of four CTAs).
 // BRA_TC2_SHARE=0|1, read at every call, forces the choice.
 #ifndef BRA_TC2_SHARE_DEFAULT
 #define BRA_TC2_SHARE_DEFAULT 0

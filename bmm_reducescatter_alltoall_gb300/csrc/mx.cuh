@@ -26,9 +26,11 @@ constexpr int kUnitBytes = 1024;
 __host__ __device__ inline int64_t code_pitch(int64_t K) { return (K + 31) / 32 * 16; }
 __host__ __device__ inline int64_t units(int64_t K) { return (K + kUnitK - 1) / kUnitK; }
 // Row blocks held for R rows in E groups: of `each` rows, or (0) of any sizes
-// that add up to at most R.
+// that add up to at most R: n rows take (n + 127) / 128 blocks, and at most
+// min(R, E) groups have rows.  For one group the two are the same, as rows of
+// one group may be quantized either way.
 __host__ __device__ inline int64_t blocks_of(int64_t R, int64_t E, int64_t each) {
-  return each > 0 ? E * ((each + 127) / 128) : R / 128 + (R < E ? R : E);
+  return each > 0 ? E * ((each + 127) / 128) : (R + 127 * (R < E ? R : E)) / 128;
 }
 // Byte of scale s (of the whole row) in row r (0..127) of row block `blk`.
 __host__ __device__ inline int64_t scale_at(int64_t blk, int r, int64_t s, int64_t k_units) {

@@ -302,3 +302,22 @@ def test_dispatch_workspace(lib):
     assert lib.moe_dispatch(x, t, y, w, 16384 * 17 * 4 - 1, a, None) == INVALID
     assert lib.moe_dispatch(x, t, y, w + 128, 1 << 30, a, None) == INVALID
     assert lib.moe_dispatch(x, t, y, y + 256, 1 << 30, a, None) == INVALID
+
+
+def test_scale_blocks_hold_every_grouping(lib):
+    """The product's map of the rows' scales ends where mxfp4_scale_bytes ends, so no tile may ask
+    for a block in between the rows' last one and the map's end: with one group, which may have
+    been quantized without counts, the two sizes are the same; with several, some grouping needs
+    every block."""
+    def blocks(R, E, each):
+        return lib.mxfp4_scale_bytes(ctypes.byref(mx(rows=R, groups=E, rows_per_group=each))) // 1024
+    for R in list(range(1, 1300)) + [16512, 16513, (1 << 31) - (1 << 16)]:
+        assert blocks(R, 1, 0) == blocks(R, 1, R) == -(-R // 128), R
+    for E in (2, 3, 8, 512):
+        for R in (1, 2, 127, 128, 129, 255, 256, 257, 383, 384, 385, 1000, 4096, 70000):
+            few = min(E, R)
+            counts = [1] * (few - 1) + [R - few + 1]         # one row here, the rest there
+            most = max(sum(-(-n // 128) for n in counts),
+                       sum(-(-n // 128) for n in [129] * ((R - 1) // 129) + [R - (R - 1) // 129 * 129])
+                       if -(-R // 129) <= E else 0)
+            assert most <= blocks(R, E, 0) <= (R + 127 * few) // 128, (R, E)

@@ -284,3 +284,17 @@ def test_refused_arguments():
         bra.mxfp4_grouped_matmul(q, wq, c, bias=b.half())
     with pytest.raises(ValueError):
         bra.mxfp4_grouped_matmul(q, bra.mxfp4_quantize(w[:, :, :32].contiguous()), c)
+
+
+@pytest.mark.parametrize("R,N", [(384, 13312), (1152, 8192), (16512, 4096)])
+def test_one_expert_without_counts_in_256_row_tiles(R, N):
+    """An odd number of 128-row blocks in tiles of 256 rows: the second half of the last tile has
+    no rows, and no scales in the buffer either."""
+    x, w, b, c = case([R], 288, N)
+    assert bra.mxfp4_quantize(x).scales.numel() == bra.mxfp4_quantize(x, c).scales.numel()
+    a = bra.mxfp4_grouped_matmul(bra.mxfp4_quantize(x), bra.mxfp4_quantize(w), c, bias=b)
+    z = bra.mxfp4_grouped_matmul(bra.mxfp4_quantize(x, c), bra.mxfp4_quantize(w), c, bias=b)
+    assert torch.equal(a, z)
+    for at in (slice(0, 40), slice(R - 40, R)):
+        assert_close(a[at], *reference(x[at], w, b, [40]), 288)
+    assert bra.fault_status() == 0

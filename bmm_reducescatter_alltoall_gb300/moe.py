@@ -350,6 +350,25 @@ class MxTensor:
         return a
 
 
+def _holds(t: MxTensor, what: str) -> MxArgs:
+    """The arguments of an MxTensor, after a check that its buffers hold what they say."""
+    torch = _bra._torch()
+    if len(t.shape) != 2 and (len(t.shape) != 3 or t.counts is not None):
+        raise ValueError(f"{what} must hold rows (R, K) or matrices (E, N, K), got {t.shape}")
+    if t.counts is not None:
+        _counts(t.counts)
+    a, lib = t._args(), _bra.library()
+    for part, size in (("codes", lib.mxfp4_code_bytes), ("scales", lib.mxfp4_scale_bytes)):
+        buf, need = getattr(t, part), size(ctypes.byref(a))
+        if need < 0:
+            raise _bra.BraError(-need, what)
+        _bra._dev_tensor(buf, f"{what}'s {part}", torch.uint8)
+        if buf.numel() < need:
+            raise ValueError(f"{what}'s {part} have {buf.numel()} bytes, {t.shape} takes {need}")
+    _same_device(t.codes, t.scales, t.counts)
+    return a
+
+
 def mxfp4_quantize_plan(x, counts=None, out: Optional[MxTensor] = None, status=None):
     """mxfp4_quantize prepared once (see Plan); plan.run() returns the MxTensor."""
     torch = _bra._torch()
@@ -376,9 +395,10 @@ def mxfp4_quantize_plan(x, counts=None, out: Optional[MxTensor] = None, status=N
         new = lambda n: torch.empty(n, dtype=torch.uint8, device=x.device)   # noqa: E731
         out = MxTensor(new(cb).view(shape[:-1] + (-(-shape[-1] // 32) * 16,)), new(sb), shape,
                        counts)
-    elif out.shape != shape or out.codes.numel() < cb or out.scales.numel() < sb or \
-            out.counts is not counts:
+    elif out.shape != shape or out.counts is not counts:
         raise ValueError(f"out holds {out.shape} and its own counts, expected {shape} with counts")
+    else:
+        _holds(out, "out")
     _same_device(x, out.codes, out.scales, counts, status)
     a = probe
     a.x_pitch, a.dtype, a.status = pitch, code, _status(status)
@@ -405,11 +425,11 @@ def mxfp4_dequantize_plan(q: MxTensor, dtype, out=None, status=None):
     codes = {torch.float16: _bra.FP16, torch.bfloat16: _bra.BF16, torch.float32: _bra.FP32}
     if dtype not in codes:
         raise TypeError(f"mxfp4_dequantize gives float16, bfloat16 or float32, got {dtype}")
+    a = _holds(q, "q")
     if out is None:
         out = torch.empty(q.shape, dtype=dtype, device=q.device)
     _dense(out, "out", dtype, q.shape)
-    _same_device(q.codes, q.scales, q.counts, out, status)
-    a = q._args()
+    _same_device(q.codes, out, status)
     a.dtype, a.status = codes[dtype], _status(status)
     args = (_ptr(q.codes), _ptr(q.scales), _ptr(q.counts), _ptr(out), ctypes.byref(a))
     return _bra.Plan(_bra.library().mxfp4_dequantize, args, "mxfp4_dequantize", out,
@@ -434,8 +454,10 @@ def mxfp4_grouped_matmul_plan(x: MxTensor, weight: MxTensor, counts, bias=None, 
     if K != Kw:
         raise ValueError(f"x has rows of {K}, weight takes {Kw}")
     _counts(counts, E)
-    if x.counts is None and E != 1 or \
-            x.counts is not None and x.counts.data_ptr() != counts.data_ptr():
+    _holds(x, "x")
+    _holds(weight, "weight")
+    if x.counts is None and E != 1 or x.counts is not None and \
+            (x.counts.data_ptr() != counts.data_ptr() or x.counts.numel() != E):
         raise ValueError("x has to be quantized with these counts: its scales are grouped by them")
     dt = dtype if dtype is not None else out.dtype if out is not None else torch.bfloat16
     code = _bra._fused_dtype(dt)

@@ -298,3 +298,41 @@ def test_one_expert_without_counts_in_256_row_tiles(R, N):
     for at in (slice(0, 40), slice(R - 40, R)):
         assert_close(a[at], *reference(x[at], w, b, [40]), 288)
     assert bra.fault_status() == 0
+
+
+def test_buffers_and_counts_that_do_not_fit_are_refused():
+    """The kernels read what an MxTensor says it holds: its buffers have to hold it, and rows have to
+    be grouped by all of the product's counts, not by the first of them."""
+    x, w, b, c = case([20, 4, 30, 2], 320, 264)
+    q, wq = bra.mxfp4_quantize(x, c), bra.mxfp4_quantize(w)
+
+    def with_(t, codes=None, scales=None, shape=None, counts=None):
+        return bra.MxTensor(t.codes if codes is None else codes, t.scales if scales is None else scales,
+                            t.shape if shape is None else shape, t.counts if counts is None else counts)
+    part = bra.mxfp4_quantize(x, c[:2])
+    assert part.counts.data_ptr() == c.data_ptr()
+    with pytest.raises(ValueError):
+        bra.mxfp4_grouped_matmul(part, wq, c)
+    short = [with_(q, codes=q.codes[:-1]), with_(q, scales=q.scales[:-1]),
+             with_(q, shape=(57, 320)), with_(q, shape=(56, 353))]
+    wrong = [with_(q, codes=q.codes.float()), with_(q, scales=q.scales.int()),
+             with_(q, codes=None, scales=[1])]
+    other = [with_(q, codes=q.codes.cpu()), with_(q, codes=q.codes[:, ::2]),
+             with_(q, scales=q.scales[::2])]
+    for bad, error in [(t, ValueError) for t in short + other] + [(t, TypeError) for t in wrong]:
+        with pytest.raises(error):
+            bra.mxfp4_dequantize(bad, torch.float32)
+        with pytest.raises(error):
+            bra.mxfp4_quantize(torch.zeros(bad.shape, dtype=x.dtype, device="cuda"), c, out=bad)
+        if bad.shape[1] == 320:
+            with pytest.raises(error):
+                bra.mxfp4_grouped_matmul(bad, wq, c)
+    for bad in (with_(wq, codes=wq.codes[:3]), with_(wq, scales=wq.scales[:-1]),
+                with_(wq, shape=(4, 385, 320))):
+        with pytest.raises(ValueError):
+            bra.mxfp4_grouped_matmul(q, bad, c)
+    # larger buffers serve, as they did
+    big = bra.MxTensor(torch.empty(70 * 160, dtype=torch.uint8, device="cuda"),
+                       torch.empty(8 * 2048, dtype=torch.uint8, device="cuda"), (56, 320), c)
+    bra.mxfp4_quantize(x, c, out=big)
+    assert torch.equal(bra.mxfp4_grouped_matmul(big, wq, c), bra.mxfp4_grouped_matmul(q, wq, c))

@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -36,6 +37,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMostChunk = 1024;          // most tokens of a chunk
 constexpr float kLargest = 3.402823466e+38f;
 
 template <typename T>
@@ -499,6 +501,27 @@ cudaError_t by_type(int dtype, int E, F&& f) {
   return by_lanes((__half*)nullptr);
 }
 
+// Lets the kernel have the shared memory of its largest call, once a device.
+// The limit belongs to the kernel, not to a call: set to a call's own size it
+// could be lowered between another thread's setting and its launch.
+template <typename T, int L, int V>
+cudaError_t choose_ready() {
+  constexpr int most = (L * V < kMaxGroups ? L * V : kMaxGroups) * bit_stride(kMostChunk) * 4;
+  static std::mutex mu;
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!ready[dev & 63]) {
+    e = cudaFuncSetAttribute(route_choose_kernel<T, L, V>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    ready[dev & 63] = true;
+  }
+  return cudaSuccess;
+}
+
 // Whether rows of E elements can be read four at a time.
 int rows_vec(const void* p, int E, int dtype) {
   return E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & (dtype == BRA_FP32 ? 15u : 7u)) == 0;
@@ -507,10 +530,10 @@ int rows_vec(const void* p, int E, int dtype) {
 }  // namespace
 
 // Tokens of a chunk: one chunk up to 64 tokens (one launch); else chunks of at
-// most 1024 tokens, as many for each of 152 SMs.
+// most kMostChunk tokens, as many for each of 152 SMs.
 int route_chunk(int64_t T) {
   if (T <= 64) return 64;
-  const int64_t chunks = (T + 152 * 1024 - 1) / (152 * 1024) * 152;
+  const int64_t chunks = (T + 152 * kMostChunk - 1) / (152 * kMostChunk) * 152;
   return (int)(((T + chunks - 1) / chunks + 31) / 32 * 32);
 }
 
@@ -530,12 +553,8 @@ cudaError_t launch_route(const RouteCall& r, cudaStream_t st) {
   const int smem = r.E * bit_stride(p.chunk) * 4;
   const cudaError_t e = by_type(r.dtype, r.E, [&](auto* type, auto l, auto v) {
     using T = std::remove_pointer_t<decltype(type)>;
-    if (smem > 32768) {
-      const cudaError_t a =
-          cudaFuncSetAttribute(route_choose_kernel<T, decltype(l)::value, decltype(v)::value>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (a != cudaSuccess) return a;
-    }
+    const cudaError_t a = choose_ready<T, decltype(l)::value, decltype(v)::value>();
+    if (a != cudaSuccess) return a;
     return launch_overlapped(route_choose_kernel<T, decltype(l)::value, decltype(v)::value>,
                              (unsigned)p.chunks, kThreads, smem, st, p);
   });

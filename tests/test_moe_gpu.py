@@ -7,6 +7,7 @@ then errs by |l - m| units), the exponential and the quotient by a few units of
 err by one fp32 unit (2^-23 of the magnitude sum) an addition, and are rounded
 once to the row type; dot products of H by H/256 + 16 units."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -374,3 +375,33 @@ def test_refused_arguments():
     with pytest.raises(bra.BraError) as err:
         bra.moe_combine(ys, r["slots"], r["weights"], out=ys[2:6])
     assert err.value.code == bra.ERR_INVALID
+
+
+def test_routes_of_different_sizes_from_two_threads():
+    """Calls whose shared memory differs, from host threads at once: neither is refused, both are
+    right.  (512 experts: 62 KB for 150000 tokens, 42 KB for 200000.)"""
+    sizes = [(150000, 512), (200000, 512), (150000, 400), (160000, 300)]
+    plans = [bra.moe_route_plan(logits_of(T, E, torch.bfloat16, seed=E + T), 1) for T, E in sizes]
+    want = []
+    for p in plans:
+        p.run()
+        want.append({n: t.clone() for n, t in p.result.items()})
+    torch.cuda.synchronize()
+    streams, failed = [torch.cuda.Stream() for _ in plans], []
+
+    def loop(plan, stream):
+        try:
+            for _ in range(400):
+                plan.run(stream)
+        except Exception as e:                                # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=loop, args=a) for a in zip(plans, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed[:2]
+    for p, w in zip(plans, want):
+        for n in w:
+            assert torch.equal(p.result[n], w[n]), n

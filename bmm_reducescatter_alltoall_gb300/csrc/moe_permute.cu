@@ -312,11 +312,12 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
   }
   if (row_tokens) {
-    // rows without a token: a warp looks at 32 rows at once
+    // rows without a token (none in [0, tokens)): a warp looks at 32 rows at once
     const int64_t warps = (int64_t)gridDim.x * kWarps;
     const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int64_t r0 = ((int64_t)blockIdx.x * kWarps + warp) * 32; r0 < R; r0 += warps * 32) {
-      uint32_t idle = __ballot_sync(0xffffffffu, r0 + lane < R && __ldg(row_tokens + r0 + lane) < 0);
+      const int t = r0 + lane < R ? __ldg(row_tokens + r0 + lane) : 0;
+      uint32_t idle = __ballot_sync(0xffffffffu, r0 + lane < R && (t < 0 || t >= tokens));
       for (; idle; idle &= idle - 1) {
         T* row = dys + (r0 + __ffs(idle) - 1) * H;
         for (int base = 0; base < H; base += 256) Eight<T, VEC>::store(row, base, lane, H, z);

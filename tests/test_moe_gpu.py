@@ -405,3 +405,23 @@ def test_routes_of_different_sizes_from_two_threads():
     for p, w in zip(plans, want):
         for n in w:
             assert torch.equal(p.result[n], w[n]), n
+
+
+@pytest.mark.parametrize("T,dt,H", [(2, torch.float32, 64), (2, torch.bfloat16, 1031),
+                                    (0, torch.float16, 264)])
+def test_combine_gradient_of_rows_whose_token_is_out_of_range(T, dt, H):
+    """Tokens outside [0, T) count as -1: their rows get zeros."""
+    slots = torch.tensor([[0, 5], [-3, 4]], dtype=torch.int32, device="cuda")[:T]
+    w = torch.ones((T, 2), device="cuda")
+    ys = torch.randn((7, H), device="cuda").to(dt)
+    dy = torch.randn((T, H), device="cuda").to(dt)
+    tokens = torch.tensor([0, T, -5, 2 ** 31 - 1, 1, 0, -1], dtype=torch.int32, device="cuda")
+    if T == 0:
+        tokens[[0, 4, 5]] = -1
+    dys = torch.full_like(ys, float("nan"))
+    bra.moe_combine_grad(dy, ys, slots, w, tokens, dys=dys)
+    assert not dys[[1, 2, 3, 6]].any()
+    if T:
+        assert all(torch.equal(dys[r], dy[t]) for r, t in ((0, 0), (5, 0), (4, 1)))
+    else:
+        assert not dys.any()

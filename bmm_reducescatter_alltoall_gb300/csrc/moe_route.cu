@@ -451,15 +451,19 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
       for (int m = L / 2; m > 0; m >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, m));
       const float m = value_of(best);
       float sum = 0.f;
+      uint32_t open = 0u;            // bit i: whether this lane's logit i is open
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        d[i] = key_of(d[i]) ? expf(d[i] - m) : 0.f;
+        const bool is = key_of(d[i]) != 0u;
+        open |= (is ? 1u : 0u) << i;
+        d[i] = is ? expf(d[i] - m) : 0.f;
         sum += d[i];
       }
       sum = group_sum(sum, L);
       const float f = sum > 0.f ? -s / sum : 0.f;
+      // a closed expert gets 0 whatever f is: 0 times an infinite s is NaN
 #pragma unroll
-      for (int i = 0; i < V; ++i) d[i] *= f;
+      for (int i = 0; i < V; ++i) d[i] = (open >> i) & 1u ? d[i] * f : 0.f;
     }
     T* out = static_cast<T*>(p.dlogits) + t * p.E;
 #pragma unroll

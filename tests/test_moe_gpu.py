@@ -425,3 +425,21 @@ def test_combine_gradient_of_rows_whose_token_is_out_of_range(T, dt, H):
         assert all(torch.equal(dys[r], dy[t]) for r, t in ((0, 0), (5, 0), (4, 1)))
     else:
         assert not dys.any()
+
+
+@pytest.mark.parametrize("E,k", [(12, 3), (300, 16)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradients_that_are_not_finite_leave_closed_experts_at_zero(E, k, renorm):
+    l = logits_of(6, E, torch.float32, seed=E)
+    l[:, ::3] = -math.inf
+    l[4] = -math.inf
+    l[4, 5] = 1.0
+    dw = torch.randn((6, k), device="cuda")
+    r = bra.moe_route(l, k, renormalize=renorm)
+    want = bra.moe_route_grad(dw, l, r["ids"], r["weights"], renormalize=renorm)
+    dw[0, 1], dw[1, 0], dw[2] = math.inf, math.nan, -math.inf
+    dw[4, 1:] = math.nan                                      # choices that are missing
+    dl = bra.moe_route_grad(dw, l, r["ids"], r["weights"], renormalize=renorm)
+    assert not dl[l == -math.inf].any()
+    assert torch.equal(dl[3:], want[3:])
+    assert not torch.isfinite(dl[:3]).all(1).any()

@@ -26,7 +26,7 @@ __device__ __forceinline__ void build_table(GroupTable* t, const int64_t* counts
   int64_t c[kMaxGroups / 32];
 #pragma unroll
   for (int i = 0; i < kMaxGroups / 32; ++i)
-    c[i] = i * 32 + lane < E ? __ldg(reinterpret_cast<const long long*>(counts) + i * 32 + lane) : 0;
+    c[i] = i * 32 + lane < E ? __ldcg(reinterpret_cast<const long long*>(counts) + i * 32 + lane) : 0;
   int64_t rows = 0;
   int32_t tiles = 0;
   bool bad = false;

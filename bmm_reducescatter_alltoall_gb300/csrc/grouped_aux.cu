@@ -40,7 +40,7 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
 #pragma unroll
     for (int i = 0; i < kMaxGroups / 32; ++i) {
       const int g = i * 32 + tid;
-      const int64_t n = g < E ? __ldg(reinterpret_cast<const long long*>(counts) + g) : 0;
+      const int64_t n = g < E ? __ldcg(reinterpret_cast<const long long*>(counts) + g) : 0;
       wrong = wrong || n < 0 || n > R;
       total += n;
       before += g < e ? n : 0;
@@ -79,7 +79,7 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
       uint4 w[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        w[u] = __ldg(reinterpret_cast<const uint4*>(p + (r + u * kBgRows) * ld));
+        w[u] = __ldcg(reinterpret_cast<const uint4*>(p + (r + u * kBgRows) * ld));
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const T* h = reinterpret_cast<const T*>(&w[u]);
@@ -88,7 +88,7 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
       }
     }
     for (; r < b; r += kBgRows) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p + r * ld));
+      const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p + r * ld));
       const T* h = reinterpret_cast<const T*>(&w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] += static_cast<float>(h[i]);
@@ -108,9 +108,12 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
     const int col = tid & 63, q = tid >> 6;
     float t = 0.f;
     if (n0 + col < N) {
-      const T* p = dy + n0 + col;
+      const unsigned short* p = reinterpret_cast<const unsigned short*>(dy) + n0 + col;
 #pragma unroll 16
-      for (int64_t r = a + q; r < b; r += 8) t += static_cast<float>(p[r * ld]);
+      for (int64_t r = a + q; r < b; r += 8) {
+        const unsigned short h = __ldcg(p + r * ld);
+        t += static_cast<float>(*reinterpret_cast<const T*>(&h));
+      }
     }
     part[q][col] = t;
   }
@@ -165,31 +168,29 @@ __global__ void __launch_bounds__(256) pack_rows_kernel(const __grid_constant__ 
       if (total <= 0xffffffffll) r = (uint32_t)u / (uint32_t)chunks;
       else r = u / chunks;
       const int64_t c = u - r * chunks;
-      if (job.per_group > 0 &&
-          __ldg(reinterpret_cast<const long long*>(jobs.counts) + r / job.per_group) == 0)
-        continue;
+      if (job.per_group > 0 && jobs.counts[r / job.per_group] == 0) continue;
       const uint16_t* s = src + r * ld + c * 8;
       const int n = (int)min((int64_t)8, len - c * 8);
       uint32_t w[4] = {0, 0, 0, 0};
       const uintptr_t at = reinterpret_cast<uintptr_t>(s);
       if (n == 8 && (at & 15) == 0) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(s));
+        const uint4 q = *reinterpret_cast<const uint4*>(s);
         w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
       } else if (n == 8 && (at & 3) == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
+        for (int i = 0; i < 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(s)[i];
       } else if (n == 8) {
         uint32_t v[5];
-        v[0] = (uint32_t)__ldg(s) << 16;
+        v[0] = (uint32_t)*s << 16;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) v[i + 1] = __ldg(reinterpret_cast<const uint32_t*>(s + 1) + i);
-        v[4] = __ldg(s + 7);
+        for (int i = 0; i < 3; ++i) v[i + 1] = reinterpret_cast<const uint32_t*>(s + 1)[i];
+        v[4] = s[7];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], 16);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i < n) w[i >> 1] |= (uint32_t)__ldg(s + i) << ((i & 1) * 16);
+          if (i < n) w[i >> 1] |= (uint32_t)s[i] << ((i & 1) * 16);
     }
       dst[u] = make_uint4(w[0], w[1], w[2], w[3]);
     }

@@ -112,9 +112,9 @@ __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, ui
       T raw[4];
       if (t >= 0 && p.vec && at + 4 <= p.E) {
         if constexpr (sizeof(T) == 4)
-          *reinterpret_cast<uint4*>(raw) = __ldg(reinterpret_cast<const uint4*>(row + at));
+          *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(row + at);
         else
-          *reinterpret_cast<uint2*>(raw) = __ldg(reinterpret_cast<const uint2*>(row + at));
+          *reinterpret_cast<uint2*>(raw) = *reinterpret_cast<const uint2*>(row + at);
       } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c) raw[c] = t >= 0 && at + c < p.E ? row[at + c] : T(-INFINITY);
@@ -416,9 +416,9 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
     for (int o = 0; o < OWN; ++o) {
       const int j = o * L + gl;
       const bool have = t < p.T && j < p.k;
-      id_next[o] = have ? __ldg(p.ids + t * p.k + j) : -1;
-      w_next[o] = have ? __ldg(p.weights + t * p.k + j) : 0.f;
-      g_next[o] = have ? __ldg(p.dweights + t * p.k + j) : 0.f;
+      id_next[o] = have ? p.ids[t * p.k + j] : -1;
+      w_next[o] = have ? p.weights[t * p.k + j] : 0.f;
+      g_next[o] = have ? p.dweights[t * p.k + j] : 0.f;
     }
   };
   fetch(first + lane / L);

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads)
     if (vec && (b + 1) * mx::kBlock <= K) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        const uint4 q = reinterpret_cast<const uint4*>(src)[i];
         w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
       }
     } else {
@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(kThreads)
       const int64_t left = K - (int64_t)b * mx::kBlock;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const uint32_t lo = 2 * i < left ? __ldg(e + 2 * i) : 0u;
-        const uint32_t hi = 2 * i + 1 < left ? __ldg(e + 2 * i + 1) : 0u;
+        const uint32_t lo = 2 * i < left ? e[2 * i] : 0u;
+        const uint32_t hi = 2 * i + 1 < left ? e[2 * i + 1] : 0u;
         w[i] = lo | hi << 16;
       }
     }
@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < kPieces; ++i) {
       c[i] = b[i] = 0u;
       if (k0 + i * mx::kUnitK < K) {
-        c[i] = __ldg(reinterpret_cast<const uint32_t*>(code + i * (mx::kUnitK / 2)));
-        b[i] = __ldg(scale + i * mx::kUnitBytes);     // a unit's scales are a unit's bytes on
+        c[i] = *reinterpret_cast<const uint32_t*>(code + i * (mx::kUnitK / 2));
+        b[i] = scale[i * mx::kUnitBytes];     // a unit's scales are a unit's bytes on
       }
     }
 #pragma unroll

@@ -21,3 +21,22 @@ def test_no_bulk_copy_is_multicast():
     memory alone (a commit's arrivals are no copies)."""
     for name, text in sources():
         assert not re.search(r"cp\.(async|reduce)[\w.:]*multicast", text), name
+
+
+# Kernels that begin before the one ahead of them in the stream has ended, and what they share.
+OVERLAPPED = {"grouped_aux.cu", "grouped_split.cu", "grouped_tc.cu", "moe_permute.cu", "moe_route.cu",
+              "mx_quant.cu", "mx_tc.cu"}
+SHARED = {"grouped.cuh", "launch.cuh", "mx.cuh", "walk.cuh", "moe_internal.h"}
+
+
+def test_overlapped_kernels_read_with_loads_that_see_writes():
+    """Their inputs may be written while they already run: no load for constant data."""
+    seen = set()
+    for name, text in sources():
+        if name.endswith(".cu"):
+            assert (name in OVERLAPPED) == ("ProgrammaticStreamSerialization" in text or
+                                            "launch_overlapped" in text), name
+        if name in OVERLAPPED | SHARED:
+            seen.add(name)
+            assert not re.search(r"__ldg\b|__restrict__|__restrict\b|ld\.global[\w.]*\.nc\b", text), name
+    assert seen >= OVERLAPPED

@@ -129,6 +129,7 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
     if (late) grid_wait();
     return;
   }
+  __syncwarp();
   cluster_sync();
   if (rank == 0 && tid < 64 && n0 + tid < N) {
     float t = 0.f;
@@ -143,6 +144,7 @@ __global__ void __cluster_dims__(SPLIT, 1, 1) __launch_bounds__(kBgThreads)
     }
     db[(int64_t)e * N + n0 + tid] = static_cast<B>(t);
   }
+  __syncwarp();     // columns past N were left out
   cluster_sync();   // the peers' sums have been read
   if (late) grid_wait();
 }

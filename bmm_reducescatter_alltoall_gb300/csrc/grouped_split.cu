@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   }
+  __syncwarp();                     // lanes past the matrix stored nothing, or element by element
   cluster_sync();                   // the peers have read this CTA's share
   if (threadIdx.x == 0 && p.status) {
     if (gt->bad) atomicExch(p.status, (int32_t)BRA_ERR_INVALID);

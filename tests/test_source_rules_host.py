@@ -40,3 +40,14 @@ def test_overlapped_kernels_read_with_loads_that_see_writes():
             seen.add(name)
             assert not re.search(r"__ldg\b|__restrict__|__restrict\b|ld\.global[\w.]*\.nc\b", text), name
     assert seen >= OVERLAPPED
+
+
+def test_cluster_barriers_follow_a_barrier_of_the_warp():
+    """Their instructions are for whole warps (.aligned): the lanes have to be together again."""
+    found = 0
+    for name, text in sources():
+        for m in re.finditer(r"cluster_sync\(\);", text):
+            found += 1
+            assert re.search(r"__sync(threads|warp)\(\);\s*(}\s*)?(if \(CG == 2\) )?$",
+                             text[:m.start()]), (name, text[m.start() - 120:m.end()])
+    assert found > 8

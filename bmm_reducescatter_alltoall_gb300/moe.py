@@ -176,8 +176,12 @@ def _take_workspace(workspace, need: int, device, args):
             raise ValueError('workspace must be a CUDA tensor, None or "auto"')
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     if workspace is not None:
+        if not hasattr(workspace, "data_ptr"):
+            raise TypeError('workspace must be a CUDA tensor, None or "auto"')
         if not (workspace.is_cuda and workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous CUDA tensor")
+        if workspace.device != device:
+            raise ValueError(f"workspace must be on {device} (got {workspace.device})")
         if workspace.numel():
             args.workspace = workspace.data_ptr()
             args.workspace_bytes = workspace.numel() * workspace.element_size()

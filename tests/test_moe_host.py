@@ -321,3 +321,24 @@ def test_scale_blocks_hold_every_grouping(lib):
                        sum(-(-n // 128) for n in [129] * ((R - 1) // 129) + [R - (R - 1) // 129 * 129])
                        if -(-R // 129) <= E else 0)
             assert most <= blocks(R, E, 0) <= (R + 127 * few) // 128, (R, E)
+
+
+def test_workspace_of_another_device_is_refused():
+    torch = pytest.importorskip("torch")
+
+    class Scratch:
+        is_cuda, device = True, torch.device("cuda", 1)
+        is_contiguous = staticmethod(lambda: True)
+        numel = staticmethod(lambda: 4096)
+        element_size = staticmethod(lambda: 1)
+        data_ptr = staticmethod(lambda: S)
+
+    a = bra.GroupedArgs()
+    with pytest.raises(ValueError):
+        bra.moe._take_workspace(Scratch(), 256, torch.device("cuda", 0), a)
+    assert not a.workspace
+    bra.moe._take_workspace(Scratch(), 256, torch.device("cuda", 1), a)
+    assert a.workspace == S and a.workspace_bytes == 4096
+    for bad in (5, [1, 2]):
+        with pytest.raises(TypeError):
+            bra.moe._take_workspace(bad, 256, torch.device("cuda", 0), a)

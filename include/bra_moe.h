@@ -4,9 +4,12 @@
  * same products on 4-bit microscaled weights and rows; the router that makes
  * the groups, and the moves of token rows to their experts and back.
  *
- * They work on what a variable-count exchange delivers: one matrix of rows
- * sorted by expert, and the number of rows of each expert in device memory
- * (int64, the type of all_to_all_v's counts).  The conventions of
+ * They work on one matrix of rows sorted by expert, and the number of rows of
+ * each expert in device memory (int64).  all_to_all_v counts elements, not
+ * rows, and delivers by source rank: what a rank of one expert receives is
+ * such a matrix as it stands, what one of several receives is in (source,
+ * expert) order and is sorted by moe_dispatch, given the order of its rows.
+ * The conventions of
  * bmm_rs_a2a.h hold: device pointers, row-major tensors, work enqueued on
  * `stream`, status codes, no device memory allocated, thread-safe, no state
  * from one call to the next.
@@ -200,8 +203,9 @@ typedef struct {
  *   ids     (T, k) int32.
  *   weights (T, k) fp32: the softmax over the token's open experts at the
  *           chosen ones; with renormalize divided by their sum.
- *   counts  (E) int64: pairs of each expert: grouped_matmul's and, as a row
- *           of its matrix, all_to_all_v's counts.
+ *   counts  (E) int64: pairs (rows) of each expert: grouped_matmul's counts.
+ *           Added up over a rank's experts, times the elements of a row, they
+ *           are a row of all_to_all_v's send_counts.
  *   slots   (T, k) int32: the pair's row among the R = T * k rows sorted by
  *           expert, within an expert by token.
  *   tokens  (R) int32: the token of each row; -1 for the rows past the last

@@ -130,3 +130,37 @@ def test_a_training_step_in_a_graph():
             p.run()
         for a, z in zip(flat(), want):
             assert torch.equal(a, z)
+
+
+def test_rows_of_several_ranks_reach_their_experts():
+    """The router's rows through all_to_all_v to ranks of several experts and on to their products:
+    counts are turned into elements on the way, and what arrives by source is sorted by expert."""
+    P, El, T, H, N, k = 3, 4, 70, 40, 48, 2
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")                    # noqa: E731
+    x = [rnd(T, H).bfloat16() for _ in range(P)]
+    w = (rnd(P * El, H, N) * H ** -0.5).bfloat16()
+    r = [bra.moe_route(rnd(T, P * El), k) for _ in range(P)]
+    xs = [bra.moe_dispatch(x[i], r[i]["tokens"]) for i in range(P)]
+    counts = torch.stack([t["counts"] for t in r])                 # (source, expert): rows
+    to_rank = counts.view(P, P, El).sum(2)                         # (source, rank): rows
+    got = [torch.empty((n, H), dtype=torch.bfloat16, device="cuda") for n in to_rank.sum(0).tolist()]
+    bra.all_to_all_v([t.view(torch.int8).view(-1) for t in xs], to_rank * (H * 2),
+                     [t.view(torch.int8).view(-1) for t in got], P)
+    for j in range(P):
+        mine = counts[:, j * El:(j + 1) * El]                      # (source, own expert): rows
+        expert = torch.arange(El, device="cuda").repeat(P).repeat_interleave(mine.reshape(-1))
+        order = torch.argsort(expert, stable=True)
+        y = bra.grouped_matmul(bra.moe_dispatch(got[j], order.int()), w[j * El:(j + 1) * El],
+                               mine.sum(0))
+        # by the definition, source by source
+        at = 0
+        for e in range(El):
+            rows = [xs[i][r[i]["counts"][:j * El + e].sum():][:r[i]["counts"][j * El + e]]
+                    for i in range(P)]
+            want = torch.cat(rows).double() @ w[j * El + e].double()
+            # fp32 sums of 40 products, one rounding to bf16
+            assert ((y[at:at + len(want)].double() - want).abs() <=
+                    2.0 ** -8 * want.abs() + 2.0 ** -18).all()
+            at += len(want)
+        assert at == len(y)

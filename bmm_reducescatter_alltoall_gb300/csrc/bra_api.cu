@@ -312,7 +312,7 @@ int run_packed(const bra::FusedProblem& p, const bra_fused_options* opts, cudaSt
   if (q.pw) r.wp = q.wp;
   if (!bra::fused_tc_eligible(r)) return BRA_ERR_UNSUPPORTED;
   const int v = tma_kernel_for(r);
-  if (log_enabled())
+  if (bra::log_enabled())
     std::fprintf(stderr, "[bra] packed: x %s (pitch %d), weight %s (pitch %d), %lld bytes -> %s\n",
                  q.px ? "copied" : "in place", r.xp, q.pw ? "copied" : "in place", r.wp,
                  (long long)q.total, v == BRA_VARIANT_TC2 ? "tc2" : "tc");
@@ -329,11 +329,6 @@ const char* variant_name(int v) {
          : v == BRA_VARIANT_TCR ? "tcr"
          : v == BRA_VARIANT_TCU ? "tcu"
                                 : "simt";
-}
-
-bool log_enabled() {
-  const char* v = std::getenv("BRA_LOG");
-  return v && *v && *v != '0';
 }
 
 int a2av_common(const void* const input[], const int64_t* send_counts,
@@ -379,7 +374,7 @@ int a2av_common(const void* const input[], const int64_t* send_counts,
   a.check_cap = checked ? 1 : 0;
   const int blocks = bra::a2av_launch_blocks(B);
   if (blocks < 1) return BRA_ERR_CUDA;
-  if (log_enabled())
+  if (bra::log_enabled())
     std::fprintf(stderr, "[bra] all_to_all_v P=%lld L=%lld B=%lld blocks=%d\n", (long long)P,
                  (long long)core_num, (long long)B, blocks);
   cudaError_t e = bra::launch_a2av(a, blocks, stream);
@@ -431,7 +426,7 @@ int ia2av_common(const void* const input[], const int64_t in_len[],
   a.esize = dtype == BRA_FP32 ? 4 : 1;
   const int blocks = bra::ia2av_launch_blocks(core_num);
   if (blocks < 1) return BRA_ERR_CUDA;
-  if (log_enabled())
+  if (bra::log_enabled())
     std::fprintf(stderr, "[bra] indexed_all_to_all_v P=%lld L=%lld blocks=%d\n", (long long)P,
                  (long long)core_num, blocks);
   cudaError_t e = cudaSuccess;
@@ -462,7 +457,7 @@ int bmm_rs_a2a_ex(const void* const x[], const void* const weight[],
   if (rc != BRA_OK) return rc;
   const int v = choose_variant(p, opts);
   if (v < 0) return -v;
-  if (log_enabled())
+  if (bra::log_enabled())
     std::fprintf(stderr,
                  "[bra] bmm_rs_a2a ep=%lld tp=%lld E=%lld C=%lld M=%lld H=%lld type=%lld -> %s%s\n",
                  (long long)ep, (long long)tp, (long long)E, (long long)C, (long long)M,

@@ -6,9 +6,17 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cstdlib>
+
 #include "bmm_rs_a2a.h"
 
 namespace bra {
+
+// Whether calls say on stderr which kernel they take (BRA_LOG, read at every call).
+inline bool log_enabled() {
+  const char* v = std::getenv("BRA_LOG");
+  return v && *v && *v != '0';
+}
 
 // all_to_all_v keeps the whole P x P count matrix of int64 in shared memory.
 constexpr int kA2avMaxP = 64;

@@ -551,19 +551,19 @@ cudaError_t launch_t(const GroupedProblem& g, cudaStream_t st) {
 //   128 x 64, 2048, 4096  310 / 222          1024 x 64, 2048, 4096  832 / 839
 //   512 x 64, 2048, 4096  586 / 547          2048 x 64, 2048, 4096 1407 / 1511
 // It takes the pair from 1024 rows an expert on.
-cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st) {
+GroupedTile grouped_fwd_tile(const GroupedProblem& g) {
   int64_t tiles = 0;
   const int split = grouped_split(g, false, &tiles);
-  if (split > 1) return launch_grouped_split(g, false, split, tiles, st);
+  if (split > 1) return {128, 128, split, tiles};
   // rows to an expert on average, and the most experts that can have rows
   const int64_t avg = g.R / g.E, groups = g.R < g.E ? g.R : g.E;
   if (avg < 16) {
     // the weights' bytes bound the call: the widest tiles that still occupy
     // the SMs (a token's two experts, 2048 x 4096: 64 columns, 128 tiles)
     const int64_t mt = g.R / 128 + groups;
-    if (mt * ((g.N + 255) / 256) >= 100) return launch_t<1, 256, false>(g, st);
-    if (mt * ((g.N + 127) / 128) >= 152) return launch_t<1, 128, false>(g, st);
-    return launch_t<1, 64, false>(g, st);
+    if (mt * ((g.N + 255) / 256) >= 100) return {128, 256, 1, 0};
+    if (mt * ((g.N + 127) / 128) >= 152) return {128, 128, 1, 0};
+    return {128, 64, 1, 0};
   }
   const int64_t kb = (g.K + BK - 1) / BK;
   auto cycles = [&](int64_t bm, int64_t bn, int64_t slots, int64_t block, int64_t start) {
@@ -572,16 +572,32 @@ cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st) {
   };
   const int64_t pair = cycles(256, 256, 76, 560, 10000), wide = cycles(128, 256, 152, 850, 3000),
                 narrow = cycles(128, 128, 152, 565, 3000);
-  if (pair <= wide && pair <= narrow) return launch_t<2, 256, false>(g, st);
-  return wide <= narrow ? launch_t<1, 256, false>(g, st) : launch_t<1, 128, false>(g, st);
+  if (pair <= wide && pair <= narrow) return {256, 256, 1, 0};
+  return {128, wide <= narrow ? 256 : 128, 1, 0};
+}
+
+GroupedTile grouped_wgrad_tile(const GroupedProblem& g) {
+  int64_t tiles = 0;
+  const int split = grouped_split(g, true, &tiles);
+  if (split > 1) return {128, 128, split, tiles};
+  if (g.R / g.E >= 1024 && g.K > 128 && g.N > 128) return {256, 256, 1, 0};
+  return {128, g.N > 128 ? 256 : 128, 1, 0};
+}
+
+cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st) {
+  const GroupedTile t = grouped_fwd_tile(g);
+  if (t.split > 1) return launch_grouped_split(g, false, t.split, t.tiles, st);
+  if (t.rows == 256) return launch_t<2, 256, false>(g, st);
+  return t.cols == 256   ? launch_t<1, 256, false>(g, st)
+         : t.cols == 128 ? launch_t<1, 128, false>(g, st)
+                         : launch_t<1, 64, false>(g, st);
 }
 
 cudaError_t launch_grouped_wgrad(const GroupedProblem& g, cudaStream_t st) {
-  int64_t tiles = 0;
-  const int split = grouped_split(g, true, &tiles);
-  if (split > 1) return launch_grouped_split(g, true, split, tiles, st);
-  if (g.R / g.E >= 1024 && g.K > 128 && g.N > 128) return launch_t<2, 256, true>(g, st);
-  return g.N > 128 ? launch_t<1, 256, true>(g, st) : launch_t<1, 128, true>(g, st);
+  const GroupedTile t = grouped_wgrad_tile(g);
+  if (t.split > 1) return launch_grouped_split(g, true, t.split, t.tiles, st);
+  if (t.rows == 256) return launch_t<2, 256, true>(g, st);
+  return t.cols == 256 ? launch_t<1, 256, true>(g, st) : launch_t<1, 128, true>(g, st);
 }
 
 cudaError_t read_grouped_fault_word(int32_t* code, int clear) {

@@ -1,5 +1,6 @@
 // Host entry points of the ragged expert operators: argument checks and
 // launches.  Every rule cited here is stated in include/bra_moe.h.
+#include <cstdio>
 #include <cstring>
 
 #include "moe_internal.h"
@@ -106,6 +107,16 @@ int status_of(cudaError_t e) {
 int clear_status(int32_t* status, cudaStream_t st) {
   if (!status) return BRA_OK;
   return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;
+}
+
+// Says which kernel a grouped product takes.
+void log_tile(const char* what, const GroupedProblem& g, const GroupedTile& t) {
+  if (!log_enabled()) return;
+  char how[48] = "";
+  if (t.rows == 256) std::snprintf(how, sizeof(how), " by CTA pairs");
+  else if (t.split > 1) std::snprintf(how, sizeof(how), ", sums over %d CTAs", t.split);
+  std::fprintf(stderr, "[bra] %s rows=%lld experts=%d K=%d N=%d -> %dx%d tiles%s\n", what,
+               (long long)g.R, g.E, g.K, g.N, t.rows, t.cols, how);
 }
 
 // The weight as rows: (E*K) rows of N, or (E*N) rows of K when transposed.
@@ -410,6 +421,10 @@ int mxfp4_grouped_matmul(const uint8_t* x_codes, const uint8_t* x_scales, const 
   const MxProblem g = {x_codes, x_scales, w_codes,      w_scales, bias,
                        y,       counts,   args->status, s.R,      s.yp,
                        (int)s.E, (int)s.K, (int)s.N,     args->dtype};
+  if (log_enabled())
+    std::fprintf(stderr, "[bra] mxfp4_grouped_matmul rows=%lld experts=%d K=%d N=%d -> %s\n",
+                 (long long)g.R, g.E, g.K, g.N,
+                 mx_pair(g) ? "256x256 tiles by CTA pairs" : "128x128 tiles");
   return status_of(launch_mx_grouped(g, st));
 }
 
@@ -482,6 +497,7 @@ int grouped_matmul(const void* x, const void* weight, const void* bias, const in
   g.N = (int)s.N;
   g.dtype = args->dtype;
   g.wt = args->transpose_weight ? 1 : 0;
+  log_tile("grouped_matmul", g, grouped_fwd_tile(g));
   return status_of(launch_grouped_fwd(g, st));
 }
 
@@ -545,6 +561,7 @@ int grouped_matmul_grad(const void* dy, const void* x, const void* weight, const
     g.K = (int)s.N;
     g.N = (int)s.K;
     g.wt = wt ? 0 : 1;
+    log_tile("grouped_matmul_grad dx", g, grouped_fwd_tile(g));
     if ((rc = status_of(launch_grouped_fwd(g, st))) != BRA_OK) return rc;
   }
   if (dweight) {
@@ -559,6 +576,7 @@ int grouped_matmul_grad(const void* dy, const void* x, const void* weight, const
     g.ldy = g.N;
     g.wt = 0;
     g.late = dx != nullptr;      // the gradients do not need each other
+    log_tile("grouped_matmul_grad dweight", g, grouped_wgrad_tile(g));
     if ((rc = status_of(launch_grouped_wgrad(g, st))) != BRA_OK) return rc;
   }
   if (dbias) {

@@ -30,6 +30,14 @@ struct GroupedProblem {
 // multiple of 8 elements.  cudaErrorInvalidValue if a map cannot be encoded.
 cudaError_t launch_grouped_fwd(const GroupedProblem& g, cudaStream_t st);
 cudaError_t launch_grouped_wgrad(const GroupedProblem& g, cudaStream_t st);
+// The output tile they take (256 rows: a CTA pair's), by how many CTAs its
+// contraction is split, and then the most tiles there can be.
+struct GroupedTile {
+  int rows, cols, split;
+  int64_t tiles;
+};
+GroupedTile grouped_fwd_tile(const GroupedProblem& g);
+GroupedTile grouped_wgrad_tile(const GroupedProblem& g);
 // The same with each output tile's contraction split over a cluster: by how
 // much (1: not at all), the most tiles there can be, and the launch.
 int grouped_split(const GroupedProblem& g, bool wgrad, int64_t* tiles);
@@ -87,6 +95,8 @@ struct MxProblem {
   int E, K, N, dtype;
 };
 cudaError_t launch_mx_grouped(const MxProblem& g, cudaStream_t st);
+// Whether it takes the CTA pair's 256 x 256 tiles, or 128 x 128.
+bool mx_pair(const MxProblem& g);
 cudaError_t read_mx_fault_word(int32_t* code, int clear);
 
 // The router.  hist: workspace of chunks x E int32 when there are several.

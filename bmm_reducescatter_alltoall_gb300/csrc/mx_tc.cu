@@ -632,10 +632,14 @@ cudaError_t launch(const MxProblem& g, cudaStream_t st) {
 //   512 x 16, 2048, 4096   47 / 36         140 x 64, 2048, 4096   84 / 68
 //  1024 x 16, 2048, 4096   82 / 59
 //   256 x  8, 4096, 1024   10 / 12 (96 tiles)   512 x 8, 4096, 1024   15 / 13 (160)
+bool mx_pair(const MxProblem& g) {
+  const int64_t groups = g.R < g.E ? g.R : g.E;
+  return g.R / g.E >= 128 && (2 * (g.R / 256) + groups) * ((g.N + 255) / 256) >= 2 * 76;
+}
+
 cudaError_t launch_mx_grouped(const MxProblem& g, cudaStream_t st) {
   const bool bf16 = g.dtype == BRA_BF16;
-  const int64_t groups = g.R < g.E ? g.R : g.E;
-  if (g.R / g.E >= 128 && (2 * (g.R / 256) + groups) * ((g.N + 255) / 256) >= 2 * 76)
+  if (mx_pair(g))
     return bf16 ? launch<__nv_bfloat16, 2, 256>(g, st) : launch<__half, 2, 256>(g, st);
   return bf16 ? launch<__nv_bfloat16, 1, 128>(g, st) : launch<__half, 1, 128>(g, st);
 }

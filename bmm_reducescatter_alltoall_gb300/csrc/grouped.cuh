@@ -95,6 +95,33 @@ __device__ __forceinline__ bool mbar_wait_acq(uint32_t bar, uint32_t parity,
   return mbar_try_acq(bar, parity) || mbar_wait_acq_slow(bar, parity, abort_flag, fault);
 }
 
+// Wait for the end of a sum over `blocks` blocks of 64 rows, or for its last
+// block's operands: as mbar_wait, with a limit that grows with the blocks.  A
+// block takes 0.27 us (64 x 128 columns of zeros, one tile a CTA), so that a
+// group of 2^30 rows alone passes the limit of the other waits, which are each
+// for one block.
+static __device__ __noinline__ bool mbar_wait_sum_slow(uint32_t bar, uint32_t parity,
+                                                       volatile int* abort_flag, int32_t* fault,
+                                                       int blocks) {
+  const unsigned long long t0 = global_ns(), limit = kWaitTimeoutNs + blocks * 4000ull;
+  for (;;) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+      if (mbar_try(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > limit) {
+      *abort_flag = 1;
+      atomicExch(fault, (int32_t)BRA_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait_sum(uint32_t bar, uint32_t parity,
+                                              volatile int* abort_flag, int32_t* fault,
+                                              int blocks) {
+  return mbar_try(bar, parity) || mbar_wait_sum_slow(bar, parity, abort_flag, fault, blocks);
+}
+
 // Arrive on a barrier of another CTA of the cluster without ordering this
 // thread's memory accesses.
 __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_bar) {

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (WG && warp == 3 && tail) {
     // ---------------- tail rows of the group's last block ----------------
     const int s = (kb1 - 1 - kb0) % STAGES;
-    const bool got = mbar_wait(tail_bar, 0, abort_flag, fault);
+    const bool got = mbar_wait_sum(tail_bar, 0, abort_flag, fault, kb1 - kb0);
     if (__all_sync(0xffffffffu, got)) {
       const int stop = (tail + 15) & ~15;
       const uint32_t base = smem_base + s * STAGE_BYTES;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---------------- this CTA's share to shared memory ----------------
     const int q = warp & 3;
     const bool none = kb1 == kb0;
-    const bool waited = mbar_wait(tfull_bar, 0, abort_flag, fault);
+    const bool waited = mbar_wait_sum(tfull_bar, 0, abort_flag, fault, kb1 - kb0);
     if (__all_sync(0xffffffffu, waited)) {
       tc_fence_after();
       float* mine = part + (q * 32 + lane) * PART_LD;

@@ -32,7 +32,8 @@
 // 4096, 151 us forward and for the weight gradient (1820 TFLOP/s; cuBLAS's
 // batched product of equal groups 1945).  With few, the weights' bytes: 128
 // rows over 64 experts, 140 us for 949 MB, the rate of a copy.
-// Every wait is bounded (about 4 s) and reports through the fault word.
+// Every wait is bounded (about 4 s, those for a whole group's sum by its size
+// as well) and reports through the fault word.
 #include <cstring>
 #include <mutex>
 
@@ -364,7 +365,7 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
       const int s = (stage + blocks - 1) % STAGES;
       stage = (stage + blocks) % STAGES;
       if (valid == 0) continue;
-      const bool got = mbar_wait(tail_bar(s), (used >> s) & 1u, abort_flag, fault);
+      const bool got = mbar_wait_sum(tail_bar(s), (used >> s) & 1u, abort_flag, fault, blocks);
       if (!__all_sync(0xffffffffu, got)) break;
       used ^= 1u << s;
       const int stop = (valid + 15) & ~15;
@@ -404,7 +405,9 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
       }
-      const bool waited = mbar_wait(tfull_bar(acc), acc_phase, abort_flag, fault);
+      const bool waited =
+          WG ? mbar_wait_sum(tfull_bar(acc), acc_phase, abort_flag, fault, (r1 - r0 + BK - 1) / BK)
+             : mbar_wait(tfull_bar(acc), acc_phase, abort_flag, fault);
       if (!__all_sync(0xffffffffu, waited)) break;
       tc_fence_after();
       auto release = [&] {

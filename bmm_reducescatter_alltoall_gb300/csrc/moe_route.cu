@@ -544,8 +544,8 @@ int route_chunk(int64_t T) {
 // Chunks from which the counts are summed by a launch of their own.  Below,
 // each CTA of the last kernel sums the matrix itself, in all the square of the
 // chunks.  8 of 128 experts, us, by each CTA / by the launch: 65536 tokens (147
-// chunks) 35.1 / 35.8, 262144 (304) 132 / 129, 1048576 (1064) 576 / 504,
-// 4194304 (4256) 3045 / 1982.
+// chunks) 35.1 / 35.8, 262144 (304) 132 / 129, 1048576 (1058) 576 / 504,
+// 4194304 (4096) 3045 / 1982.
 constexpr int kScanChunks = 160;
 
 cudaError_t launch_route(const RouteCall& r, cudaStream_t st) {

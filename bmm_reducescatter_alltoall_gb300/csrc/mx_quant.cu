@@ -15,7 +15,7 @@
 // same work took 112 instructions an 8 elements and 34 us for 64 Mi values
 // where the bytes take 25).  Going back, a lane makes 8 elements, one 16-byte
 // store.  A warp takes up to 1024 elements of a row with their loads issued
-// together.  16384 x 4096: 28 us to codes (151 MB, 25 us at the copy rate), 32
+// together.  16384 x 4096: 28 us to codes (170 MB, 25 us at the copy rate), 30
 // back.
 #include <type_traits>
 

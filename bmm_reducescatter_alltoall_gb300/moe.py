@@ -335,6 +335,10 @@ class MxTensor:
 
     def __init__(self, codes, scales, shape, counts):
         self.codes, self.scales, self.shape, self.counts = codes, scales, tuple(shape), counts
+        self._checked = None             # the parts that _holds has found to fit
+
+    def _parts(self):
+        return self.codes, self.scales, self.shape, self.counts
 
     @property
     def device(self):
@@ -354,23 +358,30 @@ class MxTensor:
         return a
 
 
-def _holds(t: MxTensor, what: str) -> MxArgs:
-    """The arguments of an MxTensor, after a check that its buffers hold what they say."""
+def _holds(t: MxTensor, what: str) -> None:
+    """Checks that the buffers of an MxTensor hold what it says: once for the same tensors (8 us),
+    which have to keep their storage, as those of a Plan."""
+    if t._checked is not None and all(a is b for a, b in zip(t._checked, t._parts())):
+        return
     torch = _bra._torch()
     if len(t.shape) != 2 and (len(t.shape) != 3 or t.counts is not None):
         raise ValueError(f"{what} must hold rows (R, K) or matrices (E, N, K), got {t.shape}")
     if t.counts is not None:
         _counts(t.counts)
-    a, lib = t._args(), _bra.library()
-    for part, size in (("codes", lib.mxfp4_code_bytes), ("scales", lib.mxfp4_scale_bytes)):
-        buf, need = getattr(t, part), size(ctypes.byref(a))
-        if need < 0:
-            raise _bra.BraError(-need, what)
-        _bra._dev_tensor(buf, f"{what}'s {part}", torch.uint8)
+    a, lib, byte = t._args(), _bra.library(), torch.uint8
+    ref = ctypes.byref(a)
+    needs = lib.mxfp4_code_bytes(ref), lib.mxfp4_scale_bytes(ref)
+    if min(needs) < 0:
+        raise _bra.BraError(-min(needs), what)
+    for part, buf, need in zip(("codes", "scales"), (t.codes, t.scales), needs):
+        if not isinstance(buf, torch.Tensor) or buf.dtype is not byte or not buf.is_cuda or \
+                not buf.is_contiguous():
+            _bra._dev_tensor(buf, f"{what}'s {part}", byte)              # says which
         if buf.numel() < need:
             raise ValueError(f"{what}'s {part} have {buf.numel()} bytes, {t.shape} takes {need}")
-    _same_device(t.codes, t.scales, t.counts)
-    return a
+    if t.codes.device != t.scales.device or t.counts is not None and t.counts.device != t.codes.device:
+        raise ValueError(f"{what}'s buffers and counts must be on one device")
+    t._checked = t._parts()
 
 
 def mxfp4_quantize_plan(x, counts=None, out: Optional[MxTensor] = None, status=None):
@@ -399,6 +410,7 @@ def mxfp4_quantize_plan(x, counts=None, out: Optional[MxTensor] = None, status=N
         new = lambda n: torch.empty(n, dtype=torch.uint8, device=x.device)   # noqa: E731
         out = MxTensor(new(cb).view(shape[:-1] + (-(-shape[-1] // 32) * 16,)), new(sb), shape,
                        counts)
+        out._checked = out._parts()
     elif out.shape != shape or out.counts is not counts:
         raise ValueError(f"out holds {out.shape} and its own counts, expected {shape} with counts")
     else:
@@ -429,11 +441,12 @@ def mxfp4_dequantize_plan(q: MxTensor, dtype, out=None, status=None):
     codes = {torch.float16: _bra.FP16, torch.bfloat16: _bra.BF16, torch.float32: _bra.FP32}
     if dtype not in codes:
         raise TypeError(f"mxfp4_dequantize gives float16, bfloat16 or float32, got {dtype}")
-    a = _holds(q, "q")
+    _holds(q, "q")
     if out is None:
         out = torch.empty(q.shape, dtype=dtype, device=q.device)
     _dense(out, "out", dtype, q.shape)
     _same_device(q.codes, out, status)
+    a = q._args()
     a.dtype, a.status = codes[dtype], _status(status)
     args = (_ptr(q.codes), _ptr(q.scales), _ptr(q.counts), _ptr(out), ctypes.byref(a))
     return _bra.Plan(_bra.library().mxfp4_dequantize, args, "mxfp4_dequantize", out,

@@ -169,7 +169,8 @@ BRA_API int mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, const 
 
 /*
  * mxfp4_grouped_matmul -- grouped_matmul on 4-bit operands: rows quantized
- * with the same counts, weights (E, N, K) quantized as E groups of N rows.
+ * with the same counts (with one group also as a group of R rows), weights
+ * (E, N, K) quantized as E groups of N rows.
  * y[r, n] = sum of the dequantized products in fp32 + bias[e, n], one
  * rounding to args->dtype (FP16 or BF16; the bias is fp16 or fp32 as there).
  * Of bra_grouped_args, x_pitch and transpose_weight must be 0 and no

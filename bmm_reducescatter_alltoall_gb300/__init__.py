@@ -1,6 +1,6 @@
 """GB300-native fused MoE BMM -> TP ReduceScatter -> bias Add -> EP AllToAll,
 all_to_all_v and its indexed form over virtual ranks on one GPU, and the ragged
-expert operators around them (moe.py).
+expert operators around them (moe.py, fp8.py).
 
 Thin Python binding over libbmmrsa2a.so (the C ABI in include/bmm_rs_a2a.h and
 include/bra_moe.h):
@@ -105,6 +105,7 @@ def library() -> ctypes.CDLL:
     lib.bra_version.argtypes = []
     lib.bra_version.restype = ctypes.c_char_p
     moe.declare(lib)
+    fp8.declare(lib)
     _lib = lib
     return lib
 
@@ -648,5 +649,7 @@ def fault_status(clear: bool = False) -> int:
 
 from . import moe                      # noqa: E402  (uses the helpers above)
 from .moe import *                     # noqa: E402,F401,F403
+from . import fp8                      # noqa: E402
+from .fp8 import *                     # noqa: E402,F401,F403
 
-__all__ += moe.__all__
+__all__ += moe.__all__ + fp8.__all__

@@ -74,6 +74,10 @@ KERNEL_SOURCES = {
     "quantize_kernel": "mx_quant.cu",
     "dequantize_kernel": "mx_quant.cu",
     "mx_grouped_kernel": "mx_tc.cu",
+    "fp8_rows_kernel": "fp8_quant.cu",
+    "fp8_blocks_kernel": "fp8_quant.cu",
+    "fp8_back_kernel": "fp8_quant.cu",
+    "fp8_grouped_kernel": "fp8_tc.cu",
     "route_choose_kernel": "moe_route.cu",
     "route_scan_kernel": "moe_route.cu",
     "route_place_kernel": "moe_route.cu",

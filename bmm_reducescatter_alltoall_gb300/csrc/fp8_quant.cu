@@ -1,0 +1,342 @@
+// Quantisation to 8-bit block-scaled values, and back.
+//
+// Of each block (128 elements of a row, or 128 x 128 of a weight), a = max
+// |x|; the scale is the smallest 2^s, s >= -126, with a <= 2^s * L, L = 1.75 *
+// 2^8 (e4m3) or 1.75 * 2^15 (e5m2): s is a's exponent less 8 or 15, one more
+// when a's significand passes 1.75.  The code is the nearest to x / 2^s, ties
+// to even.  x / 2^s is a product with a power of two, exact but where it falls
+// far below the smallest code, so that codes are a function of x alone.  A
+// block with a NaN or an infinity gets the scale NaN and codes of zero.
+//
+// 16 bits are read and 8.25 written to an element, and HBM bounds it.  A lane
+// takes 16 consecutive elements: 16 bytes of codes a store, eight lanes to a
+// row's block, three exchanges for its maximum; a warp has the loads of 2048
+// elements of a row in flight.  A weight's block is a CTA's, held in registers
+// between its maximum and its codes, so that it too is read once.
+#include <type_traits>
+
+#include "fp8.cuh"
+#include "grouped.cuh"
+#include "walk.cuh"
+
+namespace bra {
+namespace {
+
+using namespace grp;
+
+constexpr int kThreads = 256;
+constexpr int kPieces = 4;                // 512-element pieces of a warp's unit
+constexpr int kUnit = kPieces * 512;
+
+template <typename T>
+__device__ __forceinline__ float2 pair_of(uint32_t w);
+template <>
+__device__ __forceinline__ float2 pair_of<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 pair_of<__nv_bfloat16>(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+
+// 16 consecutive elements of a row as they are stored.
+template <typename T>
+struct Piece {
+  static constexpr int W = 4 * (int)sizeof(T);          // words
+  uint32_t w[W];
+  // `left` elements of the row are left from src on (16 or more, `vec`: by
+  // 16-byte loads); zeros past it
+  __device__ __forceinline__ void load(const T* src, int64_t left, bool vec) {
+    if (vec && left >= 16) {
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        const uint4 q = reinterpret_cast<const uint4*>(src)[i];
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+      }
+    } else if constexpr (sizeof(T) == 4) {
+      const uint32_t* e = reinterpret_cast<const uint32_t*>(src);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = i < left ? e[i] : 0u;
+    } else {
+      const uint16_t* e = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t lo = 2 * i < left ? e[2 * i] : 0u;
+        const uint32_t hi = 2 * i + 1 < left ? e[2 * i + 1] : 0u;
+        w[i] = lo | hi << 16;
+      }
+    }
+  }
+  // The largest magnitude as the bits of a float: NaN above infinity above all else.
+  __device__ __forceinline__ uint32_t most() const {
+    uint32_t a = 0;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a = max(a, w[i] & 0x7fffffffu);
+      return a;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a = __vmaxu2(a, w[i] & 0x7fff7fffu);
+      return __float_as_uint(pair_of<T>(__vmaxu2(a, a >> 16)).x);
+    }
+  }
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (sizeof(T) == 4)
+      return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else
+      return pair_of<T>(w[i]);
+  }
+};
+
+// A block's scale as the exponent field of 2^s, 255 for none.
+template <bool E5>
+__device__ __forceinline__ uint32_t scale_field(uint32_t most) {
+  if (most >= 0x7f800000u) return 255u;
+  const int f = (int)(most >> 23) - (E5 ? 15 : 8) + ((most & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return (uint32_t)max(f, 1);
+}
+__device__ __forceinline__ float scale_of(uint32_t field) {
+  return __uint_as_float(field == 255u ? 0x7fc00000u : field << 23);
+}
+
+template <bool E5>
+__device__ __forceinline__ uint32_t code_pair(float lo, float hi) {
+  uint16_t r;
+  if constexpr (E5) asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 16 codes under the scale of `field`.
+template <bool E5, typename T>
+__device__ __forceinline__ uint4 codes_of(const Piece<T>& x, uint32_t field) {
+  const float inv = __uint_as_float((254u - (field == 255u ? 0u : field)) << 23);   // 2^-s
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = x.pair(2 * i), b = x.pair(2 * i + 1);
+    c[i] = code_pair<E5>(a.x * inv, a.y * inv) | code_pair<E5>(b.x * inv, b.y * inv) << 16;
+    if (field == 255u) c[i] = 0u;
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// Rows in use: R, or the counts' sum; -1 when the counts are refused.  Every thread.
+__device__ __forceinline__ int64_t rows_used(GroupTable* gt, const int64_t* counts, int E, int64_t R,
+                                             int32_t* status) {
+  if (!counts) return R;
+  if (threadIdx.x < 32) build_table<128>(gt, counts, E, R, threadIdx.x & 31);
+  __syncthreads();
+  if (!gt->bad) return gt->off[E];
+  if (blockIdx.x == 0 && threadIdx.x == 0 && status) atomicExch(status, (int32_t)BRA_ERR_INVALID);
+  return -1;
+}
+
+template <typename T, bool E5>
+__global__ void __launch_bounds__(kThreads)
+    fp8_rows_kernel(const T* x, int64_t ld, int64_t R, int64_t K, const int64_t* counts, int E,
+                    uint8_t* codes, float* scales, int vec, int32_t* status) {
+  __shared__ GroupTable gt;
+  const int lane = threadIdx.x & 31;
+  grid_wait();
+  grid_go();
+  const int64_t rows = rows_used(&gt, counts, E, R, status);
+  const int64_t cpitch = fp8::code_pitch(K), spitch = fp8::scale_pitch(K), blocks = fp8::blocks(K);
+  for (Walk at((uint32_t)((K + kUnit - 1) / kUnit)); at.row < rows; at.next()) {
+    const int64_t r = at.row, k0 = (int64_t)at.part * kUnit + lane * 16;
+    Piece<T> p[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      p[i].load(x + r * ld + k0 + i * 512, K - (k0 + i * 512), vec);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      uint32_t a = p[i].most();
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 4));
+      const uint32_t field = scale_field<E5>(a);
+      const int64_t k = k0 + i * 512, b = k / fp8::kBlock;
+      if (k < K) *reinterpret_cast<uint4*>(codes + r * cpitch + k) = codes_of<E5>(p[i], field);
+      if ((lane & 7) == 0 && b < spitch)
+        scales[r * spitch + b] = b < blocks ? scale_of(field) : 0.f;
+    }
+  }
+}
+
+// A CTA to a 128 x 128 block: eight lanes to a row, 32 rows at a time.
+template <typename T, bool E5>
+__global__ void __launch_bounds__(kThreads)
+    fp8_blocks_kernel(const T* x, int64_t ld, int64_t K, int64_t N, int64_t total, uint8_t* codes,
+                      float* scales, int vec) {
+  __shared__ uint32_t warp_most[2][kThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t cpitch = fp8::code_pitch(K);
+  const uint32_t kb = (uint32_t)fp8::blocks(K), nb = (uint32_t)fp8::blocks(N);
+  grid_wait();
+  grid_go();
+  int turn = 0;
+  for (int64_t at = blockIdx.x; at < total; at += gridDim.x, turn ^= 1) {
+    const int64_t row_block = at / kb, g = row_block / nb;
+    const int64_t n0 = (row_block - g * nb) * fp8::kBlock + (threadIdx.x >> 3);
+    const int64_t k = (at - row_block * kb) * fp8::kBlock + (threadIdx.x & 7) * 16;
+    Piece<T> p[4];
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i].load(x + (g * N + n0 + i * 32) * ld + k, n0 + i * 32 < N ? K - k : 0, vec);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a = max(a, p[i].most());
+    a = __reduce_max_sync(0xffffffffu, a);
+    if (lane == 0) warp_most[turn][warp] = a;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) a = max(a, warp_most[turn][w]);
+    const uint32_t field = scale_field<E5>(a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n0 + i * 32 < N && k < K)
+        *reinterpret_cast<uint4*>(codes + (g * N + n0 + i * 32) * cpitch + k) =
+            codes_of<E5>(p[i], field);
+    if (threadIdx.x == 0) scales[at] = scale_of(field);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t packed(float2 v);
+template <>
+__device__ __forceinline__ uint32_t packed<__half>(float2 v) {
+  return Out<__half>::pack(v.x, v.y);
+}
+template <>
+__device__ __forceinline__ uint32_t packed<__nv_bfloat16>(float2 v) {
+  return Out<__nv_bfloat16>::pack(v.x, v.y);
+}
+
+// Two codes (the low half word of w): halves hold them exactly.
+template <bool E5>
+__device__ __forceinline__ float2 values_of(uint32_t w) {
+  uint32_t h;
+  if constexpr (E5) asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  else asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// N: rows of a weight, or 0 for rows.
+template <typename T, bool E5>
+__global__ void __launch_bounds__(kThreads)
+    fp8_back_kernel(const uint8_t* codes, const float* scales, int64_t R, int64_t K, uint32_t N,
+                    const int64_t* counts, int E, T* y, int vec, int32_t* status) {
+  __shared__ GroupTable gt;
+  const int lane = threadIdx.x & 31;
+  grid_wait();
+  grid_go();
+  const int64_t rows = rows_used(&gt, counts, E, R, status);
+  const int64_t cpitch = fp8::code_pitch(K), spitch = fp8::scale_pitch(K), blocks = fp8::blocks(K);
+  for (Walk at((uint32_t)((K + kUnit - 1) / kUnit)); at.row < rows; at.next()) {
+    const int64_t r = at.row, k0 = (int64_t)at.part * kUnit + lane * 16;
+    const float* scale = scales + r * spitch;
+    if (N) {
+      const uint32_t g = (uint32_t)r / N, n = (uint32_t)r - g * N;
+      scale = scales + ((int64_t)g * fp8::blocks(N) + n / fp8::kBlock) * blocks;
+    }
+    uint4 c[kPieces];
+    float s[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t k = k0 + i * 512;
+      c[i] = k < K ? *reinterpret_cast<const uint4*>(codes + r * cpitch + k) : make_uint4(0, 0, 0, 0);
+      s[i] = k < K ? scale[k / fp8::kBlock] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t k = k0 + i * 512, left = K - k;
+      if (left <= 0) break;
+      const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+      T* out = y + r * K + k;
+      if (vec && left >= 16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 a = values_of<E5>(w[j]), b = values_of<E5>(w[j] >> 16);
+          a.x *= s[i], a.y *= s[i], b.x *= s[i], b.y *= s[i];
+          if constexpr (sizeof(T) == 4)
+            reinterpret_cast<float4*>(out)[j] = make_float4(a.x, a.y, b.x, b.y);
+          else
+            reinterpret_cast<uint2*>(out)[j] = make_uint2(packed<T>(a), packed<T>(b));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 a = values_of<E5>(w[j >> 1] >> (16 * (j & 1)));
+          if (2 * j < left) out[2 * j] = static_cast<T>(a.x * s[i]);
+          if (2 * j + 1 < left) out[2 * j + 1] = static_cast<T>(a.y * s[i]);
+        }
+      }
+    }
+  }
+}
+
+cudaError_t grid_for(int64_t ctas_wanted, int per_sm, unsigned* grid) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t full = (int64_t)sms * per_sm;
+  *grid = (unsigned)(ctas_wanted < 1 ? 1 : ctas_wanted < full ? ctas_wanted : full);
+  return cudaSuccess;
+}
+
+// CTAs of the kernels that give a warp a part of a row.
+int64_t row_ctas(int64_t R, int64_t K) {
+  return (R * ((K + kUnit - 1) / kUnit) + kThreads / 32 - 1) / (kThreads / 32);
+}
+
+// f for the element type and the format.
+template <typename F>
+cudaError_t by_type(int dtype, int format, F&& f) {
+  auto by_format = [&](auto* type) {
+    return format == BRA_E5M2 ? f(type, std::true_type{}) : f(type, std::false_type{});
+  };
+  if (dtype == BRA_BF16) return by_format((__nv_bfloat16*)nullptr);
+  if (dtype == BRA_FP16) return by_format((__half*)nullptr);
+  return by_format((float*)nullptr);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize(const Fp8Data& q, const void* x, int64_t ld, int dtype,
+                                cudaStream_t st) {
+  return by_type(dtype, q.format, [&](auto* in, auto e5) {
+    using T = std::remove_pointer_t<decltype(in)>;
+    constexpr bool E5 = decltype(e5)::value;
+    const int vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && ld * sizeof(T) % 16 == 0;
+    unsigned grid = 0;
+    if (q.each > 0) {
+      const int64_t total = q.E * fp8::blocks(q.each) * fp8::blocks(q.K);
+      const cudaError_t e = grid_for(total, 6, &grid);
+      if (e != cudaSuccess) return e;
+      return launch_clusters(fp8_blocks_kernel<T, E5>, 1, grid, kThreads, 0, st,
+                             static_cast<const T*>(x), ld, q.K, q.each, total, q.codes, q.scales,
+                             vec);
+    }
+    const cudaError_t e = grid_for(row_ctas(q.R, q.K), 8, &grid);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(fp8_rows_kernel<T, E5>, 1, grid, kThreads, 0, st,
+                           static_cast<const T*>(x), ld, q.R, q.K, q.counts, q.E, q.codes, q.scales,
+                           vec, q.status);
+  });
+}
+
+cudaError_t launch_fp8_dequantize(const Fp8Data& q, void* y, int dtype, cudaStream_t st) {
+  unsigned grid = 0;
+  const cudaError_t e = grid_for(row_ctas(q.R, q.K), 8, &grid);
+  if (e != cudaSuccess) return e;
+  return by_type(dtype, q.format, [&](auto* out, auto e5) {
+    using T = std::remove_pointer_t<decltype(out)>;
+    const int vec = (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && q.K * sizeof(T) % 16 == 0;
+    return launch_clusters(fp8_back_kernel<T, decltype(e5)::value>, 1, grid, kThreads, 0, st, q.codes,
+                           q.scales, q.R, q.K, (uint32_t)q.each, q.counts, q.E, static_cast<T*>(y),
+                           vec, q.status);
+  });
+}
+
+}  // namespace bra

@@ -1,0 +1,582 @@
+// Products of 8-bit block-scaled rows and weights, grouped by expert, on
+// tcgen05 kind::f8f6f4 (sm_103a):
+//   y[r, n]  = sum over blocks b of sx[r, b] sw[n / 128, b] * (x_b . w_b) + bias
+//   dx[r, k] = sum over blocks b of sd[r, b] sw[b, k / 128] * (dy_b . w_b)
+// with fp32 scales of any value, a block being 128 elements of the contraction.
+//
+// A block's sum of code products is the tensor core's, in fp32 and in an
+// accumulator of its own; the scales are applied as it is added to the running
+// sum, which the epilogue warps hold in registers: acc += (sx sw) * block, a
+// lane to a row, 64 or 128 columns a lane, one factor a row and block (an
+// output tile's columns share a weight block by 128).  Tensor memory holds two
+// or four block accumulators, so that one is drained while the next are
+// computed.  The walk over ragged row groups is grouped_tc.cu's.  The gradient
+// reads the same weight boxes the other way: 128 contraction rows of 128
+// columns, N-major.
+// Every wait is bounded (about 4 s) and reports through the fault word.
+#include <cstring>
+#include <mutex>
+
+#include "fp8.cuh"
+#include "grouped.cuh"
+
+namespace bra {
+
+__device__ int32_t g_bra_fault_word_fp8 = 0;
+
+namespace {
+
+using namespace tc;
+using namespace grp;
+
+constexpr int BKB = 128;                    // bytes (elements) of a K block
+constexpr int kGroupM = 8;
+constexpr int EPI_WARP0 = 4;
+constexpr int BAR_BYTES = 512;
+
+struct Fp8Params {
+  CUtensorMap ta, ta32;                     // row codes, boxes of 128 and 32 rows
+  CUtensorMap tb;                           // weight codes
+  const float* xs;
+  const float* ws;
+  const void* bias;
+  void* y;
+  const int64_t* counts;
+  int32_t* status;
+  int64_t R, ldy, xs_pitch;
+  int64_t ws_group, ws_out, ws_block;       // weight scales: from expert to expert, from output
+                                            // block to output block, from K block to K block
+  int E, N, n_tiles, k_blocks;              // N: columns of the output
+  int bias_fp16, aligned;
+  uint32_t idesc;
+};
+
+template <int CG, int BN>
+struct FShape {
+  static constexpr int A_BYTES = 128 * BKB;
+  static constexpr int B_COLS = BN / CG;                  // output columns held by one CTA
+  static constexpr int B_BYTES = B_COLS * BKB;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int EPI_WARPS = BN == 256 ? 8 : 4;
+  static constexpr int WC = BN / (EPI_WARPS / 4);         // columns of an epilogue warp
+  static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
+  static constexpr int NBUF = BN == 256 ? 2 : 4;          // block accumulators
+  static constexpr uint32_t TMEM_COLS = NBUF * BN;
+  static constexpr int EPI_BYTES = EPI_WARPS * (kSegBytes + WC * 4);
+  static constexpr int FIXED = BAR_BYTES + EPI_BYTES + (int)sizeof(GroupTable) + 16 + 1024;
+  static constexpr int FIT = (232448 - FIXED) / STAGE_BYTES;
+  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + FIXED;
+  // Registers of a thread: 168 at a launch of 384 threads, then 40 for the four
+  // role warps and 232 for the eight epilogue warps (the same sum).
+  static constexpr bool SPLIT_REGS = THREADS == 384;
+  static constexpr int LAUNCH_REGS = 168, ROLE_REGS = 40, EPI_REGS = 232;
+  static_assert(128 * ROLE_REGS + 256 * EPI_REGS <= 384 * LAUNCH_REGS, "registers");
+  static_assert(STAGES >= 4 && TMEM_COLS <= 512, "ring, tensor memory");
+  static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms");
+};
+
+// D (TMEM) [+]= A (smem) x B (smem), 8-bit codes, fp32 sums.
+template <int CG>
+__device__ __forceinline__ void fp8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Waits for this warp's tensor memory loads; v's uses stay behind it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])::"memory");
+}
+__device__ __forceinline__ uint64_t pair64(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+// acc[i] += f * v[i], two at a time.
+__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&v)[32], uint64_t ff) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i]) : "l"(pair64(v[2 * i], v[2 * i + 1])), "l"(ff));
+}
+
+// mbar_wait without a call: a kernel that splits its registers cannot have one.
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          int32_t* fault) {
+  if (mbar_try(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+      if (mbar_try(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > kWaitTimeoutNs) {
+      *abort_flag = 1;
+      atomicExch(fault, (int32_t)BRA_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void regs_to(bool up) {
+  if (up) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// GRAD: the weight's rows are the contraction.
+template <typename T, int CG, int BN, bool GRAD>
+__global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(FShape<CG, BN>::THREADS, 1)
+    fp8_grouped_kernel(const __grid_constant__ Fp8Params p) {
+  using S = FShape<CG, BN>;
+  constexpr int STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, BM = 128 * CG, WC = S::WC;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const uint32_t smem_base = smem_u32(smem);
+  uint8_t* bars = smem + STAGES * STAGE_BYTES;
+  const uint32_t bar_base = smem_u32(bars);
+  // barriers (8 bytes each): per stage full (leader: both CTAs' bytes) and
+  // empty; per block accumulator tfull and tempty (leader: both CTAs' warps)
+  auto full_bar = [&](int s) { return bar_base + 8u * s; };
+  auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * STAGES + S::NBUF + a); };
+  static_assert(8 * (2 * STAGES + 2 * S::NBUF) + 16 <= BAR_BYTES, "barrier area");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BAR_BYTES - 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_BYTES - 8);
+  GroupTable* gt = reinterpret_cast<GroupTable*>(bars + BAR_BYTES);
+  uint8_t* epi = bars + BAR_BYTES + ((sizeof(GroupTable) + 15) & ~15);
+  int32_t* fault = &g_bra_fault_word_fp8;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);     // leader: its expect_tx; the bytes of both CTAs
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < S::NBUF; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), S::EPI_WARPS * CG);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&p.ta);
+    tma_prefetch_desc(&p.ta32);
+    tma_prefetch_desc(&p.tb);
+  }
+  if (warp == 2) {
+    tmem_alloc<CG>(smem_u32(tmem_slot), S::TMEM_COLS);
+    tmem_relinquish<CG>();
+  }
+  grid_wait();
+  grid_go();
+  if (warp == 3) build_table<BM>(gt, p.counts, p.E, p.R, lane);
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = gt->bad ? 0 : gt->tile[p.E] * p.n_tiles;
+  const int walk0 = blockIdx.x / CG, step = gridDim.x / CG;
+  int e_at = 0;                      // group of this role's current tile
+  auto find = [&](int t) {
+    while (gt->tile[e_at + 1] * p.n_tiles <= t) ++e_at;
+    const int first = gt->tile[e_at];
+    TileCoord c = tile_coord(t - first * p.n_tiles, gt->tile[e_at + 1] - first, p.n_tiles, kGroupM);
+    c.g = e_at;
+    return c;
+  };
+
+  if (warp < EPI_WARP0) {
+    if (S::SPLIT_REGS) regs_to<S::ROLE_REGS>(false);
+    if ((warp == 0 || warp == 2) && lane == 0) {
+      // ---------------- producers (every CTA): warp 0 for A, warp 2 for B ----------------
+      const bool is_a = warp == 0;
+      const uint32_t leader_full0 = CG == 2 ? map_to_rank(full_bar(0), 0) : full_bar(0);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
+        if (CG == 2) tma_load_3d_pair(dst, m, bar, c0, c1, c2);
+        else tma_load_3d(dst, m, bar, c0, c1, c2);
+      };
+      for (int t = walk0; ok && t < total; t += step) {
+        const TileCoord c = find(t);
+        const int r0 = gt->off[c.g], r1 = gt->off[c.g + 1];
+        const int row = r0 + c.mt * BM + (int)rank * 128;
+        // 32-row boxes of A to fetch (none past the group), or one of 128 rows
+        auto boxes = [&](int valid) { return valid <= 64 ? (max(valid, 0) + 31) / 32 : 4; };
+        const int mine = boxes(r1 - row);
+        uint32_t bytes = CG * S::B_BYTES + mine * (S::A_BYTES / 4);
+        if (CG == 2) bytes += boxes(r1 - row - 128) * (S::A_BYTES / 4);   // used by the leader
+        const int b_col = c.nt * BN + (int)rank * S::B_COLS;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!wait_here(empty_bar(stage), phase ^ 1u, abort_flag, fault)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = leader_full0 + 8u * stage;
+          const uint32_t a_dst = smem_base + stage * STAGE_BYTES, b_dst = a_dst + S::A_BYTES;
+          if (is_a) {
+            if (rank == 0) mbar_expect_tx(full_bar(stage), bytes);
+            if (mine == 4) load(a_dst, &p.ta, fb, kb * BKB, row, 0);
+            else
+              for (int i = 0; i < mine; ++i)
+                load(a_dst + i * (S::A_BYTES / 4), &p.ta32, fb, kb * BKB, row + i * 32, 0);
+          } else if (!GRAD) {
+            load(b_dst, &p.tb, fb, kb * BKB, b_col, c.g);
+          } else {
+#pragma unroll
+            for (int i = 0; i < S::B_COLS / 128; ++i)
+              load(b_dst + i * 16384, &p.tb, fb, b_col + i * 128, kb * BKB, c.g);
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) spin_ns(2000000ull);   // let copies already issued land
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---------------- MMA issuer (leader only) ----------------
+      // K-major operands step 32 bytes per K = 32, the N-major one 32 box rows
+      const uint64_t a0 = smem_desc_sw128(smem_base, 16, 1024);
+      const uint64_t b0 = GRAD ? smem_desc_sw128(smem_base + S::A_BYTES, 16384, 1024)
+                               : smem_desc_sw128(smem_base + S::A_BYTES, 16, 1024);
+      constexpr uint32_t b_step = GRAD ? 256u : 2u;
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true;
+      for (int t = walk0; ok && t < total; t += step) {
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          ok = wait_here(tempty_bar(buf), buf_phase ^ 1u, abort_flag, fault) &&
+               wait_here(full_bar(stage), phase, abort_flag, fault);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem_base + (uint32_t)(buf * BN);
+          const uint64_t so = (uint64_t)((stage * STAGE_BYTES) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            fp8_mma<CG>(d, a0 + so + 2 * k, b0 + so + b_step * k, p.idesc, k > 0 ? 1u : 0u);
+          if (CG == 2) {
+            tc_commit_pair(tfull_bar(buf), 0x3);
+            tc_commit_pair(empty_bar(stage), 0x3);
+          } else {
+            tc_commit(tfull_bar(buf));
+            tc_commit(empty_bar(stage));
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == S::NBUF) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) spin_ns(2000000ull);   // let MMAs already issued complete
+    }
+  } else {
+    if (S::SPLIT_REGS) regs_to<S::EPI_REGS>(true);
+    // ---------------- epilogue: lane quarter q, columns h*WC .. +WC ----------------
+    const int q = warp & 3, h = (warp - EPI_WARP0) >> 2;
+    uint8_t* mine = epi + (warp - EPI_WARP0) * (kSegBytes + WC * 4);
+    const uint32_t seg = smem_u32(mine), bias_s = seg + kSegBytes;
+    const uint32_t leader_tempty0 = CG == 2 ? map_to_rank(tempty_bar(0), 0) : tempty_bar(0);
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    bool ok = true;
+    auto next_buf = [&] {
+      if (++buf == S::NBUF) {
+        buf = 0;
+        buf_phase ^= 1u;
+      }
+    };
+    // tensor memory alone is handed back: no memory of this thread to order
+    auto hand_back = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2 && rank != 0) arrive_relaxed(leader_tempty0 + 8u * buf);
+        else mbar_arrive(tempty_bar(buf));
+      }
+    };
+    for (int t = walk0; ok && t < total; t += step) {
+      const TileCoord c = find(t);
+      const int r0 = gt->off[c.g], r1 = gt->off[c.g + 1];
+      const int tile_row = c.mt * BM + (int)rank * 128 + q * 32;
+      const int n0 = c.nt * BN + h * WC;
+      const int valid = min(32, r1 - r0 - tile_row);
+      const bool any = valid > 0 && n0 < p.N;
+      if (!any) {
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          const bool got = wait_here(tfull_bar(buf), buf_phase, abort_flag, fault);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+          hand_back();
+          next_buf();
+        }
+        continue;
+      }
+      if (p.bias) {   // while the first block is being computed
+        for (int i = lane; i < WC; i += 32) {
+          const int64_t at = (int64_t)c.g * p.N + n0 + i;
+          const float b = n0 + i >= p.N  ? 0.f
+                          : p.bias_fp16 ? Num<__half>::bias(p.bias, at)
+                                        : static_cast<const float*>(p.bias)[at];
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias_s + i * 4), "f"(b) : "memory");
+        }
+        __syncwarp();
+      }
+      // scales: four blocks of this lane's row in a load, 32 blocks of the
+      // weight over the lanes, each fetched ahead of its use
+      const float* sx = p.xs + ((int64_t)r0 + tile_row + min(lane, valid - 1)) * p.xs_pitch;
+      const float* sw = p.ws + c.g * p.ws_group + (n0 / fp8::kBlock) * p.ws_out;
+      auto fetch_x = [&](int kb) {
+        return kb < p.k_blocks ? *reinterpret_cast<const float4*>(sx + kb) : make_float4(0, 0, 0, 0);
+      };
+      auto fetch_w = [&](int kb) {
+        return kb + lane < p.k_blocks ? sw[(int64_t)(kb + lane) * p.ws_block] : 0.f;
+      };
+      float4 x_at = fetch_x(0), x_next = fetch_x(4);
+      float w_at = fetch_w(0), w_next = fetch_w(32);
+      uint64_t acc[WC / 2];
+#pragma unroll
+      for (int i = 0; i < WC / 2; ++i) acc[i] = 0ull;
+#pragma unroll 1
+      for (int kb = 0; kb < p.k_blocks; ++kb) {
+        float f = x_at.x * __shfl_sync(0xffffffffu, w_at, kb & 31);
+        f = f > 3.402823466e+38f ? 3.402823466e+38f : f;            // NaN stays
+        const uint64_t ff = pair64(__float_as_uint(f), __float_as_uint(f));
+        if ((kb & 3) == 3) {
+          x_at = x_next;
+          x_next = fetch_x(kb + 5);
+          if ((kb & 31) == 31) {
+            w_at = w_next;
+            w_next = fetch_w(kb + 33);
+          }
+        } else {
+          x_at = make_float4(x_at.y, x_at.z, x_at.w, 0.f);
+        }
+        const bool got = wait_here(tfull_bar(buf), buf_phase, abort_flag, fault);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t t_base =
+            tmem_base + (uint32_t)(buf * BN + h * WC) + ((uint32_t)(q * 32) << 16);
+        uint32_t v0[32], v1[32];
+        tmem_ld32(t_base, v0);
+        tmem_ld32(t_base + 32, v1);
+        tmem_ld_wait_for(v0);
+        tmem_ld_wait_for(v1);
+        if constexpr (WC == 128) {
+          add_scaled(acc, v0, ff);
+          tmem_ld32(t_base + 64, v0);
+          add_scaled(acc + 16, v1, ff);
+          tmem_ld32(t_base + 96, v1);
+          tmem_ld_wait_for(v0);
+          tmem_ld_wait_for(v1);
+          hand_back();
+          add_scaled(acc + 32, v0, ff);
+          add_scaled(acc + 48, v1, ff);
+        } else {
+          hand_back();
+          add_scaled(acc, v0, ff);
+          add_scaled(acc + 16, v1, ff);
+        }
+        next_buf();
+      }
+      if (!ok) break;
+      T* y0 = static_cast<T*>(p.y) + ((int64_t)r0 + tile_row) * p.ldy;
+      const int segs = min(WC / 64, (p.N - n0 + 63) / 64);
+      uint32_t o[WC / 64][32];
+#pragma unroll
+      for (int ch = 0; ch < WC / 64; ++ch) {
+        uint32_t v[64];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          v[2 * i] = (uint32_t)acc[ch * 32 + i];
+          v[2 * i + 1] = (uint32_t)(acc[ch * 32 + i] >> 32);
+        }
+        pack_segment<T>(v, o[ch], p.bias ? bias_s + ch * 256 : 0u, false);
+      }
+      Carry carry;
+#pragma unroll
+      for (int ch = 0; ch < WC / 64; ++ch)
+        if (ch < segs)
+          put_segment<T>(o[ch], carry, ch == 0, ch + 1 == segs, y0, p.ldy, valid, n0 + ch * 64, p.N,
+                         seg, p.aligned != 0, lane, [] {});
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync();   // no remote arrive or MMA of the pair still pending
+  if (threadIdx.x == 0 && p.status) {
+    if (gt->bad) atomicExch(p.status, (int32_t)BRA_ERR_INVALID);
+    else if (*abort_flag) atomicExch(p.status, (int32_t)BRA_ERR_TIMEOUT);
+  }
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc<CG>(tmem_base, S::TMEM_COLS);
+  }
+}
+
+// Clusters of the kernel that are resident at once, found on first use.
+template <typename T, int CG, int BN, bool GRAD>
+cudaError_t resident(int* clusters) {
+  static std::mutex mu;
+  static int known[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  int& n = known[dev & 63];
+  if (n == 0) {
+    using S = FShape<CG, BN>;
+    const auto kernel = fp8_grouped_kernel<T, CG, BN, GRAD>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    // the register split waits for ever unless the launch brings its sum
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, kernel);
+    if (e != cudaSuccess) return e;
+    if (S::SPLIT_REGS && at.numRegs < S::LAUNCH_REGS) return cudaErrorLaunchOutOfResources;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CG, 1, 1);
+    cfg.blockDim = dim3(S::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = S::SMEM_BYTES;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = CG;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int m = 0;
+    e = cudaOccupancyMaxActiveClusters(&m, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    n = m < 1 ? 1 : m;
+  }
+  *clusters = n;
+  return cudaSuccess;
+}
+
+// Codes {K bytes, rows, groups} at a pitch of whole 16 bytes, box {128 bytes, b1, 1},
+// 128-byte swizzle, zeros outside.
+bool encode_codes(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, uint64_t groups,
+                  uint32_t b1) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const uint64_t pitch = (uint64_t)fp8::code_pitch((int64_t)K);
+  const cuuint64_t dims[3] = {K, rows, groups};
+  const cuuint64_t strides[2] = {pitch, pitch * rows};
+  const cuuint32_t box[3] = {BKB, b1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int CG, int BN, bool GRAD>
+cudaError_t launch(const Fp8Problem& g, cudaStream_t st) {
+  using S = FShape<CG, BN>;
+  int clusters = 0;
+  cudaError_t e = resident<T, CG, BN, GRAD>(&clusters);
+  if (e != cudaSuccess) return e;
+  Fp8Params p;
+  std::memset(&p, 0, sizeof(p));
+  const int K = GRAD ? g.out : g.in, N = GRAD ? g.in : g.out;      // contraction, columns
+  if (!encode_codes(&p.ta, g.xc, K, g.R, 1, 128) || !encode_codes(&p.ta32, g.xc, K, g.R, 1, 32) ||
+      !encode_codes(&p.tb, g.wc, g.in, g.out, g.E, GRAD ? 128 : S::B_COLS))
+    return cudaErrorInvalidValue;
+  p.xs = g.xs;
+  p.ws = g.ws;
+  p.bias = g.bias;
+  p.y = g.y;
+  p.counts = g.counts;
+  p.status = g.status;
+  p.R = g.R;
+  p.ldy = g.ldy;
+  p.xs_pitch = fp8::scale_pitch(K);
+  const int64_t in_blocks = fp8::blocks(g.in);
+  p.ws_group = fp8::blocks(g.out) * in_blocks;
+  p.ws_out = GRAD ? 1 : in_blocks;
+  p.ws_block = GRAD ? in_blocks : 1;
+  p.E = g.E;
+  p.N = N;
+  p.n_tiles = (N + BN - 1) / BN;
+  p.k_blocks = (int)fp8::blocks(K);
+  p.bias_fp16 = g.dtype == BRA_FP16;
+  p.aligned = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0 && N % 8 == 0;
+  // D fp32 (bit 4), the codes' formats (bits 7, 10: 0 e4m3, 1 e5m2), B N-major
+  // (bit 16), N >> 3 at 17, M >> 4 at 24
+  p.idesc = 1u << 4 | (uint32_t)g.xf << 7 | (uint32_t)g.wf << 10 | (GRAD ? 1u << 16 : 0u) |
+            (uint32_t)(BN >> 3) << 17 | (uint32_t)(8 * CG) << 24;
+  const int64_t groups = g.R < g.E ? g.R : g.E;
+  const int64_t tiles = (g.R / (128 * CG) + groups) * p.n_tiles;         // at most
+  if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+  const int nc = (int)(tiles < clusters ? tiles : clusters);
+  return launch_clusters(fp8_grouped_kernel<T, CG, BN, GRAD>, 1, CG * nc, S::THREADS, S::SMEM_BYTES,
+                         st, p);
+}
+
+template <int CG, int BN, bool GRAD>
+cudaError_t launch_t(const Fp8Problem& g, cudaStream_t st) {
+  return g.dtype == BRA_BF16 ? launch<__nv_bfloat16, CG, BN, GRAD>(g, st)
+                             : launch<__half, CG, BN, GRAD>(g, st);
+}
+
+}  // namespace
+
+GroupedTile fp8_tile(const Fp8Problem& g) {
+  const int64_t N = g.grad ? g.in : g.out, groups = g.R < g.E ? g.R : g.E;
+  if (g.R / g.E >= 128 && (2 * (g.R / 256) + groups) * ((N + 255) / 256) >= 2 * 76)
+    return {256, 256, 1, 0};
+  return {128, 128, 1, 0};
+}
+
+cudaError_t launch_fp8_grouped(const Fp8Problem& g, cudaStream_t st) {
+  const GroupedTile t = fp8_tile(g);
+  if (t.rows == 256) return g.grad ? launch_t<2, 256, true>(g, st) : launch_t<2, 256, false>(g, st);
+  return g.grad ? launch_t<1, 128, true>(g, st) : launch_t<1, 128, false>(g, st);
+}
+
+cudaError_t read_fp8_fault_word(int32_t* code, int clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(code, g_bra_fault_word_fp8, sizeof(int32_t));
+  if (e != cudaSuccess) return e;
+  if (clear) {
+    const int32_t z = 0;
+    e = cudaMemcpyToSymbol(g_bra_fault_word_fp8, &z, sizeof(int32_t));
+  }
+  return e;
+}
+
+}  // namespace bra

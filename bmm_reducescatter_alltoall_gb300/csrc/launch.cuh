@@ -45,4 +45,25 @@ cudaError_t launch_overlapped(void (*kernel)(Params...), unsigned grid, unsigned
   return cudaLaunchKernelEx(&cfg, kernel, Params(std::forward<Args>(args))...);
 }
 
+// The same with the grid in clusters of `cluster` CTAs, a size chosen at the launch.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(Params...), unsigned cluster, unsigned grid,
+                            unsigned threads, size_t smem, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(std::forward<Args>(args))...);
+}
+
 }  // namespace bra

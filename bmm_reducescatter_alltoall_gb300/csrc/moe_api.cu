@@ -3,33 +3,12 @@
 #include <cstdio>
 #include <cstring>
 
-#include "moe_internal.h"
+#include "moe_checks.h"
 #include "mx.cuh"
 
 namespace {
 
 using namespace bra;
-
-// Rows of a call: a tile's last row index stays in 32 bits.
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - (int64_t(1) << 16);
-
-bool off_by(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
-
-bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
-  if (!a || !b || an <= 0 || bn <= 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
-}
-
-// Whether `rows` rows `pitch` elements apart (of at most 8 bytes) count in 64 bits.
-bool counts_in_64_bits(int64_t rows, int64_t pitch) {
-  return rows <= 0 || pitch <= (int64_t(1) << 59) / rows;
-}
-
-// Bytes of `rows` rows of n elements, ld apart (the last one without padding).
-int64_t span(int64_t rows, int64_t ld, int64_t n, int64_t es) {
-  return rows > 0 ? ((rows - 1) * ld + n) * es : 0;
-}
 
 struct GroupedSizes {
   int64_t R, E, K, N, xp, yp;
@@ -99,16 +78,6 @@ int check_workspace(const bra_grouped_args* a, int64_t need) {
   return a->workspace_bytes >= need ? BRA_OK : BRA_ERR_INVALID;
 }
 
-int status_of(cudaError_t e) {
-  return e == cudaSuccess ? BRA_OK : e == cudaErrorInvalidValue ? BRA_ERR_UNSUPPORTED
-                                                                : BRA_ERR_CUDA;
-}
-
-int clear_status(int32_t* status, cudaStream_t st) {
-  if (!status) return BRA_OK;
-  return cudaMemsetAsync(status, 0, sizeof(int32_t), st) == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;
-}
-
 // Says which kernel a grouped product takes.
 void log_tile(const char* what, const GroupedProblem& g, const GroupedTile& t) {
   if (!log_enabled()) return;
@@ -167,29 +136,6 @@ MxRows mx_rows(const uint8_t* codes, const uint8_t* scales, const int64_t* count
           a->k,
           a->rows_per_group,
           (int)a->groups};
-}
-
-// A range of memory of a call.
-struct Span {
-  const void* p;
-  int64_t n;
-};
-
-// Whether an output overlaps an input or another output.
-bool any_overlap(const Span* outs, int no, const Span* ins, int ni) {
-  for (int i = 0; i < no; ++i) {
-    for (int j = 0; j < ni; ++j)
-      if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return true;
-    for (int j = 0; j < i; ++j)
-      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
-  }
-  return false;
-}
-
-int64_t element_size(int dtype) { return dtype == BRA_FP32 ? 4 : 2; }
-
-bool row_dtype_ok(int dtype) {
-  return dtype == BRA_FP16 || dtype == BRA_BF16 || dtype == BRA_FP32;
 }
 
 int check_route(const bra_route_args* a) {

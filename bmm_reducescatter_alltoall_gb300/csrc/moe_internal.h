@@ -99,6 +99,38 @@ cudaError_t launch_mx_grouped(const MxProblem& g, cudaStream_t st);
 bool mx_pair(const MxProblem& g);
 cudaError_t read_mx_fault_word(int32_t* code, int clear);
 
+// Codes and scales in the 8-bit block-scaled layout (fp8.cuh): rows (each 0),
+// or weights of E groups of `each` rows.
+struct Fp8Data {
+  uint8_t* codes;
+  float* scales;
+  const int64_t* counts;   // rows: device [E], or nullptr
+  int32_t* status;
+  int64_t R, K, each;
+  int E, format;
+};
+cudaError_t launch_fp8_quantize(const Fp8Data& q, const void* x, int64_t ld, int dtype,
+                                cudaStream_t st);
+cudaError_t launch_fp8_dequantize(const Fp8Data& q, void* y, int dtype, cudaStream_t st);
+struct Fp8Problem {
+  const uint8_t* xc;     // rows (x, or dy)
+  const float* xs;
+  const uint8_t* wc;     // weights (E, out, in)
+  const float* ws;
+  const void* bias;      // [E][N] or nullptr
+  void* y;               // [R][ldy]
+  const int64_t* counts;
+  int32_t* status;
+  int64_t R, ldy;
+  int E, in, out;        // the weight's sizes
+  int grad;              // rows of `out` elements to rows of `in`, not the other way
+  int dtype, xf, wf;
+};
+cudaError_t launch_fp8_grouped(const Fp8Problem& g, cudaStream_t st);
+// The output tile it takes (256 rows: a CTA pair's).
+GroupedTile fp8_tile(const Fp8Problem& g);
+cudaError_t read_fp8_fault_word(int32_t* code, int clear);
+
 // The router.  hist: workspace of chunks x E int32 when there are several.
 struct RouteCall {
   const void* logits;

@@ -1,8 +1,9 @@
 /*
  * bra_moe.h -- ragged expert operators of libbmmrsa2a.so: matrix products
  * grouped by expert with row groups of any size, and their gradients; the
- * same products on 4-bit microscaled weights and rows; the router that makes
- * the groups, and the moves of token rows to their experts and back.
+ * same products on 4-bit microscaled and on 8-bit block-scaled weights and
+ * rows; the router that makes the groups, and the moves of token rows to
+ * their experts and back.
  *
  * They work on one matrix of rows sorted by expert, and the number of rows of
  * each expert in device memory (int64).  all_to_all_v counts elements, not
@@ -181,6 +182,105 @@ BRA_API int mxfp4_grouped_matmul(const uint8_t* x_codes, const uint8_t* x_scales
                                  const uint8_t* w_codes, const uint8_t* w_scales,
                                  const void* bias, const int64_t* counts, void* y,
                                  const bra_grouped_args* args, bra_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit floating point with a scale to each block of 128                    */
+/* ------------------------------------------------------------------------ */
+
+/* Formats of the codes: e4m3 (largest 448, no infinity), e5m2 (57344). */
+#define BRA_E4M3 0
+#define BRA_E5M2 1
+
+/*
+ * Rows of 8-bit codes with one fp32 scale to each 128 elements of a row, or
+ * weights with one to each 128 x 128.  An element's value is its code's times
+ * its block's scale.  fp8_quantize takes for a block with largest magnitude a
+ * the smallest power of two 2^s, s >= -126, with a <= 2^s times the format's
+ * largest value (a = 0: 2^-126), and the nearest code to x / 2^s, ties to the
+ * even one.  A block with a NaN or an infinity gets the scale NaN and codes
+ * of zero: every value of it is NaN.  The products take any scales.
+ *
+ * codes: fp8_code_bytes: rows of ceil(K/16) * 16 bytes; those past K are
+ * written as zeros and never read.  scales, fp8_scale_bytes:
+ *   rows     (R, S) fp32, S = ceil(K/128) rounded up to a multiple of 4; those
+ *            past ceil(K/128) are written as zeros and never used.
+ *   weights  (E, ceil(N/128), ceil(K/128)) fp32, N the rows of a group.
+ */
+typedef struct {
+  int64_t rows;            /* R: 0 .. 2^31 - 2^16                              */
+  int64_t k;               /* K: elements of a row, 1 .. 2^24                  */
+  int64_t groups;          /* E: 1 .. BRA_MAX_GROUPS                           */
+  int64_t rows_per_group;  /* 0: rows.  Else weights: E groups of this many    */
+                           /* rows (R = E * that)                              */
+  int64_t x_pitch;         /* quantize: elements between rows of x; 0 = K; at  */
+                           /* most 2^36, and rows times it 2^59                */
+  int32_t dtype;           /* x, dequantized y: BRA_FP16, BRA_BF16 or BRA_FP32 */
+  int32_t format;          /* codes: BRA_E4M3 or BRA_E5M2                      */
+  int32_t* status;         /* device int32 of this call, or NULL               */
+} bra_fp8_args;
+
+/* Bytes of the two buffers (or a negative bra_status).  Pure host. */
+BRA_API int64_t fp8_code_bytes(const bra_fp8_args* args);
+BRA_API int64_t fp8_scale_bytes(const bra_fp8_args* args);
+
+/*
+ * fp8_quantize -- x (R, K) to codes and scales; fp8_dequantize -- back to y
+ * (R, K), dense: the product of code and scale in fp32, rounded to dtype.
+ * counts: NULL, or for rows device int64 (E): rows past their sum are neither
+ * read nor written, and counts are checked on the device as in
+ * grouped_matmul.  A row's codes and scales do not depend on its group.
+ * Errors: BRA_ERR_NULLPTR for a NULL args, or data with R > 0;
+ * BRA_ERR_INVALID for sizes outside the ranges, rows other than groups *
+ * rows_per_group, counts with weights, another dtype or format, a pitch below
+ * K (quantize) or any (dequantize), codes or scales not 16-byte aligned, x, y
+ * or counts not element-aligned, an output overlapping an input or the other
+ * output; BRA_ERR_CUDA.
+ */
+BRA_API int fp8_quantize(const void* x, const int64_t* counts, uint8_t* codes, float* scales,
+                         const bra_fp8_args* args, bra_stream_t stream);
+BRA_API int fp8_dequantize(const uint8_t* codes, const float* scales, const int64_t* counts,
+                           void* y, const bra_fp8_args* args, bra_stream_t stream);
+
+/* Sizes and options of an 8-bit product.  Zero-initialise. */
+typedef struct {
+  int64_t rows;        /* R: 0 .. 2^31 - 2^16                                 */
+  int64_t groups;      /* E: 1 .. BRA_MAX_GROUPS                              */
+  int64_t in;          /* K: 1 .. 2^24                                        */
+  int64_t out;         /* N: 1 .. 2^24                                        */
+  int32_t dtype;       /* y, dx: BRA_FP16 or BRA_BF16                         */
+  int32_t x_format;    /* rows (x or dy): BRA_E4M3 or BRA_E5M2                */
+  int32_t w_format;    /* weights: BRA_E4M3 or BRA_E5M2                       */
+  int32_t reserved;    /* 0                                                   */
+  int64_t y_pitch;     /* elements between rows of y (or dx); 0 = dense; at   */
+                       /* most 2^36, and rows times it 2^59                   */
+  int32_t* status;     /* device int32 of this call, or NULL                  */
+} bra_fp8_product_args;
+
+/*
+ * fp8_grouped_matmul -- grouped_matmul on 8-bit operands: x rows (R, K), the
+ * weight E groups of N rows (E, N, K).  For the rows r of expert e
+ *   y[r, n] = sum over blocks b of sx[r, b] * sw[e, n/128, b] *
+ *             (sum of the codes' products of block b) + bias[e, n],
+ * sums, scales' products and the bias in fp32, one rounding to dtype.  The
+ * product of two finite scales that passes the largest float counts as that.
+ * fp8_grouped_matmul_grad -- its gradient of x for the output's gradient, on
+ * the same weight: dy rows (R, N),
+ *   dx[r, k] = sum over blocks b of N of sd[r, b] * sw[e, b, k/128] * (...).
+ * (The weight's gradient contracts over the rows, across the rows' scales:
+ * grouped_matmul_grad on 16-bit operands.)
+ * bias, counts and status as grouped_matmul; y and dx may have any
+ * element-aligned pointer and pitch.  Errors as grouped_matmul, without its
+ * workspace; codes and the rows' scales have to be 16-byte aligned, the
+ * weight's scales 4-byte (BRA_ERR_INVALID).
+ */
+BRA_API int fp8_grouped_matmul(const uint8_t* x_codes, const float* x_scales,
+                               const uint8_t* w_codes, const float* w_scales, const void* bias,
+                               const int64_t* counts, void* y, const bra_fp8_product_args* args,
+                               bra_stream_t stream);
+BRA_API int fp8_grouped_matmul_grad(const uint8_t* dy_codes, const float* dy_scales,
+                                    const uint8_t* w_codes, const float* w_scales,
+                                    const int64_t* counts, void* dx,
+                                    const bra_fp8_product_args* args, bra_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Router                                                                    */

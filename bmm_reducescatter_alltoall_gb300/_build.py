@@ -82,6 +82,7 @@ KERNEL_SOURCES = {
     "route_scan_kernel": "moe_route.cu",
     "route_place_kernel": "moe_route.cu",
     "route_grad_kernel": "moe_route.cu",
+    "route_scored_kernel": "moe_score.cu",
     "dispatch_kernel": "moe_permute.cu",
     "list_rows_kernel": "moe_permute.cu",
     "spread_kernel": "moe_permute.cu",

@@ -138,14 +138,69 @@ MxRows mx_rows(const uint8_t* codes, const uint8_t* scales, const int64_t* count
           (int)a->groups};
 }
 
+bool route_sizes_ok(int64_t T, int64_t E, int64_t k, int dtype) {
+  return T >= 0 && E >= 1 && E <= BRA_MAX_GROUPS && k >= 1 && k <= BRA_MAX_CHOICES && k <= E &&
+         T < (int64_t(1) << 31) && T * k < (int64_t(1) << 31) && row_dtype_ok(dtype);
+}
+
 int check_route(const bra_route_args* a) {
   if (!a) return BRA_ERR_NULLPTR;
-  if (a->tokens < 0 || a->experts < 1 || a->experts > BRA_MAX_GROUPS || a->choices < 1 ||
-      a->choices > BRA_MAX_CHOICES || a->choices > a->experts ||
-      a->tokens >= (int64_t(1) << 31) || a->tokens * a->choices >= (int64_t(1) << 31) ||
-      !row_dtype_ok(a->dtype))
+  return route_sizes_ok(a->tokens, a->experts, a->choices, a->dtype) ? BRA_OK : BRA_ERR_INVALID;
+}
+
+int check_score(const bra_score_args* a) {
+  if (!a) return BRA_ERR_NULLPTR;
+  const float c = a->scale < 0.f ? -a->scale : a->scale;
+  if (!route_sizes_ok(a->tokens, a->experts, a->choices, a->dtype) ||
+      (a->score != BRA_SCORE_SOFTMAX && a->score != BRA_SCORE_SIGMOID) || a->groups < 1 ||
+      a->groups > BRA_MAX_EXPERT_GROUPS || a->experts % a->groups != 0 || a->top_groups < 1 ||
+      a->top_groups > a->groups || (a->group_best != 1 && a->group_best != 2) ||
+      !(c >= 0x1p-100f && c <= 0x1p100f) || a->reserved != 0)
     return BRA_ERR_INVALID;
   return BRA_OK;
+}
+
+int64_t route_workspace(int64_t T, int64_t E) {
+  const int64_t chunk = route_chunk(T), chunks = (T + chunk - 1) / chunk;
+  return chunks > 1 ? (chunks * E * 4 + 255) / 256 * 256 : 0;
+}
+
+// moe_route, and with `s` moe_route_scored; sizes are checked.
+int run_route(const RouteCall& r, const ScoreCall* s, int64_t workspace_bytes, cudaStream_t st) {
+  const int64_t need = route_workspace(r.T, r.E);
+  const bool some = r.T > 0;
+  if (!r.counts || (some && (!r.logits || !r.ids || !r.weights || !r.slots || !r.tokens)) ||
+      (need > 0 && !r.hist))
+    return BRA_ERR_NULLPTR;
+  const int64_t es = element_size(r.dtype), n = r.T * r.k * 4;
+  const float* bias = s ? s->bias : nullptr;
+  if (off_by(r.logits, es - 1) || off_by(r.ids, 3u) || off_by(r.weights, 3u) || off_by(r.counts, 7u) ||
+      off_by(r.slots, 3u) || off_by(r.tokens, 3u) || off_by(bias, 3u) || off_by(r.hist, 255u) ||
+      workspace_bytes < need)
+    return BRA_ERR_INVALID;
+  const Span outs[6] = {{r.ids, n},   {r.weights, n}, {r.counts, (int64_t)r.E * 8},
+                        {r.slots, n}, {r.tokens, n},  {r.hist, need}};
+  const Span ins[2] = {{r.logits, r.T * r.E * es}, {bias, (int64_t)r.E * 4}};
+  if (any_overlap(outs, 6, ins, 2)) return BRA_ERR_INVALID;
+  if (!some)
+    return cudaMemsetAsync(r.counts, 0, (size_t)r.E * 8, st) == cudaSuccess ? BRA_OK : BRA_ERR_CUDA;
+  return status_of(s ? launch_route_scored(r, *s, st) : launch_route(r, st));
+}
+
+// The gradient of either; sizes are checked.
+int run_route_grad(const RouteGradCall& r, cudaStream_t st) {
+  if (r.T == 0) return BRA_OK;
+  if (!r.dweights || !r.ids || !r.weights || !r.dlogits ||
+      ((r.sigmoid || !r.renorm) && !r.logits))
+    return BRA_ERR_NULLPTR;
+  const int64_t es = element_size(r.dtype), n = r.T * r.k * 4, lb = r.T * r.E * es;
+  if (off_by(r.logits, es - 1) || off_by(r.dlogits, es - 1) || off_by(r.dweights, 3u) ||
+      off_by(r.ids, 3u) || off_by(r.weights, 3u))
+    return BRA_ERR_INVALID;
+  const Span outs[1] = {{r.dlogits, lb}};
+  const Span ins[4] = {{r.dweights, n}, {r.ids, n}, {r.weights, n}, {r.logits, lb}};
+  if (any_overlap(outs, 1, ins, 4)) return BRA_ERR_INVALID;
+  return status_of(launch_route_grad(r, st));
 }
 
 int check_permute(const bra_permute_args* a) {
@@ -185,41 +240,36 @@ extern "C" {
 
 int64_t moe_route_workspace_size(const bra_route_args* args) {
   const int rc = check_route(args);
-  if (rc != BRA_OK) return -rc;
-  const int64_t chunk = route_chunk(args->tokens);
-  const int64_t chunks = (args->tokens + chunk - 1) / chunk;
-  return chunks > 1 ? (chunks * args->experts * 4 + 255) / 256 * 256 : 0;
+  return rc != BRA_OK ? -rc : route_workspace(args->tokens, args->experts);
+}
+
+int64_t moe_route_scored_workspace_size(const bra_score_args* args) {
+  const int rc = check_score(args);
+  return rc != BRA_OK ? -rc : route_workspace(args->tokens, args->experts);
 }
 
 int moe_route(const void* logits, int32_t* ids, float* weights, int64_t* counts, int32_t* slots,
               int32_t* tokens, void* workspace, int64_t workspace_bytes,
               const bra_route_args* args, bra_stream_t stream) {
-  const int64_t need = moe_route_workspace_size(args);
-  if (need < 0) return (int)-need;
-  const bool some = args->tokens > 0;
-  if (!counts || (some && (!logits || !ids || !weights || !slots || !tokens)) ||
-      (need > 0 && !workspace))
-    return BRA_ERR_NULLPTR;
-  const int64_t es = element_size(args->dtype), n = args->tokens * args->choices * 4;
-  if (off_by(logits, es - 1) || off_by(ids, 3u) || off_by(weights, 3u) || off_by(counts, 7u) ||
-      off_by(slots, 3u) || off_by(tokens, 3u) || off_by(workspace, 255u) || workspace_bytes < need)
-    return BRA_ERR_INVALID;
-  const Span outs[6] = {{ids, n},   {weights, n}, {counts, args->experts * 8},
-                        {slots, n}, {tokens, n},  {workspace, need}};
-  const Span ins[1] = {{logits, args->tokens * args->experts * es}};
-  if (any_overlap(outs, 6, ins, 1)) return BRA_ERR_INVALID;
-  const cudaStream_t st = (cudaStream_t)stream;
-  if (!some)
-    return cudaMemsetAsync(counts, 0, (size_t)args->experts * 8, st) == cudaSuccess ? BRA_OK
-                                                                                    : BRA_ERR_CUDA;
-  const RouteCall r = {logits,       ids,
-                       weights,      counts,
-                       slots,        tokens,
-                       static_cast<int32_t*>(workspace),
-                       args->tokens, (int)args->experts,
-                       (int)args->choices, args->renormalize ? 1 : 0,
-                       args->dtype};
-  return status_of(launch_route(r, st));
+  const int rc = check_route(args);
+  if (rc != BRA_OK) return rc;
+  const RouteCall r = {logits, ids, weights, counts, slots, tokens, static_cast<int32_t*>(workspace),
+                       args->tokens, (int)args->experts, (int)args->choices,
+                       args->renormalize ? 1 : 0, args->dtype};
+  return run_route(r, nullptr, workspace_bytes, (cudaStream_t)stream);
+}
+
+int moe_route_scored(const void* logits, const float* bias, int32_t* ids, float* weights,
+                     int64_t* counts, int32_t* slots, int32_t* tokens, void* workspace,
+                     int64_t workspace_bytes, const bra_score_args* args, bra_stream_t stream) {
+  const int rc = check_score(args);
+  if (rc != BRA_OK) return rc;
+  const RouteCall r = {logits, ids, weights, counts, slots, tokens, static_cast<int32_t*>(workspace),
+                       args->tokens, (int)args->experts, (int)args->choices,
+                       args->renormalize ? 1 : 0, args->dtype};
+  const ScoreCall s = {bias, args->score == BRA_SCORE_SIGMOID ? 1 : 0, args->groups,
+                       args->top_groups, args->group_best, args->scale};
+  return run_route(r, &s, workspace_bytes, (cudaStream_t)stream);
 }
 
 int moe_route_grad(const float* dweights, const void* logits, const int32_t* ids,
@@ -227,23 +277,21 @@ int moe_route_grad(const float* dweights, const void* logits, const int32_t* ids
                    bra_stream_t stream) {
   const int rc = check_route(args);
   if (rc != BRA_OK) return rc;
-  if (args->tokens == 0) return BRA_OK;
-  if (!dweights || !ids || !weights || !dlogits || (!args->renormalize && !logits))
-    return BRA_ERR_NULLPTR;
-  const int64_t es = element_size(args->dtype), n = args->tokens * args->choices * 4,
-                lb = args->tokens * args->experts * es;
-  if (off_by(logits, es - 1) || off_by(dlogits, es - 1) || off_by(dweights, 3u) || off_by(ids, 3u) ||
-      off_by(weights, 3u))
-    return BRA_ERR_INVALID;
-  const Span outs[1] = {{dlogits, lb}};
-  const Span ins[4] = {{dweights, n}, {ids, n}, {weights, n}, {logits, lb}};
-  if (any_overlap(outs, 1, ins, 4)) return BRA_ERR_INVALID;
-  const RouteGradCall r = {dweights,     logits,
-                           ids,          weights,
-                           dlogits,      args->tokens,
-                           (int)args->experts, (int)args->choices,
-                           args->renormalize ? 1 : 0, args->dtype};
-  return status_of(launch_route_grad(r, (cudaStream_t)stream));
+  const RouteGradCall r = {dweights, logits, ids, weights, dlogits, args->tokens,
+                           (int)args->experts, (int)args->choices, args->renormalize ? 1 : 0,
+                           args->dtype, 0, 1.f};
+  return run_route_grad(r, (cudaStream_t)stream);
+}
+
+int moe_route_scored_grad(const float* dweights, const void* logits, const int32_t* ids,
+                          const float* weights, void* dlogits, const bra_score_args* args,
+                          bra_stream_t stream) {
+  const int rc = check_score(args);
+  if (rc != BRA_OK) return rc;
+  const RouteGradCall r = {dweights, logits, ids, weights, dlogits, args->tokens,
+                           (int)args->experts, (int)args->choices, args->renormalize ? 1 : 0,
+                           args->dtype, args->score == BRA_SCORE_SIGMOID ? 1 : 0, args->scale};
+  return run_route_grad(r, (cudaStream_t)stream);
 }
 
 int64_t moe_dispatch_workspace_size(const bra_permute_args* args) {

@@ -145,6 +145,18 @@ struct RouteCall {
 };
 int route_chunk(int64_t T);                     // tokens of a chunk
 cudaError_t launch_route(const RouteCall& r, cudaStream_t st);
+// The router by scores, and how it lays out E experts of `groups` groups:
+// lanes of a token, most experts of a lane, lanes of a group, experts of a lane.
+struct ScoreCall {
+  const float* bias;
+  int sigmoid, groups, top_groups, best;
+  float scale;
+};
+struct ScoreShape {
+  int L, V, lanes, per;
+};
+ScoreShape score_shape(int E, int groups);
+cudaError_t launch_route_scored(const RouteCall& r, const ScoreCall& s, cudaStream_t st);
 struct RouteGradCall {
   const float* dweights;
   const void* logits;
@@ -153,6 +165,8 @@ struct RouteGradCall {
   void* dlogits;
   int64_t T;
   int E, k, renorm, dtype;
+  int sigmoid;                 // weights of scores, times scale
+  float scale;
 };
 cudaError_t launch_route_grad(const RouteGradCall& r, cudaStream_t st);
 // Row permutation; in and out are token rows (T) or expert rows (R).

@@ -24,71 +24,15 @@
 // where the logits' 34 MB take 5, 12 for the rows, 13 for the gradient.  For
 // few tokens it is one launch (64 tokens, 8 of 64: 4.7 us); a million tokens,
 // 8 of 128, take 504 us.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <mutex>
 #include <type_traits>
 
-#include "moe_internal.h"
+#include "route.cuh"
 
 namespace bra {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMostChunk = 1024;          // most tokens of a chunk
-constexpr float kLargest = 3.402823466e+38f;
-
-template <typename T>
-__device__ __forceinline__ float logit(const T* p) {
-  const float v = static_cast<float>(*p);
-  // NaN stays NaN; +0 for -0, so that equal logits are equal as integers
-  return (v > kLargest ? kLargest : v) + 0.0f;
-}
-// Order of floats as unsigned integers; 0 for -inf and NaN: not a choice.
-__device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t u = __float_as_uint(v);
-  return v >= -kLargest ? (u & 0x80000000u ? ~u : u | 0x80000000u) : 0u;
-}
-__device__ __forceinline__ float value_of(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
-}
-struct RouteParams {
-  const void* logits;
-  int32_t* ids;        // [T][k]
-  float* weights;      // [T][k]
-  int64_t* counts;     // [E]
-  int32_t* slots;      // [T][k]
-  int32_t* tokens;     // [T*k]
-  int32_t* hist;       // [chunks][E], unless there is one chunk
-  int T, E, k, renorm;
-  int chunk, chunks;   // tokens of a chunk (a multiple of 32)
-  int vec;             // logits' rows are read four at a time
-  int scanned;         // hist holds sums over the chunks up to each one
-};
-
-__device__ __forceinline__ float group_sum(float v, int L) {
-  for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
-}
-
-// Sorts eight (key, index) pairs, largest key first, equal keys by index:
-// Batcher's odd-even merge sort, 19 exchanges.
-__device__ __forceinline__ void sort_eight(uint32_t (&key)[8], int (&idx)[8]) {
-  auto put = [&](int a, int b) {
-    const bool swap = key[b] > key[a] || (key[b] == key[a] && idx[b] < idx[a]);
-    const uint32_t ka = swap ? key[b] : key[a], kb = swap ? key[a] : key[b];
-    const int ia = swap ? idx[b] : idx[a], ib = swap ? idx[a] : idx[b];
-    key[a] = ka, key[b] = kb, idx[a] = ia, idx[b] = ib;
-  };
-  put(0, 1), put(2, 3), put(4, 5), put(6, 7);
-  put(0, 2), put(1, 3), put(4, 6), put(5, 7);
-  put(1, 2), put(5, 6);
-  put(0, 4), put(1, 5), put(2, 6), put(3, 7);
-  put(2, 4), put(3, 5);
-  put(1, 2), put(3, 4), put(5, 6);
-}
+using namespace route;
 
 // The experts of one token to each group of L lanes (t < 0: none); lane l of
 // the group holds logits l * V ..  Writes ids and weights and sets the
@@ -190,104 +134,16 @@ __device__ __forceinline__ void choose(const RouteParams& p, int t, int lane, ui
     }
 }
 
-// Words from one expert's bits to the next: odd, so that the same word of
-// different experts lies in different banks (1024 tokens a chunk, 32 words
-// apart: 262144 tokens, 8 of 128, 257 us in place of 130).
-__host__ __device__ constexpr int bit_stride(int chunk) { return (chunk / 32) | 1; }
-
-// The chunk's experts as bits: chunk / 32 words to an expert.
-__device__ __forceinline__ void clear_bits(uint32_t* bits, int n) {
-  for (int i = threadIdx.x; i < n; i += kThreads) bits[i] = 0u;
-}
-
-// Rows before each expert's in this chunk: base[e], from the counts of the
-// chunks before (before[e]) and of all chunks (total[e]).  Every thread; ends
-// with a barrier.
-__device__ __forceinline__ void scan_experts(const RouteParams& p, const int* total,
-                                             const int* before, int* base, int* used) {
-  __shared__ int sums[kMaxGroups / 32];
-  const int e = threadIdx.x, lane = e & 31;
-  int n = 0, inc = 0;
-  if (e < kMaxGroups) {
-    n = e < p.E ? total[e] : 0;
-    inc = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += a;
-    }
-    if (lane == 31) sums[e >> 5] = inc;
-  }
-  __syncthreads();
-  if (e < kMaxGroups) {
-    int at = inc - n;
-    for (int w = 0; w < (e >> 5); ++w) at += sums[w];
-    if (e < p.E) base[e] = at + before[e];
-    if (e == kMaxGroups - 1) *used = at + n;
-  }
-  __syncthreads();
-}
-
-// This chunk's share of the rows that no pair has.
-__device__ __forceinline__ void mark_unused(const RouteParams& p, int c, int used) {
-  const int64_t R = (int64_t)p.T * p.k;
-  for (int64_t r = used + (int64_t)c * kThreads + threadIdx.x; r < R;
-       r += (int64_t)p.chunks * kThreads)
-    p.tokens[r] = -1;
-}
-
-// Choices of one chunk, and each pair's place among the chunk's rows of its
-// expert in `slots`; with a single chunk, everything.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteParams p) {
   extern __shared__ uint32_t bits[];                    // [E][stride]
-  __shared__ int total[kMaxGroups], base[kMaxGroups], zero[kMaxGroups];
-  __shared__ int used;
-  const int words = p.chunk / 32, stride = bit_stride(p.chunk), c = blockIdx.x, t0 = c * p.chunk;
-  const int n = min(p.chunk, p.T - t0);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  clear_bits(bits, p.E * stride);
+  clear_bits(bits, p.E * bit_stride(p.chunk));
   __syncthreads();
   grid_wait();
   grid_go();
-  constexpr int G = 32 / L;                             // tokens of a warp
-  for (int i0 = warp * G; i0 < n; i0 += kWarps * G) {
-    const int i = i0 + lane / L;
-    choose<T, L, V>(p, i < n ? t0 + i : -1, lane, bits, stride, i >> 5, 1u << (i & 31));
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
-    int s = 0;
-    for (int w = 0; w < words; ++w) s += __popc(bits[e * stride + w]);
-    if (p.chunks > 1) {
-      p.hist[(int64_t)c * p.E + e] = s;
-    } else {
-      total[e] = s;
-      zero[e] = 0;
-      p.counts[e] = s;
-    }
-  }
-  if (p.chunks == 1) {
-    __syncthreads();
-    scan_experts(p, total, zero, base, &used);
-    mark_unused(p, 0, used);
-  }
-  for (int i = threadIdx.x; i < n * p.k; i += kThreads) {
-    const int local = i / p.k;
-    const int64_t at = (int64_t)t0 * p.k + i;
-    const int e = p.ids[at];
-    int slot = -1;
-    if (e >= 0) {
-      const uint32_t* b = bits + e * stride;
-      slot = __popc(b[local >> 5] & ((1u << (local & 31)) - 1u));
-      for (int w = 0; w < (local >> 5); ++w) slot += __popc(b[w]);
-      if (p.chunks == 1) {
-        slot += base[e];
-        p.tokens[slot] = local;
-      }
-    }
-    p.slots[at] = slot;
-  }
+  route_chunk_of<L>(p, bits, [&](int t, int lane, int stride, int word, uint32_t bit) {
+    choose<T, L, V>(p, t, lane, bits, stride, word, bit);
+  });
 }
 
 // The matrix of counts, summed down its columns in place: a CTA to 32 experts,
@@ -382,6 +238,9 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteParams
 // Gradient of the logits: with g the gradient of the weights and s = sum w g,
 //   renormalised:  dl_i = w_j (g_j - s) for the chosen i = id_j, else 0
 //   otherwise:     dl_i = p_i ([i = id_j] g_j - s), p the softmax
+// Weights that were multiplied by c: w and s are c times as large, and g_j
+// loses s / c.  Sigmoid scores: the chosen ones' dl_i times 1 - sigmoid(l_i),
+// with s = 0 when not renormalised.
 // --------------------------------------------------------------------------
 struct RouteGradParams {
   const float* dweights;
@@ -391,6 +250,8 @@ struct RouteGradParams {
   void* dlogits;
   int T, E, k, renorm;
   int vec;             // rows are written four at a time
+  int sigmoid;
+  float inv_scale;     // one over what the weights were multiplied by
 };
 
 template <typename T>
@@ -439,8 +300,15 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
     float d[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) d[i] = 0.f;
-    if (!p.renorm) {
-      const T* row = static_cast<const T*>(p.logits) + t * p.E;
+    float rest[OWN];                 // 1 - sigmoid of the chosen logits
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) rest[o] = 1.f;
+    const T* row = static_cast<const T*>(p.logits) + t * p.E;
+    if (p.sigmoid) {
+#pragma unroll
+      for (int o = 0; o < OWN; ++o)
+        if (id[o] >= 0) rest[o] = 1.f / (1.f + expf(logit(row + id[o])));
+    } else if (!p.renorm) {
       uint32_t best = 0u;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -482,9 +350,10 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradParams p
       }
     }
     __syncwarp();                    // the row lies before its chosen elements are written
+    const float mean = p.sigmoid && !p.renorm ? 0.f : s * p.inv_scale;
 #pragma unroll
     for (int o = 0; o < OWN; ++o)
-      if (id[o] >= 0) out[id[o]] = rounded<T>(w[o] * (g[o] - s));
+      if (id[o] >= 0) out[id[o]] = rounded<T>(w[o] * (g[o] - mean) * rest[o]);
     __syncwarp();
   }
 }
@@ -526,11 +395,6 @@ cudaError_t choose_ready() {
   return cudaSuccess;
 }
 
-// Whether rows of E elements can be read four at a time.
-int rows_vec(const void* p, int E, int dtype) {
-  return E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & (dtype == BRA_FP32 ? 15u : 7u)) == 0;
-}
-
 }  // namespace
 
 // Tokens of a chunk: one chunk up to 64 tokens (one launch); else chunks of at
@@ -548,12 +412,26 @@ int route_chunk(int64_t T) {
 // 4194304 (4096) 3045 / 1982.
 constexpr int kScanChunks = 160;
 
+void route_chunks(RouteParams* p) {
+  p->chunk = route_chunk(p->T);
+  p->chunks = (int)(((int64_t)p->T + p->chunk - 1) / p->chunk);
+  p->scanned = p->chunks >= kScanChunks;
+}
+
+cudaError_t launch_route_places(const RouteParams& p, cudaStream_t st) {
+  if (p.chunks == 1) return cudaSuccess;
+  if (p.scanned) {
+    const cudaError_t a =
+        launch_overlapped(route_scan_kernel, (unsigned)(p.E + 31) / 32, kThreads, 0, st, p);
+    if (a != cudaSuccess) return a;
+  }
+  return launch_overlapped(route_place_kernel, (unsigned)p.chunks, kThreads, 0, st, p);
+}
+
 cudaError_t launch_route(const RouteCall& r, cudaStream_t st) {
-  RouteParams p = {r.logits, r.ids,   r.weights, r.counts, r.slots, r.tokens, r.hist, (int)r.T,
-                   r.E,      r.k,     r.renorm,  route_chunk(r.T), 0,
-                   rows_vec(r.logits, r.E, r.dtype), 0};
-  p.chunks = (int)((r.T + p.chunk - 1) / p.chunk);
-  p.scanned = p.chunks >= kScanChunks;
+  RouteParams p = {r.logits, r.ids, r.weights, r.counts, r.slots, r.tokens, r.hist, (int)r.T,
+                   r.E,      r.k,   r.renorm,  0,        0,       rows_vec(r.logits, r.E, r.dtype), 0};
+  route_chunks(&p);
   const int smem = r.E * bit_stride(p.chunk) * 4;
   const cudaError_t e = by_type(r.dtype, r.E, [&](auto* type, auto l, auto v) {
     using T = std::remove_pointer_t<decltype(type)>;
@@ -562,19 +440,13 @@ cudaError_t launch_route(const RouteCall& r, cudaStream_t st) {
     return launch_overlapped(route_choose_kernel<T, decltype(l)::value, decltype(v)::value>,
                              (unsigned)p.chunks, kThreads, smem, st, p);
   });
-  if (e != cudaSuccess || p.chunks == 1) return e;
-  if (p.scanned) {
-    const cudaError_t a =
-        launch_overlapped(route_scan_kernel, (unsigned)(r.E + 31) / 32, kThreads, 0, st, p);
-    if (a != cudaSuccess) return a;
-  }
-  return launch_overlapped(route_place_kernel, (unsigned)p.chunks, kThreads, 0, st, p);
+  return e != cudaSuccess ? e : launch_route_places(p, st);
 }
 
 cudaError_t launch_route_grad(const RouteGradCall& r, cudaStream_t st) {
   const RouteGradParams p = {r.dweights, r.logits, r.ids, r.weights, r.dlogits,
                              (int)r.T,   r.E,      r.k,   r.renorm,
-                             rows_vec(r.dlogits, r.E, r.dtype)};
+                             rows_vec(r.dlogits, r.E, r.dtype), r.sigmoid, 1.f / r.scale};
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -1,0 +1,463 @@
+// The router by scores: experts chosen by score plus bias, from the best
+// groups of experts, weighted by the scores alone.
+//
+//   s_i    = 1 / (1 + exp(-l_i)), or the softmax of the open logits
+//   r_i    = s_i + bias_i, or without a bias l_i (which orders alike)
+//   v_g    = the largest r of a group, or the sum of its two largest (without
+//            a bias of the scores' two largest)
+//   ids    = the k largest r of the groups with the largest v; ties to the
+//            lowest group, then the lowest expert
+//   w_j    = scale * s, divided by the chosen scores' sum when renormalised
+//
+// The choice is that of r and v computed in 64 bits.  They are computed in 32
+// first, with bounds on the error: where two neighbours of the order that
+// matter (the chosen ones and the next one; the last group kept and the first
+// left out) lie closer than the bounds, and are not the same logit and bias,
+// the token is chosen again in 64 bits.  Of 65536 tokens, 8 of 256 by sigmoid,
+// that is one in some 1000; 64-bit exponentials for all would take
+// milliseconds.
+//
+// As in moe_route.cu a group of L lanes takes a token.  A group of experts has
+// lanes of its own (a power of two), so that its two largest are found in the
+// sorted lists' heads and exchanges among these lanes; places of the lanes
+// past a group's experts stay empty.  Chunks, bits and places are shared
+// with moe_route.cu.
+#include <mutex>
+#include <type_traits>
+
+#include "route.cuh"
+
+namespace bra {
+namespace {
+
+using namespace route;
+
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct ScoreParams {
+  RouteParams r;
+  const float* bias;   // [E], or nullptr
+  float scale;
+  int sigmoid;
+  int groups, top_groups, best;   // groups 1: no restriction
+  int size;            // experts of a group
+  int lanes;           // lanes of a group, a power of two
+  int per;             // experts of a lane, a multiple of four, at most V
+  int bias_vec;        // bias is read four at a time
+};
+
+// The two largest of (a1 >= a2) and (b1 >= b2).
+template <typename F>
+__device__ __forceinline__ void best_two(F& a1, F& a2, F b1, F b2) {
+  const F low = a1 < b1 ? a1 : b1, next = a2 > b2 ? a2 : b2;
+  a1 = a1 < b1 ? b1 : a1;
+  a2 = low > next ? low : next;
+}
+
+// Where a lane's experts are.
+struct Place {
+  uint32_t group;      // this token's lanes
+  int gl, g, first, own;
+  template <int L>
+  __device__ __forceinline__ static Place of(const ScoreParams& p, int lane) {
+    Place a;
+    a.group = L == 32 ? kAll : ((1u << (L & 31)) - 1u) << (lane & ~(L - 1));
+    a.gl = lane % L;
+    a.g = a.gl / p.lanes;
+    const int off = (a.gl - a.g * p.lanes) * p.per;
+    a.first = a.g * p.size + off;
+    a.own = a.g < p.groups ? max(0, min(p.per, p.size - off)) : 0;
+    return a;
+  }
+};
+
+// The choice in 64 bits: the ids of one token, by the lanes of `at.group`.
+template <typename T, int L, int V>
+__device__ __noinline__ void choose_exact(const ScoreParams& p, int t, int lane) {
+  const Place at = Place::of<L>(p, lane);
+  const T* row = static_cast<const T*>(p.r.logits) + (int64_t)t * p.r.E + at.first;
+  const double inf = INFINITY;
+  float m = -INFINITY;
+  double sum = 0.0;
+  if (!p.sigmoid) {
+#pragma unroll 1
+    for (int i = 0; i < at.own; ++i) m = fmaxf(m, logit(row + i));         // NaN is passed over
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(at.group, m, d));
+#pragma unroll 1
+    for (int i = 0; i < at.own; ++i) {
+      const float v = logit(row + i);
+      if (v >= -kLargest) sum += exp((double)v - (double)m);
+    }
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(at.group, sum, d);
+  }
+  double r[V], f1 = -inf, f2 = -inf;
+#pragma unroll 1
+  for (int i = 0; i < V; ++i) {
+    const float v = i < at.own ? logit(row + i) : -INFINITY;
+    r[i] = -inf;
+    if (v >= -kLargest) {
+      const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)m) / sum;
+      double x = p.bias ? s + (double)p.bias[at.first + i] : (double)v;
+      if (!(x > -inf)) x = -inf;
+      r[i] = x < 1e300 ? x : 1e300;
+      best_two(f1, f2, p.bias || p.best == 1 ? r[i] : s, -inf);
+    }
+  }
+  if (p.top_groups < p.groups) {
+    for (int d = 1; d < p.lanes; d <<= 1) {
+      const double b1 = __shfl_xor_sync(at.group, f1, d), b2 = __shfl_xor_sync(at.group, f2, d);
+      best_two(f1, f2, b1, b2);
+    }
+    const double v = p.best == 2 && f2 > -inf ? f1 + f2 : f1;
+    int better = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const double o = __shfl_sync(at.group, v, g * p.lanes, L);
+      better += o > v || (o == v && g < at.g) ? 1 : 0;
+    }
+    if (better >= p.top_groups)
+#pragma unroll 1
+      for (int i = 0; i < V; ++i) r[i] = -inf;
+  }
+  for (int j = 0; j < p.r.k; ++j) {
+    double most = -inf;
+    int mine = 0;
+#pragma unroll 1
+    for (int i = 0; i < V; ++i)
+      if (r[i] > most) most = r[i], mine = i;
+    double top = most;
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) {
+      const double o = __shfl_xor_sync(at.group, top, d);
+      top = o > top ? o : top;
+    }
+    const int win = __ffs(__ballot_sync(at.group, most == top)) - 1;
+    const int id = __shfl_sync(at.group, at.first + mine, win);
+    if (lane == win) r[mine] = -inf;
+    if (at.gl == j % L) p.r.ids[(int64_t)t * p.r.k + j] = top > -inf ? id : -1;
+  }
+}
+
+// The experts of one token to each group of L lanes (t < 0: none): as choose
+// of moe_route.cu.  Whole warps.
+template <typename T, int L, int V>
+__device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place& at, int t, int lane,
+                                              const float* bias, uint32_t* bits, int stride, int word,
+                                              uint32_t bit) {
+  constexpr int OWN = (BRA_MAX_CHOICES + L - 1) / L;   // choices a lane keeps
+  constexpr int NL = V / 8;
+  const T* row = static_cast<const T*>(p.r.logits) + (int64_t)t * p.r.E;
+  float l[V];
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    T raw[4];
+    if (t >= 0 && p.r.vec && i + 4 <= at.own) {
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<uint4*>(raw) = *reinterpret_cast<const uint4*>(row + at.first + i);
+      else
+        *reinterpret_cast<uint2*>(raw) = *reinterpret_cast<const uint2*>(row + at.first + i);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        raw[c] = t >= 0 && i + c < at.own ? row[at.first + i + c] : T(-INFINITY);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) l[i + c] = logit(&raw[c]);
+  }
+  const bool limited = p.top_groups < p.groups, ranked = p.bias != nullptr;
+  // softmax: the largest logit and the sum, where scores are needed
+  float m = 0.f, sum = 1.f;
+  if (!p.sigmoid && (ranked || !p.r.renorm || (limited && p.best == 2))) {
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, d));
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (l[i] >= -kLargest) sum += expf(l[i] - m);
+    sum = group_sum(sum, L);
+  }
+  const float inv = p.sigmoid ? 1.f : 1.f / sum;          // the largest score there can be
+  // of an open logit, for the choice: within 2^-21.8 (sigmoid: __expf's units
+  // times s (1 - s) |l|, the sum's and the quotient's)
+  auto score = [&](float v) {
+    return p.sigmoid ? __fdividef(1.f, 1.f + __expf(-v)) : expf(v - m) * inv;
+  };
+  // the least distance at which 32 bits decide: two scores' errors (softmax:
+  // also the sum's, one unit of 2^-24 a term of a lane and level), two sums'
+  const float slack = (p.sigmoid ? 0x1p-20f : 0x1p-18f) * inv;
+  auto close = [&](float hi, float lo) {
+    return hi - lo <= slack + fmaxf(fabsf(hi), fabsf(lo)) * 0x1p-22f;
+  };
+  bool again = false;
+
+  uint32_t key[NL][8], order[NL];               // order: sorted places, four bits each
+#pragma unroll
+  for (int n = 0; n < NL; ++n) {
+    int idx[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float x = l[n * 8 + i];
+      if (ranked && x >= -kLargest) {
+        x = score(x) + bias[n * 8 + i];
+        x = (x > kLargest ? kLargest : x) + 0.f;           // NaN stays
+      }
+      key[n][i] = key_of(x);
+      idx[i] = i;
+    }
+    sort_eight(key[n], idx);
+    order[n] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) order[n] |= (uint32_t)idx[i] << (4 * i);
+  }
+
+  if (limited) {
+    uint32_t k1 = key[0][0], k2 = key[0][1];
+#pragma unroll
+    for (int n = 1; n < NL; ++n) best_two(k1, k2, key[n][0], key[n][1]);
+    for (int d = 1; d < p.lanes; d <<= 1) {
+      const uint32_t b1 = __shfl_xor_sync(kAll, k1, d), b2 = __shfl_xor_sync(kAll, k2, d);
+      best_two(k1, k2, b1, b2);
+    }
+    float v = k1 ? value_of(k1) : -INFINITY;
+    if (p.best == 2 && k1) {
+      float w = k2 ? value_of(k2) : 0.f;
+      if (!ranked) {
+        v = score(v);
+        if (k2) w = score(w);
+      }
+      v = fmaxf(fminf(v + w, kLargest), -kLargest);
+    }
+    int better = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const float o = __shfl_sync(kAll, v, g * p.lanes, L);
+      better += o > v || (o == v && g < at.g) ? 1 : 0;
+    }
+    if (ranked || p.best == 2) {
+      // the last group kept and the first left out
+      const bool head = at.g < p.groups && at.gl == at.g * p.lanes;
+      const uint32_t in = __ballot_sync(kAll, head && better == p.top_groups - 1) & at.group;
+      const uint32_t out = __ballot_sync(kAll, head && better == p.top_groups) & at.group;
+      const float vi = __shfl_sync(kAll, v, __ffs(in) - 1), vo = __shfl_sync(kAll, v, __ffs(out) - 1);
+      again = vo > -INFINITY && vi - vo <= 2.f * (slack + fmaxf(fabsf(vi), fabsf(vo)) * 0x1p-22f);
+    }
+    if (better >= p.top_groups) {
+#pragma unroll
+      for (int n = 0; n < NL; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) key[n][i] = 0u;
+    }
+  }
+
+  int my_id[OWN];
+  float last = 0.f;
+  int last_id = -1;
+#pragma unroll
+  for (int o = 0; o < OWN; ++o) my_id[o] = -1;
+  const int rounds = p.r.k + (ranked ? 1 : 0);   // with a bias also the best one left out
+#pragma unroll
+  for (int o = 0; o <= BRA_MAX_CHOICES / L; ++o) {
+    for (int j = o * L; j < min(rounds, (o + 1) * L); ++j) {
+      uint32_t head = key[0][0];
+      int from = 0;
+#pragma unroll
+      for (int n = 1; n < NL; ++n)
+        if (key[n][0] > head) {
+          head = key[n][0];
+          from = n;
+        }
+      int place = 0;
+#pragma unroll
+      for (int n = 0; n < NL; ++n)
+        if (from == n) place = n * 8 + (int)(order[n] & 15u);
+      uint32_t most = head;
+      if constexpr (L == 32) {
+        most = __reduce_max_sync(kAll, head);
+      } else {
+#pragma unroll
+        for (int d = L / 2; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
+      }
+      const int win = __ffs(__ballot_sync(kAll, head == most) & at.group) - 1;
+      const int id = __shfl_sync(kAll, at.first + place, win);
+      if (ranked) {
+        const float x = value_of(most);
+        if (j > 0 && most && close(last, x)) {
+          // equal logits and equal biases are a tie in any precision
+          again |= logit(row + last_id) != logit(row + id) || p.bias[last_id] != p.bias[id];
+        }
+        last = x;
+        last_id = id;
+      }
+      if (o < OWN && at.gl == j - o * L && j < p.r.k && most) my_id[o < OWN ? o : 0] = id;
+      // the winner drops its head (with most = 0 there is nothing to drop)
+#pragma unroll
+      for (int n = 0; n < NL; ++n) {
+        const bool drop = lane == win && from == n;
+#pragma unroll
+        for (int i = 0; i + 1 < 8; ++i) key[n][i] = drop ? key[n][i + 1] : key[n][i];
+        key[n][7] = drop ? 0u : key[n][7];
+        order[n] = drop ? order[n] >> 4 : order[n];
+      }
+    }
+  }
+  const int64_t out = (int64_t)t * p.r.k;
+  if (again) {                                   // the same for all lanes of a token
+    choose_exact<T, L, V>(p, t, lane);
+#pragma unroll
+    for (int o = 0; o < OWN; ++o)
+      my_id[o] = o * L + at.gl < p.r.k ? p.r.ids[out + o * L + at.gl] : -1;
+  }
+  __syncwarp();
+  // the weights, from the chosen logits
+  float w[OWN], total = 0.f, peak = -INFINITY;
+#pragma unroll
+  for (int o = 0; o < OWN; ++o) {
+    w[o] = my_id[o] >= 0 && o * L + at.gl < p.r.k ? logit(row + my_id[o]) : -INFINITY;
+    peak = fmaxf(peak, w[o]);
+  }
+  if (!p.sigmoid && p.r.renorm) {
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) peak = fmaxf(peak, __shfl_xor_sync(kAll, peak, d));
+  }
+#pragma unroll
+  for (int o = 0; o < OWN; ++o) {
+    if (w[o] < -kLargest) w[o] = 0.f;            // no choice
+    else if (p.sigmoid) w[o] = 1.f / (1.f + expf(-w[o]));
+    else w[o] = expf(w[o] - (p.r.renorm ? peak : m));
+    total += w[o];
+  }
+  if (p.r.renorm) {
+    total = group_sum(total, L);
+    if (p.sigmoid) total += 1e-20f;
+  } else {
+    total = sum;
+  }
+#pragma unroll
+  for (int o = 0; o < OWN; ++o)
+    if (t >= 0 && o * L + at.gl < p.r.k) {
+      p.r.ids[out + o * L + at.gl] = my_id[o];
+      p.r.weights[out + o * L + at.gl] = my_id[o] >= 0 ? w[o] / total * p.scale : 0.f;
+      if (my_id[o] >= 0) atomicOr(&bits[my_id[o] * stride + word], bit);
+    }
+}
+
+template <typename T, int L, int V>
+__global__ void __launch_bounds__(kThreads)
+    route_scored_kernel(const __grid_constant__ ScoreParams p) {
+  extern __shared__ uint32_t bits[];                    // [E][stride]
+  const Place at = Place::of<L>(p, threadIdx.x & 31);
+  clear_bits(bits, p.r.E * bit_stride(p.r.chunk));
+  __syncthreads();
+  grid_wait();
+  grid_go();
+  float bias[V];                          // the same for every token
+  auto load_bias = [&] {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      if (p.bias && p.bias_vec && i + 4 <= at.own) {
+        const float4 b = *reinterpret_cast<const float4*>(p.bias + at.first + i);
+        bias[i] = b.x, bias[i + 1] = b.y, bias[i + 2] = b.z, bias[i + 3] = b.w;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          bias[i + c] = p.bias && i + c < at.own ? p.bias[at.first + i + c] : 0.f;
+      }
+    }
+  };
+  if (V == 8) load_bias();
+  route_chunk_of<L>(p.r, bits, [&](int t, int lane, int stride, int word, uint32_t bit) {
+    if (V > 8) load_bias();               // too many to keep: from L1
+    choose_scored<T, L, V>(p, at, t, lane, bias, bits, stride, word, bit);
+  });
+}
+
+// f for the lanes of a token and the experts of a lane.
+template <typename F>
+cudaError_t by_shape(int L, int V, F&& f) {
+  using std::integral_constant;
+  if (V == 8) {
+    if (L == 4) return f(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+    if (L == 8) return f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    if (L == 16) return f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+    return f(integral_constant<int, 32>{}, integral_constant<int, 8>{});
+  }
+  if (V == 16) return f(integral_constant<int, 32>{}, integral_constant<int, 16>{});
+  return f(integral_constant<int, 32>{}, integral_constant<int, 32>{});
+}
+
+// The kernel with the shared memory of its largest call, once a device (as in
+// moe_route.cu: the limit belongs to the kernel, not to a call).
+template <typename T, int L, int V>
+cudaError_t scored_ready() {
+  constexpr int most = (L * V < kMaxGroups ? L * V : kMaxGroups) * bit_stride(kMostChunk) * 4;
+  static std::mutex mu;
+  static bool ready[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!ready[dev & 63]) {
+    e = cudaFuncSetAttribute(route_scored_kernel<T, L, V>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    ready[dev & 63] = true;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+ScoreShape score_shape(int E, int groups) {
+  int g = 1;
+  while (g < groups) g <<= 1;
+  const int size = E / groups;
+  for (int i = 0;; ++i) {
+    const int L = i < 4 ? 4 << i : 32, V = i < 4 ? 8 : i == 4 ? 16 : 32;
+    if (L < g) continue;
+    const int lanes = L / g, per = ((size + lanes - 1) / lanes + 3) / 4 * 4;
+    if (per <= V || i == 5) return {L, V, lanes, per};
+  }
+}
+
+cudaError_t launch_route_scored(const RouteCall& r, const ScoreCall& s, cudaStream_t st) {
+  // without a restriction the experts are one group
+  const int groups = s.top_groups < s.groups ? s.groups : 1;
+  const ScoreShape shape = score_shape(r.E, groups);
+  if (shape.per > shape.V) return cudaErrorInvalidValue;
+  ScoreParams p = {};
+  p.r = {r.logits, r.ids, r.weights, r.counts, r.slots, r.tokens, r.hist, (int)r.T,
+         r.E,      r.k,   r.renorm,  0,        0,       0,        0};
+  p.bias = s.bias;
+  p.scale = s.scale;
+  p.sigmoid = s.sigmoid;
+  p.groups = groups;
+  p.top_groups = groups > 1 ? s.top_groups : 1;
+  p.best = s.best;
+  p.size = r.E / groups;
+  p.lanes = shape.lanes;
+  p.per = shape.per;
+  const bool fours = p.size % 4 == 0;
+  p.r.vec = fours && rows_vec(r.logits, r.E, r.dtype);
+  p.bias_vec = fours && (reinterpret_cast<uintptr_t>(s.bias) & 15u) == 0;
+  route_chunks(&p.r);
+  const int smem = r.E * bit_stride(p.r.chunk) * 4;
+  auto run = [&](auto* type) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    return by_shape(shape.L, shape.V, [&](auto l, auto v) {
+      constexpr int L = decltype(l)::value, V = decltype(v)::value;
+      const cudaError_t a = scored_ready<T, L, V>();
+      if (a != cudaSuccess) return a;
+      return launch_clusters(route_scored_kernel<T, L, V>, 1, (unsigned)p.r.chunks, kThreads, smem,
+                             st, p);
+    });
+  };
+  const cudaError_t e = r.dtype == BRA_FP32   ? run((float*)nullptr)
+                        : r.dtype == BRA_BF16 ? run((__nv_bfloat16*)nullptr)
+                                              : run((__half*)nullptr);
+  return e != cudaSuccess ? e : launch_route_places(p.r, st);
+}
+
+}  // namespace bra

@@ -23,12 +23,13 @@ __all__ = ["GroupedArgs", "MAX_GROUPS", "grouped_matmul", "grouped_matmul_plan",
            "grouped_matmul_grad", "grouped_matmul_grad_plan", "MxArgs", "MxTensor",
            "mxfp4_quantize", "mxfp4_quantize_plan", "mxfp4_dequantize", "mxfp4_dequantize_plan",
            "mxfp4_grouped_matmul", "mxfp4_grouped_matmul_plan", "MAX_CHOICES", "RouteArgs",
-           "PermuteArgs", "moe_route", "moe_route_plan", "moe_route_grad", "moe_route_grad_plan",
+           "PermuteArgs", "ScoreArgs", "MAX_EXPERT_GROUPS", "moe_route", "moe_route_plan", "moe_route_grad", "moe_route_grad_plan",
            "moe_dispatch", "moe_dispatch_plan", "moe_dispatch_grad", "moe_dispatch_grad_plan",
            "moe_combine", "moe_combine_plan", "moe_combine_grad", "moe_combine_grad_plan"]
 
 MAX_GROUPS = 512
 MAX_CHOICES = 16
+MAX_EXPERT_GROUPS = 32
 
 
 class GroupedArgs(ctypes.Structure):
@@ -53,6 +54,16 @@ class RouteArgs(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64),
                 ("choices", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("renormalize", ctypes.c_int32)]
+
+
+class ScoreArgs(ctypes.Structure):
+    """bra_score_args of the C header."""
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int64),
+                ("choices", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
 
 
 class PermuteArgs(ctypes.Structure):
@@ -86,13 +97,19 @@ def declare(lib) -> None:
     lib.moe_route_workspace_size.argtypes = [rp]
     lib.moe_route_workspace_size.restype = i64
     lib.moe_route_grad.argtypes = [vp, vp, vp, vp, vp, rp, vp]
+    sp = ctypes.POINTER(ScoreArgs)
+    lib.moe_route_scored.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, sp, vp]
+    lib.moe_route_scored_workspace_size.argtypes = [sp]
+    lib.moe_route_scored_workspace_size.restype = i64
+    lib.moe_route_scored_grad.argtypes = [vp, vp, vp, vp, vp, sp, vp]
     lib.moe_dispatch.argtypes = [vp, vp, vp, vp, i64, pp, vp]
     lib.moe_dispatch_workspace_size.argtypes = [pp]
     lib.moe_dispatch_workspace_size.restype = i64
     lib.moe_dispatch_grad.argtypes = [vp, vp, vp, pp, vp]
     lib.moe_combine.argtypes = [vp, vp, vp, vp, pp, vp]
     lib.moe_combine_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, pp, vp]
-    for fn in (lib.moe_route, lib.moe_route_grad, lib.moe_dispatch, lib.moe_dispatch_grad,
+    for fn in (lib.moe_route, lib.moe_route_grad, lib.moe_route_scored, lib.moe_route_scored_grad,
+               lib.moe_dispatch, lib.moe_dispatch_grad,
                lib.moe_combine, lib.moe_combine_grad):
         fn.restype = c_int
 
@@ -523,22 +540,40 @@ def _matrix(t, what: str, dtype=None, shape=None):
     return t
 
 
-def _route_args(logits, k: int, renormalize: bool) -> RouteArgs:
-    a = RouteArgs()
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _route_args(logits, k: int, renormalize: bool, score: str = "softmax", bias=None,
+                groups: int = 1, top_groups=None, group_best: int = 2, scale: float = 1.0):
+    """RouteArgs, or ScoreArgs where a call asks for more than they say."""
+    if score not in SCORES:
+        raise ValueError(f"score is one of {sorted(SCORES)}, got {score!r}")
+    groups, group_best, scale = int(groups), int(group_best), float(scale)
+    top = groups if top_groups is None else int(top_groups)
+    plain = score == "softmax" and bias is None and scale == 1.0 and groups == top == 1
+    a = RouteArgs() if plain else ScoreArgs()
     a.tokens, a.experts = logits.shape
     a.choices = int(k)
     a.dtype = _row_dtype(logits.dtype, "moe_route")
     a.renormalize = 1 if renormalize else 0
+    if not plain:
+        if abs(max(groups, top, group_best, key=abs)) >= 1 << 31:
+            raise ValueError("groups, top_groups and group_best are 32-bit numbers")
+        a.score, a.groups, a.top_groups, a.group_best = SCORES[score], groups, top, group_best
+        a.scale = scale
     return a
 
 
 def moe_route_plan(logits, k: int, renormalize: bool = True, ids=None, weights=None, counts=None,
-                   slots=None, tokens=None, workspace="auto"):
+                   slots=None, tokens=None, workspace="auto", *, score: str = "softmax", bias=None,
+                   groups: int = 1, top_groups=None, group_best: int = 2, scale: float = 1.0):
     """moe_route prepared once (see Plan); plan.run() returns its dict."""
     torch = _bra._torch()
     _matrix(logits, "logits")
-    a = _route_args(logits, k, renormalize)
+    a = _route_args(logits, k, renormalize, score, bias, groups, top_groups, group_best, scale)
     T, E = logits.shape
+    if bias is not None:
+        _dense(bias, "bias", torch.float32, (E,))
     new = lambda shape, dt: torch.empty(shape, dtype=dt, device=logits.device)   # noqa: E731
     i32 = torch.int32
     ids = _dense(new((T, k), i32) if ids is None else ids, "ids", i32, (T, k))
@@ -547,19 +582,25 @@ def moe_route_plan(logits, k: int, renormalize: bool = True, ids=None, weights=N
     counts = _counts(new((E,), torch.int64) if counts is None else counts, E)
     slots = _dense(new((T, k), i32) if slots is None else slots, "slots", i32, (T, k))
     tokens = _dense(new((T * k,), i32) if tokens is None else tokens, "tokens", i32, (T * k,))
-    _same_device(logits, ids, weights, counts, slots, tokens)
+    _same_device(logits, ids, weights, counts, slots, tokens, bias)
     lib = _bra.library()
+    plain = isinstance(a, RouteArgs)
+    need = (lib.moe_route_workspace_size if plain else lib.moe_route_scored_workspace_size)(
+        ctypes.byref(a))
     box = GroupedArgs()                                   # holds the workspace's address
-    workspace = _take_workspace(workspace, lib.moe_route_workspace_size(ctypes.byref(a)),
-                                logits.device, box)
+    workspace = _take_workspace(workspace, need, logits.device, box)
     result = {"ids": ids, "weights": weights, "counts": counts, "slots": slots, "tokens": tokens}
-    args = (_ptr(logits), _ptr(ids), _ptr(weights), _ptr(counts), _ptr(slots), _ptr(tokens),
-            box.workspace, box.workspace_bytes, ctypes.byref(a))
-    return _bra.Plan(lib.moe_route, args, "moe_route", result, (logits, a, workspace))
+    args = (_ptr(logits),) + (() if plain else (_ptr(bias),)) + (
+        _ptr(ids), _ptr(weights), _ptr(counts), _ptr(slots), _ptr(tokens), box.workspace,
+        box.workspace_bytes, ctypes.byref(a))
+    name = "moe_route" if plain else "moe_route_scored"
+    return _bra.Plan(getattr(lib, name), args, name, result, (logits, bias, a, workspace))
 
 
 def moe_route(logits, k: int, renormalize: bool = True, ids=None, weights=None, counts=None,
-              slots=None, tokens=None, workspace="auto", stream=None) -> dict:
+              slots=None, tokens=None, workspace="auto", stream=None, *, score: str = "softmax",
+              bias=None, groups: int = 1, top_groups=None, group_best: int = 2,
+              scale: float = 1.0) -> dict:
     """Each token's k experts, and the order that sorts the pairs by expert.
 
     logits: CUDA (T, E), fp16, bf16 or fp32; -inf or NaN closes an expert to
@@ -569,19 +610,29 @@ def moe_route(logits, k: int, renormalize: bool = True, ids=None, weights=None, 
     weights (renormalised over the chosen by default), rows of each expert,
     the row of each pair when sorted by expert, and the token of each row.  A
     token with fewer than k open experts has -1, weight 0 and slot -1 for the
-    rest; rows past the last pair have token -1."""
+    rest; rows past the last pair have token -1.
+
+    score: "softmax", or "sigmoid" of each logit.  bias: CUDA (E,) fp32, added
+    to the scores for the choice (largest sum first), not to the weights.
+    groups, top_groups: choose from the experts of the top_groups best of
+    `groups` groups of consecutive experts (None: all), a group ranked by its
+    best expert (group_best=1) or the sum of its two best (2).  scale: a
+    factor of the weights.  The choice is what scores, sums and ranks in 64
+    bits give, ties to the lowest group and index."""
     with _on(stream):
         return moe_route_plan(logits, k, renormalize, ids, weights, counts, slots, tokens,
-                              workspace).run()
+                              workspace, score=score, bias=bias, groups=groups,
+                              top_groups=top_groups, group_best=group_best, scale=scale).run()
 
 
-def moe_route_grad_plan(dweights, logits, ids, weights, renormalize: bool = True, out=None):
+def moe_route_grad_plan(dweights, logits, ids, weights, renormalize: bool = True, out=None, *,
+                        score: str = "softmax", scale: float = 1.0):
     """moe_route_grad prepared once (see Plan); plan.run() returns out."""
     torch = _bra._torch()
     _matrix(logits, "logits")
     _matrix(ids, "ids", torch.int32)
     T, k = ids.shape
-    a = _route_args(logits, k, renormalize)
+    a = _route_args(logits, k, renormalize, score, scale=scale)
     if logits.shape[0] != T:
         raise ValueError(f"logits have {logits.shape[0]} tokens, ids {T}")
     _matrix(dweights, "dweights", torch.float32, (T, k))
@@ -591,15 +642,18 @@ def moe_route_grad_plan(dweights, logits, ids, weights, renormalize: bool = True
     _matrix(out, "out", logits.dtype, logits.shape)
     _same_device(logits, dweights, ids, weights, out)
     args = (_ptr(dweights), _ptr(logits), _ptr(ids), _ptr(weights), _ptr(out), ctypes.byref(a))
-    return _bra.Plan(_bra.library().moe_route_grad, args, "moe_route_grad", out,
+    name = "moe_route_grad" if isinstance(a, RouteArgs) else "moe_route_scored_grad"
+    return _bra.Plan(getattr(_bra.library(), name), args, name, out,
                      (dweights, logits, ids, weights, a))
 
 
 def moe_route_grad(dweights, logits, ids, weights, renormalize: bool = True, out=None,
-                   stream=None):
-    """Gradient of the logits for the gradient of moe_route's weights."""
+                   stream=None, *, score: str = "softmax", scale: float = 1.0):
+    """Gradient of the logits for the gradient of moe_route's weights, of the
+    same score, renormalize and scale (the choice itself is constant)."""
     with _on(stream):
-        return moe_route_grad_plan(dweights, logits, ids, weights, renormalize, out).run()
+        return moe_route_grad_plan(dweights, logits, ids, weights, renormalize, out, score=score,
+                                   scale=scale).run()
 
 
 def _permute_args(T: int, R: int, k: int, rows, what: str) -> PermuteArgs:

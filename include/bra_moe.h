@@ -27,6 +27,8 @@ extern "C" {
 /* Most row groups (experts) of one call, and most experts of one token. */
 #define BRA_MAX_GROUPS 512
 #define BRA_MAX_CHOICES 16
+/* Most groups of experts that moe_route_scored chooses from. */
+#define BRA_MAX_EXPERT_GROUPS 32
 
 /* ------------------------------------------------------------------------ */
 /* Products grouped by expert                                                */
@@ -334,6 +336,59 @@ BRA_API int64_t moe_route_workspace_size(const bra_route_args* args);
 BRA_API int moe_route_grad(const float* dweights, const void* logits, const int32_t* ids,
                            const float* weights, void* dlogits, const bra_route_args* args,
                            bra_stream_t stream);
+
+/* Scores of moe_route_scored. */
+#define BRA_SCORE_SOFTMAX 0
+#define BRA_SCORE_SIGMOID 1
+
+typedef struct {
+  int64_t tokens;      /* T, E, k, dtype: as bra_route_args                   */
+  int64_t experts;
+  int64_t choices;
+  int32_t dtype;
+  int32_t renormalize; /* non-zero: weights add up to scale over the chosen   */
+  int32_t score;       /* BRA_SCORE_SOFTMAX or BRA_SCORE_SIGMOID              */
+  int32_t groups;      /* G: 1 .. BRA_MAX_EXPERT_GROUPS, a divisor of E       */
+  int32_t top_groups;  /* 1 .. G: groups that experts are chosen from         */
+  int32_t group_best;  /* 1 or 2: experts whose ranks add up to a group's     */
+  float scale;         /* of the weights; its magnitude 2^-100 .. 2^100       */
+  int32_t reserved;    /* 0                                                   */
+} bra_score_args;
+
+/*
+ * moe_route_scored -- moe_route with scores, a bias of the choice and groups
+ * of experts.  Expert i of a token has the score s_i: the softmax over its
+ * open experts, or 1 / (1 + exp(-l_i)).  Its rank is s_i + bias_i, or without
+ * a bias l_i, which orders alike.  Experts g * E/G .. are group g; a group's
+ * rank is its largest rank (group_best 1), or the sum of its two largest,
+ * without a bias of its two largest scores (2; the only open one's, if there
+ * is one).  Among the top_groups groups of the highest rank the k experts of
+ * the highest rank are chosen, highest first; ties go to the lowest group and
+ * the lowest expert.  With top_groups = G groups do not matter.  The choice is
+ * the one that scores, ranks and sums in 64 bits give.
+ *   bias    NULL, or device (E) fp32: what a user moves to balance the load.
+ *           It changes the choice alone, not the weights.  An expert whose
+ *           bias is -inf or NaN is never chosen; it stays open to the softmax.
+ *   weights (T, k) fp32: scale * s_i of the chosen; with renormalize divided
+ *           by their sum (sigmoid: the sum + 1e-20).
+ * Everything else, workspace (moe_route_scored_workspace_size) and errors as
+ * moe_route; bias has to be 4-byte aligned and no output may overlap it.
+ */
+BRA_API int moe_route_scored(const void* logits, const float* bias, int32_t* ids, float* weights,
+                             int64_t* counts, int32_t* slots, int32_t* tokens, void* workspace,
+                             int64_t workspace_bytes, const bra_score_args* args,
+                             bra_stream_t stream);
+BRA_API int64_t moe_route_scored_workspace_size(const bra_score_args* args);
+
+/*
+ * moe_route_scored_grad -- moe_route_grad for moe_route_scored's weights and
+ * ids: the choice is constant, so bias and groups play no part.  logits are
+ * read for sigmoid scores, and for the softmax without renormalize (NULL
+ * otherwise allowed).  Errors as moe_route_scored.
+ */
+BRA_API int moe_route_scored_grad(const float* dweights, const void* logits, const int32_t* ids,
+                                  const float* weights, void* dlogits, const bra_score_args* args,
+                                  bra_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Token rows to their experts and back                                      */

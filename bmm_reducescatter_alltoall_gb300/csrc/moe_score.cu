@@ -54,6 +54,12 @@ __device__ __forceinline__ void best_two(F& a1, F& a2, F b1, F b2) {
   a2 = low > next ? low : next;
 }
 
+// A sigmoid for the choice: within 2^-21.8 (__expf's units times s (1 - s) |l|,
+// the sum's and the quotient's).
+__device__ __forceinline__ float score_of(float l) {
+  return __fdividef(1.f, 1.f + __expf(-l));
+}
+
 // Where a lane's experts are.
 struct Place {
   uint32_t group;      // this token's lanes
@@ -72,13 +78,16 @@ struct Place {
 };
 
 // The choice in 64 bits: the ids of one token, by the lanes of `at.group`.
+// open: whether its groups are chosen again too; else those of lanes with
+// `kept` are, and experts whose rank in 32 bits lies below `floor` are out.
 template <typename T, int L, int V>
-__device__ __noinline__ void choose_exact(const ScoreParams& p, int t, int lane) {
+__device__ __noinline__ void choose_exact(const ScoreParams& p, int t, int lane, bool open, bool kept,
+                                          float floor) {
   const Place at = Place::of<L>(p, lane);
   const T* row = static_cast<const T*>(p.r.logits) + (int64_t)t * p.r.E + at.first;
   const double inf = INFINITY;
   float m = -INFINITY;
-  double sum = 0.0;
+  double sum = p.sigmoid ? 1.0 : 0.0;
   if (!p.sigmoid) {
 #pragma unroll 1
     for (int i = 0; i < at.own; ++i) m = fmaxf(m, logit(row + i));         // NaN is passed over
@@ -93,19 +102,30 @@ __device__ __noinline__ void choose_exact(const ScoreParams& p, int t, int lane)
     for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(at.group, sum, d);
   }
   double r[V], f1 = -inf, f2 = -inf;
+  const float inv = (float)(1.0 / sum);
+  uint32_t live = 0u;
 #pragma unroll 1
   for (int i = 0; i < V; ++i) {
-    const float v = i < at.own ? logit(row + i) : -INFINITY;
     r[i] = -inf;
-    if (v >= -kLargest) {
-      const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)m) / sum;
-      double x = p.bias ? s + (double)p.bias[at.first + i] : (double)v;
-      if (!(x > -inf)) x = -inf;
-      r[i] = x < 1e300 ? x : 1e300;
-      best_two(f1, f2, p.bias || p.best == 1 ? r[i] : s, -inf);
-    }
+    const float v = i < at.own ? logit(row + i) : -INFINITY;
+    if (!(v >= -kLargest) || !(open || kept)) continue;
+    float x = v;
+    if (p.bias) x = (p.sigmoid ? score_of(v) : expf(v - m) * inv) + p.bias[at.first + i];
+    if (open || !(x < floor)) live |= 1u << i;
   }
-  if (p.top_groups < p.groups) {
+  // each lane's next one, so that the slow 64-bit functions run as few times as can be
+  while (__any_sync(at.group, live != 0u)) {
+    if (live == 0u) continue;
+    const int i = __ffs(live) - 1;
+    live &= live - 1u;
+    const float v = logit(row + i);
+    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)m) / sum;
+    double x = p.bias ? s + (double)p.bias[at.first + i] : (double)v;
+    if (!(x > -inf)) x = -inf;
+    r[i] = x < 1e300 ? x : 1e300;
+    best_two(f1, f2, p.bias || p.best == 1 ? r[i] : s, -inf);
+  }
+  if (open) {
     for (int d = 1; d < p.lanes; d <<= 1) {
       const double b1 = __shfl_xor_sync(at.group, f1, d), b2 = __shfl_xor_sync(at.group, f2, d);
       best_two(f1, f2, b1, b2);
@@ -181,39 +201,45 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
     sum = group_sum(sum, L);
   }
   const float inv = p.sigmoid ? 1.f : 1.f / sum;          // the largest score there can be
-  // of an open logit, for the choice: within 2^-21.8 (sigmoid: __expf's units
-  // times s (1 - s) |l|, the sum's and the quotient's)
-  auto score = [&](float v) {
-    return p.sigmoid ? __fdividef(1.f, 1.f + __expf(-v)) : expf(v - m) * inv;
-  };
-  // the least distance at which 32 bits decide: two scores' errors (softmax:
+  auto score = [&](float v) { return p.sigmoid ? score_of(v) : expf(v - m) * inv; };
+  // The least distance at which 32 bits decide: two scores' errors (softmax:
   // also the sum's, one unit of 2^-24 a term of a lane and level), two sums'
-  const float slack = (p.sigmoid ? 0x1p-20f : 0x1p-18f) * inv;
-  auto close = [&](float hi, float lo) {
-    return hi - lo <= slack + fmaxf(fabsf(hi), fabsf(lo)) * 0x1p-22f;
-  };
-  bool again = false;
+  // roundings, two keys' low bits.
+  const float slack = ranked ? (p.sigmoid ? 0x1p-20f : 0x1p-18f) * inv : 0.f;
+  constexpr float part = 0x1p-22f + V * 0x1p-23f;
+  auto distance = [&](float a, float b) { return slack + fmaxf(fabsf(a), fabsf(b)) * part; };
+  // 16-bit logits leave their keys' low bits free
+  const bool exact = !ranked && sizeof(T) == 2;
 
-  uint32_t key[NL][8], order[NL];               // order: sorted places, four bits each
+  // Keys, one word each: the rank, its low bits the place in the lane, the
+  // first the largest; lists of eight, sorted (Batcher's odd-even merge sort).
+  uint32_t key[NL][8];
 #pragma unroll
   for (int n = 0; n < NL; ++n) {
-    int idx[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float x = l[n * 8 + i];
-      if (ranked && x >= -kLargest) {
-        x = score(x) + bias[n * 8 + i];
-        x = (x > kLargest ? kLargest : x) + 0.f;           // NaN stays
-      }
-      key[n][i] = key_of(x);
-      idx[i] = i;
+      const bool open = x >= -kLargest;
+      if (ranked) x = score(x) + bias[n * 8 + i];
+      const uint32_t u = __float_as_uint(x);
+      const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+      key[n][i] = open && x >= -kLargest ? (k & ~(uint32_t)(V - 1)) | (uint32_t)(V - 1 - n * 8 - i) : 0u;
     }
-    sort_eight(key[n], idx);
-    order[n] = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) order[n] |= (uint32_t)idx[i] << (4 * i);
+    auto put = [&](int a, int b) {
+      const uint32_t hi = max(key[n][a], key[n][b]), lo = min(key[n][a], key[n][b]);
+      key[n][a] = hi, key[n][b] = lo;
+    };
+    put(0, 1), put(2, 3), put(4, 5), put(6, 7);
+    put(0, 2), put(1, 3), put(4, 6), put(5, 7);
+    put(1, 2), put(5, 6);
+    put(0, 4), put(1, 5), put(2, 6), put(3, 7);
+    put(2, 4), put(3, 5);
+    put(1, 2), put(3, 4), put(5, 6);
   }
+  // what a key says of its rank: at most V - 1 units of it off
+  auto rank_of = [&](uint32_t k) { return value_of(k & ~(uint32_t)(V - 1)); };
 
+  bool again = false, kept = true;
   if (limited) {
     uint32_t k1 = key[0][0], k2 = key[0][1];
 #pragma unroll
@@ -222,9 +248,9 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
       const uint32_t b1 = __shfl_xor_sync(kAll, k1, d), b2 = __shfl_xor_sync(kAll, k2, d);
       best_two(k1, k2, b1, b2);
     }
-    float v = k1 ? value_of(k1) : -INFINITY;
+    float v = k1 ? rank_of(k1) : -INFINITY;
     if (p.best == 2 && k1) {
-      float w = k2 ? value_of(k2) : 0.f;
+      float w = k2 ? rank_of(k2) : 0.f;
       if (!ranked) {
         v = score(v);
         if (k2) w = score(w);
@@ -236,76 +262,96 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
       const float o = __shfl_sync(kAll, v, g * p.lanes, L);
       better += o > v || (o == v && g < at.g) ? 1 : 0;
     }
-    if (ranked || p.best == 2) {
-      // the last group kept and the first left out
+    kept = better < p.top_groups;
+    if (!exact || p.best == 2) {
+      // the last group kept and the first left out (a score from a logit whose
+      // low bits are gone errs by |l| s (1 - s) units more: within `part`)
       const bool head = at.g < p.groups && at.gl == at.g * p.lanes;
       const uint32_t in = __ballot_sync(kAll, head && better == p.top_groups - 1) & at.group;
       const uint32_t out = __ballot_sync(kAll, head && better == p.top_groups) & at.group;
       const float vi = __shfl_sync(kAll, v, __ffs(in) - 1), vo = __shfl_sync(kAll, v, __ffs(out) - 1);
-      again = vo > -INFINITY && vi - vo <= 2.f * (slack + fmaxf(fabsf(vi), fabsf(vo)) * 0x1p-22f);
+      const float off = ranked || p.best == 1 ? slack : (p.sigmoid ? 0x1p-20f : 0x1p-18f) * inv +
+                                                            V * 0x1p-23f * inv;
+      again = vo > -INFINITY && vi - vo <= 2.f * (off + fmaxf(fabsf(vi), fabsf(vo)) * part);
     }
-    if (better >= p.top_groups) {
+    if (!kept) {
 #pragma unroll
       for (int n = 0; n < NL; ++n)
 #pragma unroll
         for (int i = 0; i < 8; ++i) key[n][i] = 0u;
     }
   }
+  const bool open = again;
 
-  int my_id[OWN];
-  float last = 0.f;
-  int last_id = -1;
+  // the largest of the lanes' heads, k times, and the best one left out
+  constexpr int KEEP = (BRA_MAX_CHOICES + L) / L;        // of k + 1
+  uint32_t my_key[KEEP];
+  int my_lane[KEEP];
 #pragma unroll
-  for (int o = 0; o < OWN; ++o) my_id[o] = -1;
-  const int rounds = p.r.k + (ranked ? 1 : 0);   // with a bias also the best one left out
-#pragma unroll
-  for (int o = 0; o <= BRA_MAX_CHOICES / L; ++o) {
-    for (int j = o * L; j < min(rounds, (o + 1) * L); ++j) {
+  for (int o = 0; o < KEEP; ++o) {
+    my_key[o] = 0u;
+    my_lane[o] = 0;
+    for (int j = o * L; j < min(p.r.k + 1, (o + 1) * L); ++j) {
       uint32_t head = key[0][0];
-      int from = 0;
 #pragma unroll
-      for (int n = 1; n < NL; ++n)
-        if (key[n][0] > head) {
-          head = key[n][0];
-          from = n;
-        }
-      int place = 0;
-#pragma unroll
-      for (int n = 0; n < NL; ++n)
-        if (from == n) place = n * 8 + (int)(order[n] & 15u);
-      uint32_t most = head;
+      for (int n = 1; n < NL; ++n) head = max(head, key[n][0]);
+      // without the places: equal ranks go to the lowest lane
+      const uint32_t rank = head & ~(uint32_t)(V - 1);
+      uint32_t most = rank;
       if constexpr (L == 32) {
-        most = __reduce_max_sync(kAll, head);
+        most = __reduce_max_sync(kAll, rank);
       } else {
 #pragma unroll
         for (int d = L / 2; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
       }
-      const int win = __ffs(__ballot_sync(kAll, head == most) & at.group) - 1;
-      const int id = __shfl_sync(kAll, at.first + place, win);
-      if (ranked) {
-        const float x = value_of(most);
-        if (j > 0 && most && close(last, x)) {
-          // equal logits and equal biases are a tie in any precision
-          again |= logit(row + last_id) != logit(row + id) || p.bias[last_id] != p.bias[id];
-        }
-        last = x;
-        last_id = id;
-      }
-      if (o < OWN && at.gl == j - o * L && j < p.r.k && most) my_id[o < OWN ? o : 0] = id;
+      const int win = __ffs(__ballot_sync(kAll, rank == most) & at.group) - 1;
+      const uint32_t best = __shfl_sync(kAll, head, win);
+      const bool mine = at.gl == j - o * L;
+      my_key[o] = mine ? best : my_key[o];
+      my_lane[o] = mine ? win : my_lane[o];
       // the winner drops its head (with most = 0 there is nothing to drop)
 #pragma unroll
       for (int n = 0; n < NL; ++n) {
-        const bool drop = lane == win && from == n;
+        const bool drop = lane == win && key[n][0] == head;
 #pragma unroll
         for (int i = 0; i + 1 < 8; ++i) key[n][i] = drop ? key[n][i + 1] : key[n][i];
         key[n][7] = drop ? 0u : key[n][7];
-        order[n] = drop ? order[n] >> 4 : order[n];
+      }
+    }
+  }
+  int my_id[OWN];
+  int id_before = 0;
+  uint32_t key_before = 0u;
+  float low = 0.f;                               // the least rank that can be chosen
+#pragma unroll
+  for (int o = 0; o < KEEP; ++o) {
+    const int first = __shfl_sync(kAll, at.first, my_lane[o]);
+    const int id = my_key[o] ? first + (V - 1) - (int)(my_key[o] & (uint32_t)(V - 1)) : -1;
+    if (o < OWN) my_id[o < OWN ? o : 0] = o * L + at.gl < p.r.k ? id : -1;
+    if (!exact) {
+      // this one and the one before it in the order: too close, unless equal
+      // logits and equal biases make them a tie in any precision
+      uint32_t kb = __shfl_up_sync(kAll, my_key[o], 1, L);
+      int ib = __shfl_up_sync(kAll, id, 1, L);
+      if (at.gl == 0) kb = key_before, ib = id_before;
+      key_before = __shfl_sync(kAll, my_key[o], L - 1, L);
+      id_before = __shfl_sync(kAll, id, L - 1, L);
+      bool bad = false;
+      if (kb && my_key[o]) {
+        const float hi = rank_of(kb), lo = rank_of(my_key[o]);
+        if (hi - lo <= distance(hi, lo))
+          bad = logit(row + ib) != logit(row + id) || (ranked && p.bias[ib] != p.bias[id]);
+      }
+      again |= (__ballot_sync(kAll, bad) & at.group) != 0u;
+      if (o == p.r.k / L) {
+        const float last = __shfl_sync(kAll, my_key[o] ? rank_of(my_key[o]) : -INFINITY, p.r.k % L, L);
+        low = last - 2.f * distance(last, last);
       }
     }
   }
   const int64_t out = (int64_t)t * p.r.k;
   if (again) {                                   // the same for all lanes of a token
-    choose_exact<T, L, V>(p, t, lane);
+    choose_exact<T, L, V>(p, t, lane, open, kept, low);
 #pragma unroll
     for (int o = 0; o < OWN; ++o)
       my_id[o] = o * L + at.gl < p.r.k ? p.r.ids[out + o * L + at.gl] : -1;
@@ -366,6 +412,8 @@ __global__ void __launch_bounds__(kThreads)
           bias[i + c] = p.bias && i + c < at.own ? p.bias[at.first + i + c] : 0.f;
       }
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = bias[i] > kLargest ? kLargest : bias[i];   // NaN stays
   };
   if (V == 8) load_bias();
   route_chunk_of<L>(p.r, bits, [&](int t, int lane, int stride, int word, uint32_t bit) {

@@ -54,10 +54,14 @@ __device__ __forceinline__ void best_two(F& a1, F& a2, F b1, F b2) {
   a2 = low > next ? low : next;
 }
 
-// A sigmoid for the choice: within 2^-21.8 (__expf's units times s (1 - s) |l|,
-// the sum's and the quotient's).
+// A sigmoid for the choice, of four instructions: within 2^-21.8 (the two
+// approximations' units of 2^-23, the exponent's rounding times s (1 - s) |l|,
+// and the sum's).
 __device__ __forceinline__ float score_of(float l) {
-  return __fdividef(1.f, 1.f + __expf(-l));
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
 }
 
 // Where a lane's experts are.
@@ -211,6 +215,16 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
   // 16-bit logits leave their keys' low bits free
   const bool exact = !ranked && sizeof(T) == 2;
 
+  float rank[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) rank[i] = l[i];
+  if (ranked && p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) rank[i] = score_of(l[i]) + bias[i];
+  } else if (ranked) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) rank[i] = expf(l[i] - m) * inv + bias[i];
+  }
   // Keys, one word each: the rank, its low bits the place in the lane, the
   // first the largest; lists of eight, sorted (Batcher's odd-even merge sort).
   uint32_t key[NL][8];
@@ -218,9 +232,8 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
   for (int n = 0; n < NL; ++n) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float x = l[n * 8 + i];
-      const bool open = x >= -kLargest;
-      if (ranked) x = score(x) + bias[n * 8 + i];
+      const float x = rank[n * 8 + i];
+      const bool open = l[n * 8 + i] >= -kLargest;
       const uint32_t u = __float_as_uint(x);
       const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
       key[n][i] = open && x >= -kLargest ? (k & ~(uint32_t)(V - 1)) | (uint32_t)(V - 1 - n * 8 - i) : 0u;
@@ -296,15 +309,15 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
 #pragma unroll
       for (int n = 1; n < NL; ++n) head = max(head, key[n][0]);
       // without the places: equal ranks go to the lowest lane
-      const uint32_t rank = head & ~(uint32_t)(V - 1);
-      uint32_t most = rank;
+      const uint32_t part_of = head & ~(uint32_t)(V - 1);
+      uint32_t most = part_of;
       if constexpr (L == 32) {
-        most = __reduce_max_sync(kAll, rank);
+        most = __reduce_max_sync(kAll, part_of);
       } else {
 #pragma unroll
         for (int d = L / 2; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
       }
-      const int win = __ffs(__ballot_sync(kAll, rank == most) & at.group) - 1;
+      const int win = __ffs(__ballot_sync(kAll, part_of == most) & at.group) - 1;
       const uint32_t best = __shfl_sync(kAll, head, win);
       const bool mine = at.gl == j - o * L;
       my_key[o] = mine ? best : my_key[o];

@@ -78,6 +78,7 @@ KERNEL_SOURCES = {
     "fp8_blocks_kernel": "fp8_quant.cu",
     "fp8_back_kernel": "fp8_quant.cu",
     "fp8_grouped_kernel": "fp8_tc.cu",
+    "fp8_few_kernel": "fp8_tc.cu",
     "route_choose_kernel": "moe_route.cu",
     "route_scan_kernel": "moe_route.cu",
     "route_place_kernel": "moe_route.cu",

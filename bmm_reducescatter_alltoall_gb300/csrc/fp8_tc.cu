@@ -31,6 +31,9 @@ using namespace grp;
 
 constexpr int BKB = 128;                    // bytes (elements) of a K block
 constexpr int kGroupM = 8;
+// Rows an expert, on average, up to which a tile is 32 rows by 128 columns of
+// the weight (below).
+constexpr int64_t kFewRows = 32;
 constexpr int EPI_WARP0 = 4;
 constexpr int BAR_BYTES = 512;
 
@@ -449,6 +452,263 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(FShape<CG, BN>::THR
   }
 }
 
+// --------------------------------------------------------------------------
+// Few rows an expert: the operands change places.  A tile is 128 columns of the
+// output (rows of the weight: the M side, a lane each) by up to 32 rows (the N
+// side), so that a block's sum is 32 columns of tensor memory in place of 128
+// that hold few rows.  The factors then go with the columns: a warp lays those
+// of 16 blocks out in shared memory while the 16 before are being added, and
+// reads them as pairs.  HBM bounds it: ten stages of 16 KB of weights in flight
+// an SM (16 tokens x 8 of 64 experts, 2048 x 4096: 76 us in place of 123).
+// --------------------------------------------------------------------------
+struct FewShape {
+  static constexpr int ROWS = 32, CHUNK = 16;             // rows of a tile; blocks of factors
+  static constexpr int A_BYTES = 128 * BKB, B_BYTES = ROWS * BKB;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int THREADS = (EPI_WARP0 + 4) * 32;
+  static constexpr int NBUF = 8;
+  static constexpr uint32_t TMEM_COLS = NBUF * ROWS;
+  static constexpr int FACTORS = CHUNK * ROWS * 4;        // bytes of a warp
+  static constexpr int STAGES = 10;
+  static constexpr int SMEM_BYTES =
+      STAGES * STAGE_BYTES + BAR_BYTES + 4 * FACTORS + (int)sizeof(GroupTable) + 16 + 1024;
+  static_assert(SMEM_BYTES <= 232448 && STAGE_BYTES % 1024 == 0, "shared memory");
+  static_assert(8 * (2 * STAGES + 2 * NBUF) + 16 <= BAR_BYTES, "barrier area");
+};
+
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(FewShape::THREADS, 1)
+    fp8_few_kernel(const __grid_constant__ Fp8Params p) {
+  using S = FewShape;
+  constexpr int STAGES = S::STAGES, STAGE_BYTES = S::STAGE_BYTES, ROWS = S::ROWS;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const uint32_t smem_base = smem_u32(smem);
+  uint8_t* bars = smem + STAGES * STAGE_BYTES;
+  const uint32_t bar_base = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar_base + 8u * s; };
+  auto empty_bar = [&](int s) { return bar_base + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar_base + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar_base + 8u * (2 * STAGES + S::NBUF + a); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BAR_BYTES - 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_BYTES - 8);
+  uint8_t* factors = bars + BAR_BYTES;
+  GroupTable* gt = reinterpret_cast<GroupTable*>(factors + 4 * S::FACTORS);
+  int32_t* fault = &g_bra_fault_word_fp8;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < S::NBUF; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 4);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&p.ta32);
+    tma_prefetch_desc(&p.tb);
+  }
+  if (warp == 2) {
+    tmem_alloc<1>(smem_u32(tmem_slot), S::TMEM_COLS);
+    tmem_relinquish<1>();
+  }
+  grid_wait();
+  grid_go();
+  if (warp == 3) build_table<ROWS>(gt, p.counts, p.E, p.R, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = gt->bad ? 0 : gt->tile[p.E] * p.n_tiles;
+  const int walk0 = blockIdx.x, step = gridDim.x;
+  int e_at = 0;                      // group of this role's current tile
+  auto find = [&](int t) {
+    while (gt->tile[e_at + 1] * p.n_tiles <= t) ++e_at;
+    const int first = gt->tile[e_at];
+    TileCoord c = tile_coord(t - first * p.n_tiles, gt->tile[e_at + 1] - first, p.n_tiles, kGroupM);
+    c.g = e_at;
+    return c;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- producer ----------------
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = walk0; ok && t < total; t += step) {
+      const TileCoord c = find(t);
+      const int row = gt->off[c.g] + c.mt * ROWS, n0 = c.nt * 128;
+      for (int kb = 0; kb < p.k_blocks; ++kb) {
+        if (!wait_here(empty_bar(stage), phase ^ 1u, abort_flag, fault)) {
+          ok = false;
+          break;
+        }
+        const uint32_t a_dst = smem_base + stage * STAGE_BYTES;
+        mbar_expect_tx(full_bar(stage), STAGE_BYTES);
+        if (GRAD) tma_load_3d(a_dst, &p.tb, full_bar(stage), n0, kb * BKB, c.g);
+        else tma_load_3d(a_dst, &p.tb, full_bar(stage), kb * BKB, n0, c.g);
+        tma_load_3d(a_dst + S::A_BYTES, &p.ta32, full_bar(stage), kb * BKB, row, 0);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) spin_ns(2000000ull);   // let copies already issued land
+  } else if (warp == 1 && lane == 0) {
+    // ---------------- MMA issuer ----------------
+    const uint64_t a0 = GRAD ? smem_desc_sw128(smem_base, 16384, 1024)
+                             : smem_desc_sw128(smem_base, 16, 1024);
+    const uint64_t b0 = smem_desc_sw128(smem_base + S::A_BYTES, 16, 1024);
+    constexpr uint32_t a_step = GRAD ? 256u : 2u;
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, buf_phase = 0;
+    bool ok = true;
+    for (int t = walk0; ok && t < total; t += step) {
+      for (int kb = 0; kb < p.k_blocks; ++kb) {
+        ok = wait_here(tempty_bar(buf), buf_phase ^ 1u, abort_flag, fault) &&
+             wait_here(full_bar(stage), phase, abort_flag, fault);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t so = (uint64_t)((stage * STAGE_BYTES) >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          fp8_mma<1>(tmem_base + (uint32_t)(buf * ROWS), a0 + so + a_step * k, b0 + so + 2 * k,
+                     p.idesc, k > 0 ? 1u : 0u);
+        tc_commit(tfull_bar(buf));
+        tc_commit(empty_bar(stage));
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++buf == S::NBUF) {
+          buf = 0;
+          buf_phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) spin_ns(2000000ull);   // let MMAs already issued complete
+  } else if (warp >= EPI_WARP0) {
+    // ---------------- epilogue: output column n0 + q * 32 + lane ----------------
+    const int q = warp & 3;
+    const uint32_t fac = smem_u32(factors) + (warp - EPI_WARP0) * S::FACTORS;
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    bool ok = true;
+    struct Tile {
+      int g, row, n0, valid;
+    };
+    auto tile_of = [&](int t) {
+      const TileCoord c = find(t);
+      const int row = gt->off[c.g] + c.mt * ROWS;
+      return Tile{c.g, row, c.nt * 128, min(ROWS, gt->off[c.g + 1] - row)};
+    };
+    // the factors of 16 blocks: this lane's row's scales, and (lanes 0 to 15)
+    // the weight's
+    float4 fx[S::CHUNK / 4];
+    float fw = 0.f;
+    auto fetch = [&](const Tile& c, int kb0) {
+      const float* sx = p.xs + ((int64_t)c.row + min(lane, c.valid - 1)) * p.xs_pitch + kb0;
+      const float* sw = p.ws + c.g * p.ws_group + (c.n0 / fp8::kBlock) * p.ws_out;
+#pragma unroll
+      for (int i = 0; i < S::CHUNK / 4; ++i)
+        fx[i] = kb0 + 4 * i < p.k_blocks ? *reinterpret_cast<const float4*>(sx + 4 * i)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      fw = lane < S::CHUNK && kb0 + lane < p.k_blocks ? sw[(int64_t)(kb0 + lane) * p.ws_block] : 0.f;
+    };
+    Tile next = {0, 0, 0, 1};
+    if (walk0 < total) {
+      next = tile_of(walk0);
+      fetch(next, 0);
+    }
+    for (int t = walk0; ok && t < total; t += step) {
+      const Tile c = next;
+      const int n = c.n0 + q * 32 + lane;
+      float bias = 0.f;
+      if (p.bias && n < p.N) {
+        const int64_t at = (int64_t)c.g * p.N + n;
+        bias = p.bias_fp16 ? Num<__half>::bias(p.bias, at) : static_cast<const float*>(p.bias)[at];
+      }
+      uint64_t acc[ROWS / 2];
+#pragma unroll
+      for (int i = 0; i < ROWS / 2; ++i) acc[i] = 0ull;
+      for (int kb0 = 0; ok && kb0 < p.k_blocks; kb0 += S::CHUNK) {
+        __syncwarp();                       // the factors before have been read
+#pragma unroll
+        for (int i = 0; i < S::CHUNK; ++i) {
+          const float4 x = fx[i / 4];
+          float f = (i % 4 == 0 ? x.x : i % 4 == 1 ? x.y : i % 4 == 2 ? x.z : x.w) *
+                    __shfl_sync(0xffffffffu, fw, i);
+          f = f > 3.402823466e+38f ? 3.402823466e+38f : f;          // NaN stays
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(fac + (i * ROWS + lane) * 4), "f"(f) : "memory");
+        }
+        __syncwarp();
+        if (kb0 + S::CHUNK < p.k_blocks) {
+          fetch(c, kb0 + S::CHUNK);
+        } else if (t + step < total) {
+          next = tile_of(t + step);
+          fetch(next, 0);
+        }
+        const int blocks = min(S::CHUNK, p.k_blocks - kb0);
+#pragma unroll 1
+        for (int b = 0; b < blocks; ++b) {
+          const bool got = wait_here(tfull_bar(buf), buf_phase, abort_flag, fault);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          uint32_t v[32];
+          tmem_ld32(tmem_base + (uint32_t)(buf * ROWS) + ((uint32_t)(q * 32) << 16), v);
+          tmem_ld_wait_for(v);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty_bar(buf));
+#pragma unroll
+          for (int i = 0; i < ROWS / 4; ++i) {
+            uint64_t f0, f1;
+            asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];"
+                         : "=l"(f0), "=l"(f1)
+                         : "r"(fac + (b * ROWS + 4 * i) * 4)
+                         : "memory");
+            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[2 * i]) : "l"(pair64(v[4 * i], v[4 * i + 1])), "l"(f0));
+            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[2 * i + 1]) : "l"(pair64(v[4 * i + 2], v[4 * i + 3])), "l"(f1));
+          }
+          if (++buf == S::NBUF) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) break;
+      if (n < p.N) {
+        T* y0 = static_cast<T*>(p.y) + (int64_t)c.row * p.ldy + n;
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j)
+          if (j < c.valid)
+            y0[j * p.ldy] = static_cast<T>(
+                __uint_as_float((uint32_t)(acc[j / 2] >> (32 * (j & 1)))) + bias);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && p.status) {
+    if (gt->bad) atomicExch(p.status, (int32_t)BRA_ERR_INVALID);
+    else if (*abort_flag) atomicExch(p.status, (int32_t)BRA_ERR_TIMEOUT);
+  }
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem_base, S::TMEM_COLS);
+  }
+}
+
 // Clusters of the kernel that are resident at once, found on first use.
 template <typename T, int CG, int BN, bool GRAD>
 cudaError_t resident(int* clusters) {
@@ -505,18 +765,15 @@ bool encode_codes(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, u
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int CG, int BN, bool GRAD>
-cudaError_t launch(const Fp8Problem& g, cudaStream_t st) {
-  using S = FShape<CG, BN>;
-  int clusters = 0;
-  cudaError_t e = resident<T, CG, BN, GRAD>(&clusters);
-  if (e != cudaSuccess) return e;
-  Fp8Params p;
+// Parameters of a launch with tiles of `rows` rows and `cols` columns, the
+// weight read in boxes of `box` rows; the instruction is the caller's.
+bool fill(Fp8Params* out, const Fp8Problem& g, int rows, int cols, uint32_t box, int64_t* tiles) {
+  Fp8Params& p = *out;
   std::memset(&p, 0, sizeof(p));
-  const int K = GRAD ? g.out : g.in, N = GRAD ? g.in : g.out;      // contraction, columns
+  const int K = g.grad ? g.out : g.in, N = g.grad ? g.in : g.out;      // contraction, columns
   if (!encode_codes(&p.ta, g.xc, K, g.R, 1, 128) || !encode_codes(&p.ta32, g.xc, K, g.R, 1, 32) ||
-      !encode_codes(&p.tb, g.wc, g.in, g.out, g.E, GRAD ? 128 : S::B_COLS))
-    return cudaErrorInvalidValue;
+      !encode_codes(&p.tb, g.wc, g.in, g.out, g.E, box))
+    return false;
   p.xs = g.xs;
   p.ws = g.ws;
   p.bias = g.bias;
@@ -528,24 +785,66 @@ cudaError_t launch(const Fp8Problem& g, cudaStream_t st) {
   p.xs_pitch = fp8::scale_pitch(K);
   const int64_t in_blocks = fp8::blocks(g.in);
   p.ws_group = fp8::blocks(g.out) * in_blocks;
-  p.ws_out = GRAD ? 1 : in_blocks;
-  p.ws_block = GRAD ? in_blocks : 1;
+  p.ws_out = g.grad ? 1 : in_blocks;
+  p.ws_block = g.grad ? in_blocks : 1;
   p.E = g.E;
   p.N = N;
-  p.n_tiles = (N + BN - 1) / BN;
+  p.n_tiles = (N + cols - 1) / cols;
   p.k_blocks = (int)fp8::blocks(K);
   p.bias_fp16 = g.dtype == BRA_FP16;
   p.aligned = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0 && N % 8 == 0;
+  const int64_t groups = g.R < g.E ? g.R : g.E;
+  *tiles = (g.R / rows + groups) * p.n_tiles;                          // at most
+  return *tiles < (int64_t(1) << 31);
+}
+
+template <typename T, int CG, int BN, bool GRAD>
+cudaError_t launch(const Fp8Problem& g, cudaStream_t st) {
+  using S = FShape<CG, BN>;
+  int clusters = 0;
+  cudaError_t e = resident<T, CG, BN, GRAD>(&clusters);
+  if (e != cudaSuccess) return e;
+  Fp8Params p;
+  int64_t tiles = 0;
+  if (!fill(&p, g, 128 * CG, BN, GRAD ? 128 : S::B_COLS, &tiles)) return cudaErrorInvalidValue;
   // D fp32 (bit 4), the codes' formats (bits 7, 10: 0 e4m3, 1 e5m2), B N-major
   // (bit 16), N >> 3 at 17, M >> 4 at 24
   p.idesc = 1u << 4 | (uint32_t)g.xf << 7 | (uint32_t)g.wf << 10 | (GRAD ? 1u << 16 : 0u) |
             (uint32_t)(BN >> 3) << 17 | (uint32_t)(8 * CG) << 24;
-  const int64_t groups = g.R < g.E ? g.R : g.E;
-  const int64_t tiles = (g.R / (128 * CG) + groups) * p.n_tiles;         // at most
-  if (tiles >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   const int nc = (int)(tiles < clusters ? tiles : clusters);
   return launch_clusters(fp8_grouped_kernel<T, CG, BN, GRAD>, 1, CG * nc, S::THREADS, S::SMEM_BYTES,
                          st, p);
+}
+
+template <typename T, bool GRAD>
+cudaError_t launch_few(const Fp8Problem& g, cudaStream_t st) {
+  using S = FewShape;
+  static std::mutex mu;
+  static int known[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int sms = 0;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    int& n = known[dev & 63];
+    if (n == 0) {
+      e = cudaFuncSetAttribute(fp8_few_kernel<T, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               S::SMEM_BYTES);
+      if (e != cudaSuccess) return e;
+      e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+      if (e != cudaSuccess) return e;
+    }
+    sms = n;
+  }
+  Fp8Params p;
+  int64_t tiles = 0;
+  if (!fill(&p, g, S::ROWS, 128, 128, &tiles)) return cudaErrorInvalidValue;
+  // as above, with the weight as A (M-major, bit 15, in the gradient)
+  p.idesc = 1u << 4 | (uint32_t)g.wf << 7 | (uint32_t)g.xf << 10 | (GRAD ? 1u << 15 : 0u) |
+            (uint32_t)(S::ROWS >> 3) << 17 | 8u << 24;
+  return launch_clusters(fp8_few_kernel<T, GRAD>, 1, (unsigned)(tiles < sms ? tiles : sms),
+                         S::THREADS, S::SMEM_BYTES, st, p);
 }
 
 template <int CG, int BN, bool GRAD>
@@ -554,10 +853,16 @@ cudaError_t launch_t(const Fp8Problem& g, cudaStream_t st) {
                              : launch<__half, CG, BN, GRAD>(g, st);
 }
 
+template <bool GRAD>
+cudaError_t launch_few_t(const Fp8Problem& g, cudaStream_t st) {
+  return g.dtype == BRA_BF16 ? launch_few<__nv_bfloat16, GRAD>(g, st) : launch_few<__half, GRAD>(g, st);
+}
+
 }  // namespace
 
 GroupedTile fp8_tile(const Fp8Problem& g) {
   const int64_t N = g.grad ? g.in : g.out, groups = g.R < g.E ? g.R : g.E;
+  if (g.R <= kFewRows * g.E) return {FewShape::ROWS, 128, 1, 0};
   if (g.R / g.E >= 128 && (2 * (g.R / 256) + groups) * ((N + 255) / 256) >= 2 * 76)
     return {256, 256, 1, 0};
   return {128, 128, 1, 0};
@@ -565,6 +870,7 @@ GroupedTile fp8_tile(const Fp8Problem& g) {
 
 cudaError_t launch_fp8_grouped(const Fp8Problem& g, cudaStream_t st) {
   const GroupedTile t = fp8_tile(g);
+  if (t.rows == FewShape::ROWS) return g.grad ? launch_few_t<true>(g, st) : launch_few_t<false>(g, st);
   if (t.rows == 256) return g.grad ? launch_t<2, 256, true>(g, st) : launch_t<2, 256, false>(g, st);
   return g.grad ? launch_t<1, 128, true>(g, st) : launch_t<1, 128, false>(g, st);
 }

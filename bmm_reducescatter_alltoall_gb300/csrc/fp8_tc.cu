@@ -13,6 +13,11 @@
 // computed.  The walk over ragged row groups is grouped_tc.cu's.  The gradient
 // reads the same weight boxes the other way: 128 contraction rows of 128
 // columns, N-major.
+//
+// What bounds it: with 256 x 256 tiles the tensor pipe is busy 46% of the time
+// (65536 rows, 4096 x 4096: 1060 us, 2070 TFLOP/s); a K block's MMAs take 512
+// cycles, and the two accumulators come back every 1100, as a drain waits for
+// its loads from tensor memory twice.  With few rows HBM does (below).
 // Every wait is bounded (about 4 s) and reports through the fault word.
 #include <cstring>
 #include <mutex>
@@ -32,7 +37,9 @@ using namespace grp;
 constexpr int BKB = 128;                    // bytes (elements) of a K block
 constexpr int kGroupM = 8;
 // Rows an expert, on average, up to which a tile is 32 rows by 128 columns of
-// the weight (below).
+// the weight (below).  2048 x 4096, us, by 32 x 128 / by 128 x 128 tiles: 64
+// experts of 32 rows 92 / 118, of 33 (two tiles of rows) 167 / 118; 8 experts
+// of 32 rows 18.5 / 20.9, of 33 28.8 / 20.9.
 constexpr int64_t kFewRows = 32;
 constexpr int EPI_WARP0 = 4;
 constexpr int BAR_BYTES = 512;
@@ -459,7 +466,8 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(FShape<CG, BN>::THR
 // that hold few rows.  The factors then go with the columns: a warp lays those
 // of 16 blocks out in shared memory while the 16 before are being added, and
 // reads them as pairs.  HBM bounds it: ten stages of 16 KB of weights in flight
-// an SM (16 tokens x 8 of 64 experts, 2048 x 4096: 76 us in place of 123).
+// an SM (64 experts x 2 rows, 2048 x 4096: 537 MB in 89 us, 6.0 TB/s; by 128 x
+// 128 tiles 120).
 // --------------------------------------------------------------------------
 struct FewShape {
   static constexpr int ROWS = 32, CHUNK = 16;             // rows of a tile; blocks of factors
@@ -860,10 +868,13 @@ cudaError_t launch_few_t(const Fp8Problem& g, cudaStream_t st) {
 
 }  // namespace
 
+// The pair's tiles from 128 rows an expert, when there are tiles for a wave of
+// pairs (12 experts, 3063 rows, 1026 x 775 and its gradient, 112 and 140 tiles:
+// 14.8 us, by 128 x 128 tiles 19.6).
 GroupedTile fp8_tile(const Fp8Problem& g) {
   const int64_t N = g.grad ? g.in : g.out, groups = g.R < g.E ? g.R : g.E;
   if (g.R <= kFewRows * g.E) return {FewShape::ROWS, 128, 1, 0};
-  if (g.R / g.E >= 128 && (2 * (g.R / 256) + groups) * ((N + 255) / 256) >= 2 * 76)
+  if (g.R / g.E >= 128 && (2 * (g.R / 256) + groups) * ((N + 255) / 256) >= 76)
     return {256, 256, 1, 0};
   return {128, 128, 1, 0};
 }

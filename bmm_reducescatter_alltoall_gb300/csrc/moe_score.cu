@@ -280,14 +280,17 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
     }
     kept = better < p.top_groups;
     if (!exact || p.best == 2) {
-      // the last group kept and the first left out (a score from a logit whose
-      // low bits are gone errs by |l| s (1 - s) units more: within `part`)
+      // the last group kept and the first left out; a score from a logit whose
+      // low bits are gone errs by |l| s (1 - s) V units more (sigmoid: at most
+      // V / 4), or by |l| s V (softmax: (|m| + 0.4) V at most)
       const bool head = at.g < p.groups && at.gl == at.g * p.lanes;
       const uint32_t in = __ballot_sync(kAll, head && better == p.top_groups - 1) & at.group;
       const uint32_t out = __ballot_sync(kAll, head && better == p.top_groups) & at.group;
       const float vi = __shfl_sync(kAll, v, __ffs(in) - 1), vo = __shfl_sync(kAll, v, __ffs(out) - 1);
-      const float off = ranked || p.best == 1 ? slack : (p.sigmoid ? 0x1p-20f : 0x1p-18f) * inv +
-                                                            V * 0x1p-23f * inv;
+      float off = slack;
+      if (!ranked && p.best == 2)
+        off = (p.sigmoid ? 0x1p-20f + V * 0x1p-23f
+                         : 0x1p-18f + V * 0x1p-23f * (exact ? 1.f : 1.f + fabsf(m))) * inv;
       again = vo > -INFINITY && vi - vo <= 2.f * (off + fmaxf(fabsf(vi), fabsf(vo)) * part);
     }
     if (!kept) {
@@ -299,6 +302,43 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
   }
   const bool open = again;
 
+  // Takes the largest of the lanes' heads from the lists of the tokens with
+  // `on`: its key, and the lane that had it.  Whole warps.
+  auto take = [&](bool on, int* lane_of) {
+    uint32_t head = key[0][0];
+#pragma unroll
+    for (int n = 1; n < NL; ++n) head = max(head, key[n][0]);
+    // without the places: equal ranks go to the lowest lane
+    const uint32_t part_of = head & ~(uint32_t)(V - 1);
+    uint32_t most = part_of;
+    if constexpr (L == 32) {
+      most = __reduce_max_sync(kAll, part_of);
+    } else {
+#pragma unroll
+      for (int d = L / 2; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
+    }
+    const int win = __ffs(__ballot_sync(kAll, part_of == most) & at.group) - 1;
+    // the winner drops its head (with most = 0 there is nothing to drop)
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const bool drop = on && lane == win && key[n][0] == head;
+#pragma unroll
+      for (int i = 0; i + 1 < 8; ++i) key[n][i] = drop ? key[n][i + 1] : key[n][i];
+      key[n][7] = drop ? 0u : key[n][7];
+    }
+    *lane_of = win;
+    return __shfl_sync(kAll, head, win);
+  };
+  // Whether two experts' order is open in 32 bits: too close, unless equal
+  // logits and equal biases make them a tie in any precision.
+  auto too_close = [&](uint32_t ka, uint32_t kb) {
+    const float hi = rank_of(ka), lo = rank_of(kb);
+    return ka && kb && hi - lo <= distance(hi, lo);
+  };
+  auto same = [&](int a, int b) {
+    return logit(row + a) == logit(row + b) && (!ranked || p.bias[a] == p.bias[b]);
+  };
+
   // the largest of the lanes' heads, k times, and the best one left out
   constexpr int KEEP = (BRA_MAX_CHOICES + L) / L;        // of k + 1
   uint32_t my_key[KEEP];
@@ -308,31 +348,11 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
     my_key[o] = 0u;
     my_lane[o] = 0;
     for (int j = o * L; j < min(p.r.k + 1, (o + 1) * L); ++j) {
-      uint32_t head = key[0][0];
-#pragma unroll
-      for (int n = 1; n < NL; ++n) head = max(head, key[n][0]);
-      // without the places: equal ranks go to the lowest lane
-      const uint32_t part_of = head & ~(uint32_t)(V - 1);
-      uint32_t most = part_of;
-      if constexpr (L == 32) {
-        most = __reduce_max_sync(kAll, part_of);
-      } else {
-#pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(kAll, most, d));
-      }
-      const int win = __ffs(__ballot_sync(kAll, part_of == most) & at.group) - 1;
-      const uint32_t best = __shfl_sync(kAll, head, win);
+      int win;
+      const uint32_t best = take(true, &win);
       const bool mine = at.gl == j - o * L;
       my_key[o] = mine ? best : my_key[o];
       my_lane[o] = mine ? win : my_lane[o];
-      // the winner drops its head (with most = 0 there is nothing to drop)
-#pragma unroll
-      for (int n = 0; n < NL; ++n) {
-        const bool drop = lane == win && key[n][0] == head;
-#pragma unroll
-        for (int i = 0; i + 1 < 8; ++i) key[n][i] = drop ? key[n][i + 1] : key[n][i];
-        key[n][7] = drop ? 0u : key[n][7];
-      }
     }
   }
   int my_id[OWN];
@@ -345,22 +365,34 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
     const int id = my_key[o] ? first + (V - 1) - (int)(my_key[o] & (uint32_t)(V - 1)) : -1;
     if (o < OWN) my_id[o < OWN ? o : 0] = o * L + at.gl < p.r.k ? id : -1;
     if (!exact) {
-      // this one and the one before it in the order: too close, unless equal
-      // logits and equal biases make them a tie in any precision
+      // this one and the one before it in the order
       uint32_t kb = __shfl_up_sync(kAll, my_key[o], 1, L);
       int ib = __shfl_up_sync(kAll, id, 1, L);
       if (at.gl == 0) kb = key_before, ib = id_before;
       key_before = __shfl_sync(kAll, my_key[o], L - 1, L);
       id_before = __shfl_sync(kAll, id, L - 1, L);
-      bool bad = false;
-      if (kb && my_key[o]) {
-        const float hi = rank_of(kb), lo = rank_of(my_key[o]);
-        if (hi - lo <= distance(hi, lo))
-          bad = logit(row + ib) != logit(row + id) || (ranked && p.bias[ib] != p.bias[id]);
-      }
-      again |= (__ballot_sync(kAll, bad) & at.group) != 0u;
+      const bool near = too_close(kb, my_key[o]), tie = near && same(ib, id);
+      again |= (__ballot_sync(kAll, near && !tie) & at.group) != 0u;
       if (o == p.r.k / L) {
-        const float last = __shfl_sync(kAll, my_key[o] ? rank_of(my_key[o]) : -INFINITY, p.r.k % L, L);
+        // A tie of the last chosen with the first left out: whoever comes
+        // after them may stand above both, so that the order is followed until
+        // it leaves their neighbourhood.
+        const int end = p.r.k % L;
+        const uint32_t k0 = __shfl_sync(kAll, my_key[o], end, L);
+        const int i0 = __shfl_sync(kAll, id, end, L);
+        // (every lane votes, those of tokens that are open already too)
+        const uint32_t ties = __ballot_sync(kAll, tie && at.gl == end) & at.group;
+        bool on = ties != 0u && !again;
+        while (__any_sync(kAll, on)) {
+          int win;
+          const uint32_t k1 = take(on, &win);
+          const int i1 = __shfl_sync(kAll, at.first, win) + (V - 1) - (int)(k1 & (uint32_t)(V - 1));
+          if (on) {
+            on = too_close(k0, k1);
+            if (on && !same(i0, i1)) again = true, on = false;
+          }
+        }
+        const float last = k0 ? rank_of(k0) : -INFINITY;
         low = last - 2.f * distance(last, last);
       }
     }

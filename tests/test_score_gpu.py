@@ -202,6 +202,38 @@ def test_borders_are_decided_in_64_bits(score, dt):
         check(l, k, True, score, None, 8, 3, 2)
 
 
+@pytest.mark.parametrize("E", [16, 64, 200, 512])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_a_better_one_behind_ties(E, dt):
+    """The last chosen and the first ones left out are a tie; one behind them is better by less
+    than 32 bits hold."""
+    for ties in (2, 3, 9):
+        l = torch.full((3, E), -3.0, dtype=dt, device="cuda")
+        l[:, 0] = 5.0
+        l[:, 1:ties + 2] = 1.0
+        b = torch.zeros(E, device="cuda")
+        b[1:ties + 1] = 0.25
+        b[ties + 1] = torch.nextafter(torch.tensor(0.25), torch.tensor(1.0))
+        for k in (2, min(3, ties)):
+            r = check(l, k, True, "sigmoid", b)
+            assert (r["ids"][:, 1] == ties + 1).all()
+            check(l, k, False, "softmax", b)
+    if dt == torch.float32:                               # without a bias: logits one unit apart
+        l = torch.full((3, E), -3.0, device="cuda")
+        l[:, 2:8] = 1.0
+        l[:, 9] = torch.nextafter(torch.tensor(1.0), torch.tensor(2.0))
+        assert (check(l, 1, True, "sigmoid")["ids"] == 9).all()
+        assert (check(l, 2, True, "softmax", scale=2.0)["ids"][:, 0] == 9).all()
+
+
+@pytest.mark.parametrize("offset", [0.0, 100.0, -1000.0, 1e6])
+@pytest.mark.parametrize("E,G,top", [(64, 8, 3), (510, 3, 1), (256, 16, 5)])
+def test_groups_of_scores_of_large_logits(E, G, top, offset):
+    """Group sums of softmax scores whose logits are large: their last bits count."""
+    l = logits_of(4000, E, torch.float32) * 0.1 + offset
+    check(l, 4, True, "softmax", None, G, top, 2)
+
+
 @pytest.mark.parametrize("T", [64, 5000, 131073, 170000])
 def test_many_tokens(T):
     """One chunk, several, and as many as are summed by a launch of their own."""

@@ -166,6 +166,75 @@ __device__ __noinline__ void choose_exact(const ScoreParams& p, int t, int lane,
   }
 }
 
+// The best experts of a token in the order of their 32-bit ranks, at least all
+// that can be among the k chosen: the o-th of lane gl is number o * L + gl.
+template <int KEEP>
+struct Listed {
+  float rank[KEEP];
+  int id[KEEP];        // -1: none
+  uint32_t close;      // bit o: the neighbours' ranks are too close to tell
+};
+
+// The choice from a list, by the lanes of a token: ranks that are too close are
+// computed in 64 bits, one expert to a lane at a time, and every expert's place
+// is the number of those before it.  A softmax's sum is the one in 32 bits
+// (within 2^-18): whether it decides an order is checked; false: it does.
+template <typename T, int L, int KEEP>
+__device__ __noinline__ bool settle(const ScoreParams& p, int t, int lane, Listed<KEEP> of, int n,
+                                    float m, float sum) {
+  const uint32_t group = L == 32 ? kAll : ((1u << (L & 31)) - 1u) << (lane & ~(L - 1));
+  const int gl = lane % L;
+  const T* row = static_cast<const T*>(p.r.logits) + (int64_t)t * p.r.E;
+  const bool sums = p.bias != nullptr && !p.sigmoid;
+  double r[KEEP], score[KEEP];
+  float l[KEEP], b[KEEP];
+  int place[KEEP];
+#pragma unroll
+  for (int o = 0; o < KEEP; ++o) {
+    r[o] = of.rank[o];
+    score[o] = 0.0;
+    l[o] = b[o] = 0.f;
+    place[o] = 0;
+    if (of.id[o] >= 0 && (of.close >> o & 1u)) {
+      l[o] = logit(row + of.id[o]);
+      r[o] = l[o];
+      if (p.bias) {
+        b[o] = p.bias[of.id[o]];
+        score[o] = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l[o])) : exp((double)l[o] - (double)m) / sum;
+        r[o] = score[o] + (double)b[o];
+        if (!(r[o] < 1e300)) r[o] = 1e300;
+      }
+    }
+  }
+  bool sure = true;
+#pragma unroll
+  for (int from = 0; from < KEEP; ++from)
+#pragma unroll 1
+    for (int i = 0; i < L && from * L + i < n; ++i) {
+      const double x = __shfl_sync(group, r[from], i, L);
+      const int id = __shfl_sync(group, of.id[from], i, L);
+#pragma unroll
+      for (int o = 0; o < KEEP; ++o)
+        place[o] += id >= 0 && (x > r[o] || (x == r[o] && id < of.id[o])) ? 1 : 0;
+      if (sums) {
+        const double s = __shfl_sync(group, score[from], i, L);
+        const float lx = __shfl_sync(group, l[from], i, L), bx = __shfl_sync(group, b[from], i, L);
+        const bool close = __shfl_sync(group, of.close, i, L) >> from & 1u;
+#pragma unroll
+        for (int o = 0; o < KEEP; ++o)
+          if (close && (of.close >> o & 1u) && id >= 0 && of.id[o] >= 0 && (lx != l[o] || bx != b[o]))
+            sure &= fabs(x - r[o]) > 0x1p-17 * fabs(s - score[o]) + 0x1p-48 * fabs(x);
+      }
+    }
+  if (__any_sync(group, !sure)) return false;
+#pragma unroll
+  for (int o = 0; o < KEEP; ++o) {
+    const int at = of.id[o] >= 0 ? place[o] : o * L + gl;   // those without an expert are the last
+    if (at < p.r.k) p.r.ids[(int64_t)t * p.r.k + at] = of.id[o];
+  }
+  return true;
+}
+
 // The experts of one token to each group of L lanes (t < 0: none): as choose
 // of moe_route.cu.  Whole warps.
 template <typename T, int L, int V>
@@ -255,7 +324,7 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
   // what a key says of its rank: at most V - 1 units of it off
   auto rank_of = [&](uint32_t k) { return value_of(k & ~(uint32_t)(V - 1)); };
 
-  bool again = false, kept = true;
+  bool open = false, kept = true;                // open: 32 bits do not decide the groups
   if (limited) {
     uint32_t k1 = key[0][0], k2 = key[0][1];
 #pragma unroll
@@ -291,7 +360,7 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
       if (!ranked && p.best == 2)
         off = (p.sigmoid ? 0x1p-20f + V * 0x1p-23f
                          : 0x1p-18f + V * 0x1p-23f * (exact ? 1.f : 1.f + fabsf(m))) * inv;
-      again = vo > -INFINITY && vi - vo <= 2.f * (off + fmaxf(fabsf(vi), fabsf(vo)) * part);
+      open = vo > -INFINITY && vi - vo <= 2.f * (off + fmaxf(fabsf(vi), fabsf(vo)) * part);
     }
     if (!kept) {
 #pragma unroll
@@ -300,8 +369,6 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
         for (int i = 0; i < 8; ++i) key[n][i] = 0u;
     }
   }
-  const bool open = again;
-
   // Takes the largest of the lanes' heads from the lists of the tokens with
   // `on`: its key, and the lane that had it.  Whole warps.
   auto take = [&](bool on, int* lane_of) {
@@ -355,51 +422,86 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
       my_lane[o] = mine ? win : my_lane[o];
     }
   }
-  int my_id[OWN];
+  // Neighbours in the order: too close, and no tie, is an order that 32 bits
+  // do not decide.
+  Listed<KEEP> list;
+  list.close = 0u;
   int id_before = 0;
   uint32_t key_before = 0u;
-  float low = 0.f;                               // the least rank that can be chosen
+  bool unsure = false, border = false;           // border: the first left out is close
 #pragma unroll
   for (int o = 0; o < KEEP; ++o) {
     const int first = __shfl_sync(kAll, at.first, my_lane[o]);
-    const int id = my_key[o] ? first + (V - 1) - (int)(my_key[o] & (uint32_t)(V - 1)) : -1;
-    if (o < OWN) my_id[o < OWN ? o : 0] = o * L + at.gl < p.r.k ? id : -1;
+    list.id[o] = my_key[o] ? first + (V - 1) - (int)(my_key[o] & (uint32_t)(V - 1)) : -1;
     if (!exact) {
-      // this one and the one before it in the order
       uint32_t kb = __shfl_up_sync(kAll, my_key[o], 1, L);
-      int ib = __shfl_up_sync(kAll, id, 1, L);
+      int ib = __shfl_up_sync(kAll, list.id[o], 1, L);
       if (at.gl == 0) kb = key_before, ib = id_before;
       key_before = __shfl_sync(kAll, my_key[o], L - 1, L);
-      id_before = __shfl_sync(kAll, id, L - 1, L);
-      const bool near = too_close(kb, my_key[o]), tie = near && same(ib, id);
-      again |= (__ballot_sync(kAll, near && !tie) & at.group) != 0u;
-      if (o == p.r.k / L) {
-        // A tie of the last chosen with the first left out: whoever comes
-        // after them may stand above both, so that the order is followed until
-        // it leaves their neighbourhood.
-        const int end = p.r.k % L;
-        const uint32_t k0 = __shfl_sync(kAll, my_key[o], end, L);
-        const int i0 = __shfl_sync(kAll, id, end, L);
-        // (every lane votes, those of tokens that are open already too)
-        const uint32_t ties = __ballot_sync(kAll, tie && at.gl == end) & at.group;
-        bool on = ties != 0u && !again;
-        while (__any_sync(kAll, on)) {
-          int win;
-          const uint32_t k1 = take(on, &win);
-          const int i1 = __shfl_sync(kAll, at.first, win) + (V - 1) - (int)(k1 & (uint32_t)(V - 1));
-          if (on) {
-            on = too_close(k0, k1);
-            if (on && !same(i0, i1)) again = true, on = false;
-          }
-        }
-        const float last = k0 ? rank_of(k0) : -INFINITY;
-        low = last - 2.f * distance(last, last);
-      }
+      id_before = __shfl_sync(kAll, list.id[o], L - 1, L);
+      const bool near = too_close(kb, my_key[o]);
+      const uint32_t pairs = __ballot_sync(kAll, near) & at.group;
+      const uint32_t open_pairs = __ballot_sync(kAll, near && !same(ib, list.id[o])) & at.group;
+      unsure |= open_pairs != 0u;
+      // this one and the one behind it
+      const uint32_t own = pairs >> (lane & ~(L - 1));
+      list.close |= (own >> at.gl & 1u) << o;
+      if (at.gl < L - 1) list.close |= (own >> (at.gl + 1) & 1u) << o;
+      if (o > 0 && at.gl == L - 1) list.close |= (own & 1u) << (o - 1);
+      if (o == p.r.k / L) border = (own >> (p.r.k % L) & 1u) != 0u;
     }
   }
+  int n = p.r.k + 1;                             // experts in the list
+  bool full = false;
+  float low = 0.f;                               // the least rank that can be chosen
+  if (!exact) {
+    uint32_t last = 0u, out_key = 0u;            // the last chosen, the first left out
+    int out_id = 0;
+#pragma unroll
+    for (int o = 0; o < KEEP; ++o) {
+      const uint32_t a = __shfl_sync(kAll, my_key[o], (p.r.k - 1) % L, L);
+      const uint32_t b = __shfl_sync(kAll, my_key[o], p.r.k % L, L);
+      const int c = __shfl_sync(kAll, list.id[o], p.r.k % L, L);
+      if (o == (p.r.k - 1) / L) last = a;
+      if (o == p.r.k / L) out_key = b, out_id = c;
+    }
+    // Whoever is close to the last chosen may stand above it: the order is
+    // followed until it leaves its neighbourhood.
+    bool on = border;
+    while (__any_sync(kAll, on)) {
+      int win;
+      const uint32_t next = take(on, &win);
+      const int id = __shfl_sync(kAll, at.first, win) + (V - 1) - (int)(next & (uint32_t)(V - 1));
+      on = on && too_close(last, next);
+      if (on) {
+        unsure |= !same(out_id, id);
+        full |= n >= L * KEEP;
+#pragma unroll
+        for (int o = 0; o < KEEP; ++o)
+          if (o * L + at.gl == n) {
+            my_key[o] = next;
+            list.id[o] = id;
+            list.close |= 1u << o;
+          }
+        ++n;
+      }
+    }
+    const float least = out_key ? rank_of(out_key) : -INFINITY;
+    low = least - 2.f * distance(least, least);
+  }
+  int my_id[OWN];
+#pragma unroll
+  for (int o = 0; o < OWN; ++o) my_id[o] = o * L + at.gl < p.r.k ? list.id[o] : -1;
   const int64_t out = (int64_t)t * p.r.k;
-  if (again) {                                   // the same for all lanes of a token
-    choose_exact<T, L, V>(p, t, lane, open, kept, low);
+  if (open || unsure) {                          // the same for all lanes of a token
+    bool done = false;
+    if (!open && !full) {
+#pragma unroll
+      for (int o = 0; o < KEEP; ++o) list.rank[o] = my_key[o] ? rank_of(my_key[o]) : 0.f;
+      done = settle<T, L, KEEP>(p, t, lane, list, n, m, sum);
+    }
+    if (!done) choose_exact<T, L, V>(p, t, lane, open, kept, low);
+    __syncwarp(at.group);                        // the ids, by other lanes of this token
 #pragma unroll
     for (int o = 0; o < OWN; ++o)
       my_id[o] = o * L + at.gl < p.r.k ? p.r.ids[out + o * L + at.gl] : -1;

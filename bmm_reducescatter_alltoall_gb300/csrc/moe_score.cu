@@ -84,6 +84,22 @@ struct Place {
   }
 };
 
+// The paths below run for few tokens, and mostly on an SM that has not run them:
+// loops stay loops and the 64-bit functions are there once, as fetching the
+// instructions takes most of their time (1518 tokens, 9 of 22, one of them
+// settled: 16 us with unrolled loops, 8 without the token).
+
+// A score in 64 bits; of a softmax with the largest logit m.
+__device__ __noinline__ double score64(float l, float m, double sum, int sigmoid) {
+  const double e = exp(sigmoid ? -(double)l : (double)l - (double)m);
+  return (sigmoid ? 1.0 : e) / (sigmoid ? 1.0 + e : sum);
+}
+// Whether a softmax's sum that is off by up to 2^-18 leaves the order of two
+// ranks as it is: x and y with the scores sx and sy in them.
+__device__ __forceinline__ bool apart(double x, double sx, double y, double sy) {
+  return (x == y && sx == sy) || fabs(x - y) > 0x1p-17 * fabs(sx - sy) + 0x1p-48 * fabs(x);
+}
+
 // The choice in 64 bits: the ids of one token, by the lanes of `at.group`.
 // open: whether its groups are chosen again too; else those of lanes with
 // `kept` are, and experts whose rank in 32 bits lies below `floor` are out.
@@ -103,7 +119,7 @@ __device__ __noinline__ void choose_exact(const ScoreParams& p, int t, int lane,
 #pragma unroll 1
     for (int i = 0; i < at.own; ++i) {
       const float v = logit(row + i);
-      if (v >= -kLargest) sum += exp((double)v - (double)m);
+      if (v >= -kLargest) sum += score64(v, m, 1.0, 0);
     }
 #pragma unroll
     for (int d = L / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(at.group, sum, d);
@@ -126,7 +142,7 @@ __device__ __noinline__ void choose_exact(const ScoreParams& p, int t, int lane,
     const int i = __ffs(live) - 1;
     live &= live - 1u;
     const float v = logit(row + i);
-    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : exp((double)v - (double)m) / sum;
+    const double s = score64(v, m, sum, p.sigmoid);
     double x = p.bias ? s + (double)p.bias[at.first + i] : (double)v;
     if (!(x > -inf)) x = -inf;
     r[i] = x < 1e300 ? x : 1e300;
@@ -170,69 +186,108 @@ __device__ __noinline__ void choose_exact(const ScoreParams& p, int t, int lane,
 // that can be among the k chosen: the o-th of lane gl is number o * L + gl.
 template <int KEEP>
 struct Listed {
-  float rank[KEEP];
   int id[KEEP];        // -1: none
   uint32_t close;      // bit o: the neighbours' ranks are too close to tell
 };
 
 // The choice from a list, by the lanes of a token: ranks that are too close are
-// computed in 64 bits, one expert to a lane at a time, and every expert's place
-// is the number of those before it.  A softmax's sum is the one in 32 bits
-// (within 2^-18): whether it decides an order is checked; false: it does.
+// computed in 64 bits, and their experts' places are those of their ranks among
+// them; the other places stand.  A softmax's sum is the one in 32 bits; false:
+// it decides an order.
 template <typename T, int L, int KEEP>
-__device__ __noinline__ bool settle(const ScoreParams& p, int t, int lane, Listed<KEEP> of, int n,
-                                    float m, float sum) {
+__device__ __noinline__ bool settle(const ScoreParams& p, int t, int lane, Listed<KEEP> of, float m,
+                                    float sum) {
   const uint32_t group = L == 32 ? kAll : ((1u << (L & 31)) - 1u) << (lane & ~(L - 1));
   const int gl = lane % L;
   const T* row = static_cast<const T*>(p.r.logits) + (int64_t)t * p.r.E;
-  const bool sums = p.bias != nullptr && !p.sigmoid;
   double r[KEEP], score[KEEP];
-  float l[KEEP], b[KEEP];
   int place[KEEP];
-#pragma unroll
+#pragma unroll 1
   for (int o = 0; o < KEEP; ++o) {
-    r[o] = of.rank[o];
-    score[o] = 0.0;
-    l[o] = b[o] = 0.f;
-    place[o] = 0;
-    if (of.id[o] >= 0 && (of.close >> o & 1u)) {
-      l[o] = logit(row + of.id[o]);
-      r[o] = l[o];
-      if (p.bias) {
-        b[o] = p.bias[of.id[o]];
-        score[o] = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l[o])) : exp((double)l[o] - (double)m) / sum;
-        r[o] = score[o] + (double)b[o];
-        if (!(r[o] < 1e300)) r[o] = 1e300;
-      }
+    place[o] = o * L + gl;
+    r[o] = score[o] = 0.0;
+    if (of.close >> o & 1u) {
+      const float l = logit(row + of.id[o]);
+      if (p.bias) score[o] = score64(l, m, sum, p.sigmoid);
+      const double x = p.bias ? score[o] + (double)p.bias[of.id[o]] : (double)l;
+      r[o] = x < 1e300 ? x : 1e300;
     }
   }
   bool sure = true;
-#pragma unroll
-  for (int from = 0; from < KEEP; ++from)
 #pragma unroll 1
-    for (int i = 0; i < L && from * L + i < n; ++i) {
-      const double x = __shfl_sync(group, r[from], i, L);
-      const int id = __shfl_sync(group, of.id[from], i, L);
-#pragma unroll
+  for (int from = 0; from < KEEP; ++from) {
+    uint32_t left = __ballot_sync(group, of.close >> from & 1u) & group;
+#pragma unroll 1
+    while (left) {
+      const int src = __ffs(left) - 1, at = from * L + src % L;
+      left &= left - 1u;
+      const double x = __shfl_sync(group, r[from], src), sx = __shfl_sync(group, score[from], src);
+      const int id = __shfl_sync(group, of.id[from], src);
+#pragma unroll 1
       for (int o = 0; o < KEEP; ++o)
-        place[o] += id >= 0 && (x > r[o] || (x == r[o] && id < of.id[o])) ? 1 : 0;
-      if (sums) {
-        const double s = __shfl_sync(group, score[from], i, L);
-        const float lx = __shfl_sync(group, l[from], i, L), bx = __shfl_sync(group, b[from], i, L);
-        const bool close = __shfl_sync(group, of.close, i, L) >> from & 1u;
-#pragma unroll
-        for (int o = 0; o < KEEP; ++o)
-          if (close && (of.close >> o & 1u) && id >= 0 && of.id[o] >= 0 && (lx != l[o] || bx != b[o]))
-            sure &= fabs(x - r[o]) > 0x1p-17 * fabs(s - score[o]) + 0x1p-48 * fabs(x);
-      }
+        if (of.close >> o & 1u) {
+          place[o] += (x > r[o] || (x == r[o] && id < of.id[o]) ? 1 : 0) - (at < o * L + gl ? 1 : 0);
+          sure = sure && (!p.bias || p.sigmoid || apart(x, sx, r[o], score[o]));
+        }
     }
-  if (__any_sync(group, !sure)) return false;
-#pragma unroll
-  for (int o = 0; o < KEEP; ++o) {
-    const int at = of.id[o] >= 0 ? place[o] : o * L + gl;   // those without an expert are the last
-    if (at < p.r.k) p.r.ids[(int64_t)t * p.r.k + at] = of.id[o];
   }
+  if (__any_sync(group, !sure)) return false;
+#pragma unroll 1
+  for (int o = 0; o < KEEP; ++o)
+    if (place[o] < p.r.k) p.r.ids[(int64_t)t * p.r.k + place[o]] = of.id[o];
   return true;
+}
+
+// How many groups of experts of a token come before this lane's, by the lanes
+// of the token: the values of groups with `near` in 64 bits, from their experts
+// whose ranks in 32 bits are `floor` or more; the other values are v.  -1: a
+// softmax's sum in 32 bits decides an order.
+template <typename T, int L, int V>
+__device__ __noinline__ int settle_groups(const ScoreParams& p, int t, int lane, float v, bool near,
+                                          float floor, float m, float sum) {
+  const Place at = Place::of<L>(p, lane);
+  const T* row = static_cast<const T*>(p.r.logits) + (int64_t)t * p.r.E + at.first;
+  const double inf = INFINITY;
+  const float inv = 1.f / sum;
+  double f1 = -inf, f2 = -inf, s1 = 0.0, s2 = 0.0;
+  auto put = [&](double x, double s) {          // among the two largest
+    if (x > f1) {
+      f2 = f1, s2 = s1;
+      f1 = x, s1 = s;
+    } else if (x > f2) {
+      f2 = x, s2 = s;
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < at.own && near; ++i) {
+    const float l = logit(row + i), b = p.bias ? p.bias[at.first + i] : 0.f;
+    float x = l;
+    if (p.bias) x = (p.sigmoid ? score_of(l) : expf(l - m) * inv) + fminf(b, kLargest);
+    if (!(l >= -kLargest) || !(b >= -kLargest) || x < floor) continue;
+    const double s = p.bias || p.best == 2 ? score64(l, m, sum, p.sigmoid) : (double)l;
+    const double r = p.bias ? s + (double)b : s;
+    put(r < 1e300 ? r : 1e300, s);
+  }
+#pragma unroll 1
+  for (int d = 1; d < p.lanes; d <<= 1) {
+    const double a1 = __shfl_xor_sync(at.group, f1, d), b1 = __shfl_xor_sync(at.group, s1, d);
+    const double a2 = __shfl_xor_sync(at.group, f2, d), b2 = __shfl_xor_sync(at.group, s2, d);
+    put(a1, b1);
+    put(a2, b2);
+  }
+  const bool two = p.best == 2 && f2 > -inf;
+  const double value = near ? two ? f1 + f2 : f1 : (double)v, of = two ? s1 + s2 : s1;
+  int better = 0;
+  bool sure = true;
+#pragma unroll 1
+  for (int g = 0; g < p.groups; ++g) {
+    const double x = __shfl_sync(at.group, value, g * p.lanes, L);
+    const double sx = __shfl_sync(at.group, of, g * p.lanes, L);
+    const bool too = __shfl_sync(at.group, (int)near, g * p.lanes, L) != 0;
+    better += x > value || (x == value && g < at.g) ? 1 : 0;
+    if (p.bias && !p.sigmoid && near && too) sure = sure && apart(x, sx, value, of);
+  }
+  return __any_sync(at.group, !sure) ? -1 : better;
 }
 
 // The experts of one token to each group of L lanes (t < 0: none): as choose
@@ -244,6 +299,11 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
   constexpr int OWN = (BRA_MAX_CHOICES + L - 1) / L;   // choices a lane keeps
   constexpr int NL = V / 8;
   const T* row = static_cast<const T*>(p.r.logits) + (int64_t)t * p.r.E;
+  // Groups before this lane's where 64 bits had to tell (-1: they did not,
+  // -2: not asked).  The choice then begins anew, so that nothing is kept in
+  // registers over that call.
+  int before = -2;
+begin:
   float l[V];
 #pragma unroll
   for (int i = 0; i < V; i += 4) {
@@ -347,7 +407,6 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
       const float o = __shfl_sync(kAll, v, g * p.lanes, L);
       better += o > v || (o == v && g < at.g) ? 1 : 0;
     }
-    kept = better < p.top_groups;
     if (!exact || p.best == 2) {
       // the last group kept and the first left out; a score from a logit whose
       // low bits are gone errs by |l| s (1 - s) V units more (sigmoid: at most
@@ -360,8 +419,27 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
       if (!ranked && p.best == 2)
         off = (p.sigmoid ? 0x1p-20f + V * 0x1p-23f
                          : 0x1p-18f + V * 0x1p-23f * (exact ? 1.f : 1.f + fabsf(m))) * inv;
-      open = vo > -INFINITY && vi - vo <= 2.f * (off + fmaxf(fabsf(vi), fabsf(vo)) * part);
+      auto tight = [&](float a, float b) {
+        return fabsf(a - b) <= 2.f * (off + fmaxf(fabsf(a), fabsf(b)) * part);
+      };
+      open = before == -2 && vo > -INFINITY && tight(vi, vo);
+      if (__any_sync(kAll, open)) {
+        if (open) {                              // the same for all lanes of a token
+          const uint32_t least = p.best == 2 ? k2 : k1;
+          const float x = least ? rank_of(least) : -INFINITY;
+          const bool near =
+              v > -INFINITY && (v <= vi || tight(v, vi)) && (v >= vo || tight(v, vo));
+          before = settle_groups<T, L, V>(p, t, lane, v, near, x - 2.f * distance(x, x), m, sum);
+        } else {
+          before = better;
+        }
+        __syncwarp();
+        goto begin;
+      }
+      if (before >= 0) better = before;
+      open = before == -1;
     }
+    kept = better < p.top_groups;
     if (!kept) {
 #pragma unroll
       for (int n = 0; n < NL; ++n)
@@ -495,11 +573,7 @@ __device__ __forceinline__ void choose_scored(const ScoreParams& p, const Place&
   const int64_t out = (int64_t)t * p.r.k;
   if (open || unsure) {                          // the same for all lanes of a token
     bool done = false;
-    if (!open && !full) {
-#pragma unroll
-      for (int o = 0; o < KEEP; ++o) list.rank[o] = my_key[o] ? rank_of(my_key[o]) : 0.f;
-      done = settle<T, L, KEEP>(p, t, lane, list, n, m, sum);
-    }
+    if (!open && !full) done = settle<T, L, KEEP>(p, t, lane, list, m, sum);
     if (!done) choose_exact<T, L, V>(p, t, lane, open, kept, low);
     __syncwarp(at.group);                        // the ids, by other lanes of this token
 #pragma unroll

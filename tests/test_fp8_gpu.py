@@ -145,6 +145,31 @@ def test_pitched_and_unaligned_rows(K, pad, dt):
     assert not q.codes.view(torch.uint8)[:, K:].any() and not q.scales[:, -(-K // 128):].any()
 
 
+@pytest.mark.parametrize("dt", ALL)
+@pytest.mark.parametrize("K", [1, 7, 15, 17, 127, 129, 1021, 2046, 2047, 2049, 2055, 4099])
+def test_any_offset(K, dt):
+    """Rows and weights that begin at any element of memory that holds NaN before and after them,
+    and back to memory of which nothing else is written."""
+    R = 5
+    data = randn(R, K).to(dt)
+    want = bra.fp8_quantize(torch.nn.functional.pad(data, (0, -K % 8))[:, :K].contiguous(), format=E5)
+    for off in range(0, 9):
+        room = torch.full((off + R * K + 17,), float("nan"), dtype=dt, device="cuda")
+        x = room[off:off + R * K].view(R, K)
+        x.copy_(data)
+        q = bra.fp8_quantize(x, format=E5)
+        assert same(bra.fp8_dequantize(q, torch.float32).double(), quantized(data, E5, 1)[0])
+        w = bra.fp8_quantize(x.view(1, R, K))
+        assert same(bra.fp8_dequantize(w, torch.float32)[0].double(), quantized(data, E4, 128)[0])
+        assert torch.equal(q.codes.view(torch.uint8), want.codes.view(torch.uint8))
+        for t, values in ((q, quantized(data, E5, 1)[0]), (w, quantized(data, E4, 128)[0])):
+            room = torch.full((off + R * K + 17,), 7.0, dtype=dt, device="cuda")
+            y = room[off:off + R * K].view(t.shape)
+            bra.fp8_dequantize(t, dt, out=y)
+            assert torch.equal(y.view(R, K), values.to(dt))
+            assert (room[:off] == 7.0).all() and (room[off + R * K:] == 7.0).all()
+
+
 def test_rows_past_the_counts_are_left_alone():
     x = randn(70, 160).bfloat16()
     for counts in ([0, 1, 0, 5, 57, 0], [63], [1] * 63, [0, 0]):

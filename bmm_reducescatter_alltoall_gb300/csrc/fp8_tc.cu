@@ -67,7 +67,7 @@ struct FShape {
   static constexpr int B_COLS = BN / CG;                  // output columns held by one CTA
   static constexpr int B_BYTES = B_COLS * BKB;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int EPI_WARPS = BN == 256 ? 8 : 4;
+  static constexpr int EPI_WARPS = 8;
   static constexpr int WC = BN / (EPI_WARPS / 4);         // columns of an epilogue warp
   static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
   static constexpr int NBUF = BN == 256 ? 2 : 4;          // block accumulators
@@ -126,6 +126,12 @@ __device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&v)[32
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i]) : "l"(pair64(v[2 * i], v[2 * i + 1])), "l"(ff));
+}
+
+// The product of two scales within the floats; NaN stays.
+__device__ __forceinline__ float within(float f) {
+  constexpr float most = 3.402823466e+38f;
+  return f > most ? most : f < -most ? -most : f;
 }
 
 // mbar_wait without a call: a kernel that splits its registers cannot have one.
@@ -333,14 +339,61 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(FShape<CG, BN>::THR
         else mbar_arrive(tempty_bar(buf));
       }
     };
-    for (int t = walk0; ok && t < total; t += step) {
-      const TileCoord c = find(t);
-      const int r0 = gt->off[c.g], r1 = gt->off[c.g + 1];
-      const int tile_row = c.mt * BM + (int)rank * 128 + q * 32;
-      const int n0 = c.nt * BN + h * WC;
-      const int valid = min(32, r1 - r0 - tile_row);
-      const bool any = valid > 0 && n0 < p.N;
-      if (!any) {
+    // What a tile needs besides its blocks, fetched while the tile before is
+    // being stored: scales (four blocks of this lane's row in a load, 32 blocks
+    // of the weight over the lanes, each ahead of its use) and the bias.
+    struct Tile {
+      int g, row, n0, valid;
+    };
+    Tile c;
+    const float *sx = nullptr, *sw = nullptr;
+    float4 x_at, x_next;
+    float w_at = 0.f, w_next = 0.f, bias[WC / 32];
+    auto fetch_x = [&](int kb) {
+      return kb < p.k_blocks ? *reinterpret_cast<const float4*>(sx + kb) : make_float4(0, 0, 0, 0);
+    };
+    auto fetch_w = [&](int kb) {
+      return kb + lane < p.k_blocks ? sw[(int64_t)(kb + lane) * p.ws_block] : 0.f;
+    };
+    auto begin = [&](int t) {
+      const TileCoord at = find(t);
+      const int tile_row = at.mt * BM + (int)rank * 128 + q * 32;
+      c.g = at.g;
+      c.row = gt->off[at.g] + tile_row;
+      c.n0 = at.nt * BN + h * WC;
+      c.valid = c.n0 < p.N ? min(32, gt->off[at.g + 1] - c.row) : 0;
+      if (c.valid <= 0) return;
+      sx = p.xs + ((int64_t)c.row + min(lane, c.valid - 1)) * p.xs_pitch;
+      sw = p.ws + c.g * p.ws_group + (c.n0 / fp8::kBlock) * p.ws_out;
+      x_at = fetch_x(0), x_next = fetch_x(4);
+      w_at = fetch_w(0), w_next = fetch_w(32);
+      if (p.bias)
+#pragma unroll
+        for (int i = 0; i < WC / 32; ++i) {
+          const int n = c.n0 + i * 32 + lane;
+          const int64_t b = (int64_t)c.g * p.N + n;
+          bias[i] = n >= p.N      ? 0.f
+                    : p.bias_fp16 ? Num<__half>::bias(p.bias, b)
+                                  : static_cast<const float*>(p.bias)[b];
+        }
+    };
+    uint32_t o[WC / 64][32];          // the tile before, rounded
+    T* y0 = nullptr;
+    int n0 = 0, valid = 0;
+    for (int t = walk0; ok; t += step) {
+      if (t < total) begin(t);
+      if (valid > 0) {
+        const int segs = min(WC / 64, (p.N - n0 + 63) / 64);
+        Carry carry;
+#pragma unroll
+        for (int ch = 0; ch < WC / 64; ++ch)
+          if (ch < segs)
+            put_segment<T>(o[ch], carry, ch == 0, ch + 1 == segs, y0, p.ldy, valid, n0 + ch * 64, p.N,
+                           seg, p.aligned != 0, lane, [] {});
+      }
+      if (t >= total) break;
+      n0 = c.n0, valid = c.valid;
+      if (valid <= 0) {
         for (int kb = 0; kb < p.k_blocks; ++kb) {
           const bool got = wait_here(tfull_bar(buf), buf_phase, abort_flag, fault);
           if (!__all_sync(0xffffffffu, got)) {
@@ -352,35 +405,20 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(FShape<CG, BN>::THR
         }
         continue;
       }
-      if (p.bias) {   // while the first block is being computed
-        for (int i = lane; i < WC; i += 32) {
-          const int64_t at = (int64_t)c.g * p.N + n0 + i;
-          const float b = n0 + i >= p.N  ? 0.f
-                          : p.bias_fp16 ? Num<__half>::bias(p.bias, at)
-                                        : static_cast<const float*>(p.bias)[at];
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias_s + i * 4), "f"(b) : "memory");
-        }
+      y0 = static_cast<T*>(p.y) + (int64_t)c.row * p.ldy;
+      if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < WC / 32; ++i)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(bias_s + (i * 32 + lane) * 4), "f"(bias[i])
+                       : "memory");
         __syncwarp();
       }
-      // scales: four blocks of this lane's row in a load, 32 blocks of the
-      // weight over the lanes, each fetched ahead of its use
-      const float* sx = p.xs + ((int64_t)r0 + tile_row + min(lane, valid - 1)) * p.xs_pitch;
-      const float* sw = p.ws + c.g * p.ws_group + (n0 / fp8::kBlock) * p.ws_out;
-      auto fetch_x = [&](int kb) {
-        return kb < p.k_blocks ? *reinterpret_cast<const float4*>(sx + kb) : make_float4(0, 0, 0, 0);
-      };
-      auto fetch_w = [&](int kb) {
-        return kb + lane < p.k_blocks ? sw[(int64_t)(kb + lane) * p.ws_block] : 0.f;
-      };
-      float4 x_at = fetch_x(0), x_next = fetch_x(4);
-      float w_at = fetch_w(0), w_next = fetch_w(32);
       uint64_t acc[WC / 2];
 #pragma unroll
       for (int i = 0; i < WC / 2; ++i) acc[i] = 0ull;
 #pragma unroll 1
       for (int kb = 0; kb < p.k_blocks; ++kb) {
-        float f = x_at.x * __shfl_sync(0xffffffffu, w_at, kb & 31);
-        f = f > 3.402823466e+38f ? 3.402823466e+38f : f;            // NaN stays
+        const float f = within(x_at.x * __shfl_sync(0xffffffffu, w_at, kb & 31));
         const uint64_t ff = pair64(__float_as_uint(f), __float_as_uint(f));
         if ((kb & 3) == 3) {
           x_at = x_next;
@@ -423,9 +461,6 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(FShape<CG, BN>::THR
         next_buf();
       }
       if (!ok) break;
-      T* y0 = static_cast<T*>(p.y) + ((int64_t)r0 + tile_row) * p.ldy;
-      const int segs = min(WC / 64, (p.N - n0 + 63) / 64);
-      uint32_t o[WC / 64][32];
 #pragma unroll
       for (int ch = 0; ch < WC / 64; ++ch) {
         uint32_t v[64];
@@ -436,12 +471,6 @@ __global__ void __cluster_dims__(CG, 1, 1) __launch_bounds__(FShape<CG, BN>::THR
         }
         pack_segment<T>(v, o[ch], p.bias ? bias_s + ch * 256 : 0u, false);
       }
-      Carry carry;
-#pragma unroll
-      for (int ch = 0; ch < WC / 64; ++ch)
-        if (ch < segs)
-          put_segment<T>(o[ch], carry, ch == 0, ch + 1 == segs, y0, p.ldy, valid, n0 + ch * 64, p.N,
-                         seg, p.aligned != 0, lane, [] {});
     }
   }
 
@@ -649,9 +678,9 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < S::CHUNK; ++i) {
           const float4 x = fx[i / 4];
-          float f = (i % 4 == 0 ? x.x : i % 4 == 1 ? x.y : i % 4 == 2 ? x.z : x.w) *
-                    __shfl_sync(0xffffffffu, fw, i);
-          f = f > 3.402823466e+38f ? 3.402823466e+38f : f;          // NaN stays
+          const float f =
+              within((i % 4 == 0 ? x.x : i % 4 == 1 ? x.y : i % 4 == 2 ? x.z : x.w) *
+                     __shfl_sync(0xffffffffu, fw, i));
           asm volatile("st.shared.f32 [%0], %1;" ::"r"(fac + (i * ROWS + lane) * 4), "f"(f) : "memory");
         }
         __syncwarp();

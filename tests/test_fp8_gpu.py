@@ -261,6 +261,35 @@ def test_products_over_group_sizes(counts, K, N, dt):
     assert bra.fault_status() == 0
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("counts", [[3, 0, 5], [1], [32], [40], [0, 129, 0, 33], [100, 1, 300], [0, 0]],
+                         ids=str)
+@pytest.mark.parametrize("long,short", [(1025, 72), (2047, 129), (3333, 8), (4224, 300), (8200, 41)])
+def test_few_tiles_and_a_long_contraction(counts, long, short, dt):
+    """Tiles whose contraction several CTAs share; rows past the counts stay as they are."""
+    x, w, b, c = case(counts, long, short, dt=dt, extra=3)
+    n = sum(counts)
+    xq, wq = bra.fp8_quantize(x), bra.fp8_quantize(w)
+    for off in (0, 1):
+        room = torch.full((off + (n + 3) * short,), 7.0, dtype=dt, device="cuda")
+        y = room[off:].view(n + 3, short)
+        bra.fp8_grouped_matmul(xq, wq, c, bias=b, out=y)
+        part = bra.Fp8Tensor(xq.codes[:n], xq.scales[:n], (n, long))
+        assert_close(y[:n], *reference(part, wq, b, counts), long)
+        assert (y[n:] == 7.0).all() and (room[:off] == 7.0).all()
+        first = y.clone()
+        bra.fp8_grouped_matmul(xq, wq, c, bias=b, out=y)
+        assert torch.equal(first, y)
+    w2 = bra.fp8_quantize(randn(len(counts), long, short, seed=4).to(dt))
+    dq = bra.fp8_quantize(x, format=E5)
+    dx = torch.full((n + 3, short), 7.0, dtype=dt, device="cuda")
+    bra.fp8_grouped_matmul_grad(dq, w2, c, out=dx)
+    part = bra.Fp8Tensor(dq.codes[:n], dq.scales[:n], (n, long))
+    assert_close(dx[:n], *reference(part, w2, None, counts, True), long)
+    assert (dx[n:] == 7.0).all()
+    assert bra.fault_status() == 0
+
+
 @pytest.mark.parametrize("xf", [E4, E5])
 @pytest.mark.parametrize("wf", [E4, E5])
 @pytest.mark.parametrize("counts", [[6, 0, 3], [300, 41, 500, 0]], ids=str)
@@ -355,6 +384,23 @@ def test_scales_whose_product_passes_the_largest_float():
     assert torch.isinf(y[0, 0]) and not torch.isnan(y).any()
     assert (y[:, 1:] == 0).all() and (y[3] == 0).all()
     assert torch.isfinite(y[1, 0]) and abs(float(y[1, 0]) / 1e38 - 1) < 0.1
+
+
+@pytest.mark.parametrize("rows", [4, 60, 400])
+def test_negative_scales_whose_product_passes_the_largest_float(rows):
+    """A checkpoint's scales have any sign: blocks whose sum is zero stay zero."""
+    c = torch.tensor([rows], device="cuda")
+    x = bra.fp8_quantize(torch.ones((rows, 256), device="cuda"), c)
+    w = torch.ones((1, 300, 256), device="cuda")
+    w[:, :, :128:2] = -1.0                                # the first block's sum is zero
+    w = bra.fp8_quantize(w)
+    x = bra.Fp8Tensor(x.codes, x.scales.clone(), x.shape)
+    w = bra.Fp8Tensor(w.codes, w.scales.clone(), w.shape)
+    x.scales[:, 0], w.scales[:, :, 0] = 1e30, -1e30
+    y = bra.fp8_grouped_matmul(x, w, c)
+    want = 128 * float(x.codes[0, 0].float() * w.codes[0, 0, 1].float() * x.scales[0, 1] *
+                       w.scales[0, 0, 1])
+    assert (y.float() == want).all()
 
 
 @pytest.mark.parametrize("counts,N", [([3, 0, 61], 72), ([1300, 0, 1200], 2053)], ids=str)

@@ -90,9 +90,11 @@ int run_product(const uint8_t* xc, const float* xs, const uint8_t* wc, const flo
                         (int)a->out, grad ? 1 : 0, a->dtype, a->x_format, a->w_format};
   if (log_enabled()) {
     const GroupedTile t = fp8_tile(g);
+    char how[32] = "";
+    if (t.rows == 256) std::snprintf(how, sizeof(how), " by CTA pairs");
+    else if (t.split > 1) std::snprintf(how, sizeof(how), ", sums over %d CTAs", t.split);
     std::fprintf(stderr, "[bra] fp8_grouped_matmul%s rows=%lld experts=%d K=%d N=%d -> %dx%d tiles%s\n",
-                 grad ? "_grad" : "", (long long)R, g.E, (int)K, (int)N, t.rows, t.cols,
-                 t.rows == 256 ? " by CTA pairs" : "");
+                 grad ? "_grad" : "", (long long)R, g.E, (int)K, (int)N, t.rows, t.cols, how);
   }
   return status_of(launch_fp8_grouped(g, st));
 }

@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(FShape<CG, BN>::THREADS, 1)
     if (CG == 1 && split > 1) {
       __syncwarp();
       cluster_sync();
+      __syncwarp();
       cluster_sync();
     }
   } else {
@@ -827,6 +828,7 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1)
 
   __syncwarp();
   if (split > 1) {               // every split-th row of all shares, added in their order
+    __syncwarp();
     cluster_sync();
     const int n = walk0 < total ? find(walk0).nt * 128 + (warp & 3) * 32 + lane : p.N;
     if (warp >= EPI_WARP0 && n < p.N) {
@@ -924,7 +926,7 @@ bool encode_codes(CUtensorMap* m, const void* base, uint64_t K, uint64_t rows, u
 
 // Parameters of a launch with tiles of `rows` rows and `cols` columns, the
 // weight read in boxes of `box` rows; the instruction is the caller's.
-bool fill(Fp8Params* out, const Fp8Problem& g, int rows, int cols, uint32_t box, int64_t* tiles) {
+bool fill(Fp8Params* out, const Fp8Problem& g, const GroupedTile& t, uint32_t box) {
   Fp8Params& p = *out;
   std::memset(&p, 0, sizeof(p));
   const int K = g.grad ? g.out : g.in, N = g.grad ? g.in : g.out;      // contraction, columns
@@ -946,46 +948,33 @@ bool fill(Fp8Params* out, const Fp8Problem& g, int rows, int cols, uint32_t box,
   p.ws_block = g.grad ? in_blocks : 1;
   p.E = g.E;
   p.N = N;
-  p.n_tiles = (N + cols - 1) / cols;
+  p.n_tiles = (N + t.cols - 1) / t.cols;
   p.k_blocks = (int)fp8::blocks(K);
   p.bias_fp16 = g.dtype == BRA_FP16;
   p.aligned = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0 && N % 8 == 0;
-  const int64_t groups = g.R < g.E ? g.R : g.E;
-  *tiles = (g.R / rows + groups) * p.n_tiles;                          // at most
-  return *tiles < (int64_t(1) << 31);
-}
-
-// CTAs to a tile, where there are few tiles: as long as all of them have an SM
-// and each at least four blocks (6 rows, 5 experts, 3823 x 128: 13.3 us alone,
-// 9.7 with eight blocks each, 7.4 with four; 4230 rows, 3 experts, 3520 x 88,
-// 33 tiles: 15.9, 14.4, 10.9; 3 rows, 1728 x 192: 8.7, 8.7, 8.2).
-int split_of(int64_t tiles, int k_blocks) {
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= 152 && k_blocks >= 4 * split * 2) split *= 2;
-  return split;
+  p.split = t.split;
+  return t.tiles < (int64_t(1) << 31);
 }
 
 template <typename T, int CG, int BN, bool GRAD>
-cudaError_t launch(const Fp8Problem& g, cudaStream_t st) {
+cudaError_t launch(const Fp8Problem& g, const GroupedTile& t, cudaStream_t st) {
   using S = FShape<CG, BN>;
   int clusters = 0;
   cudaError_t e = resident<T, CG, BN, GRAD>(&clusters);
   if (e != cudaSuccess) return e;
   Fp8Params p;
-  int64_t tiles = 0;
-  if (!fill(&p, g, 128 * CG, BN, GRAD ? 128 : S::B_COLS, &tiles)) return cudaErrorInvalidValue;
+  if (!fill(&p, g, t, GRAD ? 128 : S::B_COLS)) return cudaErrorInvalidValue;
   // D fp32 (bit 4), the codes' formats (bits 7, 10: 0 e4m3, 1 e5m2), B N-major
   // (bit 16), N >> 3 at 17, M >> 4 at 24
   p.idesc = 1u << 4 | (uint32_t)g.xf << 7 | (uint32_t)g.wf << 10 | (GRAD ? 1u << 16 : 0u) |
             (uint32_t)(BN >> 3) << 17 | (uint32_t)(8 * CG) << 24;
-  p.split = CG == 1 ? split_of(tiles, p.k_blocks) : 1;
-  const int nc = (int)(tiles < clusters ? tiles : clusters), each = CG * p.split;
+  const int nc = (int)(t.tiles < clusters ? t.tiles : clusters), each = CG * t.split;
   return launch_clusters(fp8_grouped_kernel<T, CG, BN, GRAD>, each, each * nc, S::THREADS,
                          S::SMEM_BYTES, st, p);
 }
 
 template <typename T, bool GRAD>
-cudaError_t launch_few(const Fp8Problem& g, cudaStream_t st) {
+cudaError_t launch_few(const Fp8Problem& g, const GroupedTile& t, cudaStream_t st) {
   using S = FewShape;
   static std::mutex mu;
   static int known[64] = {};
@@ -1006,46 +995,68 @@ cudaError_t launch_few(const Fp8Problem& g, cudaStream_t st) {
     sms = n;
   }
   Fp8Params p;
-  int64_t tiles = 0;
-  if (!fill(&p, g, S::ROWS, 128, 128, &tiles)) return cudaErrorInvalidValue;
+  if (!fill(&p, g, t, 128)) return cudaErrorInvalidValue;
   // as above, with the weight as A (M-major, bit 15, in the gradient)
   p.idesc = 1u << 4 | (uint32_t)g.wf << 7 | (uint32_t)g.xf << 10 | (GRAD ? 1u << 15 : 0u) |
             (uint32_t)(S::ROWS >> 3) << 17 | 8u << 24;
-  p.split = split_of(tiles, p.k_blocks);
-  return launch_clusters(fp8_few_kernel<T, GRAD>, p.split,
-                         (unsigned)(tiles < sms ? tiles : sms) * p.split, S::THREADS, S::SMEM_BYTES,
-                         st, p);
+  return launch_clusters(fp8_few_kernel<T, GRAD>, t.split,
+                         (unsigned)(t.tiles < sms ? t.tiles : sms) * t.split, S::THREADS,
+                         S::SMEM_BYTES, st, p);
 }
 
 template <int CG, int BN, bool GRAD>
-cudaError_t launch_t(const Fp8Problem& g, cudaStream_t st) {
-  return g.dtype == BRA_BF16 ? launch<__nv_bfloat16, CG, BN, GRAD>(g, st)
-                             : launch<__half, CG, BN, GRAD>(g, st);
+cudaError_t launch_t(const Fp8Problem& g, const GroupedTile& t, cudaStream_t st) {
+  return g.dtype == BRA_BF16 ? launch<__nv_bfloat16, CG, BN, GRAD>(g, t, st)
+                             : launch<__half, CG, BN, GRAD>(g, t, st);
 }
 
 template <bool GRAD>
-cudaError_t launch_few_t(const Fp8Problem& g, cudaStream_t st) {
-  return g.dtype == BRA_BF16 ? launch_few<__nv_bfloat16, GRAD>(g, st) : launch_few<__half, GRAD>(g, st);
+cudaError_t launch_few_t(const Fp8Problem& g, const GroupedTile& t, cudaStream_t st) {
+  return g.dtype == BRA_BF16 ? launch_few<__nv_bfloat16, GRAD>(g, t, st)
+                             : launch_few<__half, GRAD>(g, t, st);
+}
+
+// CTAs to a tile, where there are few tiles: as long as all of them have an SM
+// and each at least four blocks (6 rows, 5 experts, 3823 x 128: 13.3 us alone,
+// 9.7 with eight blocks each, 7.4 with four; 4230 rows, 3 experts, 3520 x 88,
+// 33 tiles: 15.9, 14.4, 10.9; 3 rows, 1728 x 192: 8.7, 8.7, 8.2).
+int split_of(int64_t tiles, int k_blocks) {
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 152 && k_blocks >= 4 * split * 2) split *= 2;
+  return split;
 }
 
 }  // namespace
 
-// The pair's tiles from 128 rows an expert, when there are tiles for a wave of
-// pairs (12 experts, 3063 rows, 1026 x 775 and its gradient, 112 and 140 tiles:
-// 14.8 us, by 128 x 128 tiles 19.6).
+// The tiles that a model of their waves finds faster: nanoseconds of a tile as
+// fitted to 30 sizes (256 x 256 by a pair: 2400 and 540 a block, 128 x 128: 1200
+// and 410), half a tile of rows lost to each expert.  us by pairs / by 128 x 128:
+// 12 experts, 3063 rows, 1026 x 775 11.9 / 15.0; 39, 60000, 2755 x 682 141 / 206;
+// 39, 60000, 1043 x 126 29.6 / 25.5; 31, 7677, 448 x 1569 29.9 / 26.2; 58, 24444,
+// 192 x 896 26.2 / 23.2.
 GroupedTile fp8_tile(const Fp8Problem& g) {
   const int64_t N = g.grad ? g.in : g.out, groups = g.R < g.E ? g.R : g.E;
-  if (g.R <= kFewRows * g.E) return {FewShape::ROWS, 128, 1, 0};
-  if (g.R / g.E >= 128 && (2 * (g.R / 256) + groups) * ((N + 255) / 256) >= 76)
-    return {256, 256, 1, 0};
-  return {128, 128, 1, 0};
+  const int64_t blocks = fp8::blocks(g.grad ? g.out : g.in);
+  auto waves = [&](int64_t side, int64_t slots) {
+    const int64_t tiles = (2 * (g.R / side) + groups) * ((N + side - 1) / side);   // twice
+    return (tiles + 2 * slots - 1) / (2 * slots);
+  };
+  GroupedTile t = {128, 128, 1, 0};
+  if (g.R <= kFewRows * g.E) t.rows = FewShape::ROWS;
+  else if (waves(256, 76) * (2400 + 540 * blocks) < waves(128, 152) * (1200 + 410 * blocks))
+    t.rows = t.cols = 256;
+  t.tiles = (g.R / t.rows + groups) * ((N + t.cols - 1) / t.cols);                 // at most
+  if (t.rows < 256) t.split = split_of(t.tiles, (int)blocks);
+  return t;
 }
 
 cudaError_t launch_fp8_grouped(const Fp8Problem& g, cudaStream_t st) {
   const GroupedTile t = fp8_tile(g);
-  if (t.rows == FewShape::ROWS) return g.grad ? launch_few_t<true>(g, st) : launch_few_t<false>(g, st);
-  if (t.rows == 256) return g.grad ? launch_t<2, 256, true>(g, st) : launch_t<2, 256, false>(g, st);
-  return g.grad ? launch_t<1, 128, true>(g, st) : launch_t<1, 128, false>(g, st);
+  if (t.rows == FewShape::ROWS)
+    return g.grad ? launch_few_t<true>(g, t, st) : launch_few_t<false>(g, t, st);
+  if (t.rows == 256)
+    return g.grad ? launch_t<2, 256, true>(g, t, st) : launch_t<2, 256, false>(g, t, st);
+  return g.grad ? launch_t<1, 128, true>(g, t, st) : launch_t<1, 128, false>(g, t, st);
 }
 
 cudaError_t read_fp8_fault_word(int32_t* code, int clear) {

@@ -261,6 +261,34 @@ def test_products_over_group_sizes(counts, K, N, dt):
     assert bra.fault_status() == 0
 
 
+@pytest.mark.parametrize("counts,K,N,tiles", [
+    ([3, 0, 5], 8200, 300, "32x128 tiles, sums over 8 CTAs"),
+    ([3, 0, 5], 1024, 2056, "32x128 tiles, sums over 2 CTAs"),
+    ([3, 0, 5], 640, 300, "32x128 tiles"), ([1] * 40, 2048, 1030, "32x128 tiles"),
+    ([200, 1, 90], 4224, 300, "128x128 tiles, sums over 8 CTAs"),
+    ([200, 1, 90], 2050, 520, "128x128 tiles, sums over 4 CTAs"),
+    ([700, 0, 513], 300, 300, "128x128 tiles"),
+    ([700, 0, 513, 1027], 640, 8200, "256x256 tiles by CTA pairs"),
+    ([4100, 3000], 130, 3333, "128x128 tiles"),
+    ([4100, 3000], 1000, 1333, "256x256 tiles by CTA pairs")], ids=str)
+def test_tiles(counts, K, N, tiles, monkeypatch, capfd):
+    """Which kernel takes a call, by its log; the results of each."""
+    monkeypatch.setenv("BRA_LOG", "1")
+    x, w, b, c = case(counts, K, N)
+    xq, wq = bra.fp8_quantize(x, c), bra.fp8_quantize(w)
+    capfd.readouterr()
+    y = bra.fp8_grouped_matmul(xq, wq, c, bias=b)
+    assert capfd.readouterr().err.strip().endswith(f"-> {tiles}")
+    assert_close(y, *reference(xq, wq, b, counts), K)
+    del x, w
+    w2 = bra.fp8_quantize((randn(len(counts), K, N, seed=9) * K ** -0.5).bfloat16())
+    dq = bra.fp8_quantize(randn(sum(counts), K, seed=7).bfloat16(), c, E5)
+    capfd.readouterr()
+    dx = bra.fp8_grouped_matmul_grad(dq, w2, c)
+    assert capfd.readouterr().err.strip().endswith(f"-> {tiles}")
+    assert_close(dx, *reference(dq, w2, None, counts, True), K)
+
+
 @pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("counts", [[3, 0, 5], [1], [32], [40], [0, 129, 0, 33], [100, 1, 300], [0, 0]],
                          ids=str)

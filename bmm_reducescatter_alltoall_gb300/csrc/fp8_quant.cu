@@ -11,7 +11,7 @@
 // 16 bits are read and 8.25 written to an element, and HBM bounds it.  A lane
 // takes 16 consecutive elements: 16 bytes of codes a store, eight lanes to a
 // row's block, three exchanges for its maximum; a warp has the loads of 2048
-// elements of a row in flight.  A weight's block is a CTA's, held in registers
+// elements in flight.  A weight's block is a CTA's, held in registers
 // between its maximum and its codes, so that it too is read once.  16384 x 4096
 // bf16: rows 30 us (6.7 TB/s), weights 31, there and back 65 (92% of the copy
 // rate).

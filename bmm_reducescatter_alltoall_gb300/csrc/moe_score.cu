@@ -11,20 +11,24 @@
 //
 // The choice is that of r and v computed in 64 bits.  They are computed in 32
 // first, with bounds on the error: where two neighbours of the order that
-// matter (the chosen ones and the next one; the last group kept and the first
+// matter (the chosen ones and the next ones; the last group kept and the first
 // left out) lie closer than the bounds, and are not the same logit and bias,
-// the token is chosen again in 64 bits: by the bounds, for 8 of 256 by sigmoid
-// with ranks some 2^-8 apart, a few tokens in a thousand.  64-bit exponentials
-// for all 16.8 million scores would take about a millisecond.
+// these alone are computed in 64 bits, an expert to a lane: by the bounds, for
+// 8 of 256 by sigmoid with ranks some 2^-8 apart, in a few tokens in a
+// thousand.  64-bit exponentials for all 16.8 million scores would take about a
+// millisecond.  A softmax's sum stays the one in 32 bits there, as a common
+// factor of the scores it decides few orders; where it may, and where more
+// experts are close than a token's lanes list, the whole token is computed in
+// 64 bits.
 //
 // As in moe_route.cu a group of L lanes takes a token.  A group of experts has
 // lanes of its own (a power of two), so that its two largest are found in the
 // sorted lists' heads and exchanges among these lanes; places of the lanes
 // past a group's experts stay empty.  Chunks, bits and places are shared
 // with moe_route.cu.
-// The compares and selects bound it (issue slots 69% busy, some 900
+// The compares and selects bound it (issue slots 75% busy, some 900
 // instructions a token of 256 experts): 65536 tokens, 8 of 256 in 4 of 8
-// groups, 85 us for the choices, where the logits' 67 MB take 10.
+// groups, 80 us for the choices, where the logits' 67 MB take 10.
 #include <mutex>
 #include <type_traits>
 

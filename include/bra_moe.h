@@ -231,6 +231,8 @@ BRA_API int64_t fp8_scale_bytes(const bra_fp8_args* args);
  * counts: NULL, or for rows device int64 (E): rows past their sum are neither
  * read nor written, and counts are checked on the device as in
  * grouped_matmul.  A row's codes and scales do not depend on its group.
+ * Elements between two rows of x (x_pitch above K) may be read; they do not
+ * count.
  * Errors: BRA_ERR_NULLPTR for a NULL args, or data with R > 0;
  * BRA_ERR_INVALID for sizes outside the ranges, rows other than groups *
  * rows_per_group, counts with weights, another dtype or format, a pitch below
@@ -264,7 +266,8 @@ typedef struct {
  *   y[r, n] = sum over blocks b of sx[r, b] * sw[e, n/128, b] *
  *             (sum of the codes' products of block b) + bias[e, n],
  * sums, scales' products and the bias in fp32, one rounding to dtype.  The
- * product of two finite scales that passes the largest float counts as that.
+ * product of two scales that passes the largest float, of either sign, counts
+ * as that.
  * fp8_grouped_matmul_grad -- its gradient of x for the output's gradient, on
  * the same weight: dy rows (R, N),
  *   dx[r, k] = sum over blocks b of N of sd[r, b] * sw[e, b, k/128] * (...).

@@ -15,13 +15,17 @@
 // columns, N-major.
 //
 // What bounds it: with 256 x 256 tiles the two block accumulators' round trip
-// (65536 rows, 4096 x 4096: 935 us, 2350 TFLOP/s).  A block's MMAs take some
+// (65536 rows, 4096 x 4096: 905 us, 2430 TFLOP/s).  A block's MMAs take some
 // 380 ns, but an accumulator is free only after its commit, the loads of its
-// sums and the pair's hand-back, so that a block takes 540 ns: the same product
-// takes 860 us without the additions, 820 without the loads too, and 655 with
-// one hand-back a tile, as a plain 8-bit product has.  Smaller accumulators do
-// not help: a pair's MMA of 128 columns takes as long as one of 256 (tiles of
-// 256 x 128: 1420 us; accumulators in two halves: 1157).
+// sums and the pair's hand-back, so that a block takes 520 ns: at 935 us, the
+// same product took 860 without the additions, 820 without the loads too, and
+// 655 with one hand-back a tile, as a plain 8-bit product has.  Smaller
+// accumulators do not help: a pair's MMA of 128 columns takes as long as one of
+// 256 (tiles of 256 x 128: 1420 us; accumulators in two halves: 1157).
+// Storing a tile is next: whole boxes of 32 rows and 64 columns go by TMA, as
+// the epilogue warps are then free for the next tile's blocks (87108 rows, 384 x
+// 1304: 113 us by the warps' own stores, 99 so, 73 without stores); rows
+// without a 16-byte pitch and a group's last rows by the warps.
 // With few rows HBM does (below), and with few tiles the blocks of a tile, one
 // after the other: then a cluster of 2, 4 or 8 CTAs shares a tile's blocks, each
 // leaves its sums in its shared memory, and each adds up a part of the rows of
@@ -55,6 +59,7 @@ constexpr int BAR_BYTES = 512;
 struct Fp8Params {
   CUtensorMap ta, ta32;                     // row codes, boxes of 128 and 32 rows
   CUtensorMap tb;                           // weight codes
+  CUtensorMap ty;                           // y, boxes of 64 columns and 32 rows, if y_boxes
   const float* xs;
   const float* ws;
   const void* bias;
@@ -65,7 +70,7 @@ struct Fp8Params {
   int64_t ws_group, ws_out, ws_block;       // weight scales: from expert to expert, from output
                                             // block to output block, from K block to K block
   int E, N, n_tiles, k_blocks;              // N: columns of the output
-  int bias_fp16, aligned;
+  int bias_fp16, aligned, y_boxes;
   int split;                                // CTAs that share a tile's K blocks (one tile each)
   uint32_t idesc;
 };
@@ -81,7 +86,10 @@ struct FShape {
   static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
   static constexpr int NBUF = BN == 256 ? 2 : 4;          // block accumulators
   static constexpr uint32_t TMEM_COLS = NBUF * BN;
-  static constexpr int EPI_BYTES = EPI_WARPS * (kSegBytes + WC * 4);
+  // each epilogue warp's segment (also a box of 32 swizzled rows of 128 bytes)
+  static constexpr int SEG_BYTES = 5120;
+  static_assert(SEG_BYTES >= kSegBytes && SEG_BYTES % 1024 == 0, "segments");
+  static constexpr int EPI_BYTES = EPI_WARPS * (SEG_BYTES + WC * 4);
   static constexpr int FIXED = BAR_BYTES + EPI_BYTES + (int)sizeof(GroupTable) + 16 + 1024;
   static constexpr int FIT = (232448 - FIXED) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
@@ -168,6 +176,15 @@ __device__ __forceinline__ void regs_to(bool up) {
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A box of y from shared memory, behind this thread's next wait.
+__device__ __forceinline__ void put_box(const CUtensorMap* m, uint32_t src, int col, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(m),
+      "r"(src), "r"(col), "r"(row), "r"(0)
+      : "memory");
+}
+
 // The K blocks of one CTA of those that share a tile: whole groups of four, as
 // scales are read.
 __device__ __forceinline__ int share_begin(int k_blocks, int share, int split) {
@@ -195,7 +212,8 @@ __global__ void __launch_bounds__(FShape<CG, BN>::THREADS, 1)
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   const uint32_t smem_base = smem_u32(smem);
-  uint8_t* bars = smem + STAGES * STAGE_BYTES;
+  uint8_t* segs = smem + STAGES * STAGE_BYTES;
+  uint8_t* bars = segs + S::EPI_WARPS * S::SEG_BYTES;
   const uint32_t bar_base = smem_u32(bars);
   // barriers (8 bytes each): per stage full (leader: both CTAs' bytes) and
   // empty; per block accumulator tfull and tempty (leader: both CTAs' warps)
@@ -207,7 +225,7 @@ __global__ void __launch_bounds__(FShape<CG, BN>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + BAR_BYTES - 16);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + BAR_BYTES - 8);
   GroupTable* gt = reinterpret_cast<GroupTable*>(bars + BAR_BYTES);
-  uint8_t* epi = bars + BAR_BYTES + ((sizeof(GroupTable) + 15) & ~15);
+  uint8_t* bias_rows = bars + BAR_BYTES + ((sizeof(GroupTable) + 15) & ~15);
   int32_t* fault = &g_bra_fault_word_fp8;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -354,8 +372,8 @@ __global__ void __launch_bounds__(FShape<CG, BN>::THREADS, 1)
     regs_to<S::EPI_REGS>(true);
     // ---------------- epilogue: lane quarter q, columns h*WC .. +WC ----------------
     const int q = warp & 3, h = (warp - EPI_WARP0) >> 2;
-    uint8_t* mine = epi + (warp - EPI_WARP0) * (kSegBytes + WC * 4);
-    const uint32_t seg = smem_u32(mine), bias_s = seg + kSegBytes;
+    const uint32_t seg = smem_u32(segs + (warp - EPI_WARP0) * S::SEG_BYTES);
+    const uint32_t bias_s = smem_u32(bias_rows + (warp - EPI_WARP0) * WC * 4);
     const uint32_t leader_tempty0 = CG == 2 ? map_to_rank(tempty_bar(0), 0) : tempty_bar(0);
     int buf = 0;
     uint32_t buf_phase = 0;
@@ -415,20 +433,40 @@ __global__ void __launch_bounds__(FShape<CG, BN>::THREADS, 1)
     };
     uint32_t o[WC / 64][32];          // the tile before, rounded
     T* y0 = nullptr;
-    int n0 = 0, valid = 0;
+    int row = 0, n0 = 0, valid = 0;
+    auto segment_free = [&] {         // the box before has been read
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+    };
     for (int t = walk0; ok; t += step) {
       if (t < total) begin(t);
       if (valid > 0) {
-        const int segs = min(WC / 64, (p.N - n0 + 63) / 64);
-        Carry carry;
+        const int parts = min(WC / 64, (p.N - n0 + 63) / 64);
+        segment_free();
+        if (p.y_boxes && valid == 32) {
 #pragma unroll
-        for (int ch = 0; ch < WC / 64; ++ch)
-          if (ch < segs)
-            put_segment<T>(o[ch], carry, ch == 0, ch + 1 == segs, y0, p.ldy, valid, n0 + ch * 64, p.N,
-                           seg, p.aligned != 0, lane, [] {});
+          for (int ch = 0; ch < WC / 64; ++ch)
+            if (ch < parts) {
+              if (ch > 0) segment_free();
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                sts128(seg + lane * 128 + ((i ^ (lane & 7)) << 4),
+                       make_uint4(o[ch][4 * i], o[ch][4 * i + 1], o[ch][4 * i + 2], o[ch][4 * i + 3]));
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) put_box(&p.ty, seg, n0 + ch * 64, row);
+            }
+        } else {
+          Carry carry;
+#pragma unroll
+          for (int ch = 0; ch < WC / 64; ++ch)
+            if (ch < parts)
+              put_segment<T>(o[ch], carry, ch == 0, ch + 1 == parts, y0, p.ldy, valid, n0 + ch * 64,
+                             p.N, seg, p.aligned != 0, lane, [] {});
+        }
       }
       if (t >= total) break;
-      n0 = c.n0, valid = c.valid;
+      row = c.row, n0 = c.n0, valid = c.valid;
       if (valid <= 0) {
         for (int kb = kb0; kb < kb1; ++kb) {
           const bool got = wait_here(tfull_bar(buf), buf_phase, abort_flag, fault);
@@ -518,6 +556,7 @@ __global__ void __launch_bounds__(FShape<CG, BN>::THREADS, 1)
         pack_segment<T>(v, o[ch], p.bias ? bias_s + ch * 256 : 0u, false);
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (CG == 1 && split > 1) {        // 128 / split rows of all shares, added in their order
       __syncwarp();
       cluster_sync();
@@ -953,6 +992,12 @@ bool fill(Fp8Params* out, const Fp8Problem& g, const GroupedTile& t, uint32_t bo
   p.bias_fp16 = g.dtype == BRA_FP16;
   p.aligned = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0 && N % 8 == 0;
   p.split = t.split;
+  // whole boxes of rows go by TMA: rows at a 16-byte pitch (strides below 2^40)
+  const CUtensorMapDataType dt =
+      g.dtype == BRA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  p.y_boxes = t.rows >= 128 && (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0 &&
+              g.ldy <= (int64_t(1) << 38) / g.R &&
+              encode_3d(&p.ty, dt, g.y, N, g.R, 1, 64, 32, g.ldy);
   return t.tiles < (int64_t(1) << 31);
 }
 

@@ -992,11 +992,11 @@ bool fill(Fp8Params* out, const Fp8Problem& g, const GroupedTile& t, uint32_t bo
   p.bias_fp16 = g.dtype == BRA_FP16;
   p.aligned = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0 && N % 8 == 0;
   p.split = t.split;
-  // whole boxes of rows go by TMA: rows at a 16-byte pitch (strides below 2^40)
+  // whole boxes of rows go by TMA: rows of whole 16 bytes (it writes the last
+  // ones whole, also past the row's end) at such a pitch, strides below 2^40
   const CUtensorMapDataType dt =
       g.dtype == BRA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  p.y_boxes = t.rows >= 128 && (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % 8 == 0 &&
-              g.ldy <= (int64_t(1) << 38) / g.R &&
+  p.y_boxes = t.rows >= 128 && p.aligned && g.ldy <= (int64_t(1) << 38) / g.R &&
               encode_3d(&p.ty, dt, g.y, N, g.R, 1, 64, 32, g.ldy);
   return t.tiles < (int64_t(1) << 31);
 }

@@ -446,6 +446,27 @@ def test_rows_past_the_groups_and_row_pitch(counts, N):
         assert (buf[:, :shift] == 7.0).all()
 
 
+@pytest.mark.parametrize("dt", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("N,gap", [(200, 8), (1288, 16), (2053, 3), (1001, 7)])
+@pytest.mark.parametrize("counts", [[300, 33, 31, 500], [1300, 0, 1201, 64, 95]], ids=str)
+def test_whole_boxes_between_gaps(counts, N, gap, dt):
+    """Rows at a 16-byte pitch of any length, stored in boxes: whole ones, parts of groups, and
+    nothing between the rows or behind them."""
+    n = sum(counts)
+    x, w, b, c = case(counts, 200, N, dt=dt, extra=40)
+    xq, wq = bra.fp8_quantize(x), bra.fp8_quantize(w)
+    z = bra.Fp8Tensor(xq.codes[:n], xq.scales[:n], (n, 200))
+    buf = torch.full((n + 40, N + gap), 7.0, dtype=dt, device="cuda")
+    bra.fp8_grouped_matmul(xq, wq, c, bias=b, out=buf[:, :N])
+    assert_close(buf[:n, :N], *reference(z, wq, b, counts), 200)
+    assert (buf[n:] == 7.0).all() and (buf[:, N:] == 7.0).all()
+    w2 = bra.fp8_quantize(randn(len(counts), 200, N, seed=3).to(dt))
+    dx = torch.full((n + 40, N + gap), 7.0, dtype=dt, device="cuda")
+    bra.fp8_grouped_matmul_grad(xq, w2, c, out=dx[:, :N])
+    assert_close(dx[:n, :N], *reference(z, w2, None, counts, True), 200)
+    assert (dx[n:] == 7.0).all() and (dx[:, N:] == 7.0).all()
+
+
 @pytest.mark.parametrize("K,N", [(4096, 64), (64, 4104)])
 def test_matrices_that_pass_32_bit_offsets(K, N):
     """Rows (of x, or of y) whose byte offsets pass 2^32, in the last two groups."""

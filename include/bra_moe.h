@@ -368,7 +368,8 @@ typedef struct {
  * is one).  Among the top_groups groups of the highest rank the k experts of
  * the highest rank are chosen, highest first; ties go to the lowest group and
  * the lowest expert.  With top_groups = G groups do not matter.  The choice is
- * the one that scores, ranks and sums in 64 bits give.
+ * the one that scores, ranks and sums in 64 bits give (either one where only
+ * their rounding tells two apart).
  *   bias    NULL, or device (E) fp32: what a user moves to balance the load.
  *           It changes the choice alone, not the weights.  An expert whose
  *           bias is -inf or NaN is never chosen; it stays open to the softmax.
